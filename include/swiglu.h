@@ -355,6 +355,55 @@ SWIGLU_API swiglu_status_t swiglu_down_plan_string_ws(int64_t M, int64_t N, int6
                                                       size_t buflen);
 
 /*
+ * Gradients of the gated MLP, for training on the packed weights the forward
+ * calls use. No passage of the pages covers training; the formulas are the
+ * derivatives of the definition ("Tile-Level Activation Overlap for Efficient
+ * LLM Inference", gist.science, section "Problem Statement"). With G = A x W1,
+ * U = A x W2, s = 1 / (1 + exp(-G)):
+ *   dU = dY (.) G s        dG = dY (.) U s (1 + G (1 - s))
+ *   dA [M, K] = dG x W1^T + dU x W2^T
+ *   dW1 [K, N] = A^T x dG      dW2 [K, N] = A^T x dU
+ * G and U are recomputed from A and the packed weight (the forward never
+ * stores them) and stay in fp32; dG and dU are rounded once to bf16 as tensor-
+ * core operands; every sum is fp32 and every output is rounded once to bf16.
+ * Results do not depend on timing.
+ *
+ * swiglu_backward_workspace_bytes(M, K, N): bytes of the workspace the call
+ *   needs on the current device (dG and dU, and fp32 partial sums where a
+ *   product has few output tiles); 0 on M = 0, a bad shape or no usable device.
+ * swiglu_backward: A [M, K], dY [M, N] bf16; Wpacked from swiglu_pack_weights
+ *   with the same K and N; dA, dW1, dW2 are written in full, each [.] bf16
+ *   row-major as its forward counterpart. dA NULL: not computed (the block's
+ *   input needs no gradient). dW1 and dW2 both NULL: not computed (frozen
+ *   weights); one NULL: INVALID_ARG. `workspace`: device, 16-byte aligned,
+ *   `workspace_bytes` at least the size above; its contents need no set-up and
+ *   mean nothing after the call. Calls that may run at the same time need
+ *   separate workspaces. No output or workspace may overlap anything else.
+ *   M = 0: dW1 and dW2 are set to zero, A, dY and the workspace are not used.
+ * Errors as swiglu_forward.
+ */
+SWIGLU_API size_t swiglu_backward_workspace_bytes(int64_t M, int64_t K, int64_t N);
+SWIGLU_API swiglu_status_t swiglu_backward(const void* A, const void* Wpacked, const void* dY,
+                                           void* dA, void* dW1, void* dW2, int64_t M, int64_t K,
+                                           int64_t N, void* workspace, size_t workspace_bytes,
+                                           swiglu_stream_t stream);
+
+/*
+ * Gradients of the down-projection Out = Y x W3 + R:
+ *   dY [M, N] = dOut x W3^T      dW3 [N, H] = Y^T x dOut      (dR = dOut)
+ * dOut [M, H], Y [M, N] bf16; W3packed from swiglu_pack_down_weights. dY NULL:
+ * not computed (W3packed is then not used); dW3 NULL: not computed (Y is then
+ * not used). `workspace` as above; it may be NULL when
+ * swiglu_down_backward_workspace_bytes(M, N, H) is 0. M = 0: dW3 is set to
+ * zero. Errors as swiglu_forward.
+ */
+SWIGLU_API size_t swiglu_down_backward_workspace_bytes(int64_t M, int64_t N, int64_t H);
+SWIGLU_API swiglu_status_t swiglu_down_backward(const void* dOut, const void* W3packed,
+                                                const void* Y, void* dY, void* dW3, int64_t M,
+                                                int64_t N, int64_t H, void* workspace,
+                                                size_t workspace_bytes, swiglu_stream_t stream);
+
+/*
  * Allocation-free forward for callers that cannot call cudaMalloc: serving
  * runtimes that reserve all device memory for their own pools up front (a
  * library allocation would fail, or would fragment memory the runtime plans

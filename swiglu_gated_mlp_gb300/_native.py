@@ -91,6 +91,14 @@ lib.swiglu_plan_string_mxfp8.argtypes = [_i64, _i64, _i64, ctypes.c_char_p, _sz]
 lib.swiglu_plan_string_mxfp8.restype = _int
 lib.swiglu_forward_noalloc.argtypes = [_vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp]
 lib.swiglu_forward_noalloc.restype = _int
+lib.swiglu_backward_workspace_bytes.argtypes = [_i64, _i64, _i64]
+lib.swiglu_backward_workspace_bytes.restype = _sz
+lib.swiglu_backward.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _sz, _vp]
+lib.swiglu_backward.restype = _int
+lib.swiglu_down_backward_workspace_bytes.argtypes = [_i64, _i64, _i64]
+lib.swiglu_down_backward_workspace_bytes.restype = _sz
+lib.swiglu_down_backward.argtypes = [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _sz, _vp]
+lib.swiglu_down_backward.restype = _int
 lib.swiglu_testing_inject_stall.argtypes = [_int, _u32]
 lib.swiglu_testing_inject_stall.restype = None
 lib.swiglu_testing_pace_run_out.argtypes = [ctypes.POINTER(ctypes.c_uint64)]
@@ -468,6 +476,145 @@ def swiglu_down_forward(Y: torch.Tensor, W3packed: torch.Tensor, H: int,
                                        M, N, H, _stream_handle(stream, Y.device)),
                "swiglu_down_forward")
     return Out
+
+
+def _on_stream(t: torch.Tensor, stream) -> torch.Tensor:
+    """`t`, which this binding allocated on the current stream, kept until `stream` is done with it."""
+    if stream is not None:
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream), device=t.device)
+        t.record_stream(stream)
+    return t
+
+
+def _output(t, name: str, shape, like: torch.Tensor, stream) -> torch.Tensor:
+    """A caller's output tensor, checked, or a new one."""
+    if t is None:
+        return _on_stream(torch.empty(shape, dtype=torch.bfloat16, device=like.device), stream)
+    _dev_bf16(t, name)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}")
+    return t
+
+
+def _same_device(like: torch.Tensor, **others) -> None:
+    for name, t in others.items():
+        if t is not None and t.device != like.device:
+            raise ValueError(f"{name} must be on {like.device}, got {t.device}")
+
+
+def _workspace(ws, nbytes: int, like: torch.Tensor, stream) -> torch.Tensor:
+    """A caller's workspace, checked, or a new one of `nbytes`."""
+    if ws is None:
+        return _on_stream(torch.empty(nbytes, dtype=torch.uint8, device=like.device), stream)
+    if not ws.is_cuda or ws.device != like.device or not ws.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous CUDA tensor on {like.device}")
+    return ws
+
+
+def _ptr(t):
+    return t.data_ptr() if t is not None else None
+
+
+def _new_workspace(bytes_fn, device, *shape) -> torch.Tensor:
+    device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    with _on_device(device):
+        return torch.empty(bytes_fn(*shape), dtype=torch.uint8, device=device)
+
+
+def swiglu_backward_workspace_bytes(M: int, K: int, N: int) -> int:
+    return int(lib.swiglu_backward_workspace_bytes(int(M), int(K), int(N)))
+
+
+def swiglu_backward_workspace(M: int, K: int, N: int, device=None) -> torch.Tensor:
+    """A workspace for swiglu_backward at (M, K, N); one serves any number of calls in stream order."""
+    return _new_workspace(swiglu_backward_workspace_bytes, device, M, K, N)
+
+
+def swiglu_backward(A: torch.Tensor, Wpacked: torch.Tensor, dY: torch.Tensor,
+                    dA: torch.Tensor | None = None, dW1: torch.Tensor | None = None,
+                    dW2: torch.Tensor | None = None, need_input: bool = True,
+                    need_weight: bool = True, workspace: torch.Tensor | None = None, stream=None):
+    """(dA [M, K], dW1 [K, N], dW2 [K, N]) of Y = SiLU(A W1) * (A W2) from A [M, K] and dY [M, N].
+
+    Gate and Up are recomputed from A and the packed weight. What need_input
+    or need_weight turns off is None. Without `workspace` (from
+    swiglu_backward_workspace) one is allocated for the call.
+    """
+    _dev_bf16(A, "A")
+    _dev_bf16(Wpacked, "Wpacked")
+    _dev_bf16(dY, "dY")
+    if A.dim() != 2 or dY.dim() != 2 or A.shape[0] != dY.shape[0]:
+        raise ValueError("A must be [M, K] and dY [M, N]")
+    (M, K), N = A.shape, dY.shape[1]
+    if Wpacked.numel() * 2 < swiglu_packed_weight_bytes(K, N):
+        raise ValueError("Wpacked does not hold a packed weight for this K and N")
+    _same_device(A, Wpacked=Wpacked, dY=dY, dA=dA, dW1=dW1, dW2=dW2)
+    with _on_device(A.device):
+        dA = _output(dA, "dA", (M, K), A, stream) if need_input else None
+        dW1 = _output(dW1, "dW1", (K, N), A, stream) if need_weight else None
+        dW2 = _output(dW2, "dW2", (K, N), A, stream) if need_weight else None
+        if workspace is None and M:
+            workspace = _workspace(None, swiglu_backward_workspace_bytes(M, K, N), A, stream)
+        elif workspace is not None:
+            _workspace(workspace, 0, A, stream)
+        _check(lib.swiglu_backward(
+            A.data_ptr(), Wpacked.data_ptr(), dY.data_ptr(), _ptr(dA), _ptr(dW1), _ptr(dW2), M, K, N,
+            _ptr(workspace), workspace.numel() * workspace.element_size() if workspace is not None else 0,
+            _stream_handle(stream, A.device)), "swiglu_backward")
+    return dA, dW1, dW2
+
+
+def swiglu_down_backward_workspace_bytes(M: int, N: int, H: int) -> int:
+    return int(lib.swiglu_down_backward_workspace_bytes(int(M), int(N), int(H)))
+
+
+def swiglu_down_backward_workspace(M: int, N: int, H: int, device=None) -> torch.Tensor:
+    """A workspace for swiglu_down_backward at (M, N, H), possibly of no bytes."""
+    return _new_workspace(swiglu_down_backward_workspace_bytes, device, M, N, H)
+
+
+def swiglu_down_backward(dOut: torch.Tensor, W3packed: torch.Tensor | None, Y: torch.Tensor | None,
+                         dY: torch.Tensor | None = None, dW3: torch.Tensor | None = None,
+                         N: int | None = None, need_input: bool = True, need_weight: bool = True,
+                         workspace: torch.Tensor | None = None, stream=None):
+    """(dY [M, N], dW3 [N, H]) of Out = Y W3 + R from dOut [M, H], the packed W3 and Y [M, N] (dR = dOut).
+
+    W3packed is needed for dY only, Y for dW3 only; without Y, N says its width.
+    """
+    _dev_bf16(dOut, "dOut")
+    if dOut.dim() != 2:
+        raise ValueError("dOut must be [M, H]")
+    M, H = dOut.shape
+    if need_weight and Y is None:
+        raise ValueError("dW3 needs Y")
+    if need_input and W3packed is None:
+        raise ValueError("dY needs W3packed")
+    if Y is not None:
+        _dev_bf16(Y, "Y")
+        if Y.dim() != 2 or Y.shape[0] != M or (N is not None and Y.shape[1] != N):
+            raise ValueError("Y must be [M, N]")
+        N = Y.shape[1]
+    if N is None:
+        raise ValueError("N is needed without Y")
+    if W3packed is not None:
+        _dev_bf16(W3packed, "W3packed")
+        if W3packed.numel() * 2 < swiglu_down_packed_bytes(N, H):
+            raise ValueError("W3packed does not hold a packed W3 for this N and H")
+    _same_device(dOut, W3packed=W3packed, Y=Y, dY=dY, dW3=dW3)
+    with _on_device(dOut.device):
+        dY = _output(dY, "dY", (M, N), dOut, stream) if need_input else None
+        dW3 = _output(dW3, "dW3", (N, H), dOut, stream) if need_weight else None
+        if workspace is None and M:
+            workspace = _workspace(None, swiglu_down_backward_workspace_bytes(M, N, H), dOut, stream)
+        elif workspace is not None:
+            _workspace(workspace, 0, dOut, stream)
+        _check(lib.swiglu_down_backward(
+            dOut.data_ptr(), _ptr(W3packed), _ptr(Y), _ptr(dY), _ptr(dW3), M, N, H,
+            (_ptr(workspace) or None) if workspace is not None else None,
+            workspace.numel() * workspace.element_size() if workspace is not None else 0,
+            _stream_handle(stream, dOut.device)), "swiglu_down_backward")
+    return dY, dW3
 
 
 def swiglu_forward_from_host(A_host: torch.Tensor, Wpacked: torch.Tensor, N: int,

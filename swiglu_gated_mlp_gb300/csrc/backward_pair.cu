@@ -1,0 +1,529 @@
+// Gradients of the gated MLP's two projections as tcgen05 products on CTA
+// pairs (cta_group::2, 256 x 256 output tiles, fp32 accumulators in TMEM).
+//
+// Forward (fused_large_m_pair.cu): G = A W1, U = A W2, Y = SiLU(G) * U, and
+// Out = Y W3 + R. With s = 1 / (1 + e^-G) the gradients are
+//   dU = dY * G s,   dG = dY * U * s (1 + G (1 - s))          (kGrad)
+//   dA = dG W1^T + dU W2^T          or   dY = dOut W3^T       (kInput)
+//   dW1 = A^T dG, dW2 = A^T dU      or   dW3 = Y^T dOut       (kWeight)
+// G and U are not kept by the forward; kGrad recomputes them in the forward's
+// own pipeline and its epilogue turns the fp32 accumulators and dY into dG and
+// dU, each rounded once to bf16: they are operands of tensor-core products, and
+// an operand held in 32 bits would run at half the rate (tf32) or three times
+// the products (split bf16). The rounding is independent from element to
+// element, so the relative error of a gradient grows by sqrt(2) over rounding
+// its exact value to bf16, whatever the length of the sum.
+//
+// One kernel body, three operand shapes. Every load is a TMA box of 128-byte
+// rows under the 128-byte swizzle; what differs is which tensor dimension is
+// contiguous and so which "major" the MMA descriptors state:
+//   kGrad    rows [m][k] x packed weight [n][k]: both contiguous along the sum
+//   kInput   rows [m][n] contiguous along the sum; the packed weight's tiles
+//            [n][64 k] hold the sum along their rows (MN-major), so the same
+//            packed weight serves the forward and this product, no transpose
+//   kWeight  both operands are row-major with the sum (tokens) down the rows:
+//            MN-major twice, no transposed copy of anything is written
+// An MN-major operand is stored as 64-element x 64-row boxes of 8 KB: 8-row
+// groups 1024 bytes apart along the sum, the next 64 elements 8 KB further.
+//
+// Roles as in the forward pair kernel: warp 0 TMA producer, warp 1 MMA issuer
+// (even CTA), warps 2-5 epilogue; 6 stages of 32 KB per CTA; two accumulators
+// of 256 columns, so a tile's epilogue runs under the next tile's MMAs; every
+// wait is bounded (ptx.cuh).
+//
+// Few output tiles: with `splits` > 1 each tile's sum is cut into that many
+// parts, each part's fp32 accumulator goes to the workspace and
+// reduce_parts_kernel adds the parts in order (results do not depend on
+// timing) and rounds once.
+#include "kernels.h"
+#include "ptx.cuh"
+
+namespace swg {
+namespace {
+
+constexpr int kOperandBytes = 128 * kBlockK * 2;       // 16 KB: 128 rows (or columns) x 64 of the sum
+constexpr int kStageBytes = 2 * kOperandBytes;         // per CTA
+constexpr int kStages = 6;
+constexpr int kAccCols = 256;
+constexpr int kStgBytes = 32 * 128;                    // 32 rows x 128 B store staging
+constexpr int kNumStg = 8;                             // 2 per epilogue warp
+constexpr int kBarBytes = 256;
+constexpr size_t kSmem = 1024 + size_t(kStages) * kStageBytes + size_t(kNumStg) * kStgBytes + kBarBytes;
+static_assert(kSmem <= 232448, "shared memory budget");
+static_assert(8 * (2 * kStages + 5) + 8 <= kBarBytes, "barrier slots");
+
+__device__ __forceinline__ void tile_coords(int t, int tiles_m, int tiles_n, int group_m, int& mb,
+                                            int& nb) {
+  const int per_group = group_m * tiles_n;
+  const int g = t / per_group;
+  const int first_m = g * group_m;
+  const int gm = min(tiles_m - first_m, group_m);
+  const int r = t - g * per_group;
+  mb = first_m + r % gm;
+  nb = r / gm;
+}
+
+// dG and dU of one element. For |g| large s (1 - s) g -> 0 and no term
+// overflows: e^-g = +inf gives s = 0 and g * 0 = -0 for finite g.
+__device__ __forceinline__ void gate_grads(float g, float u, float dy, float& dg, float& du) {
+  const float s = __fdividef(1.0f, 1.0f + __expf(-g));
+  const float gs = g * s;
+  du = dy * gs;
+  dg = dy * u * (s + gs * (1.0f - s));
+}
+
+template <int kMode>
+__global__ void __launch_bounds__(kThreads, 1)
+    backward_pair_kernel(const __grid_constant__ BackwardParams p) {
+  constexpr bool kGradMode = kMode == kBackwardGrad;
+  constexpr bool kMnA = kMode == kBackwardWeight, kMnB = kMode != kBackwardGrad;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  const uint32_t sA = smem_addr(smem);
+  const uint32_t sB = sA + kStages * kOperandBytes;
+  const uint32_t sStg = sB + kStages * kOperandBytes;
+  uint8_t* bar_ptr = smem + size_t(kStages) * kStageBytes + kNumStg * kStgBytes;
+  const uint32_t bar0 = smem_addr(bar_ptr);
+  // barrier slots: full[S] | empty[S] | tmem_full[2] | tmem_empty[2] | drain
+  const uint32_t full0 = bar0, empty0 = bar0 + 8u * kStages;
+  const uint32_t tfull0 = bar0 + 16u * kStages, tempty0 = tfull0 + 16u;
+  const uint32_t drain_bar = tempty0 + 16u;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_ptr + 8 * (2 * kStages + 5));
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+  const int pair = static_cast<int>(cluster_id_x());
+  const int pairs = static_cast<int>(cluster_count_x());
+  const int splits = kGradMode ? 1 : p.splits;
+  const int num_units = p.tiles_m * p.tiles_n * splits;  // unit = tile * splits + part
+  const WaitCtx wc{abort_flag, p.status, p.timeout_ns};
+  const uint32_t full0_lead = mapa_shared(full0, 0);
+  const uint32_t tempty0_lead = mapa_shared(tempty0, 0);
+
+  if (threadIdx.x == 0) {
+    prefetch_tmap(&p.tmap_a0);
+    prefetch_tmap(&p.tmap_b0);
+    prefetch_tmap(&p.tmap_o0);
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(full0 + 8u * s, 1);   // rank 0's producer arrives (with both CTAs' bytes)
+      mbar_init(empty0 + 8u * s, 1);  // rank 0's MMA commit, multicast to both CTAs
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(tfull0 + 8u * b, 1);   // multicast MMA commit
+      mbar_init(tempty0 + 8u * b, 8);  // 4 epilogue warps x 2 CTAs (used on rank 0)
+    }
+    mbar_init(drain_bar, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(smem_addr(tmem_slot), 2 * kAccCols);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  cluster_sync();  // both CTAs' barriers initialised and TMEM allocated
+  tc_fence_after();
+  const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
+  pdl_wait();
+
+  if (warp == 0) {
+    // ------------------------------------------------ TMA producer (both CTAs)
+    if (lane == 0) {
+      int s = 0;
+      uint32_t ph = 0;
+      uint32_t filled = 0, fill_ph = 0;
+      bool skip_once = p.inject_stall != 0;
+      bool ok = true;
+      for (int t = pair; ok && t < num_units; t += pairs) {
+        int mb, nb;
+        const int part = t % splits;
+        tile_coords(t / splits, p.tiles_m, p.tiles_n, p.group_m, mb, nb);
+        const int r0 = mb * 2 * kTileM + static_cast<int>(rank) * kTileM;  // output row of this CTA
+        const int begin = static_cast<int>(int64_t(part) * p.slices / splits);
+        const int end = static_cast<int>(int64_t(part + 1) * p.slices / splits);
+        for (int i = begin; i < end; ++i) {
+          if (!mbar_wait(empty0 + 8u * s, ph ^ 1u, wc, kSiteProducerEmpty)) {
+            ok = false;
+            break;
+          }
+          if (skip_once) {
+            skip_once = false;  // testing hook: both CTAs leave this stage unfilled
+          } else {
+            if (leader) mbar_arrive_expect_tx(full0 + 8u * s, 2 * kStageBytes);
+            const uint32_t fb = full0_lead + 8u * s;
+            const uint32_t da = sA + s * kOperandBytes, db = sB + s * kOperandBytes;
+            if constexpr (kMode == kBackwardGrad) {
+              // A rows [r0, +128); gate (rank 0) or up (rank 1) rows of tile (nb, i)
+              tma_load_2d_pair(da, &p.tmap_a0, fb, i * kBlockK, r0);
+              tma_load_3d_pair(db, &p.tmap_b0, fb, 0, static_cast<int>(rank) * kPackBlockN,
+                               nb * p.slices + i);
+            } else if constexpr (kMode == kBackwardInput) {
+              // slice i of the sum: rows [64 c, +64) of packed tile row j. A gate/up
+              // tile holds 128 gate then 128 up columns, a down tile 256 columns.
+              const int j = i >> 2, c = i & 3;
+              if (p.two)
+                tma_load_2d_pair(da, c < 2 ? &p.tmap_a0 : &p.tmap_a1, fb,
+                                 j * kPackBlockN + (c & 1) * kBlockK, r0);
+              else
+                tma_load_2d_pair(da, &p.tmap_a0, fb, i * kBlockK, r0);
+              // this CTA's 128 output columns: two 64-column blocks of the packed tiles
+              // (a block past the last one reads another tile or zeros; its columns
+              // lie outside the output and are not stored)
+              const int b0 = nb * 4 + static_cast<int>(rank) * 2;
+              const int tile = j * p.col_slices + b0;
+              tma_load_3d_pair(db, &p.tmap_b0, fb, 0, c * kBlockK, tile);
+              tma_load_3d_pair(db + kOperandBytes / 2, &p.tmap_b0, fb, 0, c * kBlockK, tile + 1);
+            } else {
+              // tokens [64 i, +64): 128 output rows of the left operand, 128 output
+              // columns of the right one, each as two 64-wide boxes
+              tma_load_2d_pair(da, &p.tmap_a0, fb, r0, i * kBlockK);
+              tma_load_2d_pair(da + kOperandBytes / 2, &p.tmap_a0, fb, r0 + 64, i * kBlockK);
+              const CUtensorMap* mapb = p.two_out && rank ? &p.tmap_b1 : &p.tmap_b0;
+              const int c0 =
+                  p.two_out ? nb * kTileM : nb * 2 * kTileM + static_cast<int>(rank) * kTileM;
+              tma_load_2d_pair(db, mapb, fb, c0, i * kBlockK);
+              tma_load_2d_pair(db + kOperandBytes / 2, mapb, fb, c0 + 64, i * kBlockK);
+            }
+            filled |= 1u << s;
+            fill_ph = (fill_ph & ~(1u << s)) | (ph << s);
+          }
+          if (++s == kStages) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+      }
+      pdl_launch_dependents();
+      // Rank 0's full barriers count both CTAs' bytes: once they complete, every
+      // copy issued by the pair for those stages has landed.
+      if (leader)
+        for (int i = 0; i < kStages; ++i)
+          if (filled & (1u << i)) mbar_wait_drain(full0 + 8u * i, (fill_ph >> i) & 1u, wc);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------ MMA issuer (rank 0)
+    if (leader && lane == 0) {
+      constexpr uint32_t kIdesc =
+          idesc_bf16_f32(2 * kTileM, kAccCols) | (kMnA ? 1u << 15 : 0u) | (kMnB ? 1u << 16 : 0u);
+      // 16 of the sum per MMA: 32 bytes along a K-major row, 16 rows of 128 bytes MN-major
+      constexpr uint32_t kStepA = kMnA ? 2048 >> 4 : 32 >> 4, kStepB = kMnB ? 2048 >> 4 : 32 >> 4;
+      int s = 0;
+      uint32_t ph = 0;
+      int buf = 0;
+      uint32_t acc_ph = 0;
+      bool ok = true;
+      for (int t = pair; ok && t < num_units; t += pairs) {
+        if (!mbar_wait(tempty0 + 8u * buf, acc_ph ^ 1u, wc, kSiteMmaTmemEmpty)) break;
+        tc_fence_after();
+        const uint32_t d = tmem_base + buf * kAccCols;
+        const int part = t % splits;
+        const int begin = static_cast<int>(int64_t(part) * p.slices / splits);
+        const int end = static_cast<int>(int64_t(part + 1) * p.slices / splits);
+        for (int i = begin; i < end; ++i) {
+          if (!mbar_wait(full0 + 8u * s, ph, wc, kSiteMmaFull)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t adesc = kMnA ? smem_desc_sw128_mn(sA + s * kOperandBytes, kOperandBytes / 2)
+                                      : smem_desc_sw128(sA + s * kOperandBytes);
+          const uint64_t bdesc = kMnB ? smem_desc_sw128_mn(sB + s * kOperandBytes, kOperandBytes / 2)
+                                      : smem_desc_sw128(sB + s * kOperandBytes);
+#pragma unroll
+          for (uint32_t k = 0; k < 4; ++k)
+            mma_bf16_pair(d, adesc + kStepA * k, bdesc + kStepB * k, kIdesc,
+                          (i != begin || k != 0) ? 1u : 0u);
+          mma_commit_pair_multicast(empty0 + 8u * s, 0x3);  // frees the stage in both CTAs
+          if (++s == kStages) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+        if (!ok) break;
+        mma_commit_pair_multicast(tfull0 + 8u * buf, 0x3);  // both halves of the accumulator ready
+        buf ^= 1;
+        if (buf == 0) acc_ph ^= 1u;
+      }
+      mma_commit_pair_multicast(drain_bar, 0x1);
+      mbar_wait_drain(drain_bar, 0, wc);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------ epilogue (both CTAs)
+    const int q = warp & 3;
+    const int ew = warp - 2;
+    const uint32_t lane_off = static_cast<uint32_t>(q * 32) << 16;
+    int buf = 0;
+    uint32_t acc_ph = 0;
+    int sbuf = 0;
+    for (int t = pair; t < num_units; t += pairs) {
+      int mb, nb;
+      const int part = t % splits;
+      tile_coords(t / splits, p.tiles_m, p.tiles_n, p.group_m, mb, nb);
+      const int row0 = mb * 2 * kTileM + static_cast<int>(rank) * kTileM + q * 32;
+      uint4 dyv[4];
+      const __nv_bfloat16* dy_row = nullptr;
+      if constexpr (kGradMode) {
+        // this thread's row of dY, 32 columns ahead of the accumulator chunk in use
+        dy_row = static_cast<const __nv_bfloat16*>(p.dy) + static_cast<size_t>(row0 + lane) * p.cols;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int col = nb * kTileM + 8 * e;
+          dyv[e] = row0 + lane < p.rows && col < p.cols
+                       ? __ldg(reinterpret_cast<const uint4*>(dy_row + col))
+                       : make_uint4(0u, 0u, 0u, 0u);
+        }
+      }
+      int ok = 1;
+      if (lane == 0) ok = mbar_wait(tfull0 + 8u * buf, acc_ph, wc, kSiteEpiTmemFull) ? 1 : 0;
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t tacc = tmem_base + lane_off + buf * kAccCols;
+      if constexpr (kGradMode) {
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          uint32_t g[32], u[32];
+          tmem_ld_x32(tacc + c * 32, g);
+          tmem_ld_x32(tacc + 128 + c * 32, u);
+          uint4 dyc[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            dyc[e] = dyv[e];
+            const int col = nb * kTileM + (c + 1) * 32 + 8 * e;
+            if (c < 3)
+              dyv[e] = row0 + lane < p.rows && col < p.cols
+                           ? __ldg(reinterpret_cast<const uint4*>(dy_row + col))
+                           : make_uint4(0u, 0u, 0u, 0u);
+          }
+          tmem_wait_ld();
+          reg_fence(g);
+          reg_fence(u);
+          if (c == 3) {  // this CTA's half of the accumulator is read
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(tempty0_lead + 8u * buf);
+          }
+          if (lane == 0) bulk_wait_read<1>();
+          __syncwarp();
+          const uint32_t stg = sStg + (ew * 2 + sbuf) * kStgBytes;  // dG block, then dU block
+          const uint32_t row_addr = stg + lane * 64;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint32_t wg[4], wu[4];
+            const uint32_t dw[4] = {dyc[j].x, dyc[j].y, dyc[j].z, dyc[j].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int i0 = 8 * j + 2 * e;
+              const __nv_bfloat162 h = *reinterpret_cast<const __nv_bfloat162*>(&dw[e]);
+              float dg0, du0, dg1, du1;
+              gate_grads(__uint_as_float(g[i0]), __uint_as_float(u[i0]), __low2float(h), dg0, du0);
+              gate_grads(__uint_as_float(g[i0 + 1]), __uint_as_float(u[i0 + 1]), __high2float(h),
+                         dg1, du1);
+              wg[e] = pack_bf16x2(dg0, dg1);
+              wu[e] = pack_bf16x2(du0, du1);
+            }
+            const uint32_t off = (j ^ ((lane >> 1) & 3)) << 4;
+            st_shared_v4(row_addr + off, wg[0], wg[1], wg[2], wg[3]);
+            st_shared_v4(row_addr + 2048 + off, wu[0], wu[1], wu[2], wu[3]);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            const int ncol = nb * kTileM + c * 32;
+            if (ncol < p.cols && row0 < p.rows) {
+              tma_store_2d(&p.tmap_o0, stg, ncol, row0);
+              tma_store_2d(&p.tmap_o1, stg + 2048, ncol, row0);
+            }
+            bulk_commit();
+          }
+          sbuf ^= 1;
+        }
+      } else {
+        // 8 chunks of 32 columns: fp32 parts (128-byte rows) to the workspace,
+        // or two chunks at a time as 64 bf16 columns to the output
+        const bool parts = splits > 1;
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          uint32_t x[32], y[32];
+          tmem_ld_x32(tacc + c * 64, x);
+          tmem_ld_x32(tacc + c * 64 + 32, y);
+          tmem_wait_ld();
+          reg_fence(x);
+          reg_fence(y);
+          if (c == 3) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(tempty0_lead + 8u * buf);
+          }
+          const int half = c >> 1;  // accumulator columns 0-127 or 128-255
+          const CUtensorMap* mapo = p.two_out && half ? &p.tmap_o1 : &p.tmap_o0;
+          const int ncol = p.two_out ? nb * kTileM + (c & 1) * 64 : nb * 2 * kTileM + c * 64;
+          if (parts) {
+            // part-major rows: the store maps see splits * padded rows
+            const int prow = part * p.part_rows + row0;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              if (lane == 0) bulk_wait_read<1>();
+              __syncwarp();
+              const uint32_t stg = sStg + (ew * 2 + sbuf) * kStgBytes;
+              const uint32_t row_addr = stg + lane * 128;
+              const uint32_t* v = h ? y : x;
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                st_shared_v4(row_addr + ((j ^ (lane & 7)) << 4), v[4 * j], v[4 * j + 1],
+                             v[4 * j + 2], v[4 * j + 3]);
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) {
+                if (ncol + 32 * h < p.cols && row0 < p.rows)
+                  tma_store_2d(mapo, stg, ncol + 32 * h, prow);
+                bulk_commit();
+              }
+              sbuf ^= 1;
+            }
+          } else {
+            if (lane == 0) bulk_wait_read<1>();
+            __syncwarp();
+            const uint32_t stg = sStg + (ew * 2 + sbuf) * kStgBytes;
+            const uint32_t row_addr = stg + lane * 128;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const uint32_t* v = j < 4 ? x + 8 * j : y + 8 * (j - 4);
+              uint32_t w[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                w[e] = pack_bf16x2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]));
+              st_shared_v4(row_addr + ((j ^ (lane & 7)) << 4), w[0], w[1], w[2], w[3]);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              if (ncol < p.cols && row0 < p.rows) tma_store_2d(mapo, stg, ncol, row0);
+              bulk_commit();
+            }
+            sbuf ^= 1;
+          }
+        }
+      }
+      buf ^= 1;
+      if (buf == 0) acc_ph ^= 1u;
+    }
+    if (lane == 0) bulk_wait<0>();
+    __syncwarp();
+  }
+
+  // Neither CTA leaves while the pair's MMAs may still read its shared memory
+  // or the peer may still arrive on its barriers.
+  tc_fence_before();
+  cluster_sync();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, 2 * kAccCols);
+  }
+}
+
+// out[r][c] = bf16(sum over parts, in order, of parts[part][r][c]): one pass
+// over fp32 values that are mostly still in L2, 8 columns a thread.
+__global__ void __launch_bounds__(256)
+    reduce_parts_kernel(const float* __restrict__ parts, __nv_bfloat16* __restrict__ out, int rows,
+                        int cols, int part_rows, int splits) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int chunks = cols / 8;
+  const size_t items = static_cast<size_t>(rows) * chunks;
+  const size_t part_stride = static_cast<size_t>(part_rows) * cols;
+  for (size_t i = blockIdx.x * static_cast<size_t>(blockDim.x) + threadIdx.x; i < items;
+       i += static_cast<size_t>(gridDim.x) * blockDim.x) {
+    const float* src = parts + i * 8;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+#pragma unroll 4
+    for (int s = 0; s < splits; ++s) {
+      const float4 x = __ldcg(reinterpret_cast<const float4*>(src + s * part_stride));
+      const float4 y = __ldcg(reinterpret_cast<const float4*>(src + s * part_stride + 4));
+      a.x += x.x; a.y += x.y; a.z += x.z; a.w += x.w;
+      b.x += y.x; b.y += y.y; b.z += y.z; b.w += y.w;
+    }
+    uint4 o;
+    o.x = pack_bf16x2(a.x, a.y);
+    o.y = pack_bf16x2(a.z, a.w);
+    o.z = pack_bf16x2(b.x, b.y);
+    o.w = pack_bf16x2(b.z, b.w);
+    *reinterpret_cast<uint4*>(out + i * 8) = o;
+  }
+}
+
+cudaLaunchConfig_t backward_config(int grid, cudaStream_t stream, cudaLaunchAttribute* attr,
+                                   bool with_pdl) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = stream;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = with_pdl ? 1 : 0;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cfg;
+}
+
+template <int kMode>
+cudaError_t set_smem() {
+  return cudaFuncSetAttribute(backward_pair_kernel<kMode>,
+                              cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem));
+}
+
+}  // namespace
+
+cudaError_t configure_backward_pair(int* max_pairs) {
+  cudaError_t e = set_smem<kBackwardGrad>();
+  if (e == cudaSuccess) e = set_smem<kBackwardInput>();
+  if (e == cudaSuccess) e = set_smem<kBackwardWeight>();
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[2];
+  cudaLaunchConfig_t cfg = backward_config(2, nullptr, attr, false);
+  return cudaOccupancyMaxActiveClusters(max_pairs, backward_pair_kernel<kBackwardGrad>, &cfg);
+}
+
+cudaError_t launch_backward_pair(const BackwardParams& p, int mode, int grid, cudaStream_t stream) {
+  if (grid < 2 || (grid % 2) != 0 || p.splits < 1 || p.slices < p.splits || p.group_m < 1 ||
+      (p.splits > 1 && (p.part_rows < p.rows || (p.part_rows % 32) != 0)))
+    return cudaErrorInvalidValue;
+  cudaLaunchAttribute attr[2];
+  cudaLaunchConfig_t cfg = backward_config(grid, stream, attr, pdl_enabled());
+  const cudaError_t e =
+      mode == kBackwardGrad    ? cudaLaunchKernelEx(&cfg, backward_pair_kernel<kBackwardGrad>, p)
+      : mode == kBackwardInput ? cudaLaunchKernelEx(&cfg, backward_pair_kernel<kBackwardInput>, p)
+                               : cudaLaunchKernelEx(&cfg, backward_pair_kernel<kBackwardWeight>, p);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+cudaError_t launch_reduce_parts(const float* parts, void* out, int rows, int cols, int part_rows,
+                                int splits, cudaStream_t stream) {
+  const size_t items = static_cast<size_t>(rows) * (cols / 8);
+  const size_t blocks = (items + 255) / 256;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks < 1216 ? blocks : 1216));  // 8 blocks per SM
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = pdl_enabled() ? 1 : 0;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, reduce_parts_kernel, parts,
+                                           static_cast<__nv_bfloat16*>(out), rows, cols, part_rows,
+                                           splits);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace swg

@@ -287,9 +287,20 @@ __device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t saddr) {
          (static_cast<uint64_t>(2) << 61);
 }
 
+// The same for an MN-major bf16 tile: boxes of 64 elements (one 128-byte row)
+// x 64 rows of the sum, written by TMA with 128-byte swizzle. 8-row groups are
+// 1024 B apart (stride byte offset), the next 64 elements `block_bytes` further
+// (leading byte offset); 16 rows of the sum add 2048 bytes.
+__device__ __forceinline__ uint64_t smem_desc_sw128_mn(uint32_t saddr, uint32_t block_bytes) {
+  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) |
+         (static_cast<uint64_t>(block_bytes >> 4) << 16) |
+         (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) |
+         (static_cast<uint64_t>(2) << 61);
+}
+
 // Instruction descriptor, kind::f16: D fp32 (bits 4-5 = 1), A and B bf16
-// (bits 7-9 = 1, 10-12 = 1), both K-major (bits 15, 16 = 0), N >> 3 at bits
-// 17-22, M >> 4 at bits 24-28.
+// (bits 7-9 = 1, 10-12 = 1), both K-major (bits 15, 16 = 0; set for an MN-major
+// A or B), N >> 3 at bits 17-22, M >> 4 at bits 24-28.
 __host__ __device__ constexpr uint32_t idesc_bf16_f32(int m, int n) {
   return (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) |
          (static_cast<uint32_t>(m >> 4) << 24);

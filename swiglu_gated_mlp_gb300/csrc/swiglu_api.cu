@@ -12,11 +12,12 @@
 
 #include <cudaTypedefs.h>
 
+#include "api_shared.h"
 #include "kernels.h"
 
 namespace {
 
-constexpr int kMaxDevices = 64;
+using swg::api::kMaxDevices;
 constexpr int64_t kMaxKN = int64_t(1) << 21;
 constexpr int64_t kMaxM = 2147483647;
 
@@ -743,6 +744,50 @@ swiglu_status_t make_mx_plan(int64_t M, int64_t K, int64_t N, const DeviceState&
   return SWIGLU_OK;
 }
 }  // namespace
+
+namespace swg {
+namespace api {
+
+swiglu_status_t device_view(DeviceView* out) {
+  DeviceState* d = nullptr;
+  const swiglu_status_t st = ::device_state(&d);
+  if (st != SWIGLU_OK) return st;
+  *out = DeviceView{static_cast<int>(d - g_dev), d->sm_count, d->status, g_timeout_ns.load(),
+                    g_inject.load()};
+  return SWIGLU_OK;
+}
+
+swiglu_status_t check_shape(int64_t M, int64_t K, int64_t N) { return ::check_shape(M, K, N); }
+bool aligned16(const void* p) { return ::aligned16(p); }
+bool overlaps(const void* a, size_t an, const void* b, size_t bn) { return ::overlaps(a, an, b, bn); }
+int64_t padded_n(int64_t n) { return ::padded_n(n); }
+int64_t k_slices(int64_t k) { return ::k_slices(k); }
+int64_t padded_h(int64_t h) { return ::padded_h(h); }
+int64_t pair_group_rows(int64_t row_tiles) { return ::pair_group_rows(row_tiles); }
+
+bool encode_2d(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer,
+               uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer,
+               CUtensorMapSwizzle swizzle, CUtensorMapDataType dtype) {
+  return ::encode_2d(map, base, inner, outer, row_bytes, box_inner, box_outer, swizzle, dtype);
+}
+
+bool encode_3d(CUtensorMap* map, const void* base, const uint64_t dims[3],
+               const uint64_t strides[2], const uint32_t box[3], CUtensorMapSwizzle swizzle) {
+  const cuuint64_t d[3] = {dims[0], dims[1], dims[2]}, s[2] = {strides[0], strides[1]};
+  const cuuint32_t b[3] = {box[0], box[1], box[2]};
+  return encode_cached(map, base, 3, d, s, b, swizzle);
+}
+
+bool encode_packed_w(CUtensorMap* map, const void* base, int64_t K, int64_t N, uint32_t rows) {
+  return ::encode_packed_w(map, base, K, N, rows);
+}
+
+bool encode_packed_down(CUtensorMap* map, const void* base, int64_t N, int64_t H, uint32_t rows) {
+  return ::encode_packed_down(map, base, N, H, rows);
+}
+
+}  // namespace api
+}  // namespace swg
 
 extern "C" {
 
