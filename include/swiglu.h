@@ -404,6 +404,52 @@ SWIGLU_API swiglu_status_t swiglu_down_backward(const void* dOut, const void* W3
                                                 size_t workspace_bytes, swiglu_stream_t stream);
 
 /*
+ * The two projections with low-rank adapters of many requests: one shared
+ * packed weight, and per token m one adapter a = index[m] of a table (a value
+ * outside [0, adapters) means none). No passage of the pages covers adapters;
+ * the formulas are the usual ones, x W + scale_a (x La_a^T) Lb_a^T:
+ *   V1 = scale[a] A[m] La[a][0]^T         V2 = scale[a] A[m] La[a][1]^T
+ *   Y[m] = SiLU(A[m] x W1 + V1 Lb[a][0]^T) (.) (A[m] x W2 + V2 Lb[a][1]^T)
+ *   Out[m] = Y[m] x W3 + R[m] + scale[a] (Y[m] La[a]^T) Lb[a]^T
+ * Layouts, bf16 row-major: La [adapters, 2, rank, K] (gate, then up) and
+ * Lb [adapters, 2, N, rank] for the gate/up call; La [adapters, rank, N] and
+ * Lb [adapters, H, rank] for the down call (each the layout of a linear layer's
+ * weight, [out, in]). index: [M] int32; scale: [adapters] fp32. All are device
+ * memory, so requests can change between launches of a captured graph.
+ * Adapters of a smaller rank are padded with zeros.
+ *
+ * Sums are fp32, Gate, Up and their deltas meet in fp32 before SiLU, and each
+ * output is rounded once. V stays in fp32 up to 128 tokens; above, it is
+ * rounded to bf16, an operand of the tensor cores. La of one adapter never
+ * reaches another's tokens, whatever its values; Lb does not either up to 128
+ * tokens, above that Lb must be finite (an infinity or NaN in it also reaches
+ * the tokens of the same 256-row tile).
+ *
+ * swiglu_lora_workspace_bytes(M, K, N, rank) and
+ * swiglu_down_lora_workspace_bytes(M, N, H, rank): bytes of the workspace
+ *   (device-independent; 0 on a bad shape or M = 0).
+ * `workspace`: device, 16-byte aligned, at least that size, overlapping nothing
+ *   else, needing no set-up; separate for calls that may run at the same time.
+ * rank: a multiple of 8 up to 64 (else UNSUPPORTED; <= 0: INVALID_ARG).
+ * adapters = 0: the plain projection, the adapter arguments are not used.
+ * M = 0: no-op. R may be NULL or Out itself. Errors as swiglu_forward.
+ */
+SWIGLU_API size_t swiglu_lora_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t rank);
+SWIGLU_API swiglu_status_t swiglu_forward_lora(const void* A, const void* Wpacked, void* Y,
+                                               int64_t M, int64_t K, int64_t N, const void* La,
+                                               const void* Lb, const int32_t* index,
+                                               const float* scale, int64_t adapters, int64_t rank,
+                                               void* workspace, size_t workspace_bytes,
+                                               swiglu_stream_t stream);
+SWIGLU_API size_t swiglu_down_lora_workspace_bytes(int64_t M, int64_t N, int64_t H, int64_t rank);
+SWIGLU_API swiglu_status_t swiglu_down_forward_lora(const void* Y, const void* W3packed,
+                                                    const void* R, void* Out, int64_t M, int64_t N,
+                                                    int64_t H, const void* La, const void* Lb,
+                                                    const int32_t* index, const float* scale,
+                                                    int64_t adapters, int64_t rank, void* workspace,
+                                                    size_t workspace_bytes, swiglu_stream_t stream);
+
+/*
  * Allocation-free forward for callers that cannot call cudaMalloc: serving
  * runtimes that reserve all device memory for their own pools up front (a
  * library allocation would fail, or would fragment memory the runtime plans

@@ -99,6 +99,16 @@ lib.swiglu_down_backward_workspace_bytes.argtypes = [_i64, _i64, _i64]
 lib.swiglu_down_backward_workspace_bytes.restype = _sz
 lib.swiglu_down_backward.argtypes = [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _sz, _vp]
 lib.swiglu_down_backward.restype = _int
+lib.swiglu_lora_workspace_bytes.argtypes = [_i64, _i64, _i64, _i64]
+lib.swiglu_lora_workspace_bytes.restype = _sz
+lib.swiglu_forward_lora.argtypes = [_vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _i64, _i64, _vp,
+                                    _sz, _vp]
+lib.swiglu_forward_lora.restype = _int
+lib.swiglu_down_lora_workspace_bytes.argtypes = [_i64, _i64, _i64, _i64]
+lib.swiglu_down_lora_workspace_bytes.restype = _sz
+lib.swiglu_down_forward_lora.argtypes = [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _i64,
+                                         _i64, _vp, _sz, _vp]
+lib.swiglu_down_forward_lora.restype = _int
 lib.swiglu_testing_inject_stall.argtypes = [_int, _u32]
 lib.swiglu_testing_inject_stall.restype = None
 lib.swiglu_testing_pace_run_out.argtypes = [ctypes.POINTER(ctypes.c_uint64)]
@@ -615,6 +625,106 @@ def swiglu_down_backward(dOut: torch.Tensor, W3packed: torch.Tensor | None, Y: t
             workspace.numel() * workspace.element_size() if workspace is not None else 0,
             _stream_handle(stream, dOut.device)), "swiglu_down_backward")
     return dY, dW3
+
+
+def _adapters(La, Lb, index, scale, la_shape, lb_shape, M: int, like: torch.Tensor) -> None:
+    """Checks an adapter table against the shapes its projection asks for."""
+    _dev_bf16(La, "La")
+    _dev_bf16(Lb, "Lb")
+    if tuple(La.shape) != la_shape or tuple(Lb.shape) != lb_shape:
+        raise ValueError(f"La and Lb must be {list(la_shape)} and {list(lb_shape)}, "
+                         f"got {list(La.shape)} and {list(Lb.shape)}")
+    if index.dtype != torch.int32 or tuple(index.shape) != (M,) or not index.is_contiguous():
+        raise ValueError("index must be a contiguous int32 tensor of one adapter per token")
+    if scale.dtype != torch.float32 or tuple(scale.shape) != la_shape[:1] or not scale.is_contiguous():
+        raise ValueError("scale must be a contiguous float32 tensor of one value per adapter")
+    _same_device(like, La=La, Lb=Lb, index=index, scale=scale)
+
+
+def swiglu_lora_workspace_bytes(M: int, K: int, N: int, rank: int) -> int:
+    return int(lib.swiglu_lora_workspace_bytes(int(M), int(K), int(N), int(rank)))
+
+
+def swiglu_lora_workspace(M: int, K: int, N: int, rank: int, device=None) -> torch.Tensor:
+    """A workspace for swiglu_forward_lora; one serves any number of calls in stream order."""
+    return _new_workspace(swiglu_lora_workspace_bytes, device, M, K, N, rank)
+
+
+def swiglu_forward_lora(A: torch.Tensor, Wpacked: torch.Tensor, N: int, La: torch.Tensor,
+                        Lb: torch.Tensor, index: torch.Tensor, scale: torch.Tensor,
+                        Y: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                        stream=None) -> torch.Tensor:
+    """Y [M, N] = SiLU(A W1 + D1) * (A W2 + D2), Dh[m] = scale[a] A[m] La[a, h]^T Lb[a, h]^T, a = index[m].
+
+    La [adapters, 2, rank, K] and Lb [adapters, 2, N, rank] hold the gate and
+    up halves; index [M] int32 names each token's adapter (outside the table:
+    none); scale [adapters] float32. Without `workspace` (from
+    swiglu_lora_workspace) one is allocated for the call.
+    """
+    _dev_bf16(A, "A")
+    _dev_bf16(Wpacked, "Wpacked")
+    if A.dim() != 2 or La.dim() != 4:
+        raise ValueError("A must be [M, K] and La [adapters, 2, rank, K]")
+    M, K = A.shape
+    count, rank = La.shape[0], La.shape[2]
+    if Wpacked.numel() * 2 < swiglu_packed_weight_bytes(K, N):
+        raise ValueError("Wpacked does not hold a packed weight for this K and N")
+    _adapters(La, Lb, index, scale, (count, 2, rank, K), (count, 2, N, rank), M, A)
+    _same_device(A, Wpacked=Wpacked, Y=Y)
+    with _on_device(A.device):
+        Y = _output(Y, "Y", (M, N), A, stream)
+        workspace = _workspace(workspace, 0 if workspace is not None
+                               else swiglu_lora_workspace_bytes(M, K, N, rank), A, stream)
+        _check(lib.swiglu_forward_lora(
+            A.data_ptr(), Wpacked.data_ptr(), Y.data_ptr(), M, K, N, La.data_ptr(), Lb.data_ptr(),
+            index.data_ptr(), scale.data_ptr(), count, rank, workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), _stream_handle(stream, A.device)),
+            "swiglu_forward_lora")
+    return Y
+
+
+def swiglu_down_lora_workspace_bytes(M: int, N: int, H: int, rank: int) -> int:
+    return int(lib.swiglu_down_lora_workspace_bytes(int(M), int(N), int(H), int(rank)))
+
+
+def swiglu_down_lora_workspace(M: int, N: int, H: int, rank: int, device=None) -> torch.Tensor:
+    """A workspace for swiglu_down_forward_lora; one serves any number of calls in stream order."""
+    return _new_workspace(swiglu_down_lora_workspace_bytes, device, M, N, H, rank)
+
+
+def swiglu_down_forward_lora(Y: torch.Tensor, W3packed: torch.Tensor, H: int, La: torch.Tensor,
+                             Lb: torch.Tensor, index: torch.Tensor, scale: torch.Tensor,
+                             R: torch.Tensor | None = None, Out: torch.Tensor | None = None,
+                             workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Out [M, H] = Y W3 + R + D, D[m] = scale[a] Y[m] La[a]^T Lb[a]^T, a = index[m].
+
+    La [adapters, rank, N], Lb [adapters, H, rank]; index and scale as in
+    swiglu_forward_lora; Out may be R (in-place add).
+    """
+    _dev_bf16(Y, "Y")
+    _dev_bf16(W3packed, "W3packed")
+    if Y.dim() != 2 or La.dim() != 3:
+        raise ValueError("Y must be [M, N] and La [adapters, rank, N]")
+    M, N = Y.shape
+    count, rank = La.shape[:2]
+    if W3packed.numel() * 2 < swiglu_down_packed_bytes(N, H):
+        raise ValueError("W3packed does not hold a packed W3 for this N and H")
+    _adapters(La, Lb, index, scale, (count, rank, N), (count, H, rank), M, Y)
+    if R is not None:
+        _dev_bf16(R, "R")
+        if tuple(R.shape) != (M, H):
+            raise ValueError("R must be [M, H]")
+    _same_device(Y, W3packed=W3packed, R=R, Out=Out)
+    with _on_device(Y.device):
+        Out = _output(Out, "Out", (M, H), Y, stream)
+        workspace = _workspace(workspace, 0 if workspace is not None
+                               else swiglu_down_lora_workspace_bytes(M, N, H, rank), Y, stream)
+        _check(lib.swiglu_down_forward_lora(
+            Y.data_ptr(), W3packed.data_ptr(), _ptr(R), Out.data_ptr(), M, N, H, La.data_ptr(),
+            Lb.data_ptr(), index.data_ptr(), scale.data_ptr(), count, rank, workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), _stream_handle(stream, Y.device)),
+            "swiglu_down_forward_lora")
+    return Out
 
 
 def swiglu_forward_from_host(A_host: torch.Tensor, Wpacked: torch.Tensor, N: int,

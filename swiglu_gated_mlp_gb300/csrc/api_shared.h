@@ -17,6 +17,7 @@ constexpr int kMaxDevices = 64;
 struct DeviceView {  // what a launch needs of the current device's state
   int index;
   int sm_count;
+  int max_pairs;        // CTA pairs of the forward pair kernel resident at once (0: none)
   uint32_t* status;     // device status record
   uint64_t timeout_ns;  // limit of one pipeline wait
   int inject_stall;     // testing hook
@@ -33,6 +34,10 @@ int64_t k_slices(int64_t k);
 int64_t padded_h(int64_t h);
 // Row tiles (of 256 rows) per group of the CTA-pair kernels' tile order.
 int64_t pair_group_rows(int64_t row_tiles);
+
+// Decode-kernel work split for `blocks` weight blocks on the current device.
+swiglu_status_t decode_plan(int64_t M, int64_t blocks, int64_t kslices, int* mt, int* mgroups,
+                            int* stages, int* splits);
 
 // Tensor maps through the per-thread cache.
 bool encode_2d(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer,

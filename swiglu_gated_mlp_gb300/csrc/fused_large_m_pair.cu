@@ -68,13 +68,27 @@
 // accumulator into registers, release it at once, and only then apply
 // SiLU(g) * u and store, each through one store-staging buffer of its own
 // (the wait on its previous store overlaps the next tile's MMAs).
+//
+// With kLora (bf16) each token also has a low-rank adapter a = index[m]: after
+// a tile's K slices come, for every adapter present in its 256 tokens
+// (lora_shrink.cu lists them and makes V), slices whose left operand is V with
+// the rows of other adapters zero and whose right operand is Lb[a]: one with
+// gate V (MMA N = 128, into the gate columns) and one with up V (up columns),
+// or a single one over all 256 columns of the down-projection. Up to 64 ranks
+// fill one 128-byte row, so an adapter costs a tile one or two short slices
+// (rank / 16 MMAs each) of its K / 64, and Gate, Up and their deltas meet in
+// the fp32 accumulator before SiLU. Lb comes by TMA into the stage's weight
+// half; four warps write the masked V rows into its A half (thread = row) and
+// signal a barrier of their own, which the MMA issuer waits for beside the
+// stage's. A zero row times a non-finite Lb value is NaN: adapters' Lb must be
+// finite, as the shared weight must.
 #include "kernels.h"
 #include "ptx.cuh"
 
 namespace swg {
 namespace {
 
-template <bool kMx>
+template <bool kMx, bool kLora = false>
 struct PairCfg {
   static constexpr int kBN = 128;                        // output columns per tile
   static constexpr int kABytes = 128 * kBlockK * 2;      // 16 KB: this CTA's 128 A rows
@@ -83,8 +97,9 @@ struct PairCfg {
   static constexpr int kStages = 6;
   static constexpr int kEpiWarps = kMx ? 8 : 4;          // 2 per lane quarter when block-scaled
   // TMA producer and MMA issuer warps, the epilogue warps, and (block-scaled)
-  // a warp that copies each stage's scales into tensor memory
-  static constexpr int kThreadsT = 64 + 32 * kEpiWarps + (kMx ? 32 : 0);
+  // a warp that copies each stage's scales into tensor memory, or (adapters)
+  // four that write masked V rows
+  static constexpr int kThreadsT = 64 + 32 * kEpiWarps + (kMx ? 32 : kLora ? 128 : 0);
   static constexpr int kAccCols = 2 * kBN;               // 256 fp32 columns: gate | up
   static constexpr int kTmemCols = 2 * kAccCols;         // double buffered (bf16, per-tensor FP8)
   static constexpr int kStgBytes = 32 * 32 * 2;          // 32 rows x 64 B store staging
@@ -95,7 +110,8 @@ struct PairCfg {
                                   size_t(kNumStg) * kStgBytes +
                                   (kMx ? size_t(kStages) * kSfStageBytes : 0) + kBarBytes;
   static_assert(kSmem <= 232448, "shared memory budget");
-  static_assert(8 * (3 * kStages + 6) + 8 <= kBarBytes, "barrier slots");
+  static constexpr int kBars = (kLora ? 4 : 3) * kStages + 6;
+  static_assert(8 * kBars + 8 <= kBarBytes, "barrier slots");
   static constexpr int kSfCol = kAccCols;  // scale slots after the single accumulator
   static_assert(!kMx || kSfCol + kStages * kSfTmemCols <= kTmemCols, "tensor memory budget");
 };
@@ -151,10 +167,11 @@ __device__ __forceinline__ void pace_count(int r, unsigned long long epoch) {
   } while (old != assumed);
 }
 
-template <bool kFp8, bool kDown, bool kMx>
-__global__ void __launch_bounds__(PairCfg<kMx>::kThreadsT, 1)
+template <bool kFp8, bool kDown, bool kMx, bool kLora>
+__global__ void __launch_bounds__(PairCfg<kMx, kLora>::kThreadsT, 1)
     fused_large_m_pair_kernel(const __grid_constant__ LargeMParams p) {
-  using C = PairCfg<kMx>;
+  using C = PairCfg<kMx, kLora>;
+  static_assert(!kLora || !kFp8, "adapters go with bf16");
   static_assert(!kMx || (kFp8 && !kDown), "block scales go with E4M3 gate/up inputs");
   constexpr int kAccBufs = kMx ? 1 : 2;  // accumulator buffers in tensor memory
   // K values per stage: 64 bf16 or 128 E4M3, a 128-byte row either way
@@ -170,12 +187,13 @@ __global__ void __launch_bounds__(PairCfg<kMx>::kThreadsT, 1)
                      (kMx ? size_t(C::kStages) * kSfStageBytes : 0);
   const uint32_t bar0 = smem_addr(bar_ptr);
   // barrier slots: full[S] | empty[S] | tmem_full[2] | tmem_empty[2] | drain |
-  // scales_ready[S] | scale-copy drain
+  // scales_ready[S] (adapters: V rows ready) | scale-copy drain | V slot free[S] (adapters)
   const uint32_t full0 = bar0, empty0 = bar0 + 8u * C::kStages;
   const uint32_t tfull0 = bar0 + 16u * C::kStages, tempty0 = tfull0 + 16u;
   const uint32_t drain_bar = tempty0 + 16u;
   const uint32_t sready0 = drain_bar + 8u, sdrain_bar = sready0 + 8u * C::kStages;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_ptr + 8 * (3 * C::kStages + 6));
+  const uint32_t vfree0 = sdrain_bar + 8u;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_ptr + 8 * C::kBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5;
@@ -187,6 +205,7 @@ __global__ void __launch_bounds__(PairCfg<kMx>::kThreadsT, 1)
   const int num_tiles = p.tiles_m * p.tiles_n;
   const int num_kb = (p.K + kBK - 1) / kBK;
   const WaitCtx wc{abort_flag, p.status, p.timeout_ns};
+  constexpr int kHalves = kDown ? 1 : 2;  // adapter slices: gate and up, or one
   // rank 0's full and tmem_empty barriers, as seen from either CTA of the pair
   const uint32_t full0_lead = mapa_shared(full0, 0);
   const uint32_t tempty0_lead = mapa_shared(tempty0, 0);
@@ -199,6 +218,7 @@ __global__ void __launch_bounds__(PairCfg<kMx>::kThreadsT, 1)
       prefetch_tmap(&p.tmap_sw);
       prefetch_tmap(&p.tmap_sa);
     }
+    if constexpr (kLora) prefetch_tmap(&p.tmap_lb);
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(full0 + 8u * s, 1);   // rank 0's producer arrives (with both CTAs' bytes)
       mbar_init(empty0 + 8u * s, 1);  // rank 0's MMA commit, multicast to both CTAs
@@ -208,8 +228,11 @@ __global__ void __launch_bounds__(PairCfg<kMx>::kThreadsT, 1)
       mbar_init(tempty0 + 8u * b, 2 * C::kEpiWarps);  // epilogue warps x 2 CTAs (used on rank 0)
     }
     mbar_init(drain_bar, 1);
-    for (int s = 0; s < C::kStages; ++s) mbar_init(sready0 + 8u * s, 1);  // scale-copy commit
+    // scale-copy commit, or (adapters) 4 warps x 2 CTAs (used on rank 0)
+    for (int s = 0; s < C::kStages; ++s) mbar_init(sready0 + 8u * s, kLora ? 8 : 1);
     mbar_init(sdrain_bar, 1);
+    if constexpr (kLora)
+      for (int s = 0; s < C::kStages; ++s) mbar_init(vfree0 + 8u * s, 1);  // this CTA's producer
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -290,6 +313,31 @@ __global__ void __launch_bounds__(PairCfg<kMx>::kThreadsT, 1)
             ph ^= 1u;
           }
         }
+        if constexpr (kLora) {
+          // Lb rows of every adapter present in this tile, to the weight half
+          const int* list = p.lora_lists + static_cast<size_t>(mb) * kLoraListInts;
+          const int extra = list[0] * kHalves;
+          for (int i = 0; ok && i < extra; ++i) {
+            if (!mbar_wait(empty0 + 8u * s, ph ^ 1u, wc, kSiteProducerEmpty)) {
+              ok = false;
+              break;
+            }
+            mbar_arrive(vfree0 + 8u * s);  // the stage's A half is free for V rows
+            // this CTA's half of the MMA's N rows: 64 gate (up) columns, or 128 output columns
+            if (leader) mbar_arrive_expect_tx(full0 + 8u * s, 2 * C::kBBytes / kHalves);
+            const int a = list[1 + i / kHalves];
+            const int n0 = kDown ? nb * 2 * C::kBN + static_cast<int>(rank) * C::kBN
+                                 : nb * C::kBN + static_cast<int>(rank) * (C::kBN / 2);
+            tma_load_3d_pair(sB + s * C::kBBytes, &p.tmap_lb, full0_lead + 8u * s, 0, n0,
+                             a * kHalves + i % kHalves);
+            filled |= 1u << s;
+            fill_ph = (fill_ph & ~(1u << s)) | (ph << s);
+            if (++s == C::kStages) {
+              s = 0;
+              ph ^= 1u;
+            }
+          }
+        }
         if (paced && ok && round < kPaceRounds) pace_count(round, epoch);
       }
       pdl_launch_dependents();
@@ -310,8 +358,15 @@ __global__ void __launch_bounds__(PairCfg<kMx>::kThreadsT, 1)
       uint32_t ph = 0;
       int buf = 0;
       uint32_t acc_ph = 0;
+      uint32_t vph = 0;  // adapters: phase of each stage's V barrier
       bool ok = true;
       for (int t = pair; ok && t < num_tiles; t += pairs) {
+        int extra = 0;
+        if constexpr (kLora) {
+          int mb, nb;
+          pair_tile_coords(t, p.tiles_m, p.tiles_n, p.group_m, mb, nb);
+          extra = p.lora_lists[static_cast<size_t>(mb) * kLoraListInts] * kHalves;
+        }
         if (!mbar_wait(tempty0 + 8u * buf, acc_ph ^ 1u, wc, kSiteMmaTmemEmpty)) break;
         tc_fence_after();
         const uint32_t d = tmem_base + buf * C::kAccCols;
@@ -346,6 +401,29 @@ __global__ void __launch_bounds__(PairCfg<kMx>::kThreadsT, 1)
           if (++s == C::kStages) {
             s = 0;
             ph ^= 1u;
+          }
+        }
+        if constexpr (kLora) {
+          constexpr uint32_t kIdescV = idesc_bf16_f32(2 * kTileM, 2 * C::kBN / kHalves);
+          const int ksteps = (p.lora_rank + 15) / 16;
+          for (int i = 0; ok && i < extra; ++i) {
+            if (!mbar_wait(full0 + 8u * s, ph, wc, kSiteMmaFull) ||
+                !mbar_wait_cluster(sready0 + 8u * s, (vph >> s) & 1u, wc, kSiteLora)) {
+              ok = false;
+              break;
+            }
+            vph ^= 1u << s;
+            tc_fence_after();
+            const uint64_t vdesc = smem_desc_sw128(sA + s * C::kABytes);
+            const uint64_t bdesc = smem_desc_sw128(sB + s * C::kBBytes);
+            const uint32_t dv = d + (i % kHalves) * C::kBN;
+            for (int k = 0; k < ksteps; ++k)
+              mma_bf16_pair(dv, vdesc + 2u * k, bdesc + 2u * k, kIdescV, 1u);
+            mma_commit_pair_multicast(empty0 + 8u * s, 0x3);
+            if (++s == C::kStages) {
+              s = 0;
+              ph ^= 1u;
+            }
           }
         }
         if (!ok) break;
@@ -391,6 +469,52 @@ __global__ void __launch_bounds__(PairCfg<kMx>::kThreadsT, 1)
       }
       mma_commit_pair_multicast(sdrain_bar, 0x1);
       mbar_wait_drain(sdrain_bar, 0, wc);
+    }
+    __syncwarp();
+  } else if (kLora && warp >= 2 + C::kEpiWarps) {
+    // ------------------------------------------------ masked V rows (both CTAs)
+    // Thread = row of this CTA's 128; the row's own adapter's slices get its V,
+    // every other slice zeros, in the swizzled layout a TMA load would write.
+    const int row = threadIdx.x - (64 + 32 * C::kEpiWarps);
+    const uint32_t sready0_lead = mapa_shared(sready0, 0);
+    const int chunks = p.lora_rank / 8, padded = (p.lora_rank + 15) / 16 * 2;
+    int s = 0;        // stage, in step with the producer
+    uint32_t ph = 0;  // phase of each stage's V-slot-free barrier
+    bool ok = true;
+    for (int t = pair; ok && t < num_tiles; t += pairs) {
+      int mb, nb;
+      pair_tile_coords(t, p.tiles_m, p.tiles_n, p.group_m, mb, nb);
+      const int* list = p.lora_lists + static_cast<size_t>(mb) * kLoraListInts;
+      const int extra = list[0] * kHalves;
+      const int64_t m = int64_t(mb) * 2 * kTileM + static_cast<int>(rank) * kTileM + row;
+      const int own = m < p.M ? p.lora_index[m] : -1;
+      const uint4* v = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.lora_v) +
+                                                      static_cast<size_t>(m) * p.lora_rank * kHalves);
+      s = (s + num_kb) % C::kStages;
+      for (int i = 0; i < extra; ++i) {
+        const bool keep = list[1 + i / kHalves] == own;
+        uint4 x[kLoraMaxRank / 8];
+#pragma unroll
+        for (int c = 0; c < kLoraMaxRank / 8; ++c)
+          x[c] = keep && c < chunks ? __ldg(v + (i % kHalves) * chunks + c) : make_uint4(0u, 0u, 0u, 0u);
+        int go = 1;
+        if (lane == 0) go = mbar_wait(vfree0 + 8u * s, (ph >> s) & 1u, wc, kSiteLora) ? 1 : 0;
+        go = __shfl_sync(0xffffffffu, go, 0);
+        if (!go) {
+          ok = false;
+          break;
+        }
+        ph ^= 1u << s;
+        const uint32_t dst = sA + s * C::kABytes + row * 128;
+#pragma unroll
+        for (int c = 0; c < kLoraMaxRank / 8; ++c)
+          if (c < padded)
+            st_shared_v4(dst + ((c ^ (row & 7)) << 4), x[c].x, x[c].y, x[c].z, x[c].w);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(sready0_lead + 8u * s);
+        if (++s == C::kStages) s = 0;
+      }
     }
     __syncwarp();
   } else {
@@ -571,10 +695,12 @@ __global__ void __launch_bounds__(PairCfg<kMx>::kThreadsT, 1)
 }
 
 cudaLaunchConfig_t pair_config(int grid, cudaStream_t stream, cudaLaunchAttribute* attr,
-                               bool with_pdl, bool mx = false) {
+                               bool with_pdl, bool mx = false, bool lora = false) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(mx ? PairCfg<true>::kThreadsT : PairCfg<false>::kThreadsT);
+  cfg.blockDim = dim3(mx     ? PairCfg<true>::kThreadsT
+                      : lora ? PairCfg<false, true>::kThreadsT
+                             : PairCfg<false>::kThreadsT);
   cfg.dynamicSmemBytes = mx ? PairCfg<true>::kSmem : PairCfg<false>::kSmem;
   cfg.stream = stream;
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -591,29 +717,39 @@ cudaLaunchConfig_t pair_config(int grid, cudaStream_t stream, cudaLaunchAttribut
 }  // namespace
 
 cudaError_t configure_large_m_pair(int* max_pairs) {
-  cudaError_t e = cudaFuncSetAttribute(fused_large_m_pair_kernel<false, false, false>,
+  cudaError_t e = cudaFuncSetAttribute(fused_large_m_pair_kernel<false, false, false, false>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(PairCfg<false>::kSmem));
   if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(fused_large_m_pair_kernel<true, false, false>,
+    e = cudaFuncSetAttribute(fused_large_m_pair_kernel<true, false, false, false>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(PairCfg<false>::kSmem));
   if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(fused_large_m_pair_kernel<false, true, false>,
+    e = cudaFuncSetAttribute(fused_large_m_pair_kernel<false, true, false, false>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(PairCfg<false>::kSmem));
   if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(fused_large_m_pair_kernel<true, false, true>,
+    e = cudaFuncSetAttribute(fused_large_m_pair_kernel<true, false, true, false>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(PairCfg<true>::kSmem));
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg = pair_config(2, nullptr, attr, false);
   int clusters = 0;
-  e = cudaOccupancyMaxActiveClusters(&clusters, fused_large_m_pair_kernel<false, false, false>, &cfg);
+  e = cudaOccupancyMaxActiveClusters(&clusters, fused_large_m_pair_kernel<false, false, false, false>, &cfg);
   if (e != cudaSuccess) return e;
   *max_pairs = clusters;
   return cudaSuccess;
+}
+
+cudaError_t configure_large_m_pair_lora() {
+  const cudaError_t e = cudaFuncSetAttribute(fused_large_m_pair_kernel<false, false, false, true>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(PairCfg<false, true>::kSmem));
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(fused_large_m_pair_kernel<false, true, false, true>,
+                              cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              static_cast<int>(PairCfg<false, true>::kSmem));
 }
 
 size_t large_m_pair_smem_bytes() { return PairCfg<false>::kSmem; }
@@ -626,14 +762,19 @@ cudaError_t large_m_pair_pace_run_out(unsigned long long* count) {
 cudaError_t launch_large_m_pair(const LargeMParams& p, cudaStream_t stream) {
   if (p.grid < 2 || (p.grid % 2) != 0 || p.bn != PairCfg<false>::kBN) return cudaErrorInvalidValue;
   cudaLaunchAttribute attr[2];
-  cudaLaunchConfig_t cfg = pair_config(p.grid, stream, attr, pdl_enabled(), p.mx != 0);
+  cudaLaunchConfig_t cfg = pair_config(p.grid, stream, attr, pdl_enabled(), p.mx != 0, p.lora != 0);
   if (p.fp8 && p.down) return cudaErrorInvalidValue;  // no FP8 down-projection
   if (p.mx && !p.fp8) return cudaErrorInvalidValue;   // block scales go with E4M3 values
+  if (p.lora && (p.fp8 || p.lora_rank < 8 || p.lora_rank > kLoraMaxRank || (p.lora_rank % 8) != 0 ||
+                 !p.lora_v || !p.lora_index || !p.lora_lists))
+    return cudaErrorInvalidValue;
   const cudaError_t e =
-      p.down  ? cudaLaunchKernelEx(&cfg, fused_large_m_pair_kernel<false, true, false>, p)
-      : p.mx  ? cudaLaunchKernelEx(&cfg, fused_large_m_pair_kernel<true, false, true>, p)
-      : p.fp8 ? cudaLaunchKernelEx(&cfg, fused_large_m_pair_kernel<true, false, false>, p)
-              : cudaLaunchKernelEx(&cfg, fused_large_m_pair_kernel<false, false, false>, p);
+      p.lora && p.down ? cudaLaunchKernelEx(&cfg, fused_large_m_pair_kernel<false, true, false, true>, p)
+      : p.lora ? cudaLaunchKernelEx(&cfg, fused_large_m_pair_kernel<false, false, false, true>, p)
+      : p.down  ? cudaLaunchKernelEx(&cfg, fused_large_m_pair_kernel<false, true, false, false>, p)
+      : p.mx  ? cudaLaunchKernelEx(&cfg, fused_large_m_pair_kernel<true, false, true, false>, p)
+      : p.fp8 ? cudaLaunchKernelEx(&cfg, fused_large_m_pair_kernel<true, false, false, false>, p)
+              : cudaLaunchKernelEx(&cfg, fused_large_m_pair_kernel<false, false, false, false>, p);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 

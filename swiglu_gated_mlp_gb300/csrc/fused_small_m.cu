@@ -37,6 +37,21 @@
 // and the activations' scale block for the same K slice; the MMA thread copies
 // them into a per-stage slot of tensor memory (tcgen05.cp) and issues
 // kind::mxf8f6f4 MMAs that apply both scales inside the tensor core.
+//
+// With kLora (bf16) each token m also has a low-rank adapter a = index[m] of a
+// table shared by the batch (none where the index names none):
+//   Gate += V1 Lb[a][0]^T, Up += V2 Lb[a][1]^T   (down: Out += V Lb[a]^T),
+// V [M, rank] per product from lora_shrink.cu, fp32. The delta is 2 * M * rank
+// products a weight column, far less than the weight stream takes, and reads
+// only the adapters present. The warps that otherwise wait for the accumulators
+// compute it during the stream with fp32 FMAs: thread = weight column, one
+// token's adapter row at a time, so tokens never meet another's adapter and
+// nothing is padded or masked. Four more warps join them; the deltas wait in
+// tensor memory beside the accumulators (columns 2 mt to 4 mt) and the epilogue
+// adds the two. The producer does not wait for the grid before this one, which
+// is always the kernel that makes V: that grid lets this one start only after
+// everything before it has completed. With K split, part k computes the deltas
+// of every kparts-th chunk of 8 tokens, once in all.
 #include "kernels.h"
 #include "ptx.cuh"
 
@@ -167,10 +182,80 @@ __device__ __noinline__ void cross_cluster_finish(const SmallMParams& p, int uni
   }
 }
 
-template <bool kFp8, bool kDown, bool kMx>
-__global__ void __launch_bounds__(kThreads, 1)
+constexpr int kLoraThreads = kThreads + 128;   // kLora: 8 warps compute the adapters' deltas
+constexpr int kLoraChunk = 8;                  // tokens a warp has in registers
+
+// The adapters' deltas of this CTA's weight rows and its share of the tokens,
+// to tensor memory at `tdelta` (gate, or the low 128 columns) and `tdelta` + mt.
+template <bool kDown>
+__device__ __forceinline__ void lora_deltas(const SmallMParams& p, uint32_t tdelta, int mt, int m0,
+                                            int mcount, int nblk, int row, int set, int kpart,
+                                            int kparts) {
+  const int rank = p.lora_rank;
+  const int n = (kDown ? 2 : 1) * nblk * kPackBlockN + row;
+  const size_t per_adapter = static_cast<size_t>(kDown ? 1 : 2) * p.N * rank;
+  // gate row n and up row n of an adapter, or its output columns n and n + 128
+  const size_t second = static_cast<size_t>(kDown ? kPackBlockN : p.N) * rank;
+  const bool lo = n < p.N, hi = kDown ? n + kPackBlockN < p.N : lo;
+  const __nv_bfloat16* lb = static_cast<const __nv_bfloat16*>(p.lora_b) + static_cast<size_t>(n) * rank;
+  const int hr = kDown ? rank : 2 * rank;
+  for (int c = set * kparts + kpart; c * kLoraChunk < mcount; c += 2 * kparts) {
+    float g[kLoraChunk] = {}, u[kLoraChunk] = {};
+#pragma unroll
+    for (int h = 0; h < kLoraChunk; h += 4) {  // four tokens' loads at a time
+      const __nv_bfloat16* src[4];
+      const float* v[4];
+      bool has[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int m = c * kLoraChunk + h + j;
+        const int a = m < mcount ? __ldg(p.lora_index + m0 + m) : -1;
+        has[j] = a >= 0 && a < p.lora_count;
+        src[j] = lb + (has[j] ? a : 0) * per_adapter;
+        v[j] = p.lora_v + static_cast<size_t>(m0 + (m < mcount ? m : 0)) * hr;
+      }
+      for (int r = 0; r < rank; r += 8) {
+        uint4 x[4], y[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          x[j] = y[j] = make_uint4(0u, 0u, 0u, 0u);
+          if (has[j] && lo) x[j] = __ldg(reinterpret_cast<const uint4*>(src[j] + r));
+          if (has[j] && hi) y[j] = __ldg(reinterpret_cast<const uint4*>(src[j] + second + r));
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (!has[j]) continue;  // the same in the whole warp
+          const uint32_t xw[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+          const uint32_t yw[4] = {y[j].x, y[j].y, y[j].z, y[j].w};
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float4 vg = __ldcg(reinterpret_cast<const float4*>(v[j] + r) + e);
+            const float4 vu =
+                kDown ? vg : __ldcg(reinterpret_cast<const float4*>(v[j] + rank + r) + e);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const float g0 = i ? vg.z : vg.x, g1 = i ? vg.w : vg.y;
+              const float u0 = i ? vu.z : vu.x, u1 = i ? vu.w : vu.y;
+              const uint32_t xv = xw[2 * e + i], yv = yw[2 * e + i];
+              g[h + j] = fmaf(g0, __uint_as_float(xv << 16), g[h + j]);
+              g[h + j] = fmaf(g1, __uint_as_float(xv & 0xffff0000u), g[h + j]);
+              u[h + j] = fmaf(u0, __uint_as_float(yv << 16), u[h + j]);
+              u[h + j] = fmaf(u1, __uint_as_float(yv & 0xffff0000u), u[h + j]);
+            }
+          }
+        }
+      }
+    }
+    tmem_st_x8(tdelta + c * kLoraChunk, g);
+    tmem_st_x8(tdelta + mt + c * kLoraChunk, u);
+  }
+}
+
+template <bool kFp8, bool kDown, bool kMx, bool kLora>
+__global__ void __launch_bounds__(kLora ? kLoraThreads : kThreads, kLora ? 2 : 1)
     fused_small_m_kernel(const __grid_constant__ SmallMParams p) {
   static_assert(!kMx || (kFp8 && !kDown), "block scales go with E4M3 gate/up inputs");
+  static_assert(!kLora || !kFp8, "adapters go with bf16");
   // K values per stage: 64 bf16 or 128 E4M3, a 128-byte row either way
   constexpr int kBK = kFp8 ? kBlockK8 : kBlockK;
   extern __shared__ uint8_t smem_raw[];
@@ -192,9 +277,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   // accumulators: gate [0, mt), up [mt, 2 mt); then kSfTmemCols scale columns per stage
+  // (block-scaled), or the adapters' gate and up deltas
   const uint32_t sf_col = 2u * mt;
   uint32_t tmem_cols = 32;
-  while (tmem_cols < sf_col + (kMx ? uint32_t(kSfTmemCols) * stages : 0u)) tmem_cols <<= 1;
+  while (tmem_cols < sf_col + (kMx ? uint32_t(kSfTmemCols) * stages : kLora ? 2u * mt : 0u))
+    tmem_cols <<= 1;
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -250,7 +337,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
-  pdl_wait();  // the set-up and L2 staging above overlap the previous grid; loads start here
+  // the set-up and L2 staging above overlap the previous grid; loads start here
+  // (with adapters the previous grid makes V, which only warps 2 and up read)
+  if (!kLora || warp >= 2) pdl_wait();
 
   if (warp == 0) {
     // ------------------------------------------------ TMA producer -----
@@ -351,9 +440,37 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int q = warp & 3;
     const uint32_t lane_off = static_cast<uint32_t>(q * 32) << 16;
     const int n = nblk * kPackBlockN + q * 32 + lane;  // this thread's output column
-    int ok = 1;
-    if (lane == 0) ok = mbar_wait(tfull_bar, 0, wc, kSiteEpiTmemFull) ? 1 : 0;
+    if constexpr (kLora) {
+      lora_deltas<kDown>(p, tmem_base + lane_off + 2u * mt, mt, m0, mcount, nblk, q * 32 + lane,
+                         warp >= 6 ? 1 : 0, kpart, kparts);
+      tmem_wait_st();
+      tc_fence_before();
+      named_barrier(1, kLoraThreads - 64);
+      tc_fence_after();
+    }
+    int ok = !kLora || warp < 6;  // the other warps' work ends here
+    if (ok && lane == 0) ok = mbar_wait(tfull_bar, 0, wc, kSiteEpiTmemFull) ? 1 : 0;
     ok = __shfl_sync(0xffffffffu, ok, 0);
+    // accumulators of 16 tokens, with the adapters' deltas this CTA computed
+    const auto add_deltas = [&](int mc, uint32_t (&g)[16], uint32_t (&u)[16]) {
+      if constexpr (kLora) {
+        uint32_t dg[16], du[16];
+        tmem_ld_x16(tmem_base + lane_off + 2 * mt + mc * 16, dg);
+        tmem_ld_x16(tmem_base + lane_off + 3 * mt + mc * 16, du);
+        tmem_wait_ld();
+        reg_fence(dg);
+        reg_fence(du);
+#pragma unroll
+        for (int h = 0; h < 16 / kLoraChunk; ++h) {
+          if ((mc * (16 / kLoraChunk) + h) % kparts != kpart) continue;  // another K part's
+#pragma unroll
+          for (int j = h * kLoraChunk; j < (h + 1) * kLoraChunk; ++j) {
+            g[j] = __float_as_uint(__uint_as_float(g[j]) + __uint_as_float(dg[j]));
+            u[j] = __float_as_uint(__uint_as_float(u[j]) + __uint_as_float(du[j]));
+          }
+        }
+      }
+    };
     if (ok && kparts > 1) {
       // K part only: fp32 partials to this CTA's shared memory (the ring is idle
       // now), as P[c][r] for accumulator column c (gate 0..mt-1, up mt..2mt-1)
@@ -369,6 +486,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_wait_ld();
         reg_fence(g);
         reg_fence(u);
+        add_deltas(mc, g, u);
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
           part_buf[(mc * 16 + j) * kPackBlockN + r] = __uint_as_float(g[j]);
@@ -389,6 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_wait_ld();
         reg_fence(g);
         reg_fence(u);
+        add_deltas(mc, g, u);
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
           const int m = mc * 16 + j;
@@ -414,6 +533,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_wait_ld();
         reg_fence(g);
         reg_fence(u);
+        add_deltas(mc, g, u);
         if (n < p.N) {
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
@@ -511,13 +631,13 @@ size_t small_m_smem_bytes(int mt, int stages, int extra) {
          kBarBytes;
 }
 
-template <bool kFp8, bool kDown, bool kMx>
+template <bool kFp8, bool kDown, bool kMx, bool kLora = false>
 cudaError_t configure_small_m_t() {
-  cudaError_t e = cudaFuncSetAttribute(fused_small_m_kernel<kFp8, kDown, kMx>,
+  cudaError_t e = cudaFuncSetAttribute(fused_small_m_kernel<kFp8, kDown, kMx, kLora>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(kSmemLimit));
   if (e == cudaSuccess)  // all of the unified L1/shared array as shared memory (2 CTAs may share an SM)
-    e = cudaFuncSetAttribute(fused_small_m_kernel<kFp8, kDown, kMx>,
+    e = cudaFuncSetAttribute(fused_small_m_kernel<kFp8, kDown, kMx, kLora>,
                              cudaFuncAttributePreferredSharedMemoryCarveout, 100);
   return e;
 }
@@ -528,6 +648,11 @@ cudaError_t configure_small_m() {
   if (e == cudaSuccess) e = configure_small_m_t<false, true, false>();
   if (e == cudaSuccess) e = configure_small_m_t<true, false, true>();
   return e;
+}
+
+cudaError_t configure_small_m_lora() {
+  const cudaError_t e = configure_small_m_t<false, false, false, true>();
+  return e == cudaSuccess ? configure_small_m_t<false, true, false, true>() : e;
 }
 
 cudaError_t static_scratch_address(uint32_t** out) {
@@ -553,7 +678,7 @@ int small_m_max_clusters(int splits) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   int clusters = 0;
-  if (cudaOccupancyMaxActiveClusters(&clusters, fused_small_m_kernel<false, false, false>, &cfg) !=
+  if (cudaOccupancyMaxActiveClusters(&clusters, fused_small_m_kernel<false, false, false, false>, &cfg) !=
       cudaSuccess) {
     cudaGetLastError();
     return 0;
@@ -581,12 +706,16 @@ cudaError_t launch_small_m(const SmallMParams& p, cudaStream_t stream) {
   if (p.mx && (!p.fp8 || p.down || (p.mgroups > 1) || p.mt > 128 ||
                2 * p.mt + kSfTmemCols * p.stages > 512))
     return cudaErrorInvalidValue;
+  // adapters: deltas beside the accumulators, one cluster per unit
+  if (p.lora && (p.fp8 || gsplits > 1 || p.mt > 128 || p.lora_rank < 8 || (p.lora_rank % 8) != 0 ||
+                 !p.lora_v || !p.lora_index || !p.lora_b))
+    return cudaErrorInvalidValue;
   const int extra = p.mx ? kSfStageBytes : 0;
   SmallMParams q = p;
   q.l2_prefetch = small_m_l2_prefetch(p.grid, p.splits);
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(p.grid);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(p.lora ? kLoraThreads : kThreads);
   cfg.dynamicSmemBytes = small_m_smem_bytes(p.mt, p.stages, extra);
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
@@ -600,10 +729,12 @@ cudaError_t launch_small_m(const SmallMParams& p, cudaStream_t stream) {
   cfg.numAttrs = splits > 1 ? 2 : 1;
   if (p.fp8 && p.down) return cudaErrorInvalidValue;  // no FP8 down-projection
   const cudaError_t e =
-      p.down  ? cudaLaunchKernelEx(&cfg, fused_small_m_kernel<false, true, false>, q)
-      : p.mx  ? cudaLaunchKernelEx(&cfg, fused_small_m_kernel<true, false, true>, q)
-      : p.fp8 ? cudaLaunchKernelEx(&cfg, fused_small_m_kernel<true, false, false>, q)
-              : cudaLaunchKernelEx(&cfg, fused_small_m_kernel<false, false, false>, q);
+      p.lora && p.down ? cudaLaunchKernelEx(&cfg, fused_small_m_kernel<false, true, false, true>, q)
+      : p.lora         ? cudaLaunchKernelEx(&cfg, fused_small_m_kernel<false, false, false, true>, q)
+      : p.down         ? cudaLaunchKernelEx(&cfg, fused_small_m_kernel<false, true, false, false>, q)
+      : p.mx           ? cudaLaunchKernelEx(&cfg, fused_small_m_kernel<true, false, true, false>, q)
+      : p.fp8          ? cudaLaunchKernelEx(&cfg, fused_small_m_kernel<true, false, false, false>, q)
+                       : cudaLaunchKernelEx(&cfg, fused_small_m_kernel<false, false, false, false>, q);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 

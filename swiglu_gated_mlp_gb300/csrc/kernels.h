@@ -22,6 +22,11 @@ constexpr int kSfBlockBytes = 512;
 constexpr int kSfStageBytes = 3 * kSfBlockBytes;  // gate + up weight scales, activation scales
 constexpr int kSfTmemCols = 16;                   // TMEM columns per stage of scales (12 used)
 
+// Low-rank adapters beside the shared projection: ranks are multiples of 8 up
+// to this; the pair kernel's lists hold a count and up to 256 adapters a tile.
+constexpr int kLoraMaxRank = 64;
+constexpr int kLoraListInts = 260;
+
 struct LargeMParams {
   CUtensorMap tmap_a;  // A  [M, K]       box {64, 128}, 128-B swizzle
   CUtensorMap tmap_w;  // Wp {64, 256, tiles} box {64, bn, 1}, 128-B swizzle
@@ -42,6 +47,14 @@ struct LargeMParams {
   uint64_t timeout_ns;
   int inject_stall;
   int l2_prefetch;  // single-CTA kernel: K slices of its first tile each CTA stages in L2
+  // adapters (pair kernel, bf16): V [M, rank or 2 rank] bf16, each token's adapter, the
+  // adapters present per 256 tokens, and Lb {rank, N, adapters x (1 or 2)} box {64, 64 or 128, 1}
+  CUtensorMap tmap_lb;
+  int lora;
+  int lora_rank;
+  const void* lora_v;
+  const int* lora_index;
+  const int* lora_lists;
 };
 
 struct SmallMParams {
@@ -73,11 +86,43 @@ struct SmallMParams {
   int gsplits;
   float* ws;
   uint32_t* counters;
+  // adapters (bf16): V [M, rank or 2 rank] fp32, each token's adapter, Lb as
+  // [count, 2, N, rank] (gate/up) or [count, N, rank] (down)
+  int lora;
+  int lora_rank, lora_count;
+  const float* lora_v;
+  const int* lora_index;
+  const void* lora_b;
 };
+
+// V = scale_a * x La[a]^T of each token's adapter a = index[token]
+// (lora_shrink.cu); tokens whose index names no adapter get none.
+struct LoraShrinkParams {
+  CUtensorMap tmap_x;   // many tokens: x [M, K] box {64, 128}, 128-B swizzle
+  CUtensorMap tmap_la;  // many tokens: La {K, count * hr} box {64, rb}, 128-B swizzle
+  const void* x;
+  const void* la;       // [count, hr, K]
+  const int* index;     // [M]
+  const float* scale;   // [count]
+  int count, M, K, hr;
+  void* v;              // [M, hr]: fp32 (few tokens) or bf16 (many tokens)
+  // many tokens (tiles > 0): 128-token tiles, K over clusters of `splits` CTAs
+  int* lists;           // per 256 tokens: count, then the adapters present
+  int tiles, splits, slices;
+  int rb;               // hr rounded up to 16: accumulator columns of an adapter
+  int per_pass;         // adapters side by side in the accumulator
+  uint32_t* status;
+  uint64_t timeout_ns;
+  int inject_stall;
+};
+
+cudaError_t configure_lora_shrink();
+cudaError_t launch_lora_shrink(const LoraShrinkParams& p, cudaStream_t stream);
 
 // One-time per-device set-up (dynamic shared-memory limits of every instantiation).
 cudaError_t configure_large_m();
 cudaError_t configure_small_m();
+cudaError_t configure_small_m_lora();
 
 int large_m_stages(int bn);
 // K slices of its first tile a single-CTA kernel CTA stages in L2 before its
@@ -90,6 +135,7 @@ cudaError_t launch_large_m(const LargeMParams& p, cudaStream_t stream);
 // CTA-pair variant (bn = 128, 256-row tiles, grid = 2 x pairs): one-time set-up
 // also reports how many pairs can be resident at once.
 cudaError_t configure_large_m_pair(int* max_pairs);
+cudaError_t configure_large_m_pair_lora();
 size_t large_m_pair_smem_bytes();
 int large_m_pair_stages(bool mx = false);
 // Number of the pair kernel's tile-round pacing waits that ran out on the

@@ -1,0 +1,382 @@
+// First half of the low-rank adapters: each token's V = scale_a * x La[a]^T
+// with a = index[token], for the kernels that add V Lb[a]^T to the shared
+// projection (fused_small_m.cu and fused_large_m_pair.cu, kLora).
+//
+// La [L, hr, K] holds the rows that one adapter shrinks to: gate then up rows
+// of a gate/up adapter (hr = 2 rank), or the rank rows of a down adapter. Per
+// token the product is hr x K, far below the projection's, so what counts is
+// that it reads x once and each adapter present once, and ends early.
+//
+// Few tokens (the decode kernel's range): lora_shrink_dot_kernel, plain dot
+// products in fp32. One CTA takes a token and 4 rows; its 8 warps split K, so
+// every load of a CTA is in flight at once. V stays in fp32. The decode kernel
+// starts streaming the shared weight while this kernel runs (it waits for V
+// only before it needs it), so the time that matters is that of the launch.
+//
+// Many tokens: lora_shrink_tile_kernel, tcgen05 with 128 tokens as the MMA's
+// M side and the rows of the adapters present in the tile as its N side. The
+// tile's tokens are multiplied by every adapter present (a tile of one prompt
+// has one), and each token keeps its own adapter's columns: a value of another
+// adapter, finite or not, never reaches it. K is split over a cluster of up to
+// 8 CTAs, whose fp32 sums are added in order through distributed shared memory.
+// V is rounded to bf16, the operand type of the expanding product: the delta it
+// enters is a fraction of the projection, which is itself rounded to bf16. The
+// kernel also lists, per 256 tokens (a CTA pair's tile), the adapters present.
+#include "kernels.h"
+#include "ptx.cuh"
+
+namespace swg {
+namespace {
+
+// ------------------------------------------------------------- few tokens ---
+
+constexpr int kDotRows = 4;
+constexpr int kDotThreads = 256;
+
+__device__ __forceinline__ float dot8(const uint4& a, const uint4& b, float acc) {
+  const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {  // a bf16 is the high half of its fp32
+    acc = fmaf(__uint_as_float(x[i] << 16), __uint_as_float(y[i] << 16), acc);
+    acc = fmaf(__uint_as_float(x[i] & 0xffff0000u), __uint_as_float(y[i] & 0xffff0000u), acc);
+  }
+  return acc;
+}
+
+__global__ void __launch_bounds__(kDotThreads)
+    lora_shrink_dot_kernel(const __grid_constant__ LoraShrinkParams p) {
+  __shared__ float sums[kDotThreads / 32][kDotRows];
+  pdl_wait();
+  // The projection's kernel may start now: everything before this grid has
+  // completed, so it may read the tokens and weights without waiting for it.
+  pdl_launch_dependents();
+  const int row_blocks = (p.hr + kDotRows - 1) / kDotRows;
+  const int m = blockIdx.x / row_blocks;
+  const int r0 = (blockIdx.x % row_blocks) * kDotRows;
+  const int a = p.index[m];
+  if (a < 0 || a >= p.count) return;
+  const uint4* x = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.x) +
+                                                  static_cast<size_t>(m) * p.K);
+  const uint4* la = reinterpret_cast<const uint4*>(
+      static_cast<const __nv_bfloat16*>(p.la) + (static_cast<size_t>(a) * p.hr + r0) * p.K);
+  const int chunks = p.K / 8;
+  float acc[kDotRows] = {};
+#pragma unroll 4
+  for (int i = threadIdx.x; i < chunks; i += kDotThreads) {
+    const uint4 xv = __ldg(x + i);
+#pragma unroll
+    for (int r = 0; r < kDotRows; ++r)  // hr is a multiple of 8: every row exists
+      acc[r] = dot8(xv, __ldg(la + static_cast<size_t>(r) * chunks + i), acc[r]);
+  }
+#pragma unroll
+  for (int r = 0; r < kDotRows; ++r)
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) acc[r] += __shfl_xor_sync(0xffffffffu, acc[r], o);
+  if ((threadIdx.x & 31) == 0)
+#pragma unroll
+    for (int r = 0; r < kDotRows; ++r) sums[threadIdx.x >> 5][r] = acc[r];
+  __syncthreads();
+  if (threadIdx.x < kDotRows) {
+    float v = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kDotThreads / 32; ++w) v += sums[w][threadIdx.x];
+    static_cast<float*>(p.v)[static_cast<size_t>(m) * p.hr + r0 + threadIdx.x] = v * p.scale[a];
+  }
+}
+
+// ------------------------------------------------------------ many tokens ---
+
+constexpr int kTileThreads = 256;
+constexpr int kTileCols = 256;                                     // accumulator columns
+constexpr int kXBytes = 128 * kBlockK * 2;                         // 16 KB of tokens
+constexpr int kTileStage = kXBytes + kTileCols * kBlockK * 2;      // + up to 256 adapter rows
+constexpr int kTileStages = 3;
+constexpr int kPartPad = 4;                                        // floats, against bank conflicts
+constexpr int kTileBar = 128;
+constexpr size_t tile_smem(int rb) {
+  return 1024 + size_t(kTileStages) * kTileStage + size_t(128) * (rb + kPartPad) * 4 + kTileBar;
+}
+static_assert(tile_smem(2 * kLoraMaxRank) <= 232448, "shared memory budget");
+
+__global__ void __launch_bounds__(kTileThreads, 1)
+    lora_shrink_tile_kernel(const __grid_constant__ LoraShrinkParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  __shared__ __align__(16) int ids[2 * kTileM];  // adapters of the 256 tokens (-1: none)
+  __shared__ int mine[kTileM];                   // adapters present among this tile's 128 tokens
+  __shared__ int counts[2][kTileThreads / 32];
+  const int rb = p.rb;                           // accumulator columns of one adapter
+  const int part_stride = rb + kPartPad;
+  const uint32_t s0 = smem_addr(smem);
+  float* part = reinterpret_cast<float*>(smem + kTileStages * kTileStage);
+  uint8_t* bar_ptr = reinterpret_cast<uint8_t*>(part) + size_t(128) * part_stride * 4;
+  const uint32_t bar0 = smem_addr(bar_ptr);
+  // barrier slots: full[3] | empty[3] | tmem_full | tmem_empty | drain
+  const uint32_t full0 = bar0, empty0 = bar0 + 8u * kTileStages;
+  const uint32_t tfull = bar0 + 16u * kTileStages, tempty = tfull + 8u, drain_bar = tfull + 16u;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_ptr + 8 * (2 * kTileStages + 3));
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const WaitCtx wc{abort_flag, p.status, p.timeout_ns};
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int splits = p.splits;
+  const int kpart = blockIdx.x % splits, tile = blockIdx.x / splits;  // kpart: rank in the cluster
+  const int m0 = tile * kTileM;
+  const int half = tile & 1;            // which 128 of the 256 tokens
+  const int begin = kpart * p.slices / splits, end = (kpart + 1) * p.slices / splits;
+
+  if (tid == 0) {
+    prefetch_tmap(&p.tmap_x);
+    prefetch_tmap(&p.tmap_la);
+    for (int s = 0; s < kTileStages; ++s) {
+      mbar_init(full0 + 8u * s, 1);
+      mbar_init(empty0 + 8u * s, 1);
+    }
+    mbar_init(tfull, 1);
+    mbar_init(tempty, 4);
+    mbar_init(drain_bar, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_addr(tmem_slot), kTileCols);
+    tmem_relinquish();
+  }
+  pdl_wait();
+  {
+    const int64_t m = int64_t(m0) - half * kTileM + tid;
+    const int a = m < p.M ? p.index[m] : -1;
+    ids[tid] = a >= 0 && a < p.count ? a : -1;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
+  // Adapters in the order of their first token: of the 256 (for the pair
+  // kernel) and of this tile's 128.
+  const int own = ids[tid];
+  const int in_tile = tid / kTileM == half;
+  bool first256 = own >= 0, first128 = own >= 0 && in_tile;
+  for (int t = 0; t < tid; t += 4) {
+    const int4 v = *reinterpret_cast<const int4*>(ids + t);
+    const int x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (t + e < tid && x[e] == own) {
+        first256 = false;
+        if (t + e >= half * kTileM) first128 = false;
+      }
+  }
+  const uint32_t b256 = __ballot_sync(0xffffffffu, first256), b128 = __ballot_sync(0xffffffffu, first128);
+  if (lane == 0) {
+    counts[0][warp] = __popc(b256);
+    counts[1][warp] = __popc(b128);
+  }
+  __syncthreads();
+  int n256 = 0, n128 = 0, at256 = 0, at128 = 0;
+#pragma unroll
+  for (int w = 0; w < kTileThreads / 32; ++w) {
+    if (w < warp) {
+      at256 += counts[0][w];
+      at128 += counts[1][w];
+    }
+    n256 += counts[0][w];
+    n128 += counts[1][w];
+  }
+  const uint32_t below = (1u << lane) - 1u;
+  if (first128) mine[at128 + __popc(b128 & below)] = own;
+  if (half == 0 && kpart == 0) {
+    int* list = p.lists + static_cast<size_t>(tile >> 1) * kLoraListInts;
+    if (first256) list[1 + at256 + __popc(b256 & below)] = own;
+    if (tid == 0) list[0] = n256;
+  }
+  __syncthreads();
+  pdl_launch_dependents();
+
+  const int per_pass = p.per_pass;  // adapters side by side in the accumulator
+  const int passes = (n128 + per_pass - 1) / per_pass;
+  const uint32_t la_bytes = static_cast<uint32_t>(rb) * 128u;
+  if (warp == 0) {
+    if (lane == 0) {
+      int s = 0;
+      uint32_t ph = 0, filled = 0, fill_ph = 0;
+      bool skip_once = p.inject_stall != 0, ok = true;
+      for (int pass = 0; ok && pass < passes; ++pass) {
+        const int g0 = pass * per_pass, gn = min(per_pass, n128 - g0);
+        for (int i = begin; i < end; ++i) {
+          if (!mbar_wait(empty0 + 8u * s, ph ^ 1u, wc, kSiteProducerEmpty)) {
+            ok = false;
+            break;
+          }
+          if (skip_once) {
+            skip_once = false;  // testing hook: leave this stage unfilled
+          } else {
+            const uint32_t fb = full0 + 8u * s, dst = s0 + s * kTileStage;
+            mbar_arrive_expect_tx(fb, kXBytes + gn * la_bytes);
+            tma_load_2d(dst, &p.tmap_x, fb, i * kBlockK, m0);
+            for (int g = 0; g < gn; ++g)
+              tma_load_2d(dst + kXBytes + g * la_bytes, &p.tmap_la, fb, i * kBlockK,
+                          mine[g0 + g] * p.hr);
+            filled |= 1u << s;
+            fill_ph = (fill_ph & ~(1u << s)) | (ph << s);
+          }
+          if (++s == kTileStages) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+      }
+      for (int i = 0; i < kTileStages; ++i)
+        if (filled & (1u << i)) mbar_wait_drain(full0 + 8u * i, (fill_ph >> i) & 1u, wc);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint32_t idesc = idesc_bf16_f32(kTileM, rb);
+      int s = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int pass = 0; ok && pass < passes; ++pass) {
+        const int gn = min(per_pass, n128 - pass * per_pass);
+        if (pass > 0 && !mbar_wait(tempty, (pass - 1) & 1, wc, kSiteMmaTmemEmpty)) break;
+        tc_fence_after();
+        for (int i = begin; i < end; ++i) {
+          if (!mbar_wait(full0 + 8u * s, ph, wc, kSiteMmaFull)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t src = s0 + s * kTileStage;
+          const uint64_t xdesc = smem_desc_sw128(src);
+          for (int g = 0; g < gn; ++g) {
+            const uint64_t ldesc = smem_desc_sw128(src + kXBytes + g * la_bytes);
+#pragma unroll
+            for (uint32_t k = 0; k < 4; ++k)
+              mma_bf16(tmem_base + g * rb, xdesc + 2u * k, ldesc + 2u * k, idesc,
+                       (i != begin || k != 0) ? 1u : 0u);
+          }
+          mma_commit(empty0 + 8u * s);
+          if (++s == kTileStages) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+        if (ok) mma_commit(tfull);
+      }
+      mma_commit(drain_bar);
+      mbar_wait_drain(drain_bar, 0, wc);
+    }
+    __syncwarp();
+  } else if (warp < 6) {
+    // each thread keeps its token's own adapter's columns
+    const int q = warp & 3, row = q * 32 + lane;
+    const int my = ids[half * kTileM + row];
+    float* dst = part + row * part_stride;
+    for (int pass = 0; pass < passes; ++pass) {
+      int ok = 1;
+      if (lane == 0) ok = mbar_wait(tfull, pass & 1, wc, kSiteEpiTmemFull) ? 1 : 0;
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!ok) break;
+      tc_fence_after();
+      const int g0 = pass * per_pass, gn = min(per_pass, n128 - g0);
+      for (int g = 0; g < gn; ++g) {
+        const bool keep = mine[g0 + g] == my;
+        if (!__any_sync(0xffffffffu, keep)) continue;
+        for (int c = 0; c < rb; c += 16) {
+          uint32_t v[16];
+          tmem_ld_x16(tmem_base + (static_cast<uint32_t>(q * 32) << 16) + g * rb + c, v);
+          tmem_wait_ld();
+          reg_fence(v);
+          if (keep)
+#pragma unroll
+            for (int j = 0; j < 16; j += 4)
+              *reinterpret_cast<uint4*>(dst + c + j) = make_uint4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(tempty);
+    }
+    __syncwarp();
+  }
+  // Every part's sums are in its CTA's shared memory: each CTA adds its share
+  // of the rows over the parts in order, scales, rounds and stores.
+  tc_fence_before();
+  cluster_sync();
+  const int rows = kTileM / splits, chunks = p.hr / 8;
+  const uint32_t local = smem_addr(part);
+  for (int i = tid; i < rows * chunks; i += kTileThreads) {
+    const int row = kpart * rows + i / chunks, c = (i % chunks) * 8;
+    const int a = ids[half * kTileM + row];
+    if (a < 0) continue;  // no adapter (or no token): V is not read
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+    for (int s = 0; s < splits; ++s) {
+      const uint32_t src = mapa_shared(local, s) + 4u * (row * part_stride + c);
+      const float4 u = ld_shared_cluster_v4(src), w = ld_shared_cluster_v4(src + 16u);
+      x.x += u.x; x.y += u.y; x.z += u.z; x.w += u.w;
+      y.x += w.x; y.y += w.y; y.z += w.z; y.w += w.w;
+    }
+    const float f = p.scale[a];
+    uint4 o;
+    o.x = pack_bf16x2(x.x * f, x.y * f);
+    o.y = pack_bf16x2(x.z * f, x.w * f);
+    o.z = pack_bf16x2(y.x * f, y.y * f);
+    o.w = pack_bf16x2(y.z * f, y.w * f);
+    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.v) +
+                              (static_cast<size_t>(m0) + row) * p.hr + c) = o;
+  }
+  cluster_sync();  // no CTA leaves while a peer may still read its sums
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, kTileCols);
+  }
+}
+
+}  // namespace
+
+cudaError_t configure_lora_shrink() {
+  cudaError_t e = cudaFuncSetAttribute(lora_shrink_tile_kernel,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(tile_smem(2 * kLoraMaxRank)));
+  // The same split of the L1/shared array as the decode kernel's, so that its
+  // CTAs can join an SM that still runs this kernel.
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(lora_shrink_dot_kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                             100);
+  return e;
+}
+
+cudaError_t launch_lora_shrink(const LoraShrinkParams& p, cudaStream_t stream) {
+  if (p.M < 1 || p.hr < 8 || (p.hr % 8) != 0 || p.hr > 2 * kLoraMaxRank) return cudaErrorInvalidValue;
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = pdl_enabled() ? 1 : 0;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cfg.stream = stream;
+  cudaError_t e;
+  if (p.tiles == 0) {
+    cfg.gridDim = dim3(static_cast<unsigned>(p.M) * ((p.hr + kDotRows - 1) / kDotRows));
+    cfg.blockDim = dim3(kDotThreads);
+    e = cudaLaunchKernelEx(&cfg, lora_shrink_dot_kernel, p);
+  } else {
+    if (p.splits < 1 || p.splits > 8 || (kTileM % p.splits) != 0 || p.slices < p.splits ||
+        (p.rb % 16) != 0 || p.rb < p.hr || p.rb > 2 * kLoraMaxRank || p.per_pass < 1 ||
+        p.per_pass * p.rb > kTileCols)
+      return cudaErrorInvalidValue;
+    cfg.gridDim = dim3(static_cast<unsigned>(p.tiles) * p.splits);
+    cfg.blockDim = dim3(kTileThreads);
+    cfg.dynamicSmemBytes = tile_smem(p.rb);
+    attr[1].val.clusterDim.x = p.splits;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.numAttrs = 2;
+    e = cudaLaunchKernelEx(&cfg, lora_shrink_tile_kernel, p);
+  }
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace swg

@@ -71,6 +71,19 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
+// The same, acquiring what a thread of the peer CTA released before its arrival.
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // Device status word layout (uint32_t[4]): [0] error code (0 = none),
 // [1] wait site of the first failure, [2] its block index, [3] failures seen.
 enum : uint32_t { kStatusTimeout = 4 };
@@ -83,6 +96,7 @@ enum WaitSite : uint32_t {
   kSiteEpiTmemFull = 4,
   kSiteDrain = 5,
   kSiteScaleCopy = 6,
+  kSiteLora = 7,
 };
 
 struct WaitCtx {
@@ -121,6 +135,12 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, const W
                                           uint32_t site) {
   if (mbar_try_wait(bar, parity)) return true;
   return mbar_wait_slow(bar, parity, w, site, true);
+}
+
+// Bounded wait on a barrier that threads of the peer CTA arrive on too.
+__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, const WaitCtx& w,
+                                                  uint32_t site) {
+  return mbar_wait(bar, parity, w, site) && mbar_try_wait_cluster(bar, parity);
 }
 
 // Same, but keeps waiting (up to the limit) while the CTA aborts: used to let
@@ -416,6 +436,23 @@ __device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16]) {
         "=r"(r[14]), "=r"(r[15])
       : "r"(taddr)
       : "memory");
+}
+
+// 32 lanes x 8 consecutive fp32 columns, to tensor memory.
+__device__ __forceinline__ void tmem_st_x8(uint32_t taddr, const float (&r)[8]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+      "f"(r[0]), "f"(r[1]), "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]), "f"(r[7])
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// Barrier `id` (not 0) over `threads` threads of the CTA.
+__device__ __forceinline__ void named_barrier(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
 // Makes every use of the loaded registers depend on code after tcgen05.wait::ld.

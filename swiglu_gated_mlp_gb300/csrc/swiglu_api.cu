@@ -752,8 +752,17 @@ swiglu_status_t device_view(DeviceView* out) {
   DeviceState* d = nullptr;
   const swiglu_status_t st = ::device_state(&d);
   if (st != SWIGLU_OK) return st;
-  *out = DeviceView{static_cast<int>(d - g_dev), d->sm_count, d->status, g_timeout_ns.load(),
-                    g_inject.load()};
+  *out = DeviceView{static_cast<int>(d - g_dev), d->sm_count,         d->max_pairs, d->status,
+                    g_timeout_ns.load(),         g_inject.load()};
+  return SWIGLU_OK;
+}
+
+swiglu_status_t decode_plan(int64_t M, int64_t blocks, int64_t kslices, int* mt, int* mgroups,
+                            int* stages, int* splits) {
+  DeviceState* d = nullptr;
+  const swiglu_status_t st = ::device_state(&d);
+  if (st != SWIGLU_OK) return st;
+  ::decode_split_plan(M, blocks, kslices, d, mt, mgroups, stages, splits);
   return SWIGLU_OK;
 }
 

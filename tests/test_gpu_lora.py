@@ -1,0 +1,287 @@
+"""Projections with low-rank adapters on the GPU against float64 (needs a GB300).
+
+Every element is held to the worst-case bound of the roundings the kernels make
+(oracle/lora_ref.py); no other tolerance is used.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle.lora_ref import down_forward_lora, forward_lora
+from oracle.swiglu_ref import bf16_bits_to_f64
+from swiglu_gated_mlp_gb300.workloads import bf16_bits, make_inputs
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def native(native_lib):
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    return native_lib
+
+
+def f64(t):
+    if t.dtype == torch.bfloat16:
+        return bf16_bits_to_f64(bf16_bits(t.cpu()))
+    return t.cpu().double().numpy()
+
+
+def table(L, halves, r, K, N, seed):
+    g = torch.Generator().manual_seed(seed)
+    shape = (L, 2) if halves == 2 else (L,)
+    la = (torch.randn(*shape, r, K, generator=g) / K ** 0.5).to(torch.bfloat16)
+    lb = (torch.randn(*shape, N, r, generator=g) / r ** 0.5).to(torch.bfloat16)
+    return la, lb, 0.5 + torch.rand(L, generator=g)
+
+
+def indices(M, L, how, seed):
+    g = torch.Generator().manual_seed(seed + 99)
+    if how == "mixed":    # a request a token, none among them
+        return torch.randint(-1, L, (M,), generator=g, dtype=torch.int32)
+    if how == "one":
+        return torch.full((M,), L - 1, dtype=torch.int32)
+    if how == "none":     # outside the table on both sides
+        return torch.where(torch.arange(M) % 2 == 0, -1, L).to(torch.int32)
+    runs = torch.randint(-1, L, (6,), generator=g, dtype=torch.int32)  # prompts
+    return runs[(torch.arange(M) * 6) // M]
+
+
+def assert_within(out, ref_bound):
+    ref, bound = ref_bound
+    d = np.abs(f64(out) - ref)
+    worst = np.unravel_index(np.argmax(d / bound), d.shape)
+    assert (d <= bound).all(), (worst, d[worst], bound[worst], ref[worst])
+
+
+def run_gate_up(native, M, K, N, L, r, how, seed):
+    a, w1, w2 = make_inputs(M, K, N, seed)
+    la, lb, scale = table(L, 2, r, K, N, seed)
+    index = indices(M, L, how, seed)
+    wp = native.swiglu_pack_weights(w1.cuda(), w2.cuda())
+    y = native.swiglu_forward_lora(a.cuda(), wp, N, la.cuda(), lb.cuda(), index.cuda(), scale.cuda())
+    native.swiglu_check_device_status()
+    assert_within(y, forward_lora(*(f64(t) for t in (a, w1, w2, la, lb)), index.numpy(), f64(scale)))
+
+
+def run_down(native, M, N, H, L, r, how, seed, residual=True):
+    y, w3, _ = make_inputs(M, N, H, seed)
+    res = make_inputs(M, H, 8, seed + 1)[0] if residual else None
+    la, lb, scale = table(L, 1, r, N, H, seed)
+    index = indices(M, L, how, seed)
+    w3p = native.swiglu_pack_down_weights(w3.cuda())
+    out = native.swiglu_down_forward_lora(y.cuda(), w3p, H, la.cuda(), lb.cuda(), index.cuda(),
+                                          scale.cuda(), R=res.cuda() if residual else None)
+    native.swiglu_check_device_status()
+    assert_within(out, down_forward_lora(f64(y), f64(w3), f64(res) if residual else None, f64(la), f64(lb),
+                                         index.numpy(), f64(scale)))
+
+
+# single tokens, K split over clusters and not, several token groups, ragged
+# columns and K; then one and several 256-token tiles, with one adapter, runs of
+# prompts, a different one each token (many passes and slices), and none
+SHAPES = [
+    (1, 8, 8, 1, 8, "one"), (1, 896, 4864, 4, 8, "one"), (1, 200, 264, 3, 64, "none"),
+    (2, 72, 136, 2, 24, "mixed"), (7, 1000, 520, 5, 16, "mixed"), (16, 896, 1000, 8, 16, "mixed"),
+    (17, 264, 20000, 8, 8, "mixed"), (33, 512, 1032, 40, 40, "mixed"), (64, 256, 392, 3, 64, "runs"),
+    (65, 1416, 1000, 20, 24, "mixed"), (100, 200, 264, 1, 56, "one"), (128, 896, 4864, 32, 16, "mixed"),
+    (128, 64, 20000, 4, 64, "runs"),
+    (129, 200, 264, 2, 8, "runs"), (130, 8, 8, 1, 8, "one"), (256, 512, 1000, 5, 16, "runs"),
+    (257, 1000, 520, 3, 24, "mixed"), (300, 264, 392, 300, 8, "mixed"), (513, 1416, 1000, 20, 40, "mixed"),
+    (700, 128, 136, 6, 64, "none"), (1025, 896, 520, 4, 64, "runs"), (2000, 72, 72, 2, 56, "one"),
+]
+
+
+@pytest.mark.parametrize("M,K,N,L,r,how", SHAPES)
+def test_forward_lora_matches_the_formula(native, M, K, N, L, r, how):
+    run_gate_up(native, M, K, N, L, r, how, seed=M + K + N + r)
+
+
+@pytest.mark.parametrize("M,N,H,L,r,how", SHAPES)
+def test_down_forward_lora_matches_the_formula(native, M, N, H, L, r, how):
+    run_down(native, M, N, H, L, r, how, seed=M + N + H + r, residual=M % 2 == 0)
+
+
+def rows_of(M, count, seed):
+    rng = np.random.default_rng(seed)
+    return np.unique(np.concatenate([[0, M - 1], rng.integers(0, M, count)]))
+
+
+@pytest.mark.parametrize("M,L,r,how", [(16, 8, 16, "mixed"), (4096, 8, 64, "runs")])
+def test_forward_lora_at_the_7b_shape(native, M, L, r, how):
+    K, N = 3584, 18944
+    a, w1, w2 = make_inputs(M, K, N, 3)
+    la, lb, scale = table(L, 2, r, K, N, 3)
+    index = indices(M, L, how, 3)
+    wp = native.swiglu_pack_weights(w1.cuda(), w2.cuda())
+    y = native.swiglu_forward_lora(a.cuda(), wp, N, la.cuda(), lb.cuda(), index.cuda(), scale.cuda())
+    native.swiglu_check_device_status()
+    rows = rows_of(M, 24, 0)
+    at = torch.from_numpy(rows)
+    assert_within(y[at.cuda()], forward_lora(f64(a)[rows], f64(w1), f64(w2), f64(la), f64(lb),
+                                             index.numpy()[rows], f64(scale)))
+
+
+@pytest.mark.parametrize("M", [5, 300])
+def test_adapters_of_no_token_and_an_empty_table(native, M):
+    K, N = 264, 392
+    a, w1, w2 = (t.cuda() for t in make_inputs(M, K, N, 1))
+    wp = native.swiglu_pack_weights(w1, w2)
+    la, lb, scale = (t.cuda() for t in table(3, 2, 16, K, N, 1))
+    none = torch.full((M,), -1, dtype=torch.int32, device="cuda")
+    # no token has an adapter: the table's values do not matter
+    y = native.swiglu_forward_lora(a, wp, N, la * float("nan"), lb * float("nan"), none, scale)
+    ref = forward_lora(f64(a), f64(w1), f64(w2), f64(la), f64(lb), none.cpu().numpy(), f64(scale))
+    assert_within(y, ref)
+    empty = native.swiglu_forward_lora(a, wp, N, la[:0], lb[:0], none, scale[:0])
+    assert torch.equal(empty, native.swiglu_forward(a, wp, N))
+    w3p = native.swiglu_pack_down_weights(w1)
+    assert torch.equal(native.swiglu_down_forward_lora(a, w3p, N, la[:0, 0], lb[:0, 0], none, scale[:0]),
+                       native.swiglu_down_forward(a, w3p, N))
+    native.swiglu_check_device_status()
+
+
+@pytest.mark.parametrize("M", [24, 300])
+def test_another_adapters_values_do_not_reach_a_token(native, M):
+    # adapter 1 holds a NaN in La (and, for few tokens, in Lb): only its own tokens see it
+    K, N = 200, 264
+    a, w1, w2 = (t.cuda() for t in make_inputs(M, K, N, 2))
+    wp = native.swiglu_pack_weights(w1, w2)
+    la, lb, scale = (t.cuda() for t in table(3, 2, 16, K, N, 2))
+    index = (torch.arange(M, dtype=torch.int32, device="cuda") * 7) % 4 - 1
+    want = native.swiglu_forward_lora(a, wp, N, la, lb, index, scale)
+    la[1, :, 3, 5] = float("nan")
+    if M <= 128:
+        lb[1, 0] = float("inf")
+    got = native.swiglu_forward_lora(a, wp, N, la, lb, index, scale)
+    native.swiglu_check_device_status()
+    theirs = index != 1
+    assert torch.equal(got[theirs], want[theirs])
+    assert not got[~theirs].isfinite().any()
+
+
+@pytest.mark.parametrize("M", [9, 300])
+def test_down_lora_in_place_residual(native, M):
+    N, H = 264, 520
+    y, w3, _ = (t.cuda() for t in make_inputs(M, N, H, 4))
+    res = make_inputs(M, H, 8, 5)[0].cuda()
+    la, lb, scale = (t.cuda() for t in table(3, 1, 8, N, H, 4))
+    index = indices(M, 3, "mixed", 4).cuda()
+    w3p = native.swiglu_pack_down_weights(w3)
+    want = native.swiglu_down_forward_lora(y, w3p, H, la, lb, index, scale, R=res)
+    got = native.swiglu_down_forward_lora(y, w3p, H, la, lb, index, scale, R=res, Out=res)
+    assert got is res and torch.equal(got, want)
+
+
+@pytest.mark.parametrize("M,K,N,L,r", [(3, 136, 200, 2, 8), (128, 896, 1000, 9, 24), (300, 264, 392, 5, 40)])
+def test_lora_writes_its_output_and_nothing_else(native, M, K, N, L, r):
+    a, w1, w2 = (t.cuda() for t in make_inputs(M, K, N, 6))
+    wp = native.swiglu_pack_weights(w1, w2)
+    la, lb, scale = (t.cuda() for t in table(L, 2, r, K, N, 6))
+    index = indices(M, L, "mixed", 6).cuda()
+    pad = 4096
+    buf = torch.empty(M * N + 2 * pad, dtype=torch.bfloat16, device="cuda")
+    buf.view(torch.int16).fill_(0x7FBF)
+    n = native.swiglu_lora_workspace_bytes(M, K, N, r)
+    ws = torch.full((n + 2048,), 0xA5, dtype=torch.uint8, device="cuda")
+    y = native.swiglu_forward_lora(a, wp, N, la, lb, index, scale, Y=buf[pad:-pad].view(M, N),
+                                   workspace=ws[1024:1024 + n])
+    native.swiglu_check_device_status()
+    assert torch.equal(y, native.swiglu_forward_lora(a, wp, N, la, lb, index, scale))
+    for edge in (buf[:pad], buf[-pad:]):
+        assert (edge.view(torch.int16) == 0x7FBF).all()
+    assert (ws[:1024] == 0xA5).all() and (ws[-1024:] == 0xA5).all()
+
+
+@pytest.mark.parametrize("M", [1, 16, 100, 300])
+def test_back_to_back_calls_see_what_was_written_before_them(native, M):
+    # the projection starts while V is made: tokens, weights, index and table that the
+    # kernel just before the call wrote, with no synchronisation, on two streams
+    K, N, L, r = 896, 4864, 4, 16
+    base = [t.cuda() for t in make_inputs(M, K, N, 7)]
+    la, lb, scale = (t.cuda() for t in table(L, 2, r, K, N, 7))
+    index = indices(M, L, "mixed", 7).cuda()
+    wp = native.swiglu_pack_weights(base[1], base[2])
+    want = [native.swiglu_forward_lora(base[0] * f, wp, N, la * f, lb, index, scale) for f in (1.0, -2.0)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for s, stream in enumerate(streams):
+        with torch.cuda.stream(stream):
+            a, ta = torch.zeros_like(base[0]), torch.zeros_like(la)
+            ws = native.swiglu_lora_workspace(M, K, N, r)
+            wq = torch.zeros_like(wp)
+            for i in range(10):
+                f = (1.0, -2.0)[i % 2]
+                torch.mul(base[0], f, out=a)
+                torch.mul(la, f, out=ta)
+                wq.copy_(wp)
+                got.append((i % 2, native.swiglu_forward_lora(a, wq, N, ta, lb, index, scale, workspace=ws)))
+                a.fill_(float("nan"))   # the next write may not pass the call either
+                wq.fill_(float("nan"))
+    torch.cuda.synchronize()
+    native.swiglu_check_device_status()
+    for which, y in got:
+        assert torch.equal(y, want[which])
+
+
+@pytest.mark.parametrize("M", [16, 300])
+def test_lora_in_a_captured_graph_with_new_requests(native, M):
+    K, N, L, r = 264, 520, 5, 16
+    a, w1, w2 = (t.cuda() for t in make_inputs(M, K, N, 8))
+    wp = native.swiglu_pack_weights(w1, w2)
+    la, lb, scale = (t.cuda() for t in table(L, 2, r, K, N, 8))
+    index = indices(M, L, "one", 8).cuda()
+    ws, y = native.swiglu_lora_workspace(M, K, N, r), torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
+    native.swiglu_forward_lora(a, wp, N, la, lb, index, scale, Y=y, workspace=ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        native.swiglu_forward_lora(a, wp, N, la, lb, index, scale, Y=y, workspace=ws)
+    for how in ("mixed", "runs", "none", "one"):
+        index.copy_(indices(M, L, how, 8))
+        want = native.swiglu_forward_lora(a, wp, N, la, lb, index, scale)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want), how
+
+
+@pytest.mark.parametrize("M", [16, 300])
+def test_lora_stalled_wait_is_reported(native, M):
+    K, N, L, r = 512, 520, 3, 16
+    a, w1, w2 = (t.cuda() for t in make_inputs(M, K, N, 9))
+    wp = native.swiglu_pack_weights(w1, w2)
+    la, lb, scale = (t.cuda() for t in table(L, 2, r, K, N, 9))
+    index = indices(M, L, "mixed", 9).cuda()
+    want = native.swiglu_forward_lora(a, wp, N, la, lb, index, scale)
+    native.swiglu_check_device_status()
+    native.swiglu_testing_inject_stall(True, timeout_ms=200)
+    try:
+        native.swiglu_forward_lora(a, wp, N, la, lb, index, scale)
+        with pytest.raises(native.SwigluError) as err:
+            native.swiglu_check_device_status()
+        assert err.value.code == native.SWIGLU_ERR_TIMEOUT
+    finally:
+        native.swiglu_testing_inject_stall(False, timeout_ms=1000)
+    assert torch.equal(native.swiglu_forward_lora(a, wp, N, la, lb, index, scale), want)
+
+
+def test_large_table_offsets(native):
+    # an adapter whose La and Lb lie past 2^31 values of the table
+    M, K, N, L, r = 3, 8192, 8192, 2100, 64
+    a, w1, w2 = make_inputs(M, K, N, 10)
+    la = torch.zeros(L, 2, r, K, dtype=torch.bfloat16, device="cuda")
+    lb = torch.zeros(L, 2, N, r, dtype=torch.bfloat16, device="cuda")
+    assert la[:-1].numel() > 1 << 31 and lb[:-1].numel() > 1 << 31
+    last = table(1, 2, r, K, N, 10)
+    la[-1], lb[-1] = last[0][0].cuda(), last[1][0].cuda()
+    wp = native.swiglu_pack_weights(w1.cuda(), w2.cuda())
+    for m in (M, 130):
+        am = a.repeat(-(-m // M), 1)[:m]
+        index = torch.full((m,), L - 1, dtype=torch.int32)
+        y = native.swiglu_forward_lora(am.cuda(), wp, N, la, lb, index.cuda(),
+                                       last[2].repeat(L).cuda())
+        native.swiglu_check_device_status()
+        ref = forward_lora(f64(a), f64(w1), f64(w2), f64(last[0]), f64(last[1]), np.zeros(M, int), f64(last[2]))
+        assert_within(y[:M], ref)
+        if m > M:
+            assert torch.equal(y[m - 1], y[(m - 1) % M])
