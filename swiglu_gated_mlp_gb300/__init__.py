@@ -36,5 +36,6 @@ _EXPORTS = {
 def __getattr__(name):
     if name in _EXPORTS:
         from . import _native
-        return getattr(_native, name)
+        value = globals()[name] = getattr(_native, name)  # the next access finds it directly
+        return value
     raise AttributeError(name)

@@ -488,6 +488,53 @@ def swiglu_down_forward(Y: torch.Tensor, W3packed: torch.Tensor, H: int,
     return Out
 
 
+# The gradient and adapter calls take up to ten tensors, and a small one runs for
+# less time on the GPU than checking them one property at a time takes here
+# (Python on the Grace host: 0.1 us a property). So the checks below read each
+# property once and look for the reason only when something is wrong.
+_BF16 = torch.bfloat16
+
+
+def _refuse(dev: int, tensors, names) -> None:
+    for t, name in zip(tensors, names):
+        _dev_bf16(t, name)
+        if t.get_device() != dev:
+            raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
+
+
+def _all_bf16(tensors, names: tuple) -> int:
+    """The CUDA device that all the contiguous bf16 `tensors` are on."""
+    try:
+        dev = tensors[0].get_device()
+        for t in tensors:
+            if t.dtype is not _BF16 or t.get_device() != dev or dev < 0 or not t.is_contiguous():
+                break
+        else:
+            return dev
+    except AttributeError:
+        dev = -1
+    _refuse(dev, tensors, names)
+    raise ValueError(f"{', '.join(names)} must be contiguous CUDA bfloat16 tensors on one device")
+
+
+class _call_on:
+    """Makes device `dev` current where another one is."""
+    __slots__ = ("dev", "prev")
+
+    def __init__(self, dev: int):
+        self.dev = dev
+
+    def __enter__(self):
+        self.prev = torch.cuda.current_device()
+        if self.prev != self.dev:
+            torch.cuda.set_device(self.dev)
+
+    def __exit__(self, *exc):
+        if self.prev != self.dev:
+            torch.cuda.set_device(self.prev)
+        return False
+
+
 def _on_stream(t: torch.Tensor, stream) -> torch.Tensor:
     """`t`, which this binding allocated on the current stream, kept until `stream` is done with it."""
     if stream is not None:
@@ -497,33 +544,41 @@ def _on_stream(t: torch.Tensor, stream) -> torch.Tensor:
     return t
 
 
-def _output(t, name: str, shape, like: torch.Tensor, stream) -> torch.Tensor:
+def _output(t, name: str, rows: int, cols: int, dev: int, stream) -> torch.Tensor:
     """A caller's output tensor, checked, or a new one."""
     if t is None:
-        return _on_stream(torch.empty(shape, dtype=torch.bfloat16, device=like.device), stream)
-    _dev_bf16(t, name)
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must be {list(shape)}")
+        t = torch.empty((rows, cols), dtype=_BF16, device=dev)
+        return t if stream is None else _on_stream(t, stream)
+    if t.dtype is not _BF16 or t.get_device() != dev or not t.is_contiguous():
+        _refuse(dev, (t,), (name,))
+    if t.shape != (rows, cols):
+        raise ValueError(f"{name} must be [{rows}, {cols}], got {list(t.shape)}")
     return t
 
 
-def _same_device(like: torch.Tensor, **others) -> None:
-    for name, t in others.items():
-        if t is not None and t.device != like.device:
-            raise ValueError(f"{name} must be on {like.device}, got {t.device}")
-
-
-def _workspace(ws, nbytes: int, like: torch.Tensor, stream) -> torch.Tensor:
-    """A caller's workspace, checked, or a new one of `nbytes`."""
+def _scratch(ws, dev: int, stream, bytes_fn, *shape) -> torch.Tensor:
+    """A caller's workspace, checked, or a new one of bytes_fn(*shape)."""
     if ws is None:
-        return _on_stream(torch.empty(nbytes, dtype=torch.uint8, device=like.device), stream)
-    if not ws.is_cuda or ws.device != like.device or not ws.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous CUDA tensor on {like.device}")
+        return _on_stream(torch.empty(bytes_fn(*shape), dtype=torch.uint8, device=dev), stream)
+    if ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous CUDA tensor on cuda:{dev}")
     return ws
+
+
+def _handle(stream, dev: int) -> int:
+    if stream is None:
+        return _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream(dev).cuda_stream
+    return int(stream.cuda_stream) if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
 def _ptr(t):
     return t.data_ptr() if t is not None else None
+
+
+def _holds(packed: torch.Tensor, blocks: int, K: int, what: str) -> None:
+    """Whether a packed weight has room for `blocks` tiles of 32 KB for every 64 of K."""
+    if packed.numel() < blocks * -(-K // 64) * 16384:
+        raise ValueError(f"{what} does not hold a packed weight of this shape")
 
 
 def _new_workspace(bytes_fn, device, *shape) -> torch.Tensor:
@@ -551,27 +606,21 @@ def swiglu_backward(A: torch.Tensor, Wpacked: torch.Tensor, dY: torch.Tensor,
     or need_weight turns off is None. Without `workspace` (from
     swiglu_backward_workspace) one is allocated for the call.
     """
-    _dev_bf16(A, "A")
-    _dev_bf16(Wpacked, "Wpacked")
-    _dev_bf16(dY, "dY")
+    dev = _all_bf16((A, Wpacked, dY), ("A", "Wpacked", "dY"))
     if A.dim() != 2 or dY.dim() != 2 or A.shape[0] != dY.shape[0]:
         raise ValueError("A must be [M, K] and dY [M, N]")
-    (M, K), N = A.shape, dY.shape[1]
-    if Wpacked.numel() * 2 < swiglu_packed_weight_bytes(K, N):
-        raise ValueError("Wpacked does not hold a packed weight for this K and N")
-    _same_device(A, Wpacked=Wpacked, dY=dY, dA=dA, dW1=dW1, dW2=dW2)
-    with _on_device(A.device):
-        dA = _output(dA, "dA", (M, K), A, stream) if need_input else None
-        dW1 = _output(dW1, "dW1", (K, N), A, stream) if need_weight else None
-        dW2 = _output(dW2, "dW2", (K, N), A, stream) if need_weight else None
-        if workspace is None and M:
-            workspace = _workspace(None, swiglu_backward_workspace_bytes(M, K, N), A, stream)
-        elif workspace is not None:
-            _workspace(workspace, 0, A, stream)
-        _check(lib.swiglu_backward(
-            A.data_ptr(), Wpacked.data_ptr(), dY.data_ptr(), _ptr(dA), _ptr(dW1), _ptr(dW2), M, K, N,
-            _ptr(workspace), workspace.numel() * workspace.element_size() if workspace is not None else 0,
-            _stream_handle(stream, A.device)), "swiglu_backward")
+    M, K = A.shape
+    N = dY.shape[1]
+    _holds(Wpacked, -(-N // 128), K, "Wpacked")
+    with _call_on(dev):
+        dA = _output(dA, "dA", M, K, dev, stream) if need_input else None
+        dW1 = _output(dW1, "dW1", K, N, dev, stream) if need_weight else None
+        dW2 = _output(dW2, "dW2", K, N, dev, stream) if need_weight else None
+        ws = _scratch(workspace, dev, stream, swiglu_backward_workspace_bytes, M, K, N)
+        rc = lib.swiglu_backward(A.data_ptr(), Wpacked.data_ptr(), dY.data_ptr(), _ptr(dA), _ptr(dW1),
+                                 _ptr(dW2), M, K, N, ws.data_ptr(), ws.nbytes, _handle(stream, dev))
+    if rc:
+        _check(rc, "swiglu_backward")
     return dA, dW1, dW2
 
 
@@ -592,53 +641,45 @@ def swiglu_down_backward(dOut: torch.Tensor, W3packed: torch.Tensor | None, Y: t
 
     W3packed is needed for dY only, Y for dW3 only; without Y, N says its width.
     """
-    _dev_bf16(dOut, "dOut")
-    if dOut.dim() != 2:
-        raise ValueError("dOut must be [M, H]")
-    M, H = dOut.shape
     if need_weight and Y is None:
         raise ValueError("dW3 needs Y")
     if need_input and W3packed is None:
         raise ValueError("dY needs W3packed")
+    given = [(t, n) for t, n in ((dOut, "dOut"), (W3packed, "W3packed"), (Y, "Y")) if t is not None]
+    dev = _all_bf16([t for t, _ in given], tuple(n for _, n in given))
+    if dOut.dim() != 2:
+        raise ValueError("dOut must be [M, H]")
+    M, H = dOut.shape
     if Y is not None:
-        _dev_bf16(Y, "Y")
         if Y.dim() != 2 or Y.shape[0] != M or (N is not None and Y.shape[1] != N):
             raise ValueError("Y must be [M, N]")
         N = Y.shape[1]
     if N is None:
         raise ValueError("N is needed without Y")
     if W3packed is not None:
-        _dev_bf16(W3packed, "W3packed")
-        if W3packed.numel() * 2 < swiglu_down_packed_bytes(N, H):
-            raise ValueError("W3packed does not hold a packed W3 for this N and H")
-    _same_device(dOut, W3packed=W3packed, Y=Y, dY=dY, dW3=dW3)
-    with _on_device(dOut.device):
-        dY = _output(dY, "dY", (M, N), dOut, stream) if need_input else None
-        dW3 = _output(dW3, "dW3", (N, H), dOut, stream) if need_weight else None
-        if workspace is None and M:
-            workspace = _workspace(None, swiglu_down_backward_workspace_bytes(M, N, H), dOut, stream)
-        elif workspace is not None:
-            _workspace(workspace, 0, dOut, stream)
-        _check(lib.swiglu_down_backward(
-            dOut.data_ptr(), _ptr(W3packed), _ptr(Y), _ptr(dY), _ptr(dW3), M, N, H,
-            (_ptr(workspace) or None) if workspace is not None else None,
-            workspace.numel() * workspace.element_size() if workspace is not None else 0,
-            _stream_handle(stream, dOut.device)), "swiglu_down_backward")
+        _holds(W3packed, -(-H // 256), N, "W3packed")
+    with _call_on(dev):
+        dY = _output(dY, "dY", M, N, dev, stream) if need_input else None
+        dW3 = _output(dW3, "dW3", N, H, dev, stream) if need_weight else None
+        ws = _scratch(workspace, dev, stream, swiglu_down_backward_workspace_bytes, M, N, H)
+        rc = lib.swiglu_down_backward(dOut.data_ptr(), _ptr(W3packed), _ptr(Y), _ptr(dY), _ptr(dW3), M, N,
+                                      H, ws.data_ptr() or None, ws.nbytes, _handle(stream, dev))
+    if rc:
+        _check(rc, "swiglu_down_backward")
     return dY, dW3
 
 
-def _adapters(La, Lb, index, scale, la_shape, lb_shape, M: int, like: torch.Tensor) -> None:
+def _adapters(La, Lb, index, scale, la_shape, lb_shape, M: int, dev: int) -> None:
     """Checks an adapter table against the shapes its projection asks for."""
-    _dev_bf16(La, "La")
-    _dev_bf16(Lb, "Lb")
-    if tuple(La.shape) != la_shape or tuple(Lb.shape) != lb_shape:
+    if La.shape != la_shape or Lb.shape != lb_shape:
         raise ValueError(f"La and Lb must be {list(la_shape)} and {list(lb_shape)}, "
                          f"got {list(La.shape)} and {list(Lb.shape)}")
-    if index.dtype != torch.int32 or tuple(index.shape) != (M,) or not index.is_contiguous():
-        raise ValueError("index must be a contiguous int32 tensor of one adapter per token")
-    if scale.dtype != torch.float32 or tuple(scale.shape) != la_shape[:1] or not scale.is_contiguous():
-        raise ValueError("scale must be a contiguous float32 tensor of one value per adapter")
-    _same_device(like, La=La, Lb=Lb, index=index, scale=scale)
+    if (index.dtype is not torch.int32 or index.shape != (M,) or index.get_device() != dev
+            or not index.is_contiguous()):
+        raise ValueError(f"index must be a contiguous int32 tensor of one adapter per token on cuda:{dev}")
+    if (scale.dtype is not torch.float32 or scale.shape != la_shape[:1] or scale.get_device() != dev
+            or not scale.is_contiguous()):
+        raise ValueError(f"scale must be a contiguous float32 tensor of one value per adapter on cuda:{dev}")
 
 
 def swiglu_lora_workspace_bytes(M: int, K: int, N: int, rank: int) -> int:
@@ -661,25 +702,21 @@ def swiglu_forward_lora(A: torch.Tensor, Wpacked: torch.Tensor, N: int, La: torc
     none); scale [adapters] float32. Without `workspace` (from
     swiglu_lora_workspace) one is allocated for the call.
     """
-    _dev_bf16(A, "A")
-    _dev_bf16(Wpacked, "Wpacked")
+    dev = _all_bf16((A, Wpacked, La, Lb), ("A", "Wpacked", "La", "Lb"))
     if A.dim() != 2 or La.dim() != 4:
         raise ValueError("A must be [M, K] and La [adapters, 2, rank, K]")
     M, K = A.shape
-    count, rank = La.shape[0], La.shape[2]
-    if Wpacked.numel() * 2 < swiglu_packed_weight_bytes(K, N):
-        raise ValueError("Wpacked does not hold a packed weight for this K and N")
-    _adapters(La, Lb, index, scale, (count, 2, rank, K), (count, 2, N, rank), M, A)
-    _same_device(A, Wpacked=Wpacked, Y=Y)
-    with _on_device(A.device):
-        Y = _output(Y, "Y", (M, N), A, stream)
-        workspace = _workspace(workspace, 0 if workspace is not None
-                               else swiglu_lora_workspace_bytes(M, K, N, rank), A, stream)
-        _check(lib.swiglu_forward_lora(
-            A.data_ptr(), Wpacked.data_ptr(), Y.data_ptr(), M, K, N, La.data_ptr(), Lb.data_ptr(),
-            index.data_ptr(), scale.data_ptr(), count, rank, workspace.data_ptr(),
-            workspace.numel() * workspace.element_size(), _stream_handle(stream, A.device)),
-            "swiglu_forward_lora")
+    count, _, rank, _ = La.shape
+    _holds(Wpacked, -(-N // 128), K, "Wpacked")
+    _adapters(La, Lb, index, scale, (count, 2, rank, K), (count, 2, N, rank), M, dev)
+    with _call_on(dev):
+        Y = _output(Y, "Y", M, N, dev, stream)
+        ws = _scratch(workspace, dev, stream, swiglu_lora_workspace_bytes, M, K, N, rank)
+        rc = lib.swiglu_forward_lora(A.data_ptr(), Wpacked.data_ptr(), Y.data_ptr(), M, K, N,
+                                     La.data_ptr(), Lb.data_ptr(), index.data_ptr(), scale.data_ptr(),
+                                     count, rank, ws.data_ptr(), ws.nbytes, _handle(stream, dev))
+    if rc:
+        _check(rc, "swiglu_forward_lora")
     return Y
 
 
@@ -701,29 +738,24 @@ def swiglu_down_forward_lora(Y: torch.Tensor, W3packed: torch.Tensor, H: int, La
     La [adapters, rank, N], Lb [adapters, H, rank]; index and scale as in
     swiglu_forward_lora; Out may be R (in-place add).
     """
-    _dev_bf16(Y, "Y")
-    _dev_bf16(W3packed, "W3packed")
+    dev = _all_bf16((Y, W3packed, La, Lb), ("Y", "W3packed", "La", "Lb"))
     if Y.dim() != 2 or La.dim() != 3:
         raise ValueError("Y must be [M, N] and La [adapters, rank, N]")
     M, N = Y.shape
-    count, rank = La.shape[:2]
-    if W3packed.numel() * 2 < swiglu_down_packed_bytes(N, H):
-        raise ValueError("W3packed does not hold a packed W3 for this N and H")
-    _adapters(La, Lb, index, scale, (count, rank, N), (count, H, rank), M, Y)
-    if R is not None:
-        _dev_bf16(R, "R")
-        if tuple(R.shape) != (M, H):
-            raise ValueError("R must be [M, H]")
-    _same_device(Y, W3packed=W3packed, R=R, Out=Out)
-    with _on_device(Y.device):
-        Out = _output(Out, "Out", (M, H), Y, stream)
-        workspace = _workspace(workspace, 0 if workspace is not None
-                               else swiglu_down_lora_workspace_bytes(M, N, H, rank), Y, stream)
-        _check(lib.swiglu_down_forward_lora(
-            Y.data_ptr(), W3packed.data_ptr(), _ptr(R), Out.data_ptr(), M, N, H, La.data_ptr(),
-            Lb.data_ptr(), index.data_ptr(), scale.data_ptr(), count, rank, workspace.data_ptr(),
-            workspace.numel() * workspace.element_size(), _stream_handle(stream, Y.device)),
-            "swiglu_down_forward_lora")
+    count, rank, _ = La.shape
+    _holds(W3packed, -(-H // 256), N, "W3packed")
+    _adapters(La, Lb, index, scale, (count, rank, N), (count, H, rank), M, dev)
+    with _call_on(dev):
+        if R is not None:
+            _output(R, "R", M, H, dev, stream)
+        Out = _output(Out, "Out", M, H, dev, stream)
+        ws = _scratch(workspace, dev, stream, swiglu_down_lora_workspace_bytes, M, N, H, rank)
+        rc = lib.swiglu_down_forward_lora(Y.data_ptr(), W3packed.data_ptr(), _ptr(R), Out.data_ptr(), M,
+                                          N, H, La.data_ptr(), Lb.data_ptr(), index.data_ptr(),
+                                          scale.data_ptr(), count, rank, ws.data_ptr(), ws.nbytes,
+                                          _handle(stream, dev))
+    if rc:
+        _check(rc, "swiglu_down_forward_lora")
     return Out
 
 

@@ -48,10 +48,8 @@
 // token's adapter row at a time, so tokens never meet another's adapter and
 // nothing is padded or masked. Four more warps join them; the deltas wait in
 // tensor memory beside the accumulators (columns 2 mt to 4 mt) and the epilogue
-// adds the two. The producer does not wait for the grid before this one, which
-// is always the kernel that makes V: that grid lets this one start only after
-// everything before it has completed. With K split, part k computes the deltas
-// of every kparts-th chunk of 8 tokens, once in all.
+// adds the two. With K split, part k computes the deltas of every kparts-th
+// chunk of 8 tokens, once in all.
 #include "kernels.h"
 #include "ptx.cuh"
 
@@ -337,9 +335,7 @@ __global__ void __launch_bounds__(kLora ? kLoraThreads : kThreads, kLora ? 2 : 1
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
-  // the set-up and L2 staging above overlap the previous grid; loads start here
-  // (with adapters the previous grid makes V, which only warps 2 and up read)
-  if (!kLora || warp >= 2) pdl_wait();
+  pdl_wait();  // the set-up and L2 staging above overlap the previous grid; loads start here
 
   if (warp == 0) {
     // ------------------------------------------------ TMA producer -----

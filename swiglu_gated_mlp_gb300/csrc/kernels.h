@@ -51,7 +51,7 @@ struct LargeMParams {
   // adapters present per 256 tokens, and Lb {rank, N, adapters x (1 or 2)} box {64, 64 or 128, 1}
   CUtensorMap tmap_lb;
   int lora;
-  int lora_rank;
+  int lora_rank, lora_count;
   const void* lora_v;
   const int* lora_index;
   const int* lora_lists;

@@ -208,6 +208,7 @@ swiglu_status_t run_call(const Call& c, cudaStream_t stream) {
     p.residual = c.residual;
     p.lora = 1;
     p.lora_rank = static_cast<int>(c.rank);
+    p.lora_count = static_cast<int>(c.count);
     p.lora_v = c.ws;
     p.lora_index = c.index;
     p.lora_lists = lists;

@@ -10,8 +10,7 @@
 // Few tokens (the decode kernel's range): lora_shrink_dot_kernel, plain dot
 // products in fp32. One CTA takes a token and 4 rows; its 8 warps split K, so
 // every load of a CTA is in flight at once. V stays in fp32. The decode kernel
-// starts streaming the shared weight while this kernel runs (it waits for V
-// only before it needs it), so the time that matters is that of the launch.
+// does its set-up and stages its first weight tiles in L2 while this one runs.
 //
 // Many tokens: lora_shrink_tile_kernel, tcgen05 with 128 tokens as the MMA's
 // M side and the rows of the adapters present in the tile as its N side. The
@@ -46,10 +45,10 @@ __device__ __forceinline__ float dot8(const uint4& a, const uint4& b, float acc)
 __global__ void __launch_bounds__(kDotThreads)
     lora_shrink_dot_kernel(const __grid_constant__ LoraShrinkParams p) {
   __shared__ float sums[kDotThreads / 32][kDotRows];
-  pdl_wait();
-  // The projection's kernel may start now: everything before this grid has
-  // completed, so it may read the tokens and weights without waiting for it.
+  // The projection's kernel may start at once: it waits for this grid before it
+  // reads anything but weight tiles into L2, and this grid takes little room.
   pdl_launch_dependents();
+  pdl_wait();
   const int row_blocks = (p.hr + kDotRows - 1) / kDotRows;
   const int m = blockIdx.x / row_blocks;
   const int r0 = (blockIdx.x % row_blocks) * kDotRows;

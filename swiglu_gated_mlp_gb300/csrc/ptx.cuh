@@ -71,19 +71,6 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
-// The same, acquiring what a thread of the peer CTA released before its arrival.
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
 // Device status word layout (uint32_t[4]): [0] error code (0 = none),
 // [1] wait site of the first failure, [2] its block index, [3] failures seen.
 enum : uint32_t { kStatusTimeout = 4 };
@@ -135,12 +122,6 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, const W
                                           uint32_t site) {
   if (mbar_try_wait(bar, parity)) return true;
   return mbar_wait_slow(bar, parity, w, site, true);
-}
-
-// Bounded wait on a barrier that threads of the peer CTA arrive on too.
-__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, const WaitCtx& w,
-                                                  uint32_t site) {
-  return mbar_wait(bar, parity, w, site) && mbar_try_wait_cluster(bar, parity);
 }
 
 // Same, but keeps waiting (up to the limit) while the CTA aborts: used to let
@@ -512,6 +493,12 @@ __device__ __forceinline__ float4 ld_shared_cluster_v4(uint32_t cluster_addr) {
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
                : "memory");
+}
+
+// The same without cluster-scope release: what the arrival announces is not
+// read by the waiting CTA's threads.
+__device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
 // Tiled loads into this CTA's shared memory whose completion is counted on an
