@@ -45,7 +45,7 @@ swiglu_status_t backward_device(DeviceView* d, int* pairs) {
 }
 
 constexpr int64_t kTile = 2 * kTileM;       // rows and columns of an output tile
-constexpr int64_t kMaxUnits = 1 << 30;      // tiles x parts of one launch
+constexpr int64_t kMaxUnits = 1 << 30;      // tiles x parts of one product
 
 int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
@@ -54,37 +54,69 @@ size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 struct ProductPlan {
   int64_t tiles_m = 0, tiles_n = 0, slices = 0, splits = 1, part_rows = 0;
   size_t part_bytes = 0;  // fp32 parts of one output
+  int64_t tiles() const { return tiles_m * tiles_n; }
+  int64_t units() const { return tiles() * splits; }
+  // time of an unsplit tile in slices: a tile's epilogue takes about as long as
+  // the MMAs of 5 slices
+  int64_t cost() const { return std::max<int64_t>(slices / splits, 5); }
 };
 
 // `cols`: columns of one output; `outputs` of them side by side in the tiles.
-ProductPlan plan_product(int64_t rows, int64_t cols, int outputs, int64_t slices, int pairs) {
+ProductPlan plan_product(int64_t rows, int64_t cols, int outputs, int64_t slices) {
   ProductPlan pl;
   pl.tiles_m = div_up(rows, kTile);
   pl.tiles_n = outputs == 2 ? div_up(cols, kTileM) : div_up(cols, kTile);
   pl.slices = slices;
-  const int64_t tiles = pl.tiles_m * pl.tiles_n;
-  // at least 4 slices a part: fewer do not pay for writing and adding the part
-  pl.splits = std::max<int64_t>(1, std::min<int64_t>(pairs / std::max<int64_t>(tiles, 1), slices / 4));
   pl.part_rows = div_up(rows, 32) * 32;
-  if (pl.splits > 1) pl.part_bytes = size_t(pl.splits) * size_t(pl.part_rows) * size_t(cols) * 4;
   return pl;
 }
 
-ProductPlan plan_input(int64_t M, int64_t K, int64_t sum, int pairs) {  // sum: padded, in 64s
-  return plan_product(M, K, 1, sum, pairs);
+// Cuts a product's sum so that no unit is longer than all units spread evenly
+// over the pairs, in parts of at least 8 slices: shorter ones do not pay for
+// writing and adding them.
+void split(ProductPlan* pl, int64_t cols, int64_t even) {
+  if (pl->slices > even)
+    pl->splits = std::max<int64_t>(
+        1, std::min<int64_t>(div_up(pl->slices, std::max<int64_t>(even, 1)), pl->slices / 8));
+  if (pl->splits > 1) pl->part_bytes = align256(size_t(pl->splits) * size_t(pl->part_rows) * size_t(cols) * 4);
 }
 
-ProductPlan plan_weight(int64_t rows, int64_t cols, int outputs, int64_t M, int pairs) {
-  return plan_product(rows, cols, outputs, std::max<int64_t>(k_slices(M), 1), pairs);
+// The input gradient [M, in_cols] and the weight gradient(s) [w_rows, w_cols]
+// of one launch.
+struct GradientPlan {
+  ProductPlan in, w;
+  int pairs = 0, early_rounds = 0;
+  int w_outputs = 1;
+  size_t parts_bytes() const { return in.part_bytes + w_outputs * w.part_bytes; }
+  bool too_many() const { return in.units() > kMaxUnits || w.units() > kMaxUnits; }
+};
+
+GradientPlan plan_gradients(int64_t M, int64_t in_cols, int64_t in_slices, int64_t w_rows,
+                            int64_t w_cols, int w_outputs, int max_pairs) {
+  GradientPlan pl;
+  pl.in = plan_product(M, in_cols, 1, in_slices);
+  pl.w = plan_product(w_rows, w_cols, w_outputs, 2 * div_up(M, 2 * kBlockK));
+  pl.w_outputs = w_outputs;
+  const int64_t work = pl.in.tiles() * pl.in.cost() + pl.w.tiles() * pl.w.cost();
+  const int64_t even = div_up(work, max_pairs);
+  split(&pl.in, in_cols, even);
+  split(&pl.w, w_cols, even);
+  return pl;
 }
 
-bool too_many(const ProductPlan& pl) { return pl.tiles_m * pl.tiles_n * pl.splits > kMaxUnits; }
-
-int grid_of(const ProductPlan& pl, int pairs) {
-  return 2 * static_cast<int>(std::min<int64_t>(pl.tiles_m * pl.tiles_n * pl.splits, pairs));
+// The pairs of a launch of the products asked for, and how many rounds of
+// weight units the pairs with one input unit fewer take first.
+void deal_units(GradientPlan* pl, bool in, bool w, int max_pairs, BackwardParams* p) {
+  p->in_units = in ? static_cast<int>(pl->in.units()) : 0;
+  p->w_units = w ? static_cast<int>(pl->w.units()) : 0;
+  pl->pairs = static_cast<int>(std::min<int64_t>(int64_t(p->in_units) + p->w_units, max_pairs));
+  const int early = pl->pairs - p->in_units % pl->pairs;  // pairs with one input unit fewer
+  if (early == pl->pairs) return;
+  const int64_t rounds = p->w_units <= early ? 1 : pl->in.cost() / pl->w.cost();
+  p->early_rounds = static_cast<int>(std::min<int64_t>(rounds, p->w_units / early));
 }
 
-void fill(BackwardParams* p, const ProductPlan& pl, const DeviceView& d, int64_t rows, int64_t cols) {
+void fill(BackwardProduct* p, const ProductPlan& pl, int64_t rows, int64_t cols) {
   p->rows = static_cast<int>(rows);
   p->cols = static_cast<int>(cols);
   p->slices = static_cast<int>(pl.slices);
@@ -93,38 +125,48 @@ void fill(BackwardParams* p, const ProductPlan& pl, const DeviceView& d, int64_t
   p->group_m = static_cast<int>(pair_group_rows(pl.tiles_m));
   p->splits = static_cast<int>(pl.splits);
   p->part_rows = static_cast<int>(pl.part_rows);
+}
+
+void fill_status(BackwardParams* p, const DeviceView& d) {
   p->status = d.status;
   p->timeout_ns = d.timeout_ns;
   p->inject_stall = d.inject_stall;
 }
 
-// The store map of one output (64 bf16 columns), or of its fp32 parts (32 columns).
-bool encode_output(CUtensorMap* map, void* out, float* parts, const ProductPlan& pl, int64_t rows,
-                   int64_t cols) {
-  if (pl.splits > 1)
-    return encode_2d(map, parts, cols, pl.splits * pl.part_rows, cols * 4, 32, 32,
-                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_DATA_TYPE_FLOAT32);
-  return encode_2d(map, out, cols, rows, cols * 2, 64, 32, CU_TENSOR_MAP_SWIZZLE_128B);
+// The store map of one output (64 bf16 columns), or of its fp32 parts (32
+// columns), which are then added up after the launch.
+bool encode_output(CUtensorMap* map, void* out, uint8_t* parts, const ProductPlan& pl, int64_t rows,
+                   int64_t cols, ReduceParams* sums) {
+  if (pl.splits == 1)
+    return encode_2d(map, out, cols, rows, cols * 2, 64, 32, CU_TENSOR_MAP_SWIZZLE_128B);
+  sums->out[sums->count++] =
+      ReduceOutput{reinterpret_cast<const float*>(parts), out, static_cast<int>(rows),
+                   static_cast<int>(cols), static_cast<int>(pl.part_rows), static_cast<int>(pl.splits)};
+  return encode_2d(map, parts, cols, pl.splits * pl.part_rows, cols * 4, 32, 32,
+                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_DATA_TYPE_FLOAT32);
 }
 
-// Launches one product and, if its sum is in parts, adds them.
-swiglu_status_t run_product(const BackwardParams& p, int mode, const ProductPlan& pl, int pairs,
-                            void* out0, void* out1, float* parts, cudaStream_t stream) {
-  cudaError_t e = launch_backward_pair(p, mode, grid_of(pl, pairs), stream);
-  for (int i = 0; e == cudaSuccess && pl.splits > 1 && i < (out1 ? 2 : 1); ++i)
-    e = launch_reduce_parts(parts + i * (pl.part_bytes / 4), i ? out1 : out0, p.rows, p.cols,
-                            p.part_rows, p.splits, stream);
-  if (e != cudaSuccess) {
-    cudaGetLastError();
-    return SWIGLU_ERR_CUDA;
-  }
-  return SWIGLU_OK;
+// A row-major [rows, cols] operand with the sum down its rows, 64 columns x 128 rows a box.
+bool encode_operand(CUtensorMap* map, const void* base, int64_t rows, int64_t cols) {
+  return encode_2d(map, base, cols, rows, cols * 2, kBlockK, kTileM, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+swiglu_status_t launched(cudaError_t e) {
+  if (e == cudaSuccess) return SWIGLU_OK;
+  cudaGetLastError();
+  return SWIGLU_ERR_CUDA;
+}
+
+// Launches the input and weight gradients and adds what is in parts.
+swiglu_status_t run_gradients(const BackwardParams& p, const GradientPlan& pl, const ReduceParams& sums,
+                              cudaStream_t stream) {
+  cudaError_t e = launch_backward_pair(p, false, pl.pairs, stream);
+  if (e == cudaSuccess && sums.count > 0) e = launch_reduce_parts(sums, stream);
+  return launched(e);
 }
 
 swiglu_status_t zero(void* p, size_t bytes, cudaStream_t stream) {
-  if (cudaMemsetAsync(p, 0, bytes, stream) == cudaSuccess) return SWIGLU_OK;
-  cudaGetLastError();
-  return SWIGLU_ERR_CUDA;
+  return launched(cudaMemsetAsync(p, 0, bytes, stream));
 }
 
 struct Span {
@@ -145,34 +187,22 @@ bool any_overlap(const Span* out, int outs, const Span* in, int ins) {
 }
 
 struct BackwardPlan {
-  ProductPlan grad, input, weight;
-  size_t grad_bytes = 0;   // dG (and dU) in the workspace
-  size_t parts_bytes = 0;  // then the parts of one product at a time
-  size_t bytes() const { return 2 * grad_bytes + parts_bytes; }
+  ProductPlan grad;
+  GradientPlan gradients;
+  size_t grad_bytes = 0;  // dG (and dU) in the workspace, then the parts
+  size_t bytes() const { return 2 * grad_bytes + gradients.parts_bytes(); }
 };
 
 BackwardPlan plan_backward(int64_t M, int64_t K, int64_t N, int pairs) {
   BackwardPlan pl;
-  pl.grad.tiles_m = div_up(M, kTile);
-  pl.grad.tiles_n = div_up(N, kTileM);
-  pl.grad.slices = k_slices(K);
-  pl.input = plan_input(M, K, 4 * div_up(N, kTileM), pairs);
-  pl.weight = plan_weight(K, N, 2, M, pairs);
+  pl.grad = plan_product(M, N, 2, k_slices(K));
+  pl.gradients = plan_gradients(M, K, 4 * div_up(N, kTileM), K, N, 2, pairs);
   pl.grad_bytes = align256(size_t(M) * size_t(N) * 2);
-  pl.parts_bytes = align256(std::max(pl.input.part_bytes, 2 * pl.weight.part_bytes));
   return pl;
 }
 
-struct DownBackwardPlan {
-  ProductPlan input, weight;
-  size_t bytes() const { return align256(std::max(input.part_bytes, weight.part_bytes)); }
-};
-
-DownBackwardPlan plan_down_backward(int64_t M, int64_t N, int64_t H, int pairs) {
-  DownBackwardPlan pl;
-  pl.input = plan_input(M, N, 4 * div_up(H, kTile), pairs);
-  pl.weight = plan_weight(N, H, 1, M, pairs);
-  return pl;
+GradientPlan plan_down_backward(int64_t M, int64_t N, int64_t H, int pairs) {
+  return plan_gradients(M, N, 4 * div_up(H, kTile), N, H, 1, pairs);
 }
 
 }  // namespace
@@ -219,49 +249,53 @@ swiglu_status_t swiglu_backward(const void* A, const void* Wpacked, const void* 
   if (st != SWIGLU_OK) return st;
   const BackwardPlan pl = plan_backward(M, K, N, pairs);
   if (workspace_bytes < pl.bytes()) return SWIGLU_ERR_INVALID_ARG;
-  if (too_many(pl.grad) || too_many(pl.input) || too_many(pl.weight)) return SWIGLU_ERR_UNSUPPORTED;
+  if (pl.grad.units() > kMaxUnits || pl.gradients.too_many()) return SWIGLU_ERR_UNSUPPORTED;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   void* dG = ws;
   void* dU = ws + pl.grad_bytes;
-  float* parts = reinterpret_cast<float*>(ws + 2 * pl.grad_bytes);
+  uint8_t* parts = ws + 2 * pl.grad_bytes;
   {
     BackwardParams p{};
-    fill(&p, pl.grad, d, M, N);
+    fill(&p.in, pl.grad, M, N);
+    fill_status(&p, d);
+    p.in_units = static_cast<int>(pl.grad.units());
     p.dy = dY;
-    if (!encode_2d(&p.tmap_a0, A, K, M, K * 2, kBlockK, kTileM, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !encode_packed_w(&p.tmap_b0, Wpacked, K, N, kPackBlockN) ||
-        !encode_2d(&p.tmap_o0, dG, N, M, N * 2, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B) ||
-        !encode_2d(&p.tmap_o1, dU, N, M, N * 2, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
+    if (!encode_2d(&p.in.tmap_a0, A, K, M, K * 2, kBlockK, kTileM, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !encode_packed_w(&p.in.tmap_b0, Wpacked, K, N, kPackBlockN) ||
+        !encode_2d(&p.in.tmap_o0, dG, N, M, N * 2, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B) ||
+        !encode_2d(&p.in.tmap_o1, dU, N, M, N * 2, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
       return SWIGLU_ERR_CUDA;
-    st = run_product(p, kBackwardGrad, pl.grad, pairs, nullptr, nullptr, nullptr, cs);
+    st = launched(launch_backward_pair(p, true, std::min(p.in_units, pairs), cs));
     if (st != SWIGLU_OK) return st;
   }
+  GradientPlan g = pl.gradients;
+  BackwardParams p{};
+  ReduceParams sums{};
+  deal_units(&g, dA != nullptr, dW1 != nullptr, pairs, &p);
+  fill_status(&p, d);
   if (dA) {
-    BackwardParams p{};
-    fill(&p, pl.input, d, M, K);
-    p.two = 1;
-    p.col_slices = static_cast<int>(k_slices(K));
-    if (!encode_2d(&p.tmap_a0, dG, N, M, N * 2, kBlockK, kTileM, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !encode_2d(&p.tmap_a1, dU, N, M, N * 2, kBlockK, kTileM, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !encode_packed_w(&p.tmap_b0, Wpacked, K, N, kBlockK) ||
-        !encode_output(&p.tmap_o0, dA, parts, pl.input, M, K))
+    fill(&p.in, g.in, M, K);
+    p.in.two = 1;
+    p.in.col_slices = static_cast<int>(k_slices(K));
+    if (!encode_2d(&p.in.tmap_a0, dG, N, M, N * 2, kBlockK, kTileM, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !encode_2d(&p.in.tmap_a1, dU, N, M, N * 2, kBlockK, kTileM, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !encode_packed_w(&p.in.tmap_b0, Wpacked, K, N, kPackBlockN) ||
+        !encode_output(&p.in.tmap_o0, dA, parts, g.in, M, K, &sums))
       return SWIGLU_ERR_CUDA;
-    st = run_product(p, kBackwardInput, pl.input, pairs, dA, nullptr, parts, cs);
-    if (st != SWIGLU_OK) return st;
   }
   if (dW1) {
-    BackwardParams p{};
-    fill(&p, pl.weight, d, K, N);
-    p.two_out = 1;
-    if (!encode_2d(&p.tmap_a0, A, K, M, K * 2, kBlockK, kBlockK, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !encode_2d(&p.tmap_b0, dG, N, M, N * 2, kBlockK, kBlockK, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !encode_2d(&p.tmap_b1, dU, N, M, N * 2, kBlockK, kBlockK, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !encode_output(&p.tmap_o0, dW1, parts, pl.weight, K, N) ||
-        !encode_output(&p.tmap_o1, dW2, parts + pl.weight.part_bytes / 4, pl.weight, K, N))
+    uint8_t* w_parts = parts + g.in.part_bytes;
+    fill(&p.w, g.w, K, N);
+    p.w.sum = static_cast<int>(M);
+    p.w.two = 1;
+    if (!encode_operand(&p.w.tmap_a0, A, M, K) ||
+        !encode_operand(&p.w.tmap_b0, dG, M, N) ||
+        !encode_operand(&p.w.tmap_b1, dU, M, N) ||
+        !encode_output(&p.w.tmap_o0, dW1, w_parts, g.w, K, N, &sums) ||
+        !encode_output(&p.w.tmap_o1, dW2, w_parts + g.w.part_bytes, g.w, K, N, &sums))
       return SWIGLU_ERR_CUDA;
-    st = run_product(p, kBackwardWeight, pl.weight, pairs, dW1, dW2, parts, cs);
   }
-  return st;
+  return run_gradients(p, g, sums, cs);
 }
 
 size_t swiglu_down_backward_workspace_bytes(int64_t M, int64_t N, int64_t H) {
@@ -269,7 +303,7 @@ size_t swiglu_down_backward_workspace_bytes(int64_t M, int64_t N, int64_t H) {
   DeviceView d;
   int pairs = 0;
   if (backward_device(&d, &pairs) != SWIGLU_OK) return 0;
-  return plan_down_backward(M, N, H, pairs).bytes();
+  return plan_down_backward(M, N, H, pairs).parts_bytes();
 }
 
 swiglu_status_t swiglu_down_backward(const void* dOut, const void* W3packed, const void* Y, void* dY,
@@ -300,31 +334,32 @@ swiglu_status_t swiglu_down_backward(const void* dOut, const void* W3packed, con
   int pairs = 0;
   st = backward_device(&d, &pairs);
   if (st != SWIGLU_OK) return st;
-  const DownBackwardPlan pl = plan_down_backward(M, N, H, pairs);
-  if (pl.bytes() > 0 && (!workspace || workspace_bytes < pl.bytes())) return SWIGLU_ERR_INVALID_ARG;
-  if (too_many(pl.input) || too_many(pl.weight)) return SWIGLU_ERR_UNSUPPORTED;
-  float* parts = static_cast<float*>(workspace);
+  GradientPlan g = plan_down_backward(M, N, H, pairs);
+  if (g.parts_bytes() > 0 && (!workspace || workspace_bytes < g.parts_bytes()))
+    return SWIGLU_ERR_INVALID_ARG;
+  if (g.too_many()) return SWIGLU_ERR_UNSUPPORTED;
+  uint8_t* parts = static_cast<uint8_t*>(workspace);
+  BackwardParams p{};
+  ReduceParams sums{};
+  deal_units(&g, dY != nullptr, dW3 != nullptr, pairs, &p);
+  fill_status(&p, d);
   if (dY) {
-    BackwardParams p{};
-    fill(&p, pl.input, d, M, N);
-    p.col_slices = static_cast<int>(k_slices(N));
-    if (!encode_2d(&p.tmap_a0, dOut, H, M, H * 2, kBlockK, kTileM, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !encode_packed_down(&p.tmap_b0, W3packed, N, H, kBlockK) ||
-        !encode_output(&p.tmap_o0, dY, parts, pl.input, M, N))
+    fill(&p.in, g.in, M, N);
+    p.in.col_slices = static_cast<int>(k_slices(N));
+    if (!encode_2d(&p.in.tmap_a0, dOut, H, M, H * 2, kBlockK, kTileM, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !encode_packed_down(&p.in.tmap_b0, W3packed, N, H, kPackBlockN) ||
+        !encode_output(&p.in.tmap_o0, dY, parts, g.in, M, N, &sums))
       return SWIGLU_ERR_CUDA;
-    st = run_product(p, kBackwardInput, pl.input, pairs, dY, nullptr, parts, cs);
-    if (st != SWIGLU_OK) return st;
   }
   if (dW3) {
-    BackwardParams p{};
-    fill(&p, pl.weight, d, N, H);
-    if (!encode_2d(&p.tmap_a0, Y, N, M, N * 2, kBlockK, kBlockK, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !encode_2d(&p.tmap_b0, dOut, H, M, H * 2, kBlockK, kBlockK, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !encode_output(&p.tmap_o0, dW3, parts, pl.weight, N, H))
+    fill(&p.w, g.w, N, H);
+    p.w.sum = static_cast<int>(M);
+    if (!encode_operand(&p.w.tmap_a0, Y, M, N) ||
+        !encode_operand(&p.w.tmap_b0, dOut, M, H) ||
+        !encode_output(&p.w.tmap_o0, dW3, parts + g.in.part_bytes, g.w, N, H, &sums))
       return SWIGLU_ERR_CUDA;
-    st = run_product(p, kBackwardWeight, pl.weight, pairs, dW3, nullptr, parts, cs);
   }
-  return st;
+  return run_gradients(p, g, sums, cs);
 }
 
 }  // extern "C"

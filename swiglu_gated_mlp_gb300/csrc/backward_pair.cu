@@ -4,8 +4,8 @@
 // Forward (fused_large_m_pair.cu): G = A W1, U = A W2, Y = SiLU(G) * U, and
 // Out = Y W3 + R. With s = 1 / (1 + e^-G) the gradients are
 //   dU = dY * G s,   dG = dY * U * s (1 + G (1 - s))          (kGrad)
-//   dA = dG W1^T + dU W2^T          or   dY = dOut W3^T       (kInput)
-//   dW1 = A^T dG, dW2 = A^T dU      or   dW3 = Y^T dOut       (kWeight)
+//   dA = dG W1^T + dU W2^T          or   dY = dOut W3^T       (input gradient)
+//   dW1 = A^T dG, dW2 = A^T dU      or   dW3 = Y^T dOut       (weight gradient)
 // G and U are not kept by the forward; kGrad recomputes them in the forward's
 // own pipeline and its epilogue turns the fp32 accumulators and dY into dG and
 // dU, each rounded once to bf16: they are operands of tensor-core products, and
@@ -18,18 +18,31 @@
 // rows under the 128-byte swizzle; what differs is which tensor dimension is
 // contiguous and so which "major" the MMA descriptors state:
 //   kGrad    rows [m][k] x packed weight [n][k]: both contiguous along the sum
-//   kInput   rows [m][n] contiguous along the sum; the packed weight's tiles
+//   input    rows [m][n] contiguous along the sum; the packed weight's tiles
 //            [n][64 k] hold the sum along their rows (MN-major), so the same
 //            packed weight serves the forward and this product, no transpose
-//   kWeight  both operands are row-major with the sum (tokens) down the rows:
+//   weight   both operands are row-major with the sum (tokens) down the rows:
 //            MN-major twice, no transposed copy of anything is written
-// An MN-major operand is stored as 64-element x 64-row boxes of 8 KB: 8-row
-// groups 1024 bytes apart along the sum, the next 64 elements 8 KB further.
+// An MN-major operand of 128 columns x 128 of the sum comes as two boxes of 64
+// columns x 128 rows, one in each of two consecutive stages (8-row groups 1024
+// bytes apart, the other 64 columns one stage further), so the input and weight
+// gradients use their stages in pairs, 128 of the sum at a time. Boxes of 64
+// rows, two to a stage, hold the same bytes but load slower: the 7B weight
+// gradient of the down-projection took 365 us against 310 (one 3-D box for
+// both) and 415 (two 2-D boxes); the loads, not the MN-major MMAs, were what
+// it waited for (K-major descriptors on the same bytes: 365 us too).
 //
 // Roles as in the forward pair kernel: warp 0 TMA producer, warp 1 MMA issuer
 // (even CTA), warps 2-5 epilogue; 6 stages of 32 KB per CTA; two accumulators
 // of 256 columns, so a tile's epilogue runs under the next tile's MMAs; every
 // wait is bounded (ptx.cuh).
+//
+// The input and the weight gradients do not depend on one another, so one
+// launch computes both: its units are the input gradient's tiles, then the
+// weight gradient's, and unit_at() deals them to the pairs so that pairs with
+// one input tile fewer take as many weight tiles more. A launch of its own for
+// each left a part-filled last round twice, and on short sums (0.5B, 128
+// tokens) its start-up cost as much as its work.
 //
 // Few output tiles: with `splits` > 1 each tile's sum is cut into that many
 // parts, each part's fp32 accumulator goes to the workspace and
@@ -49,6 +62,7 @@ constexpr int kStgBytes = 32 * 128;                    // 32 rows x 128 B store 
 constexpr int kNumStg = 8;                             // 2 per epilogue warp
 constexpr int kBarBytes = 256;
 constexpr size_t kSmem = 1024 + size_t(kStages) * kStageBytes + size_t(kNumStg) * kStgBytes + kBarBytes;
+static_assert(kStages % 2 == 0, "stages are used in pairs");
 static_assert(kSmem <= 232448, "shared memory budget");
 static_assert(8 * (2 * kStages + 5) + 8 <= kBarBytes, "barrier slots");
 
@@ -63,6 +77,35 @@ __device__ __forceinline__ void tile_coords(int t, int tiles_m, int tiles_n, int
   nb = r / gm;
 }
 
+// The `step`-th unit of a pair: an input-gradient unit, then weight-gradient
+// units; -1 past the last. Of `in_units` = q pairs + r, pairs r.. have one unit
+// fewer (when r > 0) and first take `early_rounds` rounds of weight units among
+// themselves; all pairs share the rest round by round.
+__device__ __forceinline__ int unit_at(const BackwardParams& p, int pair, int pairs, int step,
+                                       bool& weight) {
+  const int r = p.in_units % pairs;
+  const int mine = p.in_units / pairs + (pair < r ? 1 : 0);
+  weight = step >= mine;
+  if (!weight) return pair + step * pairs;
+  int k = step - mine, first = 0;
+  if (r > 0) {
+    if (pair >= r) {
+      if (k < p.early_rounds) return pair - r + k * (pairs - r);
+      k -= p.early_rounds;
+    }
+    first = p.early_rounds * (pairs - r);
+  }
+  const int64_t u = first + pair + int64_t(k) * pairs;
+  return u < p.w_units ? static_cast<int>(u) : -1;
+}
+
+// First stage of a part of the sum; whole pairs of stages except for kGrad.
+template <bool kGrad>
+__device__ __forceinline__ int part_begin(const BackwardProduct& g, int part) {
+  constexpr int kUnit = kGrad ? 1 : 2;
+  return static_cast<int>(int64_t(part) * (g.slices / kUnit) / g.splits) * kUnit;
+}
+
 // dG and dU of one element. For |g| large s (1 - s) g -> 0 and no term
 // overflows: e^-g = +inf gives s = 0 and g * 0 = -0 for finite g.
 __device__ __forceinline__ void gate_grads(float g, float u, float dy, float& dg, float& du) {
@@ -72,11 +115,9 @@ __device__ __forceinline__ void gate_grads(float g, float u, float dy, float& dg
   dg = dy * u * (s + gs * (1.0f - s));
 }
 
-template <int kMode>
+template <bool kGrad>
 __global__ void __launch_bounds__(kThreads, 1)
     backward_pair_kernel(const __grid_constant__ BackwardParams p) {
-  constexpr bool kGradMode = kMode == kBackwardGrad;
-  constexpr bool kMnA = kMode == kBackwardWeight, kMnB = kMode != kBackwardGrad;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -98,16 +139,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   const bool leader = rank == 0;
   const int pair = static_cast<int>(cluster_id_x());
   const int pairs = static_cast<int>(cluster_count_x());
-  const int splits = kGradMode ? 1 : p.splits;
-  const int num_units = p.tiles_m * p.tiles_n * splits;  // unit = tile * splits + part
   const WaitCtx wc{abort_flag, p.status, p.timeout_ns};
   const uint32_t full0_lead = mapa_shared(full0, 0);
   const uint32_t tempty0_lead = mapa_shared(tempty0, 0);
 
   if (threadIdx.x == 0) {
-    prefetch_tmap(&p.tmap_a0);
-    prefetch_tmap(&p.tmap_b0);
-    prefetch_tmap(&p.tmap_o0);
+    const BackwardProduct& g = p.in_units > 0 ? p.in : p.w;  // the other one's maps may be unset
+    prefetch_tmap(&g.tmap_a0);
+    prefetch_tmap(&g.tmap_b0);
     for (int s = 0; s < kStages; ++s) {
       mbar_init(full0 + 8u * s, 1);   // rank 0's producer arrives (with both CTAs' bytes)
       mbar_init(empty0 + 8u * s, 1);  // rank 0's MMA commit, multicast to both CTAs
@@ -138,13 +177,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t filled = 0, fill_ph = 0;
       bool skip_once = p.inject_stall != 0;
       bool ok = true;
-      for (int t = pair; ok && t < num_units; t += pairs) {
+      bool weight;
+      for (int step = 0, u; ok && (u = unit_at(p, pair, pairs, step, weight)) >= 0; ++step) {
+        const BackwardProduct& g = weight ? p.w : p.in;
+        const int tile = u / g.splits, part = u - tile * g.splits;
         int mb, nb;
-        const int part = t % splits;
-        tile_coords(t / splits, p.tiles_m, p.tiles_n, p.group_m, mb, nb);
+        tile_coords(tile, g.tiles_m, g.tiles_n, g.group_m, mb, nb);
         const int r0 = mb * 2 * kTileM + static_cast<int>(rank) * kTileM;  // output row of this CTA
-        const int begin = static_cast<int>(int64_t(part) * p.slices / splits);
-        const int end = static_cast<int>(int64_t(part + 1) * p.slices / splits);
+        const int begin = part_begin<kGrad>(g, part), end = part_begin<kGrad>(g, part + 1);
         for (int i = begin; i < end; ++i) {
           if (!mbar_wait(empty0 + 8u * s, ph ^ 1u, wc, kSiteProducerEmpty)) {
             ok = false;
@@ -156,37 +196,31 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (leader) mbar_arrive_expect_tx(full0 + 8u * s, 2 * kStageBytes);
             const uint32_t fb = full0_lead + 8u * s;
             const uint32_t da = sA + s * kOperandBytes, db = sB + s * kOperandBytes;
-            if constexpr (kMode == kBackwardGrad) {
+            if constexpr (kGrad) {
               // A rows [r0, +128); gate (rank 0) or up (rank 1) rows of tile (nb, i)
-              tma_load_2d_pair(da, &p.tmap_a0, fb, i * kBlockK, r0);
-              tma_load_3d_pair(db, &p.tmap_b0, fb, 0, static_cast<int>(rank) * kPackBlockN,
-                               nb * p.slices + i);
-            } else if constexpr (kMode == kBackwardInput) {
-              // slice i of the sum: rows [64 c, +64) of packed tile row j. A gate/up
-              // tile holds 128 gate then 128 up columns, a down tile 256 columns.
-              const int j = i >> 2, c = i & 3;
-              if (p.two)
-                tma_load_2d_pair(da, c < 2 ? &p.tmap_a0 : &p.tmap_a1, fb,
-                                 j * kPackBlockN + (c & 1) * kBlockK, r0);
-              else
-                tma_load_2d_pair(da, &p.tmap_a0, fb, i * kBlockK, r0);
-              // this CTA's 128 output columns: two 64-column blocks of the packed tiles
-              // (a block past the last one reads another tile or zeros; its columns
-              // lie outside the output and are not stored)
-              const int b0 = nb * 4 + static_cast<int>(rank) * 2;
-              const int tile = j * p.col_slices + b0;
-              tma_load_3d_pair(db, &p.tmap_b0, fb, 0, c * kBlockK, tile);
-              tma_load_3d_pair(db + kOperandBytes / 2, &p.tmap_b0, fb, 0, c * kBlockK, tile + 1);
+              tma_load_2d_pair(da, &g.tmap_a0, fb, i * kBlockK, r0);
+              tma_load_3d_pair(db, &g.tmap_b0, fb, 0, static_cast<int>(rank) * kPackBlockN,
+                               nb * g.slices + i);
+            } else if (!weight) {
+              // stages 2 d, 2 d + 1: rows [128 h, +128) of packed tile row j (a gate/up
+              // tile holds 128 gate then 128 up columns of the sum, a down tile 256);
+              // left operand: 64 of those columns of the sum a stage; right operand:
+              // all 128, for 64 of this CTA's 128 output columns a stage (a block past
+              // the last one reads another tile or zeros; its columns lie outside the
+              // output and are not stored)
+              const int j = i >> 2, h = (i >> 1) & 1, e = i & 1;
+              const int col = (g.two ? j * kPackBlockN : j * 2 * kPackBlockN + h * kPackBlockN) + e * kBlockK;
+              tma_load_2d_pair(da, g.two && h ? &g.tmap_a1 : &g.tmap_a0, fb, col, r0);
+              tma_load_3d_pair(db, &g.tmap_b0, fb, 0, h * kPackBlockN,
+                               j * g.col_slices + nb * 4 + static_cast<int>(rank) * 2 + e);
             } else {
-              // tokens [64 i, +64): 128 output rows of the left operand, 128 output
-              // columns of the right one, each as two 64-wide boxes
-              tma_load_2d_pair(da, &p.tmap_a0, fb, r0, i * kBlockK);
-              tma_load_2d_pair(da + kOperandBytes / 2, &p.tmap_a0, fb, r0 + 64, i * kBlockK);
-              const CUtensorMap* mapb = p.two_out && rank ? &p.tmap_b1 : &p.tmap_b0;
+              // stages 2 d, 2 d + 1: tokens [128 d, +128), 64 of this CTA's 128 output
+              // rows and 64 of its 128 output columns a stage
+              const int m = (i >> 1) * 2 * kBlockK, e = (i & 1) * kBlockK;
               const int c0 =
-                  p.two_out ? nb * kTileM : nb * 2 * kTileM + static_cast<int>(rank) * kTileM;
-              tma_load_2d_pair(db, mapb, fb, c0, i * kBlockK);
-              tma_load_2d_pair(db + kOperandBytes / 2, mapb, fb, c0 + 64, i * kBlockK);
+                  g.two ? nb * kTileM : nb * 2 * kTileM + static_cast<int>(rank) * kTileM;
+              tma_load_2d_pair(da, &g.tmap_a0, fb, r0 + e, m);
+              tma_load_2d_pair(db, g.two && rank ? &g.tmap_b1 : &g.tmap_b0, fb, c0 + e, m);
             }
             filled |= 1u << s;
             fill_ph = (fill_ph & ~(1u << s)) | (ph << s);
@@ -208,40 +242,69 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 1) {
     // ------------------------------------------------ MMA issuer (rank 0)
     if (leader && lane == 0) {
-      constexpr uint32_t kIdesc =
-          idesc_bf16_f32(2 * kTileM, kAccCols) | (kMnA ? 1u << 15 : 0u) | (kMnB ? 1u << 16 : 0u);
-      // 16 of the sum per MMA: 32 bytes along a K-major row, 16 rows of 128 bytes MN-major
-      constexpr uint32_t kStepA = kMnA ? 2048 >> 4 : 32 >> 4, kStepB = kMnB ? 2048 >> 4 : 32 >> 4;
       int s = 0;
       uint32_t ph = 0;
       int buf = 0;
       uint32_t acc_ph = 0;
-      bool ok = true;
-      for (int t = pair; ok && t < num_units; t += pairs) {
+      bool ok = true, weight;
+      for (int step = 0, u; ok && (u = unit_at(p, pair, pairs, step, weight)) >= 0; ++step) {
+        const BackwardProduct& g = weight ? p.w : p.in;
+        const int part = u % g.splits;
+        const int begin = part_begin<kGrad>(g, part), end = part_begin<kGrad>(g, part + 1);
         if (!mbar_wait(tempty0 + 8u * buf, acc_ph ^ 1u, wc, kSiteMmaTmemEmpty)) break;
         tc_fence_after();
         const uint32_t d = tmem_base + buf * kAccCols;
-        const int part = t % splits;
-        const int begin = static_cast<int>(int64_t(part) * p.slices / splits);
-        const int end = static_cast<int>(int64_t(part + 1) * p.slices / splits);
-        for (int i = begin; i < end; ++i) {
-          if (!mbar_wait(full0 + 8u * s, ph, wc, kSiteMmaFull)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint64_t adesc = kMnA ? smem_desc_sw128_mn(sA + s * kOperandBytes, kOperandBytes / 2)
-                                      : smem_desc_sw128(sA + s * kOperandBytes);
-          const uint64_t bdesc = kMnB ? smem_desc_sw128_mn(sB + s * kOperandBytes, kOperandBytes / 2)
-                                      : smem_desc_sw128(sB + s * kOperandBytes);
+        if constexpr (kGrad) {
+          constexpr uint32_t kIdesc = idesc_bf16_f32(2 * kTileM, kAccCols);
+          for (int i = begin; i < end; ++i) {
+            if (!mbar_wait(full0 + 8u * s, ph, wc, kSiteMmaFull)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint64_t adesc = smem_desc_sw128(sA + s * kOperandBytes);
+            const uint64_t bdesc = smem_desc_sw128(sB + s * kOperandBytes);
 #pragma unroll
-          for (uint32_t k = 0; k < 4; ++k)
-            mma_bf16_pair(d, adesc + kStepA * k, bdesc + kStepB * k, kIdesc,
-                          (i != begin || k != 0) ? 1u : 0u);
-          mma_commit_pair_multicast(empty0 + 8u * s, 0x3);  // frees the stage in both CTAs
-          if (++s == kStages) {
-            s = 0;
-            ph ^= 1u;
+            for (uint32_t k = 0; k < 4; ++k)
+              mma_bf16_pair(d, adesc + 2u * k, bdesc + 2u * k, kIdesc, (i != begin || k != 0) ? 1u : 0u);
+            mma_commit_pair_multicast(empty0 + 8u * s, 0x3);  // frees the stage in both CTAs
+            if (++s == kStages) {
+              s = 0;
+              ph ^= 1u;
+            }
+          }
+        } else {
+          // Bits 15 (left) and 16 (right) of the descriptor mark MN-major operands.
+          // 16 of the sum are 16 rows of 128 bytes of an MN-major operand, 32 bytes
+          // along a K-major row (four in each of the two stages).
+          const uint32_t idesc =
+              idesc_bf16_f32(2 * kTileM, kAccCols) | (weight ? 1u << 15 : 0u) | (1u << 16);
+          for (int i = begin; i < end; i += 2) {  // s is even: every unit has whole pairs of stages
+            if (!mbar_wait(full0 + 8u * s, ph, wc, kSiteMmaFull) ||
+                !mbar_wait(full0 + 8u * (s + 1), ph, wc, kSiteMmaFull)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t pa = sA + s * kOperandBytes;
+            const uint64_t adesc = weight ? smem_desc_sw128_mn(pa, kOperandBytes) : smem_desc_sw128(pa);
+            const uint64_t bdesc = smem_desc_sw128_mn(sB + s * kOperandBytes, kOperandBytes);
+            // weight gradient: no MMA for 16 tokens that do not exist
+            const int ksteps = weight ? min(8, (g.sum - (i >> 1) * 2 * kBlockK + 15) / 16) : 8;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const uint64_t da = adesc + (weight ? (2048u >> 4) * k
+                                                  : 2u * (k & 3) + (k >> 2) * (kOperandBytes >> 4));
+              if (k < ksteps)
+                mma_bf16_pair(d, da, bdesc + (2048u >> 4) * k, idesc, (i != begin || k != 0) ? 1u : 0u);
+            }
+            mma_commit_pair_multicast(empty0 + 8u * s, 0x3);  // frees the stages in both CTAs
+            mma_commit_pair_multicast(empty0 + 8u * (s + 1), 0x3);
+            s += 2;
+            if (s == kStages) {
+              s = 0;
+              ph ^= 1u;
+            }
           }
         }
         if (!ok) break;
@@ -261,20 +324,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     int buf = 0;
     uint32_t acc_ph = 0;
     int sbuf = 0;
-    for (int t = pair; t < num_units; t += pairs) {
+    bool weight;
+    for (int step = 0, unit; (unit = unit_at(p, pair, pairs, step, weight)) >= 0; ++step) {
+      const BackwardProduct& pr = weight ? p.w : p.in;
+      const int tile = unit / pr.splits, part = unit - tile * pr.splits;
       int mb, nb;
-      const int part = t % splits;
-      tile_coords(t / splits, p.tiles_m, p.tiles_n, p.group_m, mb, nb);
+      tile_coords(tile, pr.tiles_m, pr.tiles_n, pr.group_m, mb, nb);
       const int row0 = mb * 2 * kTileM + static_cast<int>(rank) * kTileM + q * 32;
       uint4 dyv[4];
       const __nv_bfloat16* dy_row = nullptr;
-      if constexpr (kGradMode) {
+      if constexpr (kGrad) {
         // this thread's row of dY, 32 columns ahead of the accumulator chunk in use
-        dy_row = static_cast<const __nv_bfloat16*>(p.dy) + static_cast<size_t>(row0 + lane) * p.cols;
+        dy_row = static_cast<const __nv_bfloat16*>(p.dy) + static_cast<size_t>(row0 + lane) * pr.cols;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int col = nb * kTileM + 8 * e;
-          dyv[e] = row0 + lane < p.rows && col < p.cols
+          dyv[e] = row0 + lane < pr.rows && col < pr.cols
                        ? __ldg(reinterpret_cast<const uint4*>(dy_row + col))
                        : make_uint4(0u, 0u, 0u, 0u);
         }
@@ -285,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       tc_fence_after();
       const uint32_t tacc = tmem_base + lane_off + buf * kAccCols;
-      if constexpr (kGradMode) {
+      if constexpr (kGrad) {
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
           uint32_t g[32], u[32];
@@ -297,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             dyc[e] = dyv[e];
             const int col = nb * kTileM + (c + 1) * 32 + 8 * e;
             if (c < 3)
-              dyv[e] = row0 + lane < p.rows && col < p.cols
+              dyv[e] = row0 + lane < pr.rows && col < pr.cols
                            ? __ldg(reinterpret_cast<const uint4*>(dy_row + col))
                            : make_uint4(0u, 0u, 0u, 0u);
           }
@@ -336,9 +401,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane == 0) {
             const int ncol = nb * kTileM + c * 32;
-            if (ncol < p.cols && row0 < p.rows) {
-              tma_store_2d(&p.tmap_o0, stg, ncol, row0);
-              tma_store_2d(&p.tmap_o1, stg + 2048, ncol, row0);
+            if (ncol < pr.cols && row0 < pr.rows) {
+              tma_store_2d(&pr.tmap_o0, stg, ncol, row0);
+              tma_store_2d(&pr.tmap_o1, stg + 2048, ncol, row0);
             }
             bulk_commit();
           }
@@ -347,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else {
         // 8 chunks of 32 columns: fp32 parts (128-byte rows) to the workspace,
         // or two chunks at a time as 64 bf16 columns to the output
-        const bool parts = splits > 1;
+        const bool parts = pr.splits > 1;
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
           uint32_t x[32], y[32];
@@ -362,11 +427,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive_cluster(tempty0_lead + 8u * buf);
           }
           const int half = c >> 1;  // accumulator columns 0-127 or 128-255
-          const CUtensorMap* mapo = p.two_out && half ? &p.tmap_o1 : &p.tmap_o0;
-          const int ncol = p.two_out ? nb * kTileM + (c & 1) * 64 : nb * 2 * kTileM + c * 64;
+          const bool two = weight && pr.two;
+          const CUtensorMap* mapo = two && half ? &pr.tmap_o1 : &pr.tmap_o0;
+          const int ncol = two ? nb * kTileM + (c & 1) * 64 : nb * 2 * kTileM + c * 64;
           if (parts) {
             // part-major rows: the store maps see splits * padded rows
-            const int prow = part * p.part_rows + row0;
+            const int prow = part * pr.part_rows + row0;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               if (lane == 0) bulk_wait_read<1>();
@@ -381,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               fence_proxy_async_smem();
               __syncwarp();
               if (lane == 0) {
-                if (ncol + 32 * h < p.cols && row0 < p.rows)
+                if (ncol + 32 * h < pr.cols && row0 < pr.rows)
                   tma_store_2d(mapo, stg, ncol + 32 * h, prow);
                 bulk_commit();
               }
@@ -404,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
-              if (ncol < p.cols && row0 < p.rows) tma_store_2d(mapo, stg, ncol, row0);
+              if (ncol < pr.cols && row0 < pr.rows) tma_store_2d(mapo, stg, ncol, row0);
               bulk_commit();
             }
             sbuf ^= 1;
@@ -428,33 +494,34 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// out[r][c] = bf16(sum over parts, in order, of parts[part][r][c]): one pass
-// over fp32 values that are mostly still in L2, 8 columns a thread.
-__global__ void __launch_bounds__(256)
-    reduce_parts_kernel(const float* __restrict__ parts, __nv_bfloat16* __restrict__ out, int rows,
-                        int cols, int part_rows, int splits) {
-  pdl_wait();
+// out[r][c] = bf16(sum over parts, in order, of parts[part][r][c]) for each
+// output cut into parts: one pass over fp32 values that are mostly still in L2,
+// 8 columns a thread.
+__global__ void __launch_bounds__(256) reduce_parts_kernel(const __grid_constant__ ReduceParams p) {
   pdl_launch_dependents();
-  const int chunks = cols / 8;
-  const size_t items = static_cast<size_t>(rows) * chunks;
-  const size_t part_stride = static_cast<size_t>(part_rows) * cols;
-  for (size_t i = blockIdx.x * static_cast<size_t>(blockDim.x) + threadIdx.x; i < items;
-       i += static_cast<size_t>(gridDim.x) * blockDim.x) {
-    const float* src = parts + i * 8;
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
-#pragma unroll 4
-    for (int s = 0; s < splits; ++s) {
-      const float4 x = __ldcg(reinterpret_cast<const float4*>(src + s * part_stride));
-      const float4 y = __ldcg(reinterpret_cast<const float4*>(src + s * part_stride + 4));
-      a.x += x.x; a.y += x.y; a.z += x.z; a.w += x.w;
-      b.x += y.x; b.y += y.y; b.z += y.z; b.w += y.w;
+  pdl_wait();
+  for (int o = 0; o < p.count; ++o) {
+    const ReduceOutput& r = p.out[o];
+    const size_t items = static_cast<size_t>(r.rows) * (r.cols / 8);
+    const size_t part_stride = static_cast<size_t>(r.part_rows) * r.cols;
+    for (size_t i = blockIdx.x * static_cast<size_t>(blockDim.x) + threadIdx.x; i < items;
+         i += static_cast<size_t>(gridDim.x) * blockDim.x) {
+      const float* src = r.parts + i * 8;
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+#pragma unroll 8
+      for (int s = 0; s < r.splits; ++s) {
+        const float4 x = __ldcg(reinterpret_cast<const float4*>(src + s * part_stride));
+        const float4 y = __ldcg(reinterpret_cast<const float4*>(src + s * part_stride + 4));
+        a.x += x.x; a.y += x.y; a.z += x.z; a.w += x.w;
+        b.x += y.x; b.y += y.y; b.z += y.z; b.w += y.w;
+      }
+      uint4 v;
+      v.x = pack_bf16x2(a.x, a.y);
+      v.y = pack_bf16x2(a.z, a.w);
+      v.z = pack_bf16x2(b.x, b.y);
+      v.w = pack_bf16x2(b.z, b.w);
+      *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(r.out) + i * 8) = v;
     }
-    uint4 o;
-    o.x = pack_bf16x2(a.x, a.y);
-    o.y = pack_bf16x2(a.z, a.w);
-    o.z = pack_bf16x2(b.x, b.y);
-    o.w = pack_bf16x2(b.z, b.w);
-    *reinterpret_cast<uint4*>(out + i * 8) = o;
   }
 }
 
@@ -476,40 +543,46 @@ cudaLaunchConfig_t backward_config(int grid, cudaStream_t stream, cudaLaunchAttr
   return cfg;
 }
 
-template <int kMode>
-cudaError_t set_smem() {
-  return cudaFuncSetAttribute(backward_pair_kernel<kMode>,
-                              cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem));
+bool valid(const BackwardProduct& g, int units) {
+  return units == 0 ||
+         (g.splits >= 1 && g.slices >= g.splits && g.group_m >= 1 &&
+          int64_t(g.tiles_m) * g.tiles_n * g.splits == units &&
+          (g.splits == 1 || (g.part_rows >= g.rows && (g.part_rows % 32) == 0)));
 }
 
 }  // namespace
 
 cudaError_t configure_backward_pair(int* max_pairs) {
-  cudaError_t e = set_smem<kBackwardGrad>();
-  if (e == cudaSuccess) e = set_smem<kBackwardInput>();
-  if (e == cudaSuccess) e = set_smem<kBackwardWeight>();
+  cudaError_t e = cudaFuncSetAttribute(backward_pair_kernel<true>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmem));
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(backward_pair_kernel<false>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmem));
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg = backward_config(2, nullptr, attr, false);
-  return cudaOccupancyMaxActiveClusters(max_pairs, backward_pair_kernel<kBackwardGrad>, &cfg);
+  return cudaOccupancyMaxActiveClusters(max_pairs, backward_pair_kernel<true>, &cfg);
 }
 
-cudaError_t launch_backward_pair(const BackwardParams& p, int mode, int grid, cudaStream_t stream) {
-  if (grid < 2 || (grid % 2) != 0 || p.splits < 1 || p.slices < p.splits || p.group_m < 1 ||
-      (p.splits > 1 && (p.part_rows < p.rows || (p.part_rows % 32) != 0)))
+cudaError_t launch_backward_pair(const BackwardParams& p, bool grad, int pairs, cudaStream_t stream) {
+  const int r = pairs > 0 ? p.in_units % pairs : 0;
+  if (pairs < 1 || p.in_units + int64_t(p.w_units) < pairs || !valid(p.in, p.in_units) ||
+      !valid(p.w, p.w_units) || p.early_rounds < 0 ||
+      int64_t(p.early_rounds) * (pairs - r) > p.w_units || (grad && (p.w_units || p.in.splits != 1)))
     return cudaErrorInvalidValue;
   cudaLaunchAttribute attr[2];
-  cudaLaunchConfig_t cfg = backward_config(grid, stream, attr, pdl_enabled());
-  const cudaError_t e =
-      mode == kBackwardGrad    ? cudaLaunchKernelEx(&cfg, backward_pair_kernel<kBackwardGrad>, p)
-      : mode == kBackwardInput ? cudaLaunchKernelEx(&cfg, backward_pair_kernel<kBackwardInput>, p)
-                               : cudaLaunchKernelEx(&cfg, backward_pair_kernel<kBackwardWeight>, p);
+  cudaLaunchConfig_t cfg = backward_config(2 * pairs, stream, attr, pdl_enabled());
+  const cudaError_t e = grad ? cudaLaunchKernelEx(&cfg, backward_pair_kernel<true>, p)
+                             : cudaLaunchKernelEx(&cfg, backward_pair_kernel<false>, p);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-cudaError_t launch_reduce_parts(const float* parts, void* out, int rows, int cols, int part_rows,
-                                int splits, cudaStream_t stream) {
-  const size_t items = static_cast<size_t>(rows) * (cols / 8);
+cudaError_t launch_reduce_parts(const ReduceParams& p, cudaStream_t stream) {
+  size_t items = 1;
+  for (int o = 0; o < p.count; ++o) {
+    const size_t n = static_cast<size_t>(p.out[o].rows) * (p.out[o].cols / 8);
+    items = n > items ? n : items;
+  }
   const size_t blocks = (items + 255) / 256;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(blocks < 1216 ? blocks : 1216));  // 8 blocks per SM
@@ -520,9 +593,7 @@ cudaError_t launch_reduce_parts(const float* parts, void* out, int rows, int col
   attr[0].val.programmaticStreamSerializationAllowed = pdl_enabled() ? 1 : 0;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, reduce_parts_kernel, parts,
-                                           static_cast<__nv_bfloat16*>(out), rows, cols, part_rows,
-                                           splits);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, reduce_parts_kernel, p);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 

@@ -163,36 +163,49 @@ cudaError_t configure_sequential();
 int sequential_stages();
 cudaError_t launch_sequential(const LargeMParams& p, cudaStream_t stream);
 
-// Gradients on CTA pairs (backward_pair.cu): 256 x 256 output tiles, one
-// kernel per operand shape.
-enum BackwardMode {
-  kBackwardGrad = 0,    // recompute gate and up, write dG and dU
-  kBackwardInput = 1,   // dA = dG W1^T + dU W2^T, or dY = dOut W3^T
-  kBackwardWeight = 2,  // dW1 = A^T dG and dW2 = A^T dU, or dW3 = Y^T dOut
+// Gradients on CTA pairs (backward_pair.cu): 256 x 256 output tiles of one
+// product, its sum optionally cut into parts (unit = tile * splits + part).
+struct BackwardProduct {
+  // left operand (a1: the second one of the input gradient's sum, with `two`),
+  // right operand (b1: the second weight gradient's, with `two`), outputs
+  CUtensorMap tmap_a0, tmap_a1, tmap_b0, tmap_b1, tmap_o0, tmap_o1;
+  int rows, cols;  // of one output
+  int slices;      // stages: 64-deep slices of the sum; even (whole pairs) but for dG and dU
+  int sum;         // weight gradient: tokens
+  int col_slices;  // input gradient: packed tiles of 64 columns per row of tiles
+  int tiles_m, tiles_n, group_m;
+  int two;         // input gradient: dG and dU in the sum; weight gradient: dW1 and dW2
+  int splits;      // parts of the sum (1: none); > 1: outputs are fp32 parts of
+  int part_rows;   // this many rows each (a multiple of 32)
 };
 
 struct BackwardParams {
-  // left operand (a1: the second one of the input gradient's sum, with `two`),
-  // right operand (b1: the second weight gradient's, with `two_out`), outputs
-  CUtensorMap tmap_a0, tmap_a1, tmap_b0, tmap_b1, tmap_o0, tmap_o1;
-  const void* dy;  // kBackwardGrad: dY [rows, cols] bf16
-  int rows, cols;  // of one output
-  int slices;      // 64-deep slices of the sum
-  int col_slices;  // kBackwardInput: packed tiles of 64 columns per row of tiles
-  int tiles_m, tiles_n, group_m;
-  int two, two_out;
-  int splits;      // parts of the sum (1: none); > 1: outputs are fp32 parts of
-  int part_rows;   // this many rows each (a multiple of 32)
+  BackwardProduct in;  // dG and dU from the recomputed gate and up, or the input gradient
+  BackwardProduct w;   // the weight gradient
+  int in_units, w_units;
+  int early_rounds;    // see unit_at()
+  const void* dy;      // dG and dU: dY [rows, cols] bf16
   uint32_t* status;
   uint64_t timeout_ns;
   int inject_stall;
 };
 
+struct ReduceOutput {
+  const float* parts;  // `splits` parts of part_rows x cols
+  void* out;           // [rows, cols] bf16
+  int rows, cols, part_rows, splits;
+};
+
+struct ReduceParams {
+  ReduceOutput out[3];
+  int count;
+};
+
 cudaError_t configure_backward_pair(int* max_pairs);
-cudaError_t launch_backward_pair(const BackwardParams& p, int mode, int grid, cudaStream_t stream);
-// out [rows, cols] bf16 = sum of `splits` fp32 parts [part_rows, cols], in order.
-cudaError_t launch_reduce_parts(const float* parts, void* out, int rows, int cols, int part_rows,
-                                int splits, cudaStream_t stream);
+// `grad`: dG and dU (product `in` only); otherwise the input and weight gradients.
+cudaError_t launch_backward_pair(const BackwardParams& p, bool grad, int pairs, cudaStream_t stream);
+// Adds the fp32 parts of each output in order and rounds once.
+cudaError_t launch_reduce_parts(const ReduceParams& p, cudaStream_t stream);
 
 // Words of the static scratch array behind swiglu_forward_noalloc (256 bytes);
 // a call uses the first kStatusWords of them for its status record.
