@@ -72,10 +72,10 @@ ProductPlan plan_product(int64_t rows, int64_t cols, int outputs, int64_t slices
 }
 
 // Cuts a product's sum so that no unit is longer than all units spread evenly
-// over the pairs, in parts of at least 8 slices: shorter ones do not pay for
-// writing and adding them.
+// over the pairs, in parts of at least 8 slices, and only where that saves more
+// than the launch that adds the parts takes (about 24 slices).
 void split(ProductPlan* pl, int64_t cols, int64_t even) {
-  if (pl->slices > even)
+  if (pl->slices > even + 24)
     pl->splits = std::max<int64_t>(
         1, std::min<int64_t>(div_up(pl->slices, std::max<int64_t>(even, 1)), pl->slices / 8));
   if (pl->splits > 1) pl->part_bytes = align256(size_t(pl->splits) * size_t(pl->part_rows) * size_t(cols) * 4);
@@ -188,14 +188,23 @@ bool any_overlap(const Span* out, int outs, const Span* in, int ins) {
 
 struct BackwardPlan {
   ProductPlan grad;
+  int grad_bn = kPackBlockN;
   GradientPlan gradients;
   size_t grad_bytes = 0;  // dG (and dU) in the workspace, then the parts
   size_t bytes() const { return 2 * grad_bytes + gradients.parts_bytes(); }
 };
 
+// Whether dG and dU take tiles of 64 columns of each: where 128 leave pairs idle
+// in their only round.
+bool grad_halves(int64_t tiles, int pairs) { return 2 * tiles <= pairs; }
+
 BackwardPlan plan_backward(int64_t M, int64_t K, int64_t N, int pairs) {
   BackwardPlan pl;
   pl.grad = plan_product(M, N, 2, k_slices(K));
+  if (grad_halves(pl.grad.tiles(), pairs)) {
+    pl.grad_bn = kPackBlockN / 2;
+    pl.grad.tiles_n = 2 * div_up(N, kPackBlockN);
+  }
   pl.gradients = plan_gradients(M, K, 4 * div_up(N, kTileM), K, N, 2, pairs);
   pl.grad_bytes = align256(size_t(M) * size_t(N) * 2);
   return pl;
@@ -260,8 +269,9 @@ swiglu_status_t swiglu_backward(const void* A, const void* Wpacked, const void* 
     fill_status(&p, d);
     p.in_units = static_cast<int>(pl.grad.units());
     p.dy = dY;
+    p.grad_bn = pl.grad_bn;
     if (!encode_2d(&p.in.tmap_a0, A, K, M, K * 2, kBlockK, kTileM, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !encode_packed_w(&p.in.tmap_b0, Wpacked, K, N, kPackBlockN) ||
+        !encode_packed_w(&p.in.tmap_b0, Wpacked, K, N, pl.grad_bn) ||
         !encode_2d(&p.in.tmap_o0, dG, N, M, N * 2, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B) ||
         !encode_2d(&p.in.tmap_o1, dU, N, M, N * 2, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
       return SWIGLU_ERR_CUDA;

@@ -33,9 +33,11 @@
 // it waited for (K-major descriptors on the same bytes: 365 us too).
 //
 // Roles as in the forward pair kernel: warp 0 TMA producer, warp 1 MMA issuer
-// (even CTA), warps 2-5 epilogue; 6 stages of 32 KB per CTA; two accumulators
-// of 256 columns, so a tile's epilogue runs under the next tile's MMAs; every
-// wait is bounded (ptx.cuh).
+// (even CTA), then 8 epilogue warps, two for each 32 rows (with 4, a short sum's
+// tiles waited for them: EPI_FIGURE); 6 stages of 32 KB per CTA; two
+// accumulators of 256 columns, so a tile's epilogue runs under the next tile's
+// MMAs; every wait is bounded (ptx.cuh). kGrad has tiles of 128 or 64 gate (and
+// up) columns.
 //
 // The input and the weight gradients do not depend on one another, so one
 // launch computes both: its units are the input gradient's tiles, then the
@@ -59,7 +61,9 @@ constexpr int kStageBytes = 2 * kOperandBytes;         // per CTA
 constexpr int kStages = 6;
 constexpr int kAccCols = 256;
 constexpr int kStgBytes = 32 * 128;                    // 32 rows x 128 B store staging
-constexpr int kNumStg = 8;                             // 2 per epilogue warp
+constexpr int kEpiWarps = 8;                           // 2 per tensor-memory lane quarter
+constexpr int kNumStg = kEpiWarps;                     // 1 per epilogue warp
+constexpr int kBackThreads = 64 + 32 * kEpiWarps;
 constexpr int kBarBytes = 256;
 constexpr size_t kSmem = 1024 + size_t(kStages) * kStageBytes + size_t(kNumStg) * kStgBytes + kBarBytes;
 static_assert(kStages % 2 == 0, "stages are used in pairs");
@@ -115,8 +119,9 @@ __device__ __forceinline__ void gate_grads(float g, float u, float dy, float& dg
   dg = dy * u * (s + gs * (1.0f - s));
 }
 
-template <bool kGrad>
-__global__ void __launch_bounds__(kThreads, 1)
+// kBN: gate (and up) columns of a kGrad tile; 128 otherwise.
+template <bool kGrad, int kBN>
+__global__ void __launch_bounds__(kBackThreads, 1)
     backward_pair_kernel(const __grid_constant__ BackwardParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -153,7 +158,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(tfull0 + 8u * b, 1);   // multicast MMA commit
-      mbar_init(tempty0 + 8u * b, 8);  // 4 epilogue warps x 2 CTAs (used on rank 0)
+      mbar_init(tempty0 + 8u * b, 2 * kEpiWarps);  // epilogue warps x 2 CTAs (used on rank 0)
     }
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
@@ -193,14 +198,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (skip_once) {
             skip_once = false;  // testing hook: both CTAs leave this stage unfilled
           } else {
-            if (leader) mbar_arrive_expect_tx(full0 + 8u * s, 2 * kStageBytes);
+            if (leader) mbar_arrive_expect_tx(full0 + 8u * s, 2 * (kOperandBytes + kBN * kBlockK * 2));
             const uint32_t fb = full0_lead + 8u * s;
             const uint32_t da = sA + s * kOperandBytes, db = sB + s * kOperandBytes;
             if constexpr (kGrad) {
-              // A rows [r0, +128); gate (rank 0) or up (rank 1) rows of tile (nb, i)
+              // A rows [r0, +128); kBN gate (rank 0) or up (rank 1) rows of tile (., i)
+              constexpr int kPer = kPackBlockN / kBN;
               tma_load_2d_pair(da, &g.tmap_a0, fb, i * kBlockK, r0);
-              tma_load_3d_pair(db, &g.tmap_b0, fb, 0, static_cast<int>(rank) * kPackBlockN,
-                               nb * g.slices + i);
+              tma_load_3d_pair(db, &g.tmap_b0, fb, 0,
+                               static_cast<int>(rank) * kPackBlockN + nb % kPer * kBN,
+                               nb / kPer * g.slices + i);
             } else if (!weight) {
               // stages 2 d, 2 d + 1: rows [128 h, +128) of packed tile row j (a gate/up
               // tile holds 128 gate then 128 up columns of the sum, a down tile 256);
@@ -255,7 +262,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const uint32_t d = tmem_base + buf * kAccCols;
         if constexpr (kGrad) {
-          constexpr uint32_t kIdesc = idesc_bf16_f32(2 * kTileM, kAccCols);
+          constexpr uint32_t kIdesc = idesc_bf16_f32(2 * kTileM, 2 * kBN);
           for (int i = begin; i < end; ++i) {
             if (!mbar_wait(full0 + 8u * s, ph, wc, kSiteMmaFull)) {
               ok = false;
@@ -320,10 +327,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------ epilogue (both CTAs)
     const int q = warp & 3;
     const int ew = warp - 2;
+    const int half = ew >> 2;  // this warp's half of the tile's columns
+    const uint32_t stg = sStg + ew * kStgBytes;
     const uint32_t lane_off = static_cast<uint32_t>(q * 32) << 16;
     int buf = 0;
     uint32_t acc_ph = 0;
-    int sbuf = 0;
     bool weight;
     for (int step = 0, unit; (unit = unit_at(p, pair, pairs, step, weight)) >= 0; ++step) {
       const BackwardProduct& pr = weight ? p.w : p.in;
@@ -331,18 +339,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       int mb, nb;
       tile_coords(tile, pr.tiles_m, pr.tiles_n, pr.group_m, mb, nb);
       const int row0 = mb * 2 * kTileM + static_cast<int>(rank) * kTileM + q * 32;
+      constexpr int kChunks = kBN / 64;  // kGrad: 32-column chunks of this warp
       uint4 dyv[4];
       const __nv_bfloat16* dy_row = nullptr;
-      if constexpr (kGrad) {
-        // this thread's row of dY, 32 columns ahead of the accumulator chunk in use
-        dy_row = static_cast<const __nv_bfloat16*>(p.dy) + static_cast<size_t>(row0 + lane) * pr.cols;
+      const int col0 = nb * kBN + half * (kBN / 2);
+      const auto load_dy = [&](int c) {  // this thread's row of dY, columns of chunk c
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int col = nb * kTileM + 8 * e;
+          const int col = col0 + 32 * c + 8 * e;
           dyv[e] = row0 + lane < pr.rows && col < pr.cols
                        ? __ldg(reinterpret_cast<const uint4*>(dy_row + col))
                        : make_uint4(0u, 0u, 0u, 0u);
         }
+      };
+      if constexpr (kGrad) {
+        dy_row = static_cast<const __nv_bfloat16*>(p.dy) + static_cast<size_t>(row0 + lane) * pr.cols;
+        load_dy(0);
       }
       int ok = 1;
       if (lane == 0) ok = mbar_wait(tfull0 + 8u * buf, acc_ph, wc, kSiteEpiTmemFull) ? 1 : 0;
@@ -352,31 +364,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t tacc = tmem_base + lane_off + buf * kAccCols;
       if constexpr (kGrad) {
 #pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < kChunks; ++c) {
           uint32_t g[32], u[32];
-          tmem_ld_x32(tacc + c * 32, g);
-          tmem_ld_x32(tacc + 128 + c * 32, u);
+          tmem_ld_x32(tacc + half * (kBN / 2) + c * 32, g);
+          tmem_ld_x32(tacc + kBN + half * (kBN / 2) + c * 32, u);
           uint4 dyc[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            dyc[e] = dyv[e];
-            const int col = nb * kTileM + (c + 1) * 32 + 8 * e;
-            if (c < 3)
-              dyv[e] = row0 + lane < pr.rows && col < pr.cols
-                           ? __ldg(reinterpret_cast<const uint4*>(dy_row + col))
-                           : make_uint4(0u, 0u, 0u, 0u);
-          }
+          for (int e = 0; e < 4; ++e) dyc[e] = dyv[e];
+          if (c + 1 < kChunks) load_dy(c + 1);
           tmem_wait_ld();
           reg_fence(g);
           reg_fence(u);
-          if (c == 3) {  // this CTA's half of the accumulator is read
+          if (c == kChunks - 1) {  // this warp's part of the accumulator is read
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(tempty0_lead + 8u * buf);
           }
-          if (lane == 0) bulk_wait_read<1>();
+          if (lane == 0) bulk_wait_read<0>();  // the previous store has read the staging
           __syncwarp();
-          const uint32_t stg = sStg + (ew * 2 + sbuf) * kStgBytes;  // dG block, then dU block
           const uint32_t row_addr = stg + lane * 64;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
@@ -400,44 +405,41 @@ __global__ void __launch_bounds__(kThreads, 1)
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            const int ncol = nb * kTileM + c * 32;
+            const int ncol = col0 + c * 32;
             if (ncol < pr.cols && row0 < pr.rows) {
               tma_store_2d(&pr.tmap_o0, stg, ncol, row0);
               tma_store_2d(&pr.tmap_o1, stg + 2048, ncol, row0);
             }
             bulk_commit();
           }
-          sbuf ^= 1;
         }
       } else {
-        // 8 chunks of 32 columns: fp32 parts (128-byte rows) to the workspace,
-        // or two chunks at a time as 64 bf16 columns to the output
+        // this warp's 128 columns, 64 at a time: fp32 parts (32 columns, 128-byte
+        // rows, a store) to the workspace, or 64 bf16 columns to the output
         const bool parts = pr.splits > 1;
 #pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < 2; ++c) {
           uint32_t x[32], y[32];
-          tmem_ld_x32(tacc + c * 64, x);
-          tmem_ld_x32(tacc + c * 64 + 32, y);
+          tmem_ld_x32(tacc + half * 128 + c * 64, x);
+          tmem_ld_x32(tacc + half * 128 + c * 64 + 32, y);
           tmem_wait_ld();
           reg_fence(x);
           reg_fence(y);
-          if (c == 3) {
+          if (c == 1) {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(tempty0_lead + 8u * buf);
           }
-          const int half = c >> 1;  // accumulator columns 0-127 or 128-255
-          const bool two = weight && pr.two;
+          const bool two = weight && pr.two;  // the halves are two outputs
           const CUtensorMap* mapo = two && half ? &pr.tmap_o1 : &pr.tmap_o0;
-          const int ncol = two ? nb * kTileM + (c & 1) * 64 : nb * 2 * kTileM + c * 64;
+          const int ncol = (two ? nb * kTileM : nb * 2 * kTileM + half * kTileM) + c * 64;
           if (parts) {
             // part-major rows: the store maps see splits * padded rows
             const int prow = part * pr.part_rows + row0;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              if (lane == 0) bulk_wait_read<1>();
+              if (lane == 0) bulk_wait_read<0>();
               __syncwarp();
-              const uint32_t stg = sStg + (ew * 2 + sbuf) * kStgBytes;
               const uint32_t row_addr = stg + lane * 128;
               const uint32_t* v = h ? y : x;
 #pragma unroll
@@ -451,12 +453,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                   tma_store_2d(mapo, stg, ncol + 32 * h, prow);
                 bulk_commit();
               }
-              sbuf ^= 1;
             }
           } else {
-            if (lane == 0) bulk_wait_read<1>();
+            if (lane == 0) bulk_wait_read<0>();
             __syncwarp();
-            const uint32_t stg = sStg + (ew * 2 + sbuf) * kStgBytes;
             const uint32_t row_addr = stg + lane * 128;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
@@ -473,7 +473,6 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (ncol < pr.cols && row0 < pr.rows) tma_store_2d(mapo, stg, ncol, row0);
               bulk_commit();
             }
-            sbuf ^= 1;
           }
         }
       }
@@ -529,7 +528,7 @@ cudaLaunchConfig_t backward_config(int grid, cudaStream_t stream, cudaLaunchAttr
                                    bool with_pdl) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(kBackThreads);
   cfg.dynamicSmemBytes = kSmem;
   cfg.stream = stream;
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -552,28 +551,34 @@ bool valid(const BackwardProduct& g, int units) {
 
 }  // namespace
 
+template <bool kGrad, int kBN>
+cudaError_t set_smem() {
+  return cudaFuncSetAttribute(backward_pair_kernel<kGrad, kBN>,
+                              cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem));
+}
+
 cudaError_t configure_backward_pair(int* max_pairs) {
-  cudaError_t e = cudaFuncSetAttribute(backward_pair_kernel<true>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmem));
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(backward_pair_kernel<false>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmem));
+  cudaError_t e = set_smem<true, 128>();
+  if (e == cudaSuccess) e = set_smem<true, 64>();
+  if (e == cudaSuccess) e = set_smem<false, 128>();
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg = backward_config(2, nullptr, attr, false);
-  return cudaOccupancyMaxActiveClusters(max_pairs, backward_pair_kernel<true>, &cfg);
+  return cudaOccupancyMaxActiveClusters(max_pairs, backward_pair_kernel<true, 128>, &cfg);
 }
 
 cudaError_t launch_backward_pair(const BackwardParams& p, bool grad, int pairs, cudaStream_t stream) {
   const int r = pairs > 0 ? p.in_units % pairs : 0;
   if (pairs < 1 || p.in_units + int64_t(p.w_units) < pairs || !valid(p.in, p.in_units) ||
       !valid(p.w, p.w_units) || p.early_rounds < 0 ||
-      int64_t(p.early_rounds) * (pairs - r) > p.w_units || (grad && (p.w_units || p.in.splits != 1)))
+      int64_t(p.early_rounds) * (pairs - r) > p.w_units || (grad && (p.w_units || p.in.splits != 1 || (p.grad_bn != 128 && p.grad_bn != 64))))
     return cudaErrorInvalidValue;
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg = backward_config(2 * pairs, stream, attr, pdl_enabled());
-  const cudaError_t e = grad ? cudaLaunchKernelEx(&cfg, backward_pair_kernel<true>, p)
-                             : cudaLaunchKernelEx(&cfg, backward_pair_kernel<false>, p);
+  const cudaError_t e =
+      !grad               ? cudaLaunchKernelEx(&cfg, backward_pair_kernel<false, 128>, p)
+      : p.grad_bn == 128 ? cudaLaunchKernelEx(&cfg, backward_pair_kernel<true, 128>, p)
+                          : cudaLaunchKernelEx(&cfg, backward_pair_kernel<true, 64>, p);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 

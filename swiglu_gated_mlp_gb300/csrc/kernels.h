@@ -185,6 +185,7 @@ struct BackwardParams {
   int in_units, w_units;
   int early_rounds;    // see unit_at()
   const void* dy;      // dG and dU: dY [rows, cols] bf16
+  int grad_bn;         // dG and dU: columns of each per tile, 128 or 64
   uint32_t* status;
   uint64_t timeout_ns;
   int inject_stall;
