@@ -35,7 +35,8 @@ int64_t padded_h(int64_t h);
 // Row tiles (of 256 rows) per group of the CTA-pair kernels' tile order.
 int64_t pair_group_rows(int64_t row_tiles);
 
-// Decode-kernel work split for `blocks` weight blocks on the current device.
+// Decode-kernel work split for `blocks` weight blocks on the current device, in
+// token groups of at most 128.
 swiglu_status_t decode_plan(int64_t M, int64_t blocks, int64_t kslices, int* mt, int* mgroups,
                             int* stages, int* splits);
 

@@ -41,15 +41,20 @@
 // With kLora (bf16) each token m also has a low-rank adapter a = index[m] of a
 // table shared by the batch (none where the index names none):
 //   Gate += V1 Lb[a][0]^T, Up += V2 Lb[a][1]^T   (down: Out += V Lb[a]^T),
-// V [M, rank] per product from lora_shrink.cu, fp32. The delta is 2 * M * rank
-// products a weight column, far less than the weight stream takes, and reads
-// only the adapters present. The warps that otherwise wait for the accumulators
-// compute it during the stream with fp32 FMAs: thread = weight column, one
-// token's adapter row at a time, so tokens never meet another's adapter and
-// nothing is padded or masked. Four more warps join them; the deltas wait in
-// tensor memory beside the accumulators (columns 2 mt to 4 mt) and the epilogue
-// adds the two. With K split, part k computes the deltas of every kparts-th
-// chunk of 8 tokens, once in all.
+// V [M, rank] per product from lora_shrink.cu. For every adapter present among
+// the CTA's tokens the pipeline gets one more slice: the weight half of the
+// stage takes Lb rows of the CTA's columns (zero past the rank), the token half
+// V with the rows of other adapters zero, and the MMAs add to the same
+// accumulators (rank / 16 of them each for gate and up, so gate and up of a rank
+// up to 32 share a slice, V1 and V2 side by side; above that they take one
+// each). Four more warps, thread = token, list the adapters and write V; the
+// adapter slices alternate with weight slices once the ring has filled, so that
+// they pass while the weight stream is waited for. With K split, adapters are
+// dealt to the parts. Deltas as fp32 FMAs, thread = weight column, were built
+// first: as fast at 16 tokens of rank 16, but 300 against LORA_FIGURE us at 128
+// tokens of rank 64 (7B shape), where each token re-read its adapter's rows.
+// A zero row times a non-finite Lb value is NaN: Lb must be finite, as the
+// shared weight must.
 #include "kernels.h"
 #include "ptx.cuh"
 
@@ -180,73 +185,12 @@ __device__ __noinline__ void cross_cluster_finish(const SmallMParams& p, int uni
   }
 }
 
-constexpr int kLoraThreads = kThreads + 128;   // kLora: 8 warps compute the adapters' deltas
-constexpr int kLoraChunk = 8;                  // tokens a warp has in registers
+constexpr int kLoraThreads = kThreads + 128;  // kLora: four warps write V
+constexpr int kLoraSmem = 2048;               // kLora: more barriers, the tokens' and the listed adapters
 
-// The adapters' deltas of this CTA's weight rows and its share of the tokens,
-// to tensor memory at `tdelta` (gate, or the low 128 columns) and `tdelta` + mt.
-template <bool kDown>
-__device__ __forceinline__ void lora_deltas(const SmallMParams& p, uint32_t tdelta, int mt, int m0,
-                                            int mcount, int nblk, int row, int set, int kpart,
-                                            int kparts) {
-  const int rank = p.lora_rank;
-  const int n = (kDown ? 2 : 1) * nblk * kPackBlockN + row;
-  const size_t per_adapter = static_cast<size_t>(kDown ? 1 : 2) * p.N * rank;
-  // gate row n and up row n of an adapter, or its output columns n and n + 128
-  const size_t second = static_cast<size_t>(kDown ? kPackBlockN : p.N) * rank;
-  const bool lo = n < p.N, hi = kDown ? n + kPackBlockN < p.N : lo;
-  const __nv_bfloat16* lb = static_cast<const __nv_bfloat16*>(p.lora_b) + static_cast<size_t>(n) * rank;
-  const int hr = kDown ? rank : 2 * rank;
-  for (int c = set * kparts + kpart; c * kLoraChunk < mcount; c += 2 * kparts) {
-    float g[kLoraChunk] = {}, u[kLoraChunk] = {};
-#pragma unroll
-    for (int h = 0; h < kLoraChunk; h += 4) {  // four tokens' loads at a time
-      const __nv_bfloat16* src[4];
-      const float* v[4];
-      bool has[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int m = c * kLoraChunk + h + j;
-        const int a = m < mcount ? __ldg(p.lora_index + m0 + m) : -1;
-        has[j] = a >= 0 && a < p.lora_count;
-        src[j] = lb + (has[j] ? a : 0) * per_adapter;
-        v[j] = p.lora_v + static_cast<size_t>(m0 + (m < mcount ? m : 0)) * hr;
-      }
-      for (int r = 0; r < rank; r += 8) {
-        uint4 x[4], y[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          x[j] = y[j] = make_uint4(0u, 0u, 0u, 0u);
-          if (has[j] && lo) x[j] = __ldg(reinterpret_cast<const uint4*>(src[j] + r));
-          if (has[j] && hi) y[j] = __ldg(reinterpret_cast<const uint4*>(src[j] + second + r));
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if (!has[j]) continue;  // the same in the whole warp
-          const uint32_t xw[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
-          const uint32_t yw[4] = {y[j].x, y[j].y, y[j].z, y[j].w};
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float4 vg = __ldcg(reinterpret_cast<const float4*>(v[j] + r) + e);
-            const float4 vu =
-                kDown ? vg : __ldcg(reinterpret_cast<const float4*>(v[j] + rank + r) + e);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const float g0 = i ? vg.z : vg.x, g1 = i ? vg.w : vg.y;
-              const float u0 = i ? vu.z : vu.x, u1 = i ? vu.w : vu.y;
-              const uint32_t xv = xw[2 * e + i], yv = yw[2 * e + i];
-              g[h + j] = fmaf(g0, __uint_as_float(xv << 16), g[h + j]);
-              g[h + j] = fmaf(g1, __uint_as_float(xv & 0xffff0000u), g[h + j]);
-              u[h + j] = fmaf(u0, __uint_as_float(yv << 16), u[h + j]);
-              u[h + j] = fmaf(u1, __uint_as_float(yv & 0xffff0000u), u[h + j]);
-            }
-          }
-        }
-      }
-    }
-    tmem_st_x8(tdelta + c * kLoraChunk, g);
-    tmem_st_x8(tdelta + mt + c * kLoraChunk, u);
-  }
+// Slices of one adapter: gate and up of a rank above 32 do not fit one row of V.
+__device__ __forceinline__ int lora_slices_per_adapter(bool down, int rank) {
+  return !down && rank > 32 ? 2 : 1;
 }
 
 template <bool kFp8, bool kDown, bool kMx, bool kLora>
@@ -273,13 +217,18 @@ __global__ void __launch_bounds__(kLora ? kLoraThreads : kThreads, kLora ? 2 : 1
   const uint32_t tfull_bar = bar0 + 16u * kMaxStages, drain_bar = tfull_bar + 8u;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_ptr + 8 * (2 * kMaxStages + 2));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  // adapters: V slot free[8] | V ready[8] | list ready; then the list's length and
+  // entries, and the tokens' adapters
+  uint8_t* lora_ptr = bar_ptr + kBarBytes;
+  const uint32_t vfree0 = bar0 + kBarBytes, vready0 = vfree0 + 8u * kMaxStages;
+  const uint32_t list_bar = vready0 + 8u * kMaxStages;
+  volatile int* list = reinterpret_cast<volatile int*>(lora_ptr + 8 * (2 * kMaxStages + 2));
+  int* ids = reinterpret_cast<int*>(lora_ptr + 1024);
 
   // accumulators: gate [0, mt), up [mt, 2 mt); then kSfTmemCols scale columns per stage
-  // (block-scaled), or the adapters' gate and up deltas
   const uint32_t sf_col = 2u * mt;
   uint32_t tmem_cols = 32;
-  while (tmem_cols < sf_col + (kMx ? uint32_t(kSfTmemCols) * stages : kLora ? 2u * mt : 0u))
-    tmem_cols <<= 1;
+  while (tmem_cols < sf_col + (kMx ? uint32_t(kSfTmemCols) * stages : 0u)) tmem_cols <<= 1;
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -324,6 +273,14 @@ __global__ void __launch_bounds__(kLora ? kLoraThreads : kThreads, kLora ? 2 : 1
     }
     mbar_init(tfull_bar, 1);
     mbar_init(drain_bar, 1);
+    if constexpr (kLora) {
+      prefetch_tmap(&p.tmap_lb);
+      for (int s = 0; s < stages; ++s) {
+        mbar_init(vfree0 + 8u * s, 1);
+        mbar_init(vready0 + 8u * s, 4);
+      }
+      mbar_init(list_bar, 4);
+    }
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -335,7 +292,18 @@ __global__ void __launch_bounds__(kLora ? kLoraThreads : kThreads, kLora ? 2 : 1
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
+  // With adapters two grids follow one another per call, so the next call's first
+  // one (which needs little room) may line up from the start: its launch and the
+  // one after it then do not add up at the end of this grid.
+  if constexpr (kLora) pdl_launch_dependents();
   pdl_wait();  // the set-up and L2 staging above overlap the previous grid; loads start here
+
+  // Adapter slices alternate with weight slices after the first `lead` of those;
+  // this K part has every kparts-th adapter of the list.
+  const int lead = min(stages, kb_end - kb_begin);
+  const int per_adapter = kLora ? lora_slices_per_adapter(kDown, p.lora_rank) : 0;
+  const auto adapter_slices = [&] { return (max(list[0] - kpart, 0) + kparts - 1) / kparts * per_adapter; };
+  const auto adapter_at = [&](int i) { return list[1 + kpart + i / per_adapter * kparts]; };
 
   if (warp == 0) {
     // ------------------------------------------------ TMA producer -----
@@ -346,9 +314,45 @@ __global__ void __launch_bounds__(kLora ? kLoraThreads : kThreads, kLora ? 2 : 1
       int s = 0;
       uint32_t ph = 0;
       uint32_t filled = 0, fill_ph = 0;
-      bool skip_once = p.inject_stall != 0;
+      bool skip_once = p.inject_stall != 0, ok = true;
+      int extra = 0, done = 0;  // adapter slices, and how many are loaded
+      // Lb rows of the next adapter slice to the stage's weight half
+      const auto load_adapter = [&] {
+        if (!mbar_wait(empty0 + 8u * s, ph ^ 1u, wc, kSiteProducerEmpty)) return false;
+        mbar_arrive(vfree0 + 8u * s);  // the stage's token half is free for V
+        const uint32_t fb = full0 + 8u * s, sw = s0 + s * stage_bytes;
+        const int a = adapter_at(done), h = done % per_adapter;
+        const int n0 = (kDown ? 2 : 1) * nblk * kPackBlockN;
+        mbar_arrive_expect_tx(fb, per_adapter == 1 ? kWStageBytes : kWStageBytes / 2);
+        if (kDown) {  // output columns n0 .. + 127 and n0 + 128 .. + 255
+          tma_load_3d(sw, &p.tmap_lb, fb, 0, n0, a);
+          tma_load_3d(sw + kWStageBytes / 2, &p.tmap_lb, fb, 0, n0 + kPackBlockN, a);
+        } else {      // gate rows, up rows, or both
+          tma_load_3d(sw, &p.tmap_lb, fb, 0, n0, 2 * a + h);
+          if (per_adapter == 1) tma_load_3d(sw + kWStageBytes / 2, &p.tmap_lb, fb, 0, n0, 2 * a + 1);
+        }
+        filled |= 1u << s;
+        fill_ph = (fill_ph & ~(1u << s)) | (ph << s);
+        if (++s == stages) {
+          s = 0;
+          ph ^= 1u;
+        }
+        ++done;
+        return true;
+      };
       for (int kb = kb_begin; kb < kb_end; ++kb) {
-        if (!mbar_wait(empty0 + 8u * s, ph ^ 1u, wc, kSiteProducerEmpty)) break;
+        if constexpr (kLora) {
+          if (kb - kb_begin == lead) {
+            ok = mbar_wait(list_bar, 0, wc, kSiteLora);
+            extra = ok ? adapter_slices() : 0;
+          }
+          if (ok && kb - kb_begin >= lead && done < extra) ok = load_adapter();
+          if (!ok) break;
+        }
+        if (!mbar_wait(empty0 + 8u * s, ph ^ 1u, wc, kSiteProducerEmpty)) {
+          ok = false;
+          break;
+        }
         if (skip_once) {
           skip_once = false;  // testing hook: leave this stage unfilled
         } else {
@@ -373,6 +377,13 @@ __global__ void __launch_bounds__(kLora ? kLoraThreads : kThreads, kLora ? 2 : 1
           ph ^= 1u;
         }
       }
+      if constexpr (kLora) {
+        if (ok && kb_end - kb_begin == lead) {
+          ok = mbar_wait(list_bar, 0, wc, kSiteLora);
+          extra = ok ? adapter_slices() : 0;
+        }
+        while (ok && done < extra) ok = load_adapter();
+      }
       pdl_launch_dependents();
       for (int i = 0; i < stages; ++i)
         if (filled & (1u << i)) mbar_wait_drain(full0 + 8u * i, (fill_ph >> i) & 1u, wc);
@@ -387,7 +398,44 @@ __global__ void __launch_bounds__(kLora ? kLoraThreads : kThreads, kLora ? 2 : 1
       int s = 0;
       uint32_t ph = 0;
       bool ok = true;
+      int extra = 0, done = 0;  // adapter slices, and how many are issued
+      uint32_t vph = 0;         // phase of each stage's V barrier
+      const auto mma_adapter = [&] {
+        if (!mbar_wait(full0 + 8u * s, ph, wc, kSiteMmaFull) ||
+            !mbar_wait(vready0 + 8u * s, (vph >> s) & 1u, wc, kSiteLora))
+          return false;
+        vph ^= 1u << s;
+        tc_fence_after();
+        const uint32_t sw = s0 + s * stage_bytes;
+        const uint64_t lo = smem_desc_sw128(sw), hi = smem_desc_sw128(sw + kWStageBytes / 2);
+        const uint64_t v = smem_desc_sw128(sw + kWStageBytes);
+        const int ksteps = (p.lora_rank + 15) / 16, h = done % per_adapter;
+        for (int k = 0; k < ksteps; ++k) {
+          // down: both halves from one V; gate/up: V1 and V2 side by side, or one of them
+          if (per_adapter == 1) {
+            mma_bf16(d_gate, lo + 2u * k, v + 2u * k, idesc, 1u);
+            mma_bf16(d_up, hi + 2u * k, v + 2u * (kDown ? k : ksteps + k), idesc, 1u);
+          } else {
+            mma_bf16(h ? d_up : d_gate, lo + 2u * k, v + 2u * k, idesc, 1u);
+          }
+        }
+        mma_commit(empty0 + 8u * s);
+        if (++s == stages) {
+          s = 0;
+          ph ^= 1u;
+        }
+        ++done;
+        return true;
+      };
       for (int kb = kb_begin; kb < kb_end; ++kb) {
+        if constexpr (kLora) {
+          if (kb - kb_begin == lead) {
+            ok = mbar_wait(list_bar, 0, wc, kSiteLora);
+            extra = ok ? adapter_slices() : 0;
+          }
+          if (ok && kb - kb_begin >= lead && done < extra) ok = mma_adapter();
+          if (!ok) break;
+        }
         if (!mbar_wait(full0 + 8u * s, ph, wc, kSiteMmaFull)) {
           ok = false;
           break;
@@ -426,9 +474,92 @@ __global__ void __launch_bounds__(kLora ? kLoraThreads : kThreads, kLora ? 2 : 1
           ph ^= 1u;
         }
       }
+      if constexpr (kLora) {
+        if (ok && kb_end - kb_begin == lead) {
+          ok = mbar_wait(list_bar, 0, wc, kSiteLora);
+          extra = ok ? adapter_slices() : 0;
+        }
+        while (ok && done < extra) ok = mma_adapter();
+      }
       if (ok) mma_commit(tfull_bar);
       mma_commit(drain_bar);
       mbar_wait_drain(drain_bar, 0, wc);
+    }
+    __syncwarp();
+  } else if (kLora && warp >= 6) {
+    // ------------------------------------------------ adapters: list and V
+    const int row = threadIdx.x - kThreads;  // this thread's token of the group
+    const int own = row < mcount ? __ldg(p.lora_index + m0 + row) : -1;
+    const bool has = own >= 0 && own < p.lora_count;
+    ids[row] = has ? own : -1;
+    // the token's V, zero past the rank
+    constexpr int kChunks = kLoraMaxRank / 8;
+    constexpr int kHalves = kDown ? 1 : 2;
+    const int chunks = p.lora_rank / 8, ksteps = (p.lora_rank + 15) / 16;
+    const uint4* v = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.lora_v) +
+                                                    (static_cast<size_t>(m0) + row) * p.lora_rank * kHalves);
+    uint4 x[kHalves][kChunks];
+#pragma unroll
+    for (int h = 0; h < kHalves; ++h)
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c)
+        x[h][c] = has && c < chunks ? __ldg(v + h * chunks + c) : make_uint4(0u, 0u, 0u, 0u);
+    named_barrier(1, 128);
+    // the adapters present, in the order of their first token
+    bool first = has;
+    for (int t = 0; t < row; t += 4) {
+      const int4 w = *reinterpret_cast<const int4*>(ids + t);
+      const int y[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (t + e < row && y[e] == own) first = false;
+    }
+    const uint32_t votes = __ballot_sync(0xffffffffu, first);
+    int* counts = ids + 128;
+    if (lane == 0) counts[warp - 6] = __popc(votes);
+    named_barrier(1, 128);
+    int at = __popc(votes & ((1u << lane) - 1u)), present = 0;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      if (w < warp - 6) at += counts[w];
+      present += counts[w];
+    }
+    if (first) list[1 + at] = own;
+    if (row == 0) list[0] = present;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(list_bar);
+    named_barrier(1, 128);  // the list is complete
+    // V of each adapter slice, in the swizzled rows a TMA load would write
+    const int extra = adapter_slices();
+    const int rest = kb_end - kb_begin - lead;  // weight slices the adapter slices alternate with
+    uint32_t vph = 0;
+    for (int i = 0; i < extra; ++i) {
+      const int s = (i <= rest ? lead + 2 * i : kb_end - kb_begin + i) % stages;
+      int go = 1;
+      if (lane == 0) go = mbar_wait(vfree0 + 8u * s, (vph >> s) & 1u, wc, kSiteLora) ? 1 : 0;
+      go = __shfl_sync(0xffffffffu, go, 0);
+      if (!go) break;
+      vph ^= 1u << s;
+      if (row < mt) {
+        const bool keep = has && adapter_at(i) == own;
+        const int h = i % per_adapter;
+        const uint32_t dst = s0 + s * stage_bytes + kWStageBytes + row * 128;
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+          if (c >= 2 * ksteps) break;
+          uint4 w = make_uint4(0u, 0u, 0u, 0u);
+          if (keep) w = kHalves == 2 && h ? x[kHalves - 1][c] : x[0][c];
+          st_shared_v4(dst + ((c ^ (row & 7)) << 4), w.x, w.y, w.z, w.w);
+          if (!kDown && per_adapter == 1) {  // V2 beside V1
+            w = make_uint4(0u, 0u, 0u, 0u);
+            if (keep) w = x[kHalves - 1][c];
+            st_shared_v4(dst + (((2 * ksteps + c) ^ (row & 7)) << 4), w.x, w.y, w.z, w.w);
+          }
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(vready0 + 8u * s);
     }
     __syncwarp();
   } else {
@@ -436,37 +567,9 @@ __global__ void __launch_bounds__(kLora ? kLoraThreads : kThreads, kLora ? 2 : 1
     const int q = warp & 3;
     const uint32_t lane_off = static_cast<uint32_t>(q * 32) << 16;
     const int n = nblk * kPackBlockN + q * 32 + lane;  // this thread's output column
-    if constexpr (kLora) {
-      lora_deltas<kDown>(p, tmem_base + lane_off + 2u * mt, mt, m0, mcount, nblk, q * 32 + lane,
-                         warp >= 6 ? 1 : 0, kpart, kparts);
-      tmem_wait_st();
-      tc_fence_before();
-      named_barrier(1, kLoraThreads - 64);
-      tc_fence_after();
-    }
-    int ok = !kLora || warp < 6;  // the other warps' work ends here
-    if (ok && lane == 0) ok = mbar_wait(tfull_bar, 0, wc, kSiteEpiTmemFull) ? 1 : 0;
+    int ok = 1;
+    if (lane == 0) ok = mbar_wait(tfull_bar, 0, wc, kSiteEpiTmemFull) ? 1 : 0;
     ok = __shfl_sync(0xffffffffu, ok, 0);
-    // accumulators of 16 tokens, with the adapters' deltas this CTA computed
-    const auto add_deltas = [&](int mc, uint32_t (&g)[16], uint32_t (&u)[16]) {
-      if constexpr (kLora) {
-        uint32_t dg[16], du[16];
-        tmem_ld_x16(tmem_base + lane_off + 2 * mt + mc * 16, dg);
-        tmem_ld_x16(tmem_base + lane_off + 3 * mt + mc * 16, du);
-        tmem_wait_ld();
-        reg_fence(dg);
-        reg_fence(du);
-#pragma unroll
-        for (int h = 0; h < 16 / kLoraChunk; ++h) {
-          if ((mc * (16 / kLoraChunk) + h) % kparts != kpart) continue;  // another K part's
-#pragma unroll
-          for (int j = h * kLoraChunk; j < (h + 1) * kLoraChunk; ++j) {
-            g[j] = __float_as_uint(__uint_as_float(g[j]) + __uint_as_float(dg[j]));
-            u[j] = __float_as_uint(__uint_as_float(u[j]) + __uint_as_float(du[j]));
-          }
-        }
-      }
-    };
     if (ok && kparts > 1) {
       // K part only: fp32 partials to this CTA's shared memory (the ring is idle
       // now), as P[c][r] for accumulator column c (gate 0..mt-1, up mt..2mt-1)
@@ -482,7 +585,6 @@ __global__ void __launch_bounds__(kLora ? kLoraThreads : kThreads, kLora ? 2 : 1
         tmem_wait_ld();
         reg_fence(g);
         reg_fence(u);
-        add_deltas(mc, g, u);
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
           part_buf[(mc * 16 + j) * kPackBlockN + r] = __uint_as_float(g[j]);
@@ -503,7 +605,6 @@ __global__ void __launch_bounds__(kLora ? kLoraThreads : kThreads, kLora ? 2 : 1
         tmem_wait_ld();
         reg_fence(g);
         reg_fence(u);
-        add_deltas(mc, g, u);
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
           const int m = mc * 16 + j;
@@ -529,7 +630,6 @@ __global__ void __launch_bounds__(kLora ? kLoraThreads : kThreads, kLora ? 2 : 1
         tmem_wait_ld();
         reg_fence(g);
         reg_fence(u);
-        add_deltas(mc, g, u);
         if (n < p.N) {
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
@@ -702,9 +802,9 @@ cudaError_t launch_small_m(const SmallMParams& p, cudaStream_t stream) {
   if (p.mx && (!p.fp8 || p.down || (p.mgroups > 1) || p.mt > 128 ||
                2 * p.mt + kSfTmemCols * p.stages > 512))
     return cudaErrorInvalidValue;
-  // adapters: deltas beside the accumulators, one cluster per unit
+  // adapters: a thread for every token of a group, one cluster per unit
   if (p.lora && (p.fp8 || gsplits > 1 || p.mt > 128 || p.lora_rank < 8 || (p.lora_rank % 8) != 0 ||
-                 !p.lora_v || !p.lora_index || !p.lora_b))
+                 p.lora_rank > kLoraMaxRank || !p.lora_v || !p.lora_index))
     return cudaErrorInvalidValue;
   const int extra = p.mx ? kSfStageBytes : 0;
   SmallMParams q = p;
@@ -712,7 +812,8 @@ cudaError_t launch_small_m(const SmallMParams& p, cudaStream_t stream) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(p.grid);
   cfg.blockDim = dim3(p.lora ? kLoraThreads : kThreads);
-  cfg.dynamicSmemBytes = small_m_smem_bytes(p.mt, p.stages, extra);
+  cfg.dynamicSmemBytes = small_m_smem_bytes(p.mt, p.stages, extra) + (p.lora ? kLoraSmem : 0);
+  if (cfg.dynamicSmemBytes > kSmemLimit) return cudaErrorInvalidValue;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

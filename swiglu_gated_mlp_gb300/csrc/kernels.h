@@ -86,13 +86,13 @@ struct SmallMParams {
   int gsplits;
   float* ws;
   uint32_t* counters;
-  // adapters (bf16): V [M, rank or 2 rank] fp32, each token's adapter, Lb as
-  // [count, 2, N, rank] (gate/up) or [count, N, rank] (down)
+  // adapters (bf16): V [M, rank or 2 rank] bf16, each token's adapter, and
+  // Lb {rank, N, adapters x (1 or 2)} box {64, 128, 1}
+  CUtensorMap tmap_lb;
   int lora;
   int lora_rank, lora_count;
-  const float* lora_v;
+  const void* lora_v;
   const int* lora_index;
-  const void* lora_b;
 };
 
 // V = scale_a * x La[a]^T of each token's adapter a = index[token]
@@ -105,7 +105,7 @@ struct LoraShrinkParams {
   const int* index;     // [M]
   const float* scale;   // [count]
   int count, M, K, hr;
-  void* v;              // [M, hr]: fp32 (few tokens) or bf16 (many tokens)
+  void* v;              // [M, hr] bf16
   // many tokens (tiles > 0): 128-token tiles, K over clusters of `splits` CTAs
   int* lists;           // per 256 tokens: count, then the adapters present
   int tiles, splits, slices;

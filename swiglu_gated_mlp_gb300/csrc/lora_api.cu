@@ -15,9 +15,28 @@ namespace {
 using namespace swg;
 using namespace swg::api;
 
-// Tokens up to which the decode kernel runs: its accumulators and deltas for
-// 128 tokens fill tensor memory.
-constexpr int64_t kDecodeTokens = 128;
+// Tokens of a decode CTA: one of its threads writes each token's V.
+constexpr int64_t kGroupTokens = 128;
+
+// Whether the decode kernel runs, with its work split. It takes one group of
+// tokens, and more groups where 256-row pair tiles would leave the SMs idle or
+// take a nearly empty round. A pair's slice takes about 0.3 us, a decode CTA's
+// of 128 tokens 0.6 us (each group streams the weight), a K split 3 us. Measured,
+// decode against pairs: 333 tokens K 1416 N 5000 32.7 / 39.5 us; down 333 tokens
+// N 4864 H 896 (K over 8 CTAs) 28.6 / 42.8; 400 tokens K 2048 N 4000 39.6 / 31.8;
+// down 700 tokens N 18944 H 3584 286 / 124.
+swiglu_status_t plan_decode(int64_t M, int64_t blocks, int64_t slices, const DeviceView& d,
+                            SmallMParams* p, bool* decode) {
+  const int64_t groups = (M + kGroupTokens - 1) / kGroupTokens;
+  *decode = groups == 1;
+  if (groups > 1 && blocks * groups > d.sm_count) return SWIGLU_OK;
+  const swiglu_status_t st = decode_plan(M, blocks, slices, &p->mt, &p->mgroups, &p->stages, &p->splits);
+  if (st != SWIGLU_OK || *decode || d.max_pairs < 1) return st;
+  const int64_t tiles = (M + 2 * kTileM - 1) / (2 * kTileM) * blocks;
+  const int64_t rounds = (tiles + d.max_pairs - 1) / d.max_pairs;
+  *decode = 2 * slices / p->splits + (p->splits > 1 ? 10 : 0) <= rounds * slices;
+  return SWIGLU_OK;
+}
 
 struct LoraState {
   std::atomic<bool> ready{false};
@@ -48,13 +67,11 @@ size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // V, then (many tokens) the lists of adapters present.
-size_t v_bytes(int64_t M, int64_t hr) {
-  return align256(size_t(M) * size_t(hr) * (M <= kDecodeTokens ? 4 : 2));
-}
+size_t v_bytes(int64_t M, int64_t hr) { return align256(size_t(M) * size_t(hr) * 2); }
 
 size_t workspace_bytes_for(int64_t M, int64_t hr) {
   size_t n = v_bytes(M, hr);
-  if (M > kDecodeTokens) n += size_t(div_up(M, 2 * kTileM)) * kLoraListInts * sizeof(int);
+  if (M > kGroupTokens) n += size_t(div_up(M, 2 * kTileM)) * kLoraListInts * sizeof(int);
   return n;
 }
 
@@ -122,9 +139,14 @@ swiglu_status_t run_call(const Call& c, cudaStream_t stream) {
   DeviceView d;
   swiglu_status_t st = lora_device(&d);
   if (st != SWIGLU_OK) return st;
-  const bool down = c.halves == 1, decode = c.M <= kDecodeTokens;
+  const bool down = c.halves == 1;
+  const int64_t blocks = down ? padded_h(c.outs) / 256 : padded_n(c.outs) / kPackBlockN;
   const int hr = static_cast<int>(c.rank * c.halves);
   const int64_t slices = k_slices(c.in);
+  SmallMParams dp{};
+  bool decode = false;
+  st = plan_decode(c.M, blocks, slices, d, &dp, &decode);
+  if (st != SWIGLU_OK) return st;
   int* lists = reinterpret_cast<int*>(static_cast<uint8_t*>(c.ws) + v_bytes(c.M, hr));
 
   LoraShrinkParams sp{};
@@ -140,12 +162,34 @@ swiglu_status_t run_call(const Call& c, cudaStream_t stream) {
   sp.status = d.status;
   sp.timeout_ns = d.timeout_ns;
   sp.inject_stall = d.inject_stall;
+  if (c.M > kGroupTokens) {
+    sp.lists = lists;
+    sp.tiles = static_cast<int>(div_up(c.M, kTileM));
+    sp.slices = static_cast<int>(slices);
+    sp.rb = (hr + 15) / 16 * 16;
+    sp.per_pass = 256 / sp.rb;
+    sp.splits = 1;
+    for (int s : {8, 4, 2})  // as many K parts as keep every CTA resident at once
+      if (s <= slices && int64_t(sp.tiles) * s <= d.sm_count) {
+        sp.splits = s;
+        break;
+      }
+    if (!encode_2d(&sp.tmap_x, c.x, c.in, c.M, c.in * 2, kBlockK, kTileM, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !encode_2d(&sp.tmap_la, c.la, c.in, uint64_t(c.count) * hr, c.in * 2, kBlockK, sp.rb,
+                   CU_TENSOR_MAP_SWIZZLE_128B))
+      return SWIGLU_ERR_CUDA;
+  }
+  // Lb rows of one half of one adapter: the decode kernel takes 128 of them at a
+  // time, each CTA of a pair 64 gate or up rows or 128 output columns
+  const uint64_t lb_dims[3] = {uint64_t(c.rank), uint64_t(c.outs), uint64_t(c.count * c.halves)};
+  const uint64_t lb_strides[2] = {uint64_t(c.rank) * 2, uint64_t(c.rank) * uint64_t(c.outs) * 2};
+  const uint32_t lb_box[3] = {kBlockK, decode || down ? 128u : 64u, 1u};
+  CUtensorMap tmap_lb;
+  if (!encode_3d(&tmap_lb, c.lb, lb_dims, lb_strides, lb_box, CU_TENSOR_MAP_SWIZZLE_128B))
+    return SWIGLU_ERR_CUDA;
   cudaError_t e;
   if (decode) {
-    SmallMParams p{};
-    const int64_t blocks = down ? padded_h(c.outs) / 256 : padded_n(c.outs) / kPackBlockN;
-    st = decode_plan(c.M, blocks, slices, &p.mt, &p.mgroups, &p.stages, &p.splits);
-    if (st != SWIGLU_OK) return st;
+    SmallMParams& p = dp;
     if (!encode_2d(&p.tmap_x, c.x, c.in, c.M, c.in * 2, kBlockK, p.mt, CU_TENSOR_MAP_SWIZZLE_128B) ||
         !(down ? encode_packed_down(&p.tmap_w, c.wp, c.in, c.outs, 256)
                : encode_packed_w(&p.tmap_w, c.wp, c.in, c.outs, 2 * kPackBlockN)))
@@ -160,9 +204,9 @@ swiglu_status_t run_call(const Call& c, cudaStream_t stream) {
     p.lora = 1;
     p.lora_rank = static_cast<int>(c.rank);
     p.lora_count = static_cast<int>(c.count);
-    p.lora_v = static_cast<const float*>(c.ws);
+    p.lora_v = c.ws;
     p.lora_index = c.index;
-    p.lora_b = c.lb;
+    p.tmap_lb = tmap_lb;
     p.status = d.status;
     p.timeout_ns = d.timeout_ns;
     p.inject_stall = d.inject_stall;
@@ -171,30 +215,13 @@ swiglu_status_t run_call(const Call& c, cudaStream_t stream) {
   } else {
     LargeMParams p{};
     const int64_t tiles_m = div_up(c.M, 2 * kTileM);
-    const int64_t tiles_n = down ? padded_h(c.outs) / 256 : padded_n(c.outs) / kPackBlockN;
+    const int64_t tiles_n = blocks;
     if (d.max_pairs < 1 || tiles_m * tiles_n > 2147483647) return SWIGLU_ERR_UNSUPPORTED;
-    sp.lists = lists;
-    sp.tiles = static_cast<int>(div_up(c.M, kTileM));
-    sp.slices = static_cast<int>(slices);
-    sp.rb = (hr + 15) / 16 * 16;
-    sp.per_pass = 256 / sp.rb;
-    sp.splits = 1;
-    for (int s : {8, 4, 2})  // as many K parts as keep every CTA resident at once
-      if (s <= slices && int64_t(sp.tiles) * s <= d.sm_count) {
-        sp.splits = s;
-        break;
-      }
-    const uint64_t lb_dims[3] = {uint64_t(c.rank), uint64_t(c.outs), uint64_t(c.count * c.halves)};
-    const uint64_t lb_strides[2] = {uint64_t(c.rank) * 2, uint64_t(c.rank) * uint64_t(c.outs) * 2};
-    const uint32_t lb_box[3] = {kBlockK, down ? 128u : 64u, 1u};
-    if (!encode_2d(&sp.tmap_x, c.x, c.in, c.M, c.in * 2, kBlockK, kTileM, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !encode_2d(&sp.tmap_la, c.la, c.in, uint64_t(c.count) * hr, c.in * 2, kBlockK, sp.rb,
-                   CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !(down ? encode_packed_down(&p.tmap_w, c.wp, c.in, c.outs, kPackBlockN)
+    if (!(down ? encode_packed_down(&p.tmap_w, c.wp, c.in, c.outs, kPackBlockN)
                : encode_packed_w(&p.tmap_w, c.wp, c.in, c.outs, kPackBlockN)) ||
-        !encode_2d(&p.tmap_y, c.out, c.outs, c.M, c.outs * 2, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B) ||
-        !encode_3d(&p.tmap_lb, c.lb, lb_dims, lb_strides, lb_box, CU_TENSOR_MAP_SWIZZLE_128B))
+        !encode_2d(&p.tmap_y, c.out, c.outs, c.M, c.outs * 2, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
       return SWIGLU_ERR_CUDA;
+    p.tmap_lb = tmap_lb;
     p.tmap_a = sp.tmap_x;
     p.M = static_cast<int>(c.M);
     p.K = static_cast<int>(c.in);

@@ -7,10 +7,13 @@
 // token the product is hr x K, far below the projection's, so what counts is
 // that it reads x once and each adapter present once, and ends early.
 //
-// Few tokens (the decode kernel's range): lora_shrink_dot_kernel, plain dot
-// products in fp32. One CTA takes a token and 4 rows; its 8 warps split K, so
-// every load of a CTA is in flight at once. V stays in fp32. The decode kernel
-// does its set-up and stages its first weight tiles in L2 while this one runs.
+// V is rounded to bf16, the operand type of the expanding product: the delta it
+// enters is a fraction of the projection, which is itself rounded to bf16.
+//
+// Few tokens: lora_shrink_dot_kernel, plain dot products in fp32. One CTA takes
+// a token and 4 rows; its 8 warps split K, so every load of a CTA is in flight
+// at once. The decode kernel does its set-up and stages its first weight tiles
+// in L2 while this one runs.
 //
 // Many tokens: lora_shrink_tile_kernel, tcgen05 with 128 tokens as the MMA's
 // M side and the rows of the adapters present in the tile as its N side. The
@@ -18,9 +21,10 @@
 // has one), and each token keeps its own adapter's columns: a value of another
 // adapter, finite or not, never reaches it. K is split over a cluster of up to
 // 8 CTAs, whose fp32 sums are added in order through distributed shared memory.
-// V is rounded to bf16, the operand type of the expanding product: the delta it
-// enters is a fraction of the projection, which is itself rounded to bf16. The
-// kernel also lists, per 256 tokens (a CTA pair's tile), the adapters present.
+// A stage holds 64 of K for the tokens and for as many adapters as the tile has
+// (up to per_pass), and the ring as many stages as fit, so that with one adapter
+// most of what is in flight are tokens. The kernel also lists, per 256 tokens
+// (a CTA pair's tile), the adapters present.
 #include "kernels.h"
 #include "ptx.cuh"
 
@@ -79,7 +83,8 @@ __global__ void __launch_bounds__(kDotThreads)
     float v = 0.0f;
 #pragma unroll
     for (int w = 0; w < kDotThreads / 32; ++w) v += sums[w][threadIdx.x];
-    static_cast<float*>(p.v)[static_cast<size_t>(m) * p.hr + r0 + threadIdx.x] = v * p.scale[a];
+    static_cast<__nv_bfloat16*>(p.v)[static_cast<size_t>(m) * p.hr + r0 + threadIdx.x] =
+        __float2bfloat16_rn(v * p.scale[a]);
   }
 }
 
@@ -88,14 +93,16 @@ __global__ void __launch_bounds__(kDotThreads)
 constexpr int kTileThreads = 256;
 constexpr int kTileCols = 256;                                     // accumulator columns
 constexpr int kXBytes = 128 * kBlockK * 2;                         // 16 KB of tokens
-constexpr int kTileStage = kXBytes + kTileCols * kBlockK * 2;      // + up to 256 adapter rows
-constexpr int kTileStages = 3;
+constexpr int kTileStages = 8;                                     // at most
 constexpr int kPartPad = 4;                                        // floats, against bank conflicts
-constexpr int kTileBar = 128;
-constexpr size_t tile_smem(int rb) {
-  return 1024 + size_t(kTileStages) * kTileStage + size_t(128) * (rb + kPartPad) * 4 + kTileBar;
+constexpr int kTileBar = 256;
+constexpr size_t kTileSmem = 229376;  // with 1.6 KB of static shared memory
+// What the ring may take: the rest holds the sums of `rb` columns.
+__host__ __device__ constexpr int tile_ring(int rb) {
+  return static_cast<int>((kTileSmem - 1024 - kTileBar - size_t(128) * (rb + kPartPad) * 4) / 1024 * 1024);
 }
-static_assert(tile_smem(2 * kLoraMaxRank) <= 232448, "shared memory budget");
+static_assert(tile_ring(2 * kLoraMaxRank) >= 3 * (kXBytes + kTileCols * kBlockK * 2), "three stages");
+static_assert(8 * (2 * kTileStages + 3) + 8 <= kTileBar, "barrier slots");
 
 __global__ void __launch_bounds__(kTileThreads, 1)
     lora_shrink_tile_kernel(const __grid_constant__ LoraShrinkParams p) {
@@ -108,10 +115,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const int rb = p.rb;                           // accumulator columns of one adapter
   const int part_stride = rb + kPartPad;
   const uint32_t s0 = smem_addr(smem);
-  float* part = reinterpret_cast<float*>(smem + kTileStages * kTileStage);
+  float* part = reinterpret_cast<float*>(smem + tile_ring(rb));
   uint8_t* bar_ptr = reinterpret_cast<uint8_t*>(part) + size_t(128) * part_stride * 4;
   const uint32_t bar0 = smem_addr(bar_ptr);
-  // barrier slots: full[3] | empty[3] | tmem_full | tmem_empty | drain
+  // barrier slots: full[8] | empty[8] | tmem_full | tmem_empty | drain
   const uint32_t full0 = bar0, empty0 = bar0 + 8u * kTileStages;
   const uint32_t tfull = bar0 + 16u * kTileStages, tempty = tfull + 8u, drain_bar = tfull + 16u;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_ptr + 8 * (2 * kTileStages + 3));
@@ -196,6 +203,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const int per_pass = p.per_pass;  // adapters side by side in the accumulator
   const int passes = (n128 + per_pass - 1) / per_pass;
   const uint32_t la_bytes = static_cast<uint32_t>(rb) * 128u;
+  const uint32_t stage_bytes = kXBytes + max(min(per_pass, n128), 1) * la_bytes;
+  const int stages = min(static_cast<int>(tile_ring(rb) / stage_bytes), kTileStages);
   if (warp == 0) {
     if (lane == 0) {
       int s = 0;
@@ -211,7 +220,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           if (skip_once) {
             skip_once = false;  // testing hook: leave this stage unfilled
           } else {
-            const uint32_t fb = full0 + 8u * s, dst = s0 + s * kTileStage;
+            const uint32_t fb = full0 + 8u * s, dst = s0 + s * stage_bytes;
             mbar_arrive_expect_tx(fb, kXBytes + gn * la_bytes);
             tma_load_2d(dst, &p.tmap_x, fb, i * kBlockK, m0);
             for (int g = 0; g < gn; ++g)
@@ -220,13 +229,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             filled |= 1u << s;
             fill_ph = (fill_ph & ~(1u << s)) | (ph << s);
           }
-          if (++s == kTileStages) {
+          if (++s == stages) {
             s = 0;
             ph ^= 1u;
           }
         }
       }
-      for (int i = 0; i < kTileStages; ++i)
+      for (int i = 0; i < stages; ++i)
         if (filled & (1u << i)) mbar_wait_drain(full0 + 8u * i, (fill_ph >> i) & 1u, wc);
     }
     __syncwarp();
@@ -246,7 +255,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             break;
           }
           tc_fence_after();
-          const uint32_t src = s0 + s * kTileStage;
+          const uint32_t src = s0 + s * stage_bytes;
           const uint64_t xdesc = smem_desc_sw128(src);
           for (int g = 0; g < gn; ++g) {
             const uint64_t ldesc = smem_desc_sw128(src + kXBytes + g * la_bytes);
@@ -256,7 +265,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                        (i != begin || k != 0) ? 1u : 0u);
           }
           mma_commit(empty0 + 8u * s);
-          if (++s == kTileStages) {
+          if (++s == stages) {
             s = 0;
             ph ^= 1u;
           }
@@ -337,7 +346,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 cudaError_t configure_lora_shrink() {
   cudaError_t e = cudaFuncSetAttribute(lora_shrink_tile_kernel,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(tile_smem(2 * kLoraMaxRank)));
+                                       static_cast<int>(kTileSmem));
   // The same split of the L1/shared array as the decode kernel's, so that its
   // CTAs can join an SM that still runs this kernel.
   if (e == cudaSuccess)
@@ -368,7 +377,7 @@ cudaError_t launch_lora_shrink(const LoraShrinkParams& p, cudaStream_t stream) {
       return cudaErrorInvalidValue;
     cfg.gridDim = dim3(static_cast<unsigned>(p.tiles) * p.splits);
     cfg.blockDim = dim3(kTileThreads);
-    cfg.dynamicSmemBytes = tile_smem(p.rb);
+    cfg.dynamicSmemBytes = kTileSmem;
     attr[1].val.clusterDim.x = p.splits;
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;

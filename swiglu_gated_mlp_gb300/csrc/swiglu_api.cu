@@ -298,22 +298,15 @@ struct Plan {
 // the same weights, the repeats coming from L2), and each (block, group) unit
 // splits K over a cluster so that the units fill the SMs; all clusters must be
 // resident at once.
-void decode_split_plan(int64_t M, int64_t blocks, int64_t kslices, const DeviceState* d,
-                       int* mt, int* mgroups, int* stages, int* splits) {
+void decode_stages_splits(int64_t units, int64_t kslices, const DeviceState* d, int mt, int* stages,
+                          int* splits) {
   const int sm_count = d ? d->sm_count : 0;
-  *mt = static_cast<int>((M + 15) / 16 * 16);
-  *mgroups = 1;
-  if (d && M > 64 && blocks * 2 <= sm_count) {
-    *mt = 64;
-    *mgroups = static_cast<int>((M + 63) / 64);
-  }
-  const int64_t units = blocks * *mgroups;
-  *stages = swg::small_m_stages(*mt, 1);
-  if (sm_count > 0 && units > sm_count && swg::small_m_stages(*mt, 2) >= 3)
-    *stages = swg::small_m_stages(*mt, 2);
+  *stages = swg::small_m_stages(mt, 1);
+  if (sm_count > 0 && units > sm_count && swg::small_m_stages(mt, 2) >= 3)
+    *stages = swg::small_m_stages(mt, 2);
   *splits = 1;
-  const int64_t stage_bytes = 2 * swg::kPackBlockN * swg::kBlockK * 2 + int64_t(*mt) * 128;
-  if (d && *mt <= 128 && int64_t(*mt) * 1024 <= *stages * stage_bytes) {
+  const int64_t stage_bytes = 2 * swg::kPackBlockN * swg::kBlockK * 2 + int64_t(mt) * 128;
+  if (d && mt <= 128 && int64_t(mt) * 1024 <= *stages * stage_bytes) {
     for (int s : {8, 4, 2}) {
       if (units * s <= sm_count && s <= kslices && d->small_clusters[s] >= units) {
         *splits = s;
@@ -321,6 +314,17 @@ void decode_split_plan(int64_t M, int64_t blocks, int64_t kslices, const DeviceS
       }
     }
   }
+}
+
+void decode_split_plan(int64_t M, int64_t blocks, int64_t kslices, const DeviceState* d,
+                       int* mt, int* mgroups, int* stages, int* splits) {
+  *mt = static_cast<int>((M + 15) / 16 * 16);
+  *mgroups = 1;
+  if (d && M > 64 && blocks * 2 <= d->sm_count) {
+    *mt = 64;
+    *mgroups = static_cast<int>((M + 63) / 64);
+  }
+  decode_stages_splits(blocks * *mgroups, kslices, d, *mt, stages, splits);
 }
 
 struct DownPlan {
@@ -775,7 +779,13 @@ swiglu_status_t decode_plan(int64_t M, int64_t blocks, int64_t kslices, int* mt,
   DeviceState* d = nullptr;
   const swiglu_status_t st = ::device_state(&d);
   if (st != SWIGLU_OK) return st;
-  ::decode_split_plan(M, blocks, kslices, d, mt, mgroups, stages, splits);
+  if (M <= 128) {
+    ::decode_split_plan(M, blocks, kslices, d, mt, mgroups, stages, splits);
+  } else {  // even groups of at most 128 tokens
+    *mgroups = static_cast<int>((M + 127) / 128);
+    *mt = static_cast<int>((M + int64_t(*mgroups) * 16 - 1) / (int64_t(*mgroups) * 16) * 16);
+    ::decode_stages_splits(blocks * *mgroups, kslices, d, *mt, stages, splits);
+  }
   return SWIGLU_OK;
 }
 

@@ -64,9 +64,9 @@ def test_no_tokens_is_a_no_op(native_lib):
 
 
 def test_workspace_sizes(native_lib):
-    # fp32 V up to 128 tokens; above, bf16 V and a list per 256 tokens (256-byte parts)
+    # bf16 V; above 128 tokens a list per 256 tokens too (256-byte parts)
     f, g = native_lib.swiglu_lora_workspace_bytes, native_lib.swiglu_down_lora_workspace_bytes
-    assert f(16, 64, 64, 8) == 16 * 16 * 4 and g(16, 64, 64, 8) == 16 * 8 * 4
+    assert f(16, 64, 64, 16) == 16 * 32 * 2 and g(16, 64, 64, 16) == 16 * 16 * 2
     assert f(1, 64, 64, 8) == 256
     assert f(512, 64, 64, 16) == 512 * 32 * 2 + 2 * 260 * 4
 
