@@ -11,8 +11,8 @@
 // enters is a fraction of the projection, which is itself rounded to bf16.
 //
 // Few tokens: lora_shrink_dot_kernel, plain dot products in fp32. One CTA takes
-// a token and 4 rows; its 8 warps split K, so every load of a CTA is in flight
-// at once. The decode kernel does its set-up and stages its first weight tiles
+// a token and 4 rows; its 8 warps (32 for a long K) split K, so that few loads
+// follow one another. The decode kernel does its set-up and stages its first weight tiles
 // in L2 while this one runs.
 //
 // Many tokens: lora_shrink_tile_kernel, tcgen05 with 128 tokens as the MMA's
@@ -23,8 +23,11 @@
 // 8 CTAs, whose fp32 sums are added in order through distributed shared memory.
 // A stage holds 64 of K for the tokens and for as many adapters as the tile has
 // (up to per_pass), and the ring as many stages as fit, so that with one adapter
-// most of what is in flight are tokens. The kernel also lists, per 256 tokens
-// (a CTA pair's tile), the adapters present.
+// most of what is in flight are tokens. The first tokens are on their way before
+// the adapters are known (a hash table in shared memory finds them; comparing
+// every token with all before it took 2.6 us of 26). The kernel also lists, per
+// 256 tokens (a CTA pair's tile), the adapters present, in any order: each
+// token takes part in one adapter's slices alone, so the order changes nothing.
 #include "kernels.h"
 #include "ptx.cuh"
 
@@ -34,7 +37,7 @@ namespace {
 // ------------------------------------------------------------- few tokens ---
 
 constexpr int kDotRows = 4;
-constexpr int kDotThreads = 256;
+constexpr int kDotThreads = 1024;  // at most
 
 __device__ __forceinline__ float dot8(const uint4& a, const uint4& b, float acc) {
   const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
@@ -53,6 +56,7 @@ __global__ void __launch_bounds__(kDotThreads)
   // reads anything but weight tiles into L2, and this grid takes little room.
   pdl_launch_dependents();
   pdl_wait();
+  const int threads = blockDim.x;
   const int row_blocks = (p.hr + kDotRows - 1) / kDotRows;
   const int m = blockIdx.x / row_blocks;
   const int r0 = (blockIdx.x % row_blocks) * kDotRows;
@@ -65,7 +69,7 @@ __global__ void __launch_bounds__(kDotThreads)
   const int chunks = p.K / 8;
   float acc[kDotRows] = {};
 #pragma unroll 4
-  for (int i = threadIdx.x; i < chunks; i += kDotThreads) {
+  for (int i = threadIdx.x; i < chunks; i += threads) {
     const uint4 xv = __ldg(x + i);
 #pragma unroll
     for (int r = 0; r < kDotRows; ++r)  // hr is a multiple of 8: every row exists
@@ -81,8 +85,7 @@ __global__ void __launch_bounds__(kDotThreads)
   __syncthreads();
   if (threadIdx.x < kDotRows) {
     float v = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kDotThreads / 32; ++w) v += sums[w][threadIdx.x];
+    for (int w = 0; w < threads / 32; ++w) v += sums[w][threadIdx.x];
     static_cast<__nv_bfloat16*>(p.v)[static_cast<size_t>(m) * p.hr + r0 + threadIdx.x] =
         __float2bfloat16_rn(v * p.scale[a]);
   }
@@ -96,20 +99,34 @@ constexpr int kXBytes = 128 * kBlockK * 2;                         // 16 KB of t
 constexpr int kTileStages = 8;                                     // at most
 constexpr int kPartPad = 4;                                        // floats, against bank conflicts
 constexpr int kTileBar = 256;
-constexpr size_t kTileSmem = 229376;  // with 1.6 KB of static shared memory
+constexpr int kEarlyLoads = 3;                                     // the ring has at least as many stages
+constexpr int kHashSlots = 512;                                    // for up to 256 adapters
+constexpr size_t kTileSmem = 225280;  // with 5.7 KB of static shared memory
 // What the ring may take: the rest holds the sums of `rb` columns.
 __host__ __device__ constexpr int tile_ring(int rb) {
   return static_cast<int>((kTileSmem - 1024 - kTileBar - size_t(128) * (rb + kPartPad) * 4) / 1024 * 1024);
 }
-static_assert(tile_ring(2 * kLoraMaxRank) >= 3 * (kXBytes + kTileCols * kBlockK * 2), "three stages");
+static_assert(tile_ring(2 * kLoraMaxRank) >= kEarlyLoads * (kXBytes + kTileCols * kBlockK * 2), "stages");
 static_assert(8 * (2 * kTileStages + 3) + 8 <= kTileBar, "barrier slots");
+
+// Whether `a` is new in a table of adapters (empty slots hold -1).
+__device__ __forceinline__ bool insert_new(int* table, int a) {
+  uint32_t h = (static_cast<uint32_t>(a) * 2654435761u) >> 23;  // 9 bits: kHashSlots
+  for (;;) {  // at most 256 of the 512 slots are taken: an empty one comes
+    const int old = atomicCAS(table + h, -1, a);
+    if (old == -1) return true;
+    if (old == a) return false;
+    h = (h + 1) & (kHashSlots - 1);
+  }
+}
 
 __global__ void __launch_bounds__(kTileThreads, 1)
     lora_shrink_tile_kernel(const __grid_constant__ LoraShrinkParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  __shared__ __align__(16) int ids[2 * kTileM];  // adapters of the 256 tokens (-1: none)
+  __shared__ int ids[2 * kTileM];                // adapters of the 256 tokens (-1: none)
+  __shared__ int seen[2][kHashSlots];            // adapters of the 256 tokens, and of this tile's
   __shared__ int mine[kTileM];                   // adapters present among this tile's 128 tokens
   __shared__ int counts[2][kTileThreads / 32];
   const int rb = p.rb;                           // accumulator columns of one adapter
@@ -149,31 +166,32 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     tmem_alloc(smem_addr(tmem_slot), kTileCols);
     tmem_relinquish();
   }
+  for (int i = tid; i < 2 * kHashSlots; i += kTileThreads) seen[i / kHashSlots][i % kHashSlots] = -1;
   pdl_wait();
+  // The producer's first token loads do not need the adapters.
+  const int early = min(kEarlyLoads, end - begin);
+  if (tid == 0 && !p.inject_stall) {
+    for (int s = 0; s < early; ++s) {
+      mbar_expect_tx(full0 + 8u * s, kXBytes);
+      tma_load_2d(s0 + s * kXBytes, &p.tmap_x, full0 + 8u * s, (begin + s) * kBlockK, m0);
+    }
+  }
+  int own;
   {
     const int64_t m = int64_t(m0) - half * kTileM + tid;
     const int a = m < p.M ? p.index[m] : -1;
-    ids[tid] = a >= 0 && a < p.count ? a : -1;
+    own = a >= 0 && a < p.count ? a : -1;
+    ids[tid] = own;
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
-  // Adapters in the order of their first token: of the 256 (for the pair
-  // kernel) and of this tile's 128.
-  const int own = ids[tid];
-  const int in_tile = tid / kTileM == half;
-  bool first256 = own >= 0, first128 = own >= 0 && in_tile;
-  for (int t = 0; t < tid; t += 4) {
-    const int4 v = *reinterpret_cast<const int4*>(ids + t);
-    const int x[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (t + e < tid && x[e] == own) {
-        first256 = false;
-        if (t + e >= half * kTileM) first128 = false;
-      }
-  }
+  // The adapters of the 256 tokens (for the pair kernel) and of this tile's 128.
+  const bool in_tile = tid / kTileM == half;
+  const bool first256 = own >= 0 && insert_new(seen[0], own);
+  const bool first128 = own >= 0 && in_tile && insert_new(seen[1], own);
+  __syncwarp();
   const uint32_t b256 = __ballot_sync(0xffffffffu, first256), b128 = __ballot_sync(0xffffffffu, first128);
   if (lane == 0) {
     counts[0][warp] = __popc(b256);
@@ -203,8 +221,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const int per_pass = p.per_pass;  // adapters side by side in the accumulator
   const int passes = (n128 + per_pass - 1) / per_pass;
   const uint32_t la_bytes = static_cast<uint32_t>(rb) * 128u;
-  const uint32_t stage_bytes = kXBytes + max(min(per_pass, n128), 1) * la_bytes;
-  const int stages = min(static_cast<int>(tile_ring(rb) / stage_bytes), kTileStages);
+  // ring: tokens of every stage, then adapter rows of every stage
+  const uint32_t la_stage = max(min(per_pass, n128), 1) * la_bytes;
+  const int stages = min(static_cast<int>(tile_ring(rb) / (kXBytes + la_stage)), kTileStages);
+  const uint32_t sla = s0 + stages * kXBytes;
   if (warp == 0) {
     if (lane == 0) {
       int s = 0;
@@ -220,11 +240,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           if (skip_once) {
             skip_once = false;  // testing hook: leave this stage unfilled
           } else {
-            const uint32_t fb = full0 + 8u * s, dst = s0 + s * stage_bytes;
-            mbar_arrive_expect_tx(fb, kXBytes + gn * la_bytes);
-            tma_load_2d(dst, &p.tmap_x, fb, i * kBlockK, m0);
+            const uint32_t fb = full0 + 8u * s;
+            const bool loaded = pass == 0 && i - begin < early && !p.inject_stall;
+            mbar_arrive_expect_tx(fb, (loaded ? 0 : kXBytes) + gn * la_bytes);
+            if (!loaded) tma_load_2d(s0 + s * kXBytes, &p.tmap_x, fb, i * kBlockK, m0);
             for (int g = 0; g < gn; ++g)
-              tma_load_2d(dst + kXBytes + g * la_bytes, &p.tmap_la, fb, i * kBlockK,
+              tma_load_2d(sla + s * la_stage + g * la_bytes, &p.tmap_la, fb, i * kBlockK,
                           mine[g0 + g] * p.hr);
             filled |= 1u << s;
             fill_ph = (fill_ph & ~(1u << s)) | (ph << s);
@@ -235,6 +256,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           }
         }
       }
+      if (passes == 0 && !p.inject_stall)  // no adapter: let the early loads land
+        for (int s2 = 0; s2 < early; ++s2) {
+          mbar_arrive(full0 + 8u * s2);
+          mbar_wait_drain(full0 + 8u * s2, 0, wc);
+        }
       for (int i = 0; i < stages; ++i)
         if (filled & (1u << i)) mbar_wait_drain(full0 + 8u * i, (fill_ph >> i) & 1u, wc);
     }
@@ -255,10 +281,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             break;
           }
           tc_fence_after();
-          const uint32_t src = s0 + s * stage_bytes;
-          const uint64_t xdesc = smem_desc_sw128(src);
+          const uint64_t xdesc = smem_desc_sw128(s0 + s * kXBytes);
           for (int g = 0; g < gn; ++g) {
-            const uint64_t ldesc = smem_desc_sw128(src + kXBytes + g * la_bytes);
+            const uint64_t ldesc = smem_desc_sw128(sla + s * la_stage + g * la_bytes);
 #pragma unroll
             for (uint32_t k = 0; k < 4; ++k)
               mma_bf16(tmem_base + g * rb, xdesc + 2u * k, ldesc + 2u * k, idesc,
@@ -318,14 +343,22 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const int row = kpart * rows + i / chunks, c = (i % chunks) * 8;
     const int a = ids[half * kTileM + row];
     if (a < 0) continue;  // no adapter (or no token): V is not read
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
-    for (int s = 0; s < splits; ++s) {
-      const uint32_t src = mapa_shared(local, s) + 4u * (row * part_stride + c);
-      const float4 u = ld_shared_cluster_v4(src), w = ld_shared_cluster_v4(src + 16u);
-      x.x += u.x; x.y += u.y; x.z += u.z; x.w += u.w;
-      y.x += w.x; y.y += w.y; y.z += w.z; y.w += w.w;
-    }
     const float f = p.scale[a];
+    float4 u[8], w[8];
+#pragma unroll
+    for (int s = 0; s < 8; ++s)  // every part's loads before the sums
+      if (s < splits) {
+        const uint32_t src = mapa_shared(local, s) + 4u * (row * part_stride + c);
+        u[s] = ld_shared_cluster_v4(src);
+        w[s] = ld_shared_cluster_v4(src + 16u);
+      }
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+#pragma unroll
+    for (int s = 0; s < 8; ++s)
+      if (s < splits) {
+        x.x += u[s].x; x.y += u[s].y; x.z += u[s].z; x.w += u[s].w;
+        y.x += w[s].x; y.y += w[s].y; y.z += w[s].z; y.w += w[s].w;
+      }
     uint4 o;
     o.x = pack_bf16x2(x.x * f, x.y * f);
     o.y = pack_bf16x2(x.z * f, x.w * f);
@@ -368,7 +401,7 @@ cudaError_t launch_lora_shrink(const LoraShrinkParams& p, cudaStream_t stream) {
   cudaError_t e;
   if (p.tiles == 0) {
     cfg.gridDim = dim3(static_cast<unsigned>(p.M) * ((p.hr + kDotRows - 1) / kDotRows));
-    cfg.blockDim = dim3(kDotThreads);
+    cfg.blockDim = dim3(p.K >= 8192 ? kDotThreads : 256);
     e = cudaLaunchKernelEx(&cfg, lora_shrink_dot_kernel, p);
   } else {
     if (p.splits < 1 || p.splits > 8 || (kTileM % p.splits) != 0 || p.slices < p.splits ||
