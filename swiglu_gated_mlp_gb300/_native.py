@@ -517,22 +517,7 @@ def _all_bf16(tensors, names: tuple) -> int:
     raise ValueError(f"{', '.join(names)} must be contiguous CUDA bfloat16 tensors on one device")
 
 
-class _call_on:
-    """Makes device `dev` current where another one is."""
-    __slots__ = ("dev", "prev")
-
-    def __init__(self, dev: int):
-        self.dev = dev
-
-    def __enter__(self):
-        self.prev = torch.cuda.current_device()
-        if self.prev != self.dev:
-            torch.cuda.set_device(self.dev)
-
-    def __exit__(self, *exc):
-        if self.prev != self.dev:
-            torch.cuda.set_device(self.prev)
-        return False
+_cur_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _on_stream(t: torch.Tensor, stream) -> torch.Tensor:
@@ -567,7 +552,7 @@ def _scratch(ws, dev: int, stream, bytes_fn, *shape) -> torch.Tensor:
 
 def _handle(stream, dev: int) -> int:
     if stream is None:
-        return _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream(dev).cuda_stream
+        return _raw_stream(dev) if _raw_stream else torch.cuda.current_stream(dev).cuda_stream
     return int(stream.cuda_stream) if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
@@ -612,13 +597,15 @@ def swiglu_backward(A: torch.Tensor, Wpacked: torch.Tensor, dY: torch.Tensor,
     M, K = A.shape
     N = dY.shape[1]
     _holds(Wpacked, -(-N // 128), K, "Wpacked")
-    with _call_on(dev):
-        dA = _output(dA, "dA", M, K, dev, stream) if need_input else None
-        dW1 = _output(dW1, "dW1", K, N, dev, stream) if need_weight else None
-        dW2 = _output(dW2, "dW2", K, N, dev, stream) if need_weight else None
-        ws = _scratch(workspace, dev, stream, swiglu_backward_workspace_bytes, M, K, N)
-        rc = lib.swiglu_backward(A.data_ptr(), Wpacked.data_ptr(), dY.data_ptr(), _ptr(dA), _ptr(dW1),
-                                 _ptr(dW2), M, K, N, ws.data_ptr(), ws.nbytes, _handle(stream, dev))
+    if _cur_device() != dev:
+        with torch.cuda.device(dev):
+            return swiglu_backward(A, Wpacked, dY, dA, dW1, dW2, need_input, need_weight, workspace, stream)
+    dA = _output(dA, "dA", M, K, dev, stream) if need_input else None
+    dW1 = _output(dW1, "dW1", K, N, dev, stream) if need_weight else None
+    dW2 = _output(dW2, "dW2", K, N, dev, stream) if need_weight else None
+    ws = _scratch(workspace, dev, stream, swiglu_backward_workspace_bytes, M, K, N)
+    rc = lib.swiglu_backward(A.data_ptr(), Wpacked.data_ptr(), dY.data_ptr(), _ptr(dA), _ptr(dW1),
+                             _ptr(dW2), M, K, N, ws.data_ptr(), ws.nbytes, _handle(stream, dev))
     if rc:
         _check(rc, "swiglu_backward")
     return dA, dW1, dW2
@@ -658,12 +645,15 @@ def swiglu_down_backward(dOut: torch.Tensor, W3packed: torch.Tensor | None, Y: t
         raise ValueError("N is needed without Y")
     if W3packed is not None:
         _holds(W3packed, -(-H // 256), N, "W3packed")
-    with _call_on(dev):
-        dY = _output(dY, "dY", M, N, dev, stream) if need_input else None
-        dW3 = _output(dW3, "dW3", N, H, dev, stream) if need_weight else None
-        ws = _scratch(workspace, dev, stream, swiglu_down_backward_workspace_bytes, M, N, H)
-        rc = lib.swiglu_down_backward(dOut.data_ptr(), _ptr(W3packed), _ptr(Y), _ptr(dY), _ptr(dW3), M, N,
-                                      H, ws.data_ptr() or None, ws.nbytes, _handle(stream, dev))
+    if _cur_device() != dev:
+        with torch.cuda.device(dev):
+            return swiglu_down_backward(dOut, W3packed, Y, dY, dW3, N, need_input, need_weight, workspace,
+                                        stream)
+    dY = _output(dY, "dY", M, N, dev, stream) if need_input else None
+    dW3 = _output(dW3, "dW3", N, H, dev, stream) if need_weight else None
+    ws = _scratch(workspace, dev, stream, swiglu_down_backward_workspace_bytes, M, N, H)
+    rc = lib.swiglu_down_backward(dOut.data_ptr(), _ptr(W3packed), _ptr(Y), _ptr(dY), _ptr(dW3), M, N, H,
+                                  ws.data_ptr(), ws.nbytes, _handle(stream, dev))
     if rc:
         _check(rc, "swiglu_down_backward")
     return dY, dW3
@@ -709,12 +699,14 @@ def swiglu_forward_lora(A: torch.Tensor, Wpacked: torch.Tensor, N: int, La: torc
     count, _, rank, _ = La.shape
     _holds(Wpacked, -(-N // 128), K, "Wpacked")
     _adapters(La, Lb, index, scale, (count, 2, rank, K), (count, 2, N, rank), M, dev)
-    with _call_on(dev):
-        Y = _output(Y, "Y", M, N, dev, stream)
-        ws = _scratch(workspace, dev, stream, swiglu_lora_workspace_bytes, M, K, N, rank)
-        rc = lib.swiglu_forward_lora(A.data_ptr(), Wpacked.data_ptr(), Y.data_ptr(), M, K, N,
-                                     La.data_ptr(), Lb.data_ptr(), index.data_ptr(), scale.data_ptr(),
-                                     count, rank, ws.data_ptr(), ws.nbytes, _handle(stream, dev))
+    if _cur_device() != dev:
+        with torch.cuda.device(dev):
+            return swiglu_forward_lora(A, Wpacked, N, La, Lb, index, scale, Y, workspace, stream)
+    Y = _output(Y, "Y", M, N, dev, stream)
+    ws = _scratch(workspace, dev, stream, swiglu_lora_workspace_bytes, M, K, N, rank)
+    rc = lib.swiglu_forward_lora(A.data_ptr(), Wpacked.data_ptr(), Y.data_ptr(), M, K, N, La.data_ptr(),
+                                 Lb.data_ptr(), index.data_ptr(), scale.data_ptr(), count, rank,
+                                 ws.data_ptr(), ws.nbytes, _handle(stream, dev))
     if rc:
         _check(rc, "swiglu_forward_lora")
     return Y
@@ -745,15 +737,16 @@ def swiglu_down_forward_lora(Y: torch.Tensor, W3packed: torch.Tensor, H: int, La
     count, rank, _ = La.shape
     _holds(W3packed, -(-H // 256), N, "W3packed")
     _adapters(La, Lb, index, scale, (count, rank, N), (count, H, rank), M, dev)
-    with _call_on(dev):
-        if R is not None:
-            _output(R, "R", M, H, dev, stream)
-        Out = _output(Out, "Out", M, H, dev, stream)
-        ws = _scratch(workspace, dev, stream, swiglu_down_lora_workspace_bytes, M, N, H, rank)
-        rc = lib.swiglu_down_forward_lora(Y.data_ptr(), W3packed.data_ptr(), _ptr(R), Out.data_ptr(), M,
-                                          N, H, La.data_ptr(), Lb.data_ptr(), index.data_ptr(),
-                                          scale.data_ptr(), count, rank, ws.data_ptr(), ws.nbytes,
-                                          _handle(stream, dev))
+    if _cur_device() != dev:
+        with torch.cuda.device(dev):
+            return swiglu_down_forward_lora(Y, W3packed, H, La, Lb, index, scale, R, Out, workspace, stream)
+    if R is not None:
+        _output(R, "R", M, H, dev, stream)
+    Out = _output(Out, "Out", M, H, dev, stream)
+    ws = _scratch(workspace, dev, stream, swiglu_down_lora_workspace_bytes, M, N, H, rank)
+    rc = lib.swiglu_down_forward_lora(Y.data_ptr(), W3packed.data_ptr(), _ptr(R), Out.data_ptr(), M, N, H,
+                                      La.data_ptr(), Lb.data_ptr(), index.data_ptr(), scale.data_ptr(),
+                                      count, rank, ws.data_ptr(), ws.nbytes, _handle(stream, dev))
     if rc:
         _check(rc, "swiglu_down_forward_lora")
     return Out
