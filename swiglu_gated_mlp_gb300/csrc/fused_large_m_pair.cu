@@ -80,7 +80,8 @@
 // the fp32 accumulator before SiLU. Lb comes by TMA into the stage's weight
 // half; four warps write the masked V rows into its A half (thread = row) and
 // signal a barrier of their own, which the MMA issuer waits for beside the
-// stage's. A zero row times a non-finite Lb value is NaN: adapters' Lb must be
+// stage's. (Alternating adapter and K slices instead: 660 against 640 us on the
+// 7B shape, 4096 tokens of rank 64.) A zero row times a non-finite Lb value is NaN: adapters' Lb must be
 // finite, as the shared weight must.
 #include "kernels.h"
 #include "ptx.cuh"

@@ -26,8 +26,8 @@
 // most of what is in flight are tokens. The first tokens are on their way before
 // the adapters are known (a hash table in shared memory finds them; comparing
 // every token with all before it took 2.6 us of 26). The kernel also lists, per
-// 256 tokens (a CTA pair's tile), the adapters present, in any order: each
-// token takes part in one adapter's slices alone, so the order changes nothing.
+// 256 tokens (a CTA pair's tile), the adapters present in the order of their
+// first token, so that no sum's order depends on timing.
 #include "kernels.h"
 #include "ptx.cuh"
 
@@ -101,7 +101,7 @@ constexpr int kPartPad = 4;                                        // floats, ag
 constexpr int kTileBar = 256;
 constexpr int kEarlyLoads = 3;                                     // the ring has at least as many stages
 constexpr int kHashSlots = 512;                                    // for up to 256 adapters
-constexpr size_t kTileSmem = 225280;  // with 5.7 KB of static shared memory
+constexpr size_t kTileSmem = 223232;  // with 7.8 KB of static shared memory
 // What the ring may take: the rest holds the sums of `rb` columns.
 __host__ __device__ constexpr int tile_ring(int rb) {
   return static_cast<int>((kTileSmem - 1024 - kTileBar - size_t(128) * (rb + kPartPad) * 4) / 1024 * 1024);
@@ -109,13 +109,12 @@ __host__ __device__ constexpr int tile_ring(int rb) {
 static_assert(tile_ring(2 * kLoraMaxRank) >= kEarlyLoads * (kXBytes + kTileCols * kBlockK * 2), "stages");
 static_assert(8 * (2 * kTileStages + 3) + 8 <= kTileBar, "barrier slots");
 
-// Whether `a` is new in a table of adapters (empty slots hold -1).
-__device__ __forceinline__ bool insert_new(int* table, int a) {
+// The slot of `a` in a table of adapters (empty slots hold -1).
+__device__ __forceinline__ int slot_of(int* table, int a) {
   uint32_t h = (static_cast<uint32_t>(a) * 2654435761u) >> 23;  // 9 bits: kHashSlots
   for (;;) {  // at most 256 of the 512 slots are taken: an empty one comes
     const int old = atomicCAS(table + h, -1, a);
-    if (old == -1) return true;
-    if (old == a) return false;
+    if (old == -1 || old == a) return static_cast<int>(h);
     h = (h + 1) & (kHashSlots - 1);
   }
 }
@@ -126,7 +125,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   __shared__ int ids[2 * kTileM];                // adapters of the 256 tokens (-1: none)
-  __shared__ int seen[2][kHashSlots];            // adapters of the 256 tokens, and of this tile's
+  __shared__ int seen[kHashSlots];               // hash table of the 256 tokens' adapters
+  __shared__ int first[2][kHashSlots];           // their first token among the 256, and in this tile
   __shared__ int mine[kTileM];                   // adapters present among this tile's 128 tokens
   __shared__ int counts[2][kTileThreads / 32];
   const int rb = p.rb;                           // accumulator columns of one adapter
@@ -166,7 +166,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     tmem_alloc(smem_addr(tmem_slot), kTileCols);
     tmem_relinquish();
   }
-  for (int i = tid; i < 2 * kHashSlots; i += kTileThreads) seen[i / kHashSlots][i % kHashSlots] = -1;
+  for (int i = tid; i < kHashSlots; i += kTileThreads) {
+    seen[i] = -1;
+    first[0][i] = first[1][i] = kTileThreads;
+  }
   pdl_wait();
   // The producer's first token loads do not need the adapters.
   const int early = min(kEarlyLoads, end - begin);
@@ -189,9 +192,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
   // The adapters of the 256 tokens (for the pair kernel) and of this tile's 128.
   const bool in_tile = tid / kTileM == half;
-  const bool first256 = own >= 0 && insert_new(seen[0], own);
-  const bool first128 = own >= 0 && in_tile && insert_new(seen[1], own);
-  __syncwarp();
+  const int slot = own >= 0 ? slot_of(seen, own) : 0;
+  if (own >= 0) {
+    atomicMin(&first[0][slot], tid);
+    if (in_tile) atomicMin(&first[1][slot], tid);
+  }
+  __syncthreads();
+  const bool first256 = own >= 0 && first[0][slot] == tid;
+  const bool first128 = own >= 0 && in_tile && first[1][slot] == tid;
   const uint32_t b256 = __ballot_sync(0xffffffffu, first256), b128 = __ballot_sync(0xffffffffu, first128);
   if (lane == 0) {
     counts[0][warp] = __popc(b256);

@@ -244,6 +244,18 @@ def test_lora_in_a_captured_graph_with_new_requests(native, M):
         assert torch.equal(y, want), how
 
 
+@pytest.mark.parametrize("M,K,N", [(100, 264, 392), (300, 896, 4864), (700, 1416, 20000)])
+def test_lora_repeats_bit_for_bit(native, M, K, N):
+    # many adapters in every tile, in a different order each time they are met
+    a, w1, w2 = (t.cuda() for t in make_inputs(M, K, N, 11))
+    wp = native.swiglu_pack_weights(w1, w2)
+    la, lb, scale = (t.cuda() for t in table(20, 2, 16, K, N, 11))
+    index = indices(M, 20, "mixed", 11).cuda()
+    want = native.swiglu_forward_lora(a, wp, N, la, lb, index, scale)
+    for _ in range(8):
+        assert torch.equal(native.swiglu_forward_lora(a, wp, N, la, lb, index, scale), want)
+
+
 @pytest.mark.parametrize("M", [16, 300])
 def test_lora_stalled_wait_is_reported(native, M):
     K, N, L, r = 512, 520, 3, 16
