@@ -102,11 +102,13 @@ constexpr int kTileBar = 256;
 constexpr int kEarlyLoads = 3;                                     // the ring has at least as many stages
 constexpr int kHashSlots = 512;                                    // for up to 256 adapters
 constexpr size_t kTileSmem = 223232;  // with 7.8 KB of static shared memory
-// What the ring may take: the rest holds the sums of `rb` columns.
-__host__ __device__ constexpr int tile_ring(int rb) {
-  return static_cast<int>((kTileSmem - 1024 - kTileBar - size_t(128) * (rb + kPartPad) * 4) / 1024 * 1024);
+// What the ring may take. With one pass over the tile's adapters the sums lie
+// where the ring was; with more, the rest of it holds the sums of `rb` columns.
+__host__ __device__ constexpr int tile_ring(int rb, bool one_pass) {
+  return static_cast<int>((kTileSmem - 1024 - kTileBar -
+                           (one_pass ? 0 : size_t(128) * (rb + kPartPad) * 4)) / 1024 * 1024);
 }
-static_assert(tile_ring(2 * kLoraMaxRank) >= kEarlyLoads * (kXBytes + kTileCols * kBlockK * 2), "stages");
+static_assert(tile_ring(2 * kLoraMaxRank, false) >= kEarlyLoads * (kXBytes + kTileCols * kBlockK * 2), "stages");
 static_assert(8 * (2 * kTileStages + 3) + 8 <= kTileBar, "barrier slots");
 
 // The slot of `a` in a table of adapters (empty slots hold -1).
@@ -132,8 +134,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const int rb = p.rb;                           // accumulator columns of one adapter
   const int part_stride = rb + kPartPad;
   const uint32_t s0 = smem_addr(smem);
-  float* part = reinterpret_cast<float*>(smem + tile_ring(rb));
-  uint8_t* bar_ptr = reinterpret_cast<uint8_t*>(part) + size_t(128) * part_stride * 4;
+  uint8_t* bar_ptr = smem + kTileSmem - 1024 - kTileBar;
   const uint32_t bar0 = smem_addr(bar_ptr);
   // barrier slots: full[8] | empty[8] | tmem_full | tmem_empty | drain
   const uint32_t full0 = bar0, empty0 = bar0 + 8u * kTileStages;
@@ -231,7 +232,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const uint32_t la_bytes = static_cast<uint32_t>(rb) * 128u;
   // ring: tokens of every stage, then adapter rows of every stage
   const uint32_t la_stage = max(min(per_pass, n128), 1) * la_bytes;
-  const int stages = min(static_cast<int>(tile_ring(rb) / (kXBytes + la_stage)), kTileStages);
+  const int ring = tile_ring(rb, passes <= 1);
+  const int stages = min(static_cast<int>(ring / (kXBytes + la_stage)), kTileStages);
+  float* part = reinterpret_cast<float*>(passes <= 1 ? smem : smem + ring);
   const uint32_t sla = s0 + stages * kXBytes;
   if (warp == 0) {
     if (lane == 0) {
@@ -346,6 +349,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   tc_fence_before();
   cluster_sync();
   const int rows = kTileM / splits, chunks = p.hr / 8;
+  // a peer with another number of passes cannot be: the cluster shares the tokens
   const uint32_t local = smem_addr(part);
   for (int i = tid; i < rows * chunks; i += kTileThreads) {
     const int row = kpart * rows + i / chunks, c = (i % chunks) * 8;
