@@ -116,7 +116,14 @@ void deal_units(GradientPlan* pl, bool in, bool w, int max_pairs, BackwardParams
   p->early_rounds = static_cast<int>(std::min<int64_t>(rounds, p->w_units / early));
 }
 
-void fill(BackwardProduct* p, const ProductPlan& pl, int64_t rows, int64_t cols) {
+// Rows of a box whose rows are tokens: 128, or up to the last 16 of fewer (rows
+// past the last token are zero).
+uint32_t token_rows(int64_t M) {
+  return static_cast<uint32_t>(std::min<int64_t>(kTileM, div_up(M, 16) * 16));
+}
+
+void fill(BackwardProduct* p, const ProductPlan& pl, int64_t rows, int64_t cols, int64_t M) {
+  p->a_bytes = static_cast<int>(token_rows(M)) * kBlockK * 2;
   p->rows = static_cast<int>(rows);
   p->cols = static_cast<int>(cols);
   p->slices = static_cast<int>(pl.slices);
@@ -146,9 +153,9 @@ bool encode_output(CUtensorMap* map, void* out, uint8_t* parts, const ProductPla
                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_DATA_TYPE_FLOAT32);
 }
 
-// A row-major [rows, cols] operand with the sum down its rows, 64 columns x 128 rows a box.
+// A row-major [tokens, cols] operand, 64 columns x up to 128 tokens a box.
 bool encode_operand(CUtensorMap* map, const void* base, int64_t rows, int64_t cols) {
-  return encode_2d(map, base, cols, rows, cols * 2, kBlockK, kTileM, CU_TENSOR_MAP_SWIZZLE_128B);
+  return encode_2d(map, base, cols, rows, cols * 2, kBlockK, token_rows(rows), CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 swiglu_status_t launched(cudaError_t e) {
@@ -265,12 +272,12 @@ swiglu_status_t swiglu_backward(const void* A, const void* Wpacked, const void* 
   uint8_t* parts = ws + 2 * pl.grad_bytes;
   {
     BackwardParams p{};
-    fill(&p.in, pl.grad, M, N);
+    fill(&p.in, pl.grad, M, N, M);
     fill_status(&p, d);
     p.in_units = static_cast<int>(pl.grad.units());
     p.dy = dY;
     p.grad_bn = pl.grad_bn;
-    if (!encode_2d(&p.in.tmap_a0, A, K, M, K * 2, kBlockK, kTileM, CU_TENSOR_MAP_SWIZZLE_128B) ||
+    if (!encode_operand(&p.in.tmap_a0, A, M, K) ||
         !encode_packed_w(&p.in.tmap_b0, Wpacked, K, N, pl.grad_bn) ||
         !encode_2d(&p.in.tmap_o0, dG, N, M, N * 2, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B) ||
         !encode_2d(&p.in.tmap_o1, dU, N, M, N * 2, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
@@ -284,18 +291,18 @@ swiglu_status_t swiglu_backward(const void* A, const void* Wpacked, const void* 
   deal_units(&g, dA != nullptr, dW1 != nullptr, pairs, &p);
   fill_status(&p, d);
   if (dA) {
-    fill(&p.in, g.in, M, K);
+    fill(&p.in, g.in, M, K, M);
     p.in.two = 1;
     p.in.col_slices = static_cast<int>(k_slices(K));
-    if (!encode_2d(&p.in.tmap_a0, dG, N, M, N * 2, kBlockK, kTileM, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !encode_2d(&p.in.tmap_a1, dU, N, M, N * 2, kBlockK, kTileM, CU_TENSOR_MAP_SWIZZLE_128B) ||
+    if (!encode_operand(&p.in.tmap_a0, dG, M, N) ||
+        !encode_operand(&p.in.tmap_a1, dU, M, N) ||
         !encode_packed_w(&p.in.tmap_b0, Wpacked, K, N, kPackBlockN) ||
         !encode_output(&p.in.tmap_o0, dA, parts, g.in, M, K, &sums))
       return SWIGLU_ERR_CUDA;
   }
   if (dW1) {
     uint8_t* w_parts = parts + g.in.part_bytes;
-    fill(&p.w, g.w, K, N);
+    fill(&p.w, g.w, K, N, M);
     p.w.sum = static_cast<int>(M);
     p.w.two = 1;
     if (!encode_operand(&p.w.tmap_a0, A, M, K) ||
@@ -354,15 +361,15 @@ swiglu_status_t swiglu_down_backward(const void* dOut, const void* W3packed, con
   deal_units(&g, dY != nullptr, dW3 != nullptr, pairs, &p);
   fill_status(&p, d);
   if (dY) {
-    fill(&p.in, g.in, M, N);
+    fill(&p.in, g.in, M, N, M);
     p.in.col_slices = static_cast<int>(k_slices(N));
-    if (!encode_2d(&p.in.tmap_a0, dOut, H, M, H * 2, kBlockK, kTileM, CU_TENSOR_MAP_SWIZZLE_128B) ||
+    if (!encode_operand(&p.in.tmap_a0, dOut, M, H) ||
         !encode_packed_down(&p.in.tmap_b0, W3packed, N, H, kPackBlockN) ||
         !encode_output(&p.in.tmap_o0, dY, parts, g.in, M, N, &sums))
       return SWIGLU_ERR_CUDA;
   }
   if (dW3) {
-    fill(&p.w, g.w, N, H);
+    fill(&p.w, g.w, N, H, M);
     p.w.sum = static_cast<int>(M);
     if (!encode_operand(&p.w.tmap_a0, Y, M, N) ||
         !encode_operand(&p.w.tmap_b0, dOut, M, H) ||

@@ -190,6 +190,12 @@ __global__ void __launch_bounds__(kBackThreads, 1)
         tile_coords(tile, g.tiles_m, g.tiles_n, g.group_m, mb, nb);
         const int r0 = mb * 2 * kTileM + static_cast<int>(rank) * kTileM;  // output row of this CTA
         const int begin = part_begin<kGrad>(g, part), end = part_begin<kGrad>(g, part + 1);
+        // Few tokens: boxes end with the last 8 (16) of them, and a CTA whose rows all
+        // lie past the output loads none. What the MMA then reads past them only
+        // reaches rows that are not stored, or is left out of the sum.
+        const bool rows_here = weight || r0 < g.rows;
+        const bool rows_peer = weight || mb * 2 * kTileM + kTileM < g.rows;  // the odd CTA's
+        const uint32_t bytes = g.a_bytes * (rows_peer ? 2 : 1) + 2 * (weight ? g.a_bytes : kBN * kBlockK * 2);
         for (int i = begin; i < end; ++i) {
           if (!mbar_wait(empty0 + 8u * s, ph ^ 1u, wc, kSiteProducerEmpty)) {
             ok = false;
@@ -198,13 +204,13 @@ __global__ void __launch_bounds__(kBackThreads, 1)
           if (skip_once) {
             skip_once = false;  // testing hook: both CTAs leave this stage unfilled
           } else {
-            if (leader) mbar_arrive_expect_tx(full0 + 8u * s, 2 * (kOperandBytes + kBN * kBlockK * 2));
+            if (leader) mbar_arrive_expect_tx(full0 + 8u * s, bytes);
             const uint32_t fb = full0_lead + 8u * s;
             const uint32_t da = sA + s * kOperandBytes, db = sB + s * kOperandBytes;
             if constexpr (kGrad) {
               // A rows [r0, +128); kBN gate (rank 0) or up (rank 1) rows of tile (., i)
               constexpr int kPer = kPackBlockN / kBN;
-              tma_load_2d_pair(da, &g.tmap_a0, fb, i * kBlockK, r0);
+              if (rows_here) tma_load_2d_pair(da, &g.tmap_a0, fb, i * kBlockK, r0);
               tma_load_3d_pair(db, &g.tmap_b0, fb, 0,
                                static_cast<int>(rank) * kPackBlockN + nb % kPer * kBN,
                                nb / kPer * g.slices + i);
@@ -217,7 +223,7 @@ __global__ void __launch_bounds__(kBackThreads, 1)
               // output and are not stored)
               const int j = i >> 2, h = (i >> 1) & 1, e = i & 1;
               const int col = (g.two ? j * kPackBlockN : j * 2 * kPackBlockN + h * kPackBlockN) + e * kBlockK;
-              tma_load_2d_pair(da, g.two && h ? &g.tmap_a1 : &g.tmap_a0, fb, col, r0);
+              if (rows_here) tma_load_2d_pair(da, g.two && h ? &g.tmap_a1 : &g.tmap_a0, fb, col, r0);
               tma_load_3d_pair(db, &g.tmap_b0, fb, 0, h * kPackBlockN,
                                j * g.col_slices + nb * 4 + static_cast<int>(rank) * 2 + e);
             } else {

@@ -172,6 +172,7 @@ struct BackwardProduct {
   int rows, cols;  // of one output
   int slices;      // stages: 64-deep slices of the sum; even (whole pairs) but for dG and dU
   int sum;         // weight gradient: tokens
+  int a_bytes;     // of a box of the left operand (weight gradient: of either operand)
   int col_slices;  // input gradient: packed tiles of 64 columns per row of tiles
   int tiles_m, tiles_n, group_m;
   int two;         // input gradient: dG and dU in the sum; weight gradient: dW1 and dW2
