@@ -195,23 +195,23 @@ bool any_overlap(const Span* out, int outs, const Span* in, int ins) {
 
 struct BackwardPlan {
   ProductPlan grad;
-  int grad_bn = kPackBlockN;
+  int64_t grad_full = 0;  // whole tiles; the others are taken in halves
   GradientPlan gradients;
   size_t grad_bytes = 0;  // dG (and dU) in the workspace, then the parts
   size_t bytes() const { return 2 * grad_bytes + gradients.parts_bytes(); }
 };
 
-// Whether dG and dU take tiles of 64 columns of each: where 128 leave pairs idle
-// in their only round.
-bool grad_halves(int64_t tiles, int pairs) { return 2 * tiles <= pairs; }
+// Tiles of dG and dU that are taken whole: all of them, or those of whole rounds
+// where the last round's halves still fit one round.
+int64_t grad_full_tiles(int64_t tiles, int pairs) {
+  const int64_t rest = tiles % pairs;
+  return 2 * rest <= pairs ? tiles - rest : tiles;
+}
 
 BackwardPlan plan_backward(int64_t M, int64_t K, int64_t N, int pairs) {
   BackwardPlan pl;
   pl.grad = plan_product(M, N, 2, k_slices(K));
-  if (grad_halves(pl.grad.tiles(), pairs)) {
-    pl.grad_bn = kPackBlockN / 2;
-    pl.grad.tiles_n = 2 * div_up(N, kPackBlockN);
-  }
+  pl.grad_full = grad_full_tiles(pl.grad.tiles(), pairs);
   pl.gradients = plan_gradients(M, K, 4 * div_up(N, kTileM), K, N, 2, pairs);
   pl.grad_bytes = align256(size_t(M) * size_t(N) * 2);
   return pl;
@@ -274,11 +274,12 @@ swiglu_status_t swiglu_backward(const void* A, const void* Wpacked, const void* 
     BackwardParams p{};
     fill(&p.in, pl.grad, M, N, M);
     fill_status(&p, d);
-    p.in_units = static_cast<int>(pl.grad.units());
+    p.full_units = static_cast<int>(pl.grad_full);
+    p.in_units = static_cast<int>(2 * pl.grad.tiles() - pl.grad_full);
     p.dy = dY;
-    p.grad_bn = pl.grad_bn;
     if (!encode_operand(&p.in.tmap_a0, A, M, K) ||
-        !encode_packed_w(&p.in.tmap_b0, Wpacked, K, N, pl.grad_bn) ||
+        !encode_packed_w(&p.in.tmap_b0, Wpacked, K, N, kPackBlockN) ||
+        !encode_packed_w(&p.in.tmap_b1, Wpacked, K, N, kPackBlockN / 2) ||
         !encode_2d(&p.in.tmap_o0, dG, N, M, N * 2, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B) ||
         !encode_2d(&p.in.tmap_o1, dU, N, M, N * 2, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
       return SWIGLU_ERR_CUDA;

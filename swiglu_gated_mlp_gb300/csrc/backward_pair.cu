@@ -33,11 +33,15 @@
 // it waited for (K-major descriptors on the same bytes: 365 us too).
 //
 // Roles as in the forward pair kernel: warp 0 TMA producer, warp 1 MMA issuer
-// (even CTA), then 8 epilogue warps, two for each 32 rows (with 4, a short sum's
-// tiles waited for them: EPI_FIGURE); 6 stages of 32 KB per CTA; two
-// accumulators of 256 columns, so a tile's epilogue runs under the next tile's
-// MMAs; every wait is bounded (ptx.cuh). kGrad has tiles of 128 or 64 gate (and
-// up) columns.
+// (even CTA), then 8 epilogue warps, two for each 32 rows (with 4, short sums
+// waited for them: 16 tokens on the 7B weights 215 against 201 us); 6 stages of
+// 32 KB per CTA; two accumulators of 256 columns, so a tile's epilogue runs
+// under the next tile's MMAs; every wait is bounded (ptx.cuh).
+//
+// kGrad has tiles of 128 gate and the matching 128 up columns. Where the tiles of
+// its last round would leave half of the pairs idle, they are cut into halves of
+// 64 columns (half-width MMAs read the left operand twice as often, so whole
+// rounds of halves would be slower: 2280 against 1820 us for the 7B backward).
 //
 // The input and the weight gradients do not depend on one another, so one
 // launch computes both: its units are the input gradient's tiles, then the
@@ -119,8 +123,15 @@ __device__ __forceinline__ void gate_grads(float g, float u, float dy, float& dg
   dg = dy * u * (s + gs * (1.0f - s));
 }
 
-// kBN: gate (and up) columns of a kGrad tile; 128 otherwise.
-template <bool kGrad, int kBN>
+// A kGrad unit: a whole tile, or from unit full_units on a half of one.
+__device__ __forceinline__ void grad_unit(const BackwardParams& p, int u, int& tile, int& bn, int& off) {
+  const int h = u - p.full_units;
+  tile = h < 0 ? u : p.full_units + (h >> 1);
+  bn = h < 0 ? kPackBlockN : kPackBlockN / 2;
+  off = h < 0 ? 0 : (h & 1) * (kPackBlockN / 2);
+}
+
+template <bool kGrad>
 __global__ void __launch_bounds__(kBackThreads, 1)
     backward_pair_kernel(const __grid_constant__ BackwardParams p) {
   extern __shared__ uint8_t smem_raw[];
@@ -185,7 +196,8 @@ __global__ void __launch_bounds__(kBackThreads, 1)
       bool weight;
       for (int step = 0, u; ok && (u = unit_at(p, pair, pairs, step, weight)) >= 0; ++step) {
         const BackwardProduct& g = weight ? p.w : p.in;
-        const int tile = u / g.splits, part = u - tile * g.splits;
+        int tile = u / g.splits, part = u - tile * g.splits, bn = kPackBlockN, off = 0;
+        if constexpr (kGrad) grad_unit(p, u, tile, bn, off);
         int mb, nb;
         tile_coords(tile, g.tiles_m, g.tiles_n, g.group_m, mb, nb);
         const int r0 = mb * 2 * kTileM + static_cast<int>(rank) * kTileM;  // output row of this CTA
@@ -195,7 +207,7 @@ __global__ void __launch_bounds__(kBackThreads, 1)
         // reaches rows that are not stored, or is left out of the sum.
         const bool rows_here = weight || r0 < g.rows;
         const bool rows_peer = weight || mb * 2 * kTileM + kTileM < g.rows;  // the odd CTA's
-        const uint32_t bytes = g.a_bytes * (rows_peer ? 2 : 1) + 2 * (weight ? g.a_bytes : kBN * kBlockK * 2);
+        const uint32_t bytes = g.a_bytes * (rows_peer ? 2 : 1) + 2 * (weight ? g.a_bytes : bn * kBlockK * 2);
         for (int i = begin; i < end; ++i) {
           if (!mbar_wait(empty0 + 8u * s, ph ^ 1u, wc, kSiteProducerEmpty)) {
             ok = false;
@@ -208,12 +220,10 @@ __global__ void __launch_bounds__(kBackThreads, 1)
             const uint32_t fb = full0_lead + 8u * s;
             const uint32_t da = sA + s * kOperandBytes, db = sB + s * kOperandBytes;
             if constexpr (kGrad) {
-              // A rows [r0, +128); kBN gate (rank 0) or up (rank 1) rows of tile (., i)
-              constexpr int kPer = kPackBlockN / kBN;
+              // A rows [r0, +128); bn gate (rank 0) or up (rank 1) rows of tile (nb, i)
               if (rows_here) tma_load_2d_pair(da, &g.tmap_a0, fb, i * kBlockK, r0);
-              tma_load_3d_pair(db, &g.tmap_b0, fb, 0,
-                               static_cast<int>(rank) * kPackBlockN + nb % kPer * kBN,
-                               nb / kPer * g.slices + i);
+              tma_load_3d_pair(db, bn == kPackBlockN ? &g.tmap_b0 : &g.tmap_b1, fb, 0,
+                               static_cast<int>(rank) * kPackBlockN + off, nb * g.slices + i);
             } else if (!weight) {
               // stages 2 d, 2 d + 1: rows [128 h, +128) of packed tile row j (a gate/up
               // tile holds 128 gate then 128 up columns of the sum, a down tile 256);
@@ -268,7 +278,7 @@ __global__ void __launch_bounds__(kBackThreads, 1)
         tc_fence_after();
         const uint32_t d = tmem_base + buf * kAccCols;
         if constexpr (kGrad) {
-          constexpr uint32_t kIdesc = idesc_bf16_f32(2 * kTileM, 2 * kBN);
+          const uint32_t idesc = idesc_bf16_f32(2 * kTileM, u < p.full_units ? 256 : 128);
           for (int i = begin; i < end; ++i) {
             if (!mbar_wait(full0 + 8u * s, ph, wc, kSiteMmaFull)) {
               ok = false;
@@ -279,7 +289,7 @@ __global__ void __launch_bounds__(kBackThreads, 1)
             const uint64_t bdesc = smem_desc_sw128(sB + s * kOperandBytes);
 #pragma unroll
             for (uint32_t k = 0; k < 4; ++k)
-              mma_bf16_pair(d, adesc + 2u * k, bdesc + 2u * k, kIdesc, (i != begin || k != 0) ? 1u : 0u);
+              mma_bf16_pair(d, adesc + 2u * k, bdesc + 2u * k, idesc, (i != begin || k != 0) ? 1u : 0u);
             mma_commit_pair_multicast(empty0 + 8u * s, 0x3);  // frees the stage in both CTAs
             if (++s == kStages) {
               s = 0;
@@ -341,14 +351,15 @@ __global__ void __launch_bounds__(kBackThreads, 1)
     bool weight;
     for (int step = 0, unit; (unit = unit_at(p, pair, pairs, step, weight)) >= 0; ++step) {
       const BackwardProduct& pr = weight ? p.w : p.in;
-      const int tile = unit / pr.splits, part = unit - tile * pr.splits;
+      int tile = unit / pr.splits, part = unit - tile * pr.splits, bn = kPackBlockN, off = 0;
+      if constexpr (kGrad) grad_unit(p, unit, tile, bn, off);
       int mb, nb;
       tile_coords(tile, pr.tiles_m, pr.tiles_n, pr.group_m, mb, nb);
       const int row0 = mb * 2 * kTileM + static_cast<int>(rank) * kTileM + q * 32;
-      constexpr int kChunks = kBN / 64;  // kGrad: 32-column chunks of this warp
+      const int chunks = bn / 64;  // kGrad: 32-column chunks of this warp
       uint4 dyv[4];
       const __nv_bfloat16* dy_row = nullptr;
-      const int col0 = nb * kBN + half * (kBN / 2);
+      const int col0 = nb * kPackBlockN + off + half * (bn / 2);
       const auto load_dy = [&](int c) {  // this thread's row of dY, columns of chunk c
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -370,18 +381,18 @@ __global__ void __launch_bounds__(kBackThreads, 1)
       const uint32_t tacc = tmem_base + lane_off + buf * kAccCols;
       if constexpr (kGrad) {
 #pragma unroll 1
-        for (int c = 0; c < kChunks; ++c) {
+        for (int c = 0; c < chunks; ++c) {
           uint32_t g[32], u[32];
-          tmem_ld_x32(tacc + half * (kBN / 2) + c * 32, g);
-          tmem_ld_x32(tacc + kBN + half * (kBN / 2) + c * 32, u);
+          tmem_ld_x32(tacc + half * (bn / 2) + c * 32, g);
+          tmem_ld_x32(tacc + bn + half * (bn / 2) + c * 32, u);
           uint4 dyc[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) dyc[e] = dyv[e];
-          if (c + 1 < kChunks) load_dy(c + 1);
+          if (c + 1 < chunks) load_dy(c + 1);
           tmem_wait_ld();
           reg_fence(g);
           reg_fence(u);
-          if (c == kChunks - 1) {  // this warp's part of the accumulator is read
+          if (c == chunks - 1) {  // this warp's part of the accumulator is read
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(tempty0_lead + 8u * buf);
@@ -555,36 +566,39 @@ bool valid(const BackwardProduct& g, int units) {
           (g.splits == 1 || (g.part_rows >= g.rows && (g.part_rows % 32) == 0)));
 }
 
-}  // namespace
+bool valid_grad(const BackwardParams& p) {
+  const int halves = p.in_units - p.full_units;
+  return p.w_units == 0 && p.in.splits == 1 && p.full_units >= 0 && halves >= 0 && (halves % 2) == 0 &&
+         valid(p.in, p.full_units + halves / 2);
+}
 
-template <bool kGrad, int kBN>
+template <bool kGrad>
 cudaError_t set_smem() {
-  return cudaFuncSetAttribute(backward_pair_kernel<kGrad, kBN>,
+  return cudaFuncSetAttribute(backward_pair_kernel<kGrad>,
                               cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem));
 }
 
+}  // namespace
+
 cudaError_t configure_backward_pair(int* max_pairs) {
-  cudaError_t e = set_smem<true, 128>();
-  if (e == cudaSuccess) e = set_smem<true, 64>();
-  if (e == cudaSuccess) e = set_smem<false, 128>();
+  cudaError_t e = set_smem<true>();
+  if (e == cudaSuccess) e = set_smem<false>();
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg = backward_config(2, nullptr, attr, false);
-  return cudaOccupancyMaxActiveClusters(max_pairs, backward_pair_kernel<true, 128>, &cfg);
+  return cudaOccupancyMaxActiveClusters(max_pairs, backward_pair_kernel<true>, &cfg);
 }
 
 cudaError_t launch_backward_pair(const BackwardParams& p, bool grad, int pairs, cudaStream_t stream) {
   const int r = pairs > 0 ? p.in_units % pairs : 0;
-  if (pairs < 1 || p.in_units + int64_t(p.w_units) < pairs || !valid(p.in, p.in_units) ||
-      !valid(p.w, p.w_units) || p.early_rounds < 0 ||
-      int64_t(p.early_rounds) * (pairs - r) > p.w_units || (grad && (p.w_units || p.in.splits != 1 || (p.grad_bn != 128 && p.grad_bn != 64))))
+  if (pairs < 1 || p.in_units + int64_t(p.w_units) < pairs || !valid(p.w, p.w_units) ||
+      !(grad ? valid_grad(p) : valid(p.in, p.in_units)) || p.early_rounds < 0 ||
+      int64_t(p.early_rounds) * (pairs - r) > p.w_units)
     return cudaErrorInvalidValue;
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg = backward_config(2 * pairs, stream, attr, pdl_enabled());
-  const cudaError_t e =
-      !grad               ? cudaLaunchKernelEx(&cfg, backward_pair_kernel<false, 128>, p)
-      : p.grad_bn == 128 ? cudaLaunchKernelEx(&cfg, backward_pair_kernel<true, 128>, p)
-                          : cudaLaunchKernelEx(&cfg, backward_pair_kernel<true, 64>, p);
+  const cudaError_t e = grad ? cudaLaunchKernelEx(&cfg, backward_pair_kernel<true>, p)
+                             : cudaLaunchKernelEx(&cfg, backward_pair_kernel<false>, p);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 

@@ -186,7 +186,8 @@ struct BackwardParams {
   int in_units, w_units;
   int early_rounds;    // see unit_at()
   const void* dy;      // dG and dU: dY [rows, cols] bf16
-  int grad_bn;         // dG and dU: columns of each per tile, 128 or 64
+  int full_units;      // dG and dU: units that are whole tiles (128 columns of each); the
+                       // others are halves, loaded through b1 in boxes of 64 rows
   uint32_t* status;
   uint64_t timeout_ns;
   int inject_stall;
