@@ -81,7 +81,9 @@
 // half; four warps write the masked V rows into its A half (thread = row) and
 // signal a barrier of their own, which the MMA issuer waits for beside the
 // stage's. (Alternating adapter and K slices instead: 660 against 640 us on the
-// 7B shape, 4096 tokens of rank 64.) A zero row times a non-finite Lb value is NaN: adapters' Lb must be
+// 7B shape, 4096 tokens of rank 64.) Measured there: 613 us against 572 without
+// adapters; the adapter slices' MMAs are 2 % of the tensor pipe's work, the waits
+// around them the rest. A zero row times a non-finite Lb value is NaN: adapters' Lb must be
 // finite, as the shared weight must.
 #include "kernels.h"
 #include "ptx.cuh"
@@ -501,7 +503,7 @@ __global__ void __launch_bounds__(PairCfg<kMx, kLora>::kThreadsT, 1)
                                                       static_cast<size_t>(m) * p.lora_rank * kHalves);
       // the row's V and the first adapters of the list, loaded while the tile's K
       // slices go by (loaded per slice, their latency left the tensor pipe idle at
-      // every adapter slice: 679 against 600 us on the 7B shape, 4096 tokens, rank 64)
+      // every adapter slice: 679 against 668 us on the 7B shape, 4096 tokens, rank 64)
       constexpr int kChunks = kLoraMaxRank / 8;
       uint4 x[kHalves][kChunks];
 #pragma unroll
