@@ -396,7 +396,15 @@ SWIGLU_API swiglu_status_t swiglu_backward(const void* A, const void* Wpacked, c
  * not used). `workspace` as above; it may be NULL when
  * swiglu_down_backward_workspace_bytes(M, N, H) is 0. M = 0: dW3 is set to
  * zero. Errors as swiglu_forward.
+ *
+ * swiglu_backward_plan_string, swiglu_down_backward_plan_string: the tiles, the
+ *   parts of each sum and the CTA pairs these calls take for a shape on the
+ *   current device, as text; buf NULL or buflen 0: INVALID_ARG.
  */
+SWIGLU_API swiglu_status_t swiglu_backward_plan_string(int64_t M, int64_t K, int64_t N, char* buf,
+                                                       size_t buflen);
+SWIGLU_API swiglu_status_t swiglu_down_backward_plan_string(int64_t M, int64_t N, int64_t H,
+                                                            char* buf, size_t buflen);
 SWIGLU_API size_t swiglu_down_backward_workspace_bytes(int64_t M, int64_t N, int64_t H);
 SWIGLU_API swiglu_status_t swiglu_down_backward(const void* dOut, const void* W3packed,
                                                 const void* Y, void* dY, void* dW3, int64_t M,
@@ -433,6 +441,10 @@ SWIGLU_API swiglu_status_t swiglu_down_backward(const void* dOut, const void* W3
  * rank: a multiple of 8 up to 64 (else UNSUPPORTED; <= 0: INVALID_ARG).
  * adapters = 0: the plain projection, the adapter arguments are not used.
  * M = 0: no-op. R may be NULL or Out itself. Errors as swiglu_forward.
+ *
+ * swiglu_lora_plan_string(M, K, N), swiglu_down_lora_plan_string(M, N, H): the
+ *   kernels and launch shapes for a shape (and rank) on the current device, as
+ *   text; buf NULL or buflen 0: INVALID_ARG.
  */
 SWIGLU_API size_t swiglu_lora_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t rank);
 SWIGLU_API swiglu_status_t swiglu_forward_lora(const void* A, const void* Wpacked, void* Y,
@@ -441,6 +453,10 @@ SWIGLU_API swiglu_status_t swiglu_forward_lora(const void* A, const void* Wpacke
                                                const float* scale, int64_t adapters, int64_t rank,
                                                void* workspace, size_t workspace_bytes,
                                                swiglu_stream_t stream);
+SWIGLU_API swiglu_status_t swiglu_lora_plan_string(int64_t M, int64_t K, int64_t N, int64_t rank,
+                                                   char* buf, size_t buflen);
+SWIGLU_API swiglu_status_t swiglu_down_lora_plan_string(int64_t M, int64_t N, int64_t H, int64_t rank,
+                                                        char* buf, size_t buflen);
 SWIGLU_API size_t swiglu_down_lora_workspace_bytes(int64_t M, int64_t N, int64_t H, int64_t rank);
 SWIGLU_API swiglu_status_t swiglu_down_forward_lora(const void* Y, const void* W3packed,
                                                     const void* R, void* Out, int64_t M, int64_t N,

@@ -24,6 +24,8 @@ _EXPORTS = {
     "swiglu_down_backward", "swiglu_down_backward_workspace", "swiglu_down_backward_workspace_bytes",
     "swiglu_forward_lora", "swiglu_lora_workspace", "swiglu_lora_workspace_bytes",
     "swiglu_down_forward_lora", "swiglu_down_lora_workspace", "swiglu_down_lora_workspace_bytes",
+    "swiglu_backward_plan_string", "swiglu_down_backward_plan_string", "swiglu_lora_plan_string",
+    "swiglu_down_lora_plan_string",
     "swiglu_packed_weight_bytes", "swiglu_check_device_status", "swiglu_status_string",
     "swiglu_plan_string", "swiglu_testing_inject_stall", "swiglu_testing_pace_run_out",
     "SwigluError",

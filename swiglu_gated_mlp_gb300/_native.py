@@ -109,6 +109,10 @@ lib.swiglu_down_lora_workspace_bytes.restype = _sz
 lib.swiglu_down_forward_lora.argtypes = [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _i64,
                                          _i64, _vp, _sz, _vp]
 lib.swiglu_down_forward_lora.restype = _int
+for _f in (lib.swiglu_backward_plan_string, lib.swiglu_down_backward_plan_string):
+    _f.argtypes, _f.restype = [_i64, _i64, _i64, ctypes.c_char_p, _sz], _int
+for _f in (lib.swiglu_lora_plan_string, lib.swiglu_down_lora_plan_string):
+    _f.argtypes, _f.restype = [_i64, _i64, _i64, _i64, ctypes.c_char_p, _sz], _int
 lib.swiglu_testing_inject_stall.argtypes = [_int, _u32]
 lib.swiglu_testing_inject_stall.restype = None
 lib.swiglu_testing_pace_run_out.argtypes = [ctypes.POINTER(ctypes.c_uint64)]
@@ -581,6 +585,28 @@ def swiglu_backward_workspace(M: int, K: int, N: int, device=None) -> torch.Tens
     return _new_workspace(swiglu_backward_workspace_bytes, device, M, K, N)
 
 
+def _plan(name: str, *shape: int) -> str:
+    buf = ctypes.create_string_buffer(256)
+    _check(getattr(lib, name)(*(int(n) for n in shape), buf, 256), name)
+    return buf.value.decode()
+
+
+def swiglu_backward_plan_string(M: int, K: int, N: int) -> str:
+    return _plan("swiglu_backward_plan_string", M, K, N)
+
+
+def swiglu_down_backward_plan_string(M: int, N: int, H: int) -> str:
+    return _plan("swiglu_down_backward_plan_string", M, N, H)
+
+
+def swiglu_lora_plan_string(M: int, K: int, N: int, rank: int) -> str:
+    return _plan("swiglu_lora_plan_string", M, K, N, rank)
+
+
+def swiglu_down_lora_plan_string(M: int, N: int, H: int, rank: int) -> str:
+    return _plan("swiglu_down_lora_plan_string", M, N, H, rank)
+
+
 def swiglu_backward(A: torch.Tensor, Wpacked: torch.Tensor, dY: torch.Tensor,
                     dA: torch.Tensor | None = None, dW1: torch.Tensor | None = None,
                     dW2: torch.Tensor | None = None, need_input: bool = True,
@@ -632,8 +658,12 @@ def swiglu_down_backward(dOut: torch.Tensor, W3packed: torch.Tensor | None, Y: t
         raise ValueError("dW3 needs Y")
     if need_input and W3packed is None:
         raise ValueError("dY needs W3packed")
-    given = [(t, n) for t, n in ((dOut, "dOut"), (W3packed, "W3packed"), (Y, "Y")) if t is not None]
-    dev = _all_bf16([t for t, _ in given], tuple(n for _, n in given))
+    if Y is None:
+        dev = _all_bf16((dOut, W3packed), ("dOut", "W3packed")) if need_input else _all_bf16((dOut,), ("dOut",))
+    elif W3packed is None:
+        dev = _all_bf16((dOut, Y), ("dOut", "Y"))
+    else:
+        dev = _all_bf16((dOut, W3packed, Y), ("dOut", "W3packed", "Y"))
     if dOut.dim() != 2:
         raise ValueError("dOut must be [M, H]")
     M, H = dOut.shape

@@ -5,6 +5,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cstdio>
 #include <mutex>
 
 #include "api_shared.h"
@@ -217,6 +218,16 @@ BackwardPlan plan_backward(int64_t M, int64_t K, int64_t N, int pairs) {
   return pl;
 }
 
+// Tiles and parts of the two gradient products, as deal_units() takes them, as text.
+int format_gradients(GradientPlan g, int max_pairs, char* buf, size_t buflen) {
+  BackwardParams p{};
+  deal_units(&g, true, true, max_pairs, &p);
+  return std::snprintf(buf, buflen, "input tiles=%lld parts=%lld weight tiles=%lld parts=%lld early=%d pairs=%d",
+                       static_cast<long long>(g.in.tiles()), static_cast<long long>(g.in.splits),
+                       static_cast<long long>(g.w.tiles()), static_cast<long long>(g.w.splits),
+                       p.early_rounds, g.pairs);
+}
+
 GradientPlan plan_down_backward(int64_t M, int64_t N, int64_t H, int pairs) {
   return plan_gradients(M, N, 4 * div_up(H, kTile), N, H, 1, pairs);
 }
@@ -314,6 +325,40 @@ swiglu_status_t swiglu_backward(const void* A, const void* Wpacked, const void* 
       return SWIGLU_ERR_CUDA;
   }
   return run_gradients(p, g, sums, cs);
+}
+
+swiglu_status_t swiglu_backward_plan_string(int64_t M, int64_t K, int64_t N, char* buf, size_t buflen) {
+  if (!buf || buflen == 0) return SWIGLU_ERR_INVALID_ARG;
+  buf[0] = '\0';
+  swiglu_status_t st = swg::api::check_shape(M, K, N);
+  if (st != SWIGLU_OK) return st;
+  DeviceView d;
+  int pairs = 0;
+  st = backward_device(&d, &pairs);
+  if (st != SWIGLU_OK) return st;
+  const BackwardPlan pl = plan_backward(std::max<int64_t>(M, 1), K, N, pairs);
+  char rest[160];
+  format_gradients(pl.gradients, pairs, rest, sizeof(rest));
+  std::snprintf(buf, buflen, "backward grad whole=%lld halves=%lld %s",
+                static_cast<long long>(pl.grad_full),
+                static_cast<long long>(2 * (pl.grad.tiles() - pl.grad_full)), rest);
+  return SWIGLU_OK;
+}
+
+swiglu_status_t swiglu_down_backward_plan_string(int64_t M, int64_t N, int64_t H, char* buf,
+                                                 size_t buflen) {
+  if (!buf || buflen == 0) return SWIGLU_ERR_INVALID_ARG;
+  buf[0] = '\0';
+  swiglu_status_t st = swg::api::check_shape(M, N, H);
+  if (st != SWIGLU_OK) return st;
+  DeviceView d;
+  int pairs = 0;
+  st = backward_device(&d, &pairs);
+  if (st != SWIGLU_OK) return st;
+  char rest[160];
+  format_gradients(plan_down_backward(std::max<int64_t>(M, 1), N, H, pairs), pairs, rest, sizeof(rest));
+  std::snprintf(buf, buflen, "down_backward %s", rest);
+  return SWIGLU_OK;
 }
 
 size_t swiglu_down_backward_workspace_bytes(int64_t M, int64_t N, int64_t H) {

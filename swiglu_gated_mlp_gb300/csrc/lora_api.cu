@@ -5,6 +5,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cstdio>
 #include <mutex>
 
 #include "api_shared.h"
@@ -63,6 +64,13 @@ swiglu_status_t lora_device(DeviceView* d) {
   return l.status;
 }
 
+// K parts of the tile kernel of V: as many as keep every CTA resident at once.
+int shrink_splits(int64_t tiles, int64_t slices, int sm_count) {
+  for (int s : {8, 4, 2})
+    if (s <= slices && tiles * s <= sm_count) return s;
+  return 1;
+}
+
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -78,6 +86,10 @@ size_t workspace_bytes_for(int64_t M, int64_t hr) {
 swiglu_status_t check_rank(int64_t rank) {
   if (rank <= 0) return SWIGLU_ERR_INVALID_ARG;
   return rank % 8 == 0 && rank <= kLoraMaxRank ? SWIGLU_OK : SWIGLU_ERR_UNSUPPORTED;
+}
+
+int64_t weight_blocks(bool down, int64_t outs) {
+  return down ? padded_h(outs) / 256 : padded_n(outs) / kPackBlockN;
 }
 
 // One projection with adapters: x [M, in] -> out [M, outs], `halves` = 2 for
@@ -140,7 +152,7 @@ swiglu_status_t run_call(const Call& c, cudaStream_t stream) {
   swiglu_status_t st = lora_device(&d);
   if (st != SWIGLU_OK) return st;
   const bool down = c.halves == 1;
-  const int64_t blocks = down ? padded_h(c.outs) / 256 : padded_n(c.outs) / kPackBlockN;
+  const int64_t blocks = weight_blocks(down, c.outs);
   const int hr = static_cast<int>(c.rank * c.halves);
   const int64_t slices = k_slices(c.in);
   SmallMParams dp{};
@@ -168,12 +180,7 @@ swiglu_status_t run_call(const Call& c, cudaStream_t stream) {
     sp.slices = static_cast<int>(slices);
     sp.rb = (hr + 15) / 16 * 16;
     sp.per_pass = 256 / sp.rb;
-    sp.splits = 1;
-    for (int s : {8, 4, 2})  // as many K parts as keep every CTA resident at once
-      if (s <= slices && int64_t(sp.tiles) * s <= d.sm_count) {
-        sp.splits = s;
-        break;
-      }
+    sp.splits = shrink_splits(sp.tiles, slices, d.sm_count);
     if (!encode_2d(&sp.tmap_x, c.x, c.in, c.M, c.in * 2, kBlockK, kTileM, CU_TENSOR_MAP_SWIZZLE_128B) ||
         !encode_2d(&sp.tmap_la, c.la, c.in, uint64_t(c.count) * hr, c.in * 2, kBlockK, sp.rb,
                    CU_TENSOR_MAP_SWIZZLE_128B))
@@ -252,6 +259,39 @@ swiglu_status_t run_call(const Call& c, cudaStream_t stream) {
   return SWIGLU_OK;
 }
 
+swiglu_status_t lora_plan(int64_t M, int64_t in, int64_t outs, int64_t rank, bool down, char* buf,
+                          size_t buflen) {
+  if (!buf || buflen == 0) return SWIGLU_ERR_INVALID_ARG;
+  buf[0] = '\0';
+  swiglu_status_t st = api::check_shape(M, in, outs);
+  if (st == SWIGLU_OK) st = check_rank(rank);
+  if (st != SWIGLU_OK) return st;
+  DeviceView d;
+  st = lora_device(&d);
+  if (st != SWIGLU_OK) return st;
+  M = std::max<int64_t>(M, 1);
+  const int64_t blocks = weight_blocks(down, outs), slices = k_slices(in);
+  SmallMParams p{};
+  bool decode = false;
+  st = plan_decode(M, blocks, slices, d, &p, &decode);
+  if (st != SWIGLU_OK) return st;
+  const int64_t tiles = div_up(M, kTileM), hr = down ? rank : 2 * rank;
+  char shrink[64];
+  if (M <= kGroupTokens)
+    std::snprintf(shrink, sizeof(shrink), "dots=%lld", static_cast<long long>(M * div_up(hr, 4)));
+  else
+    std::snprintf(shrink, sizeof(shrink), "tiles=%lld parts=%d", static_cast<long long>(tiles),
+                  shrink_splits(tiles, slices, d.sm_count));
+  if (decode)
+    std::snprintf(buf, buflen, "%slora shrink %s small_m mt=%d stages=%d blocks=%lld groups=%d splits=%d",
+                  down ? "down " : "", shrink, p.mt, p.stages, static_cast<long long>(blocks), p.mgroups,
+                  p.splits);
+  else
+    std::snprintf(buf, buflen, "%slora shrink %s large_m_pair tiles=%lld max_pairs=%d", down ? "down " : "",
+                  shrink, static_cast<long long>(div_up(M, 2 * kTileM) * blocks), d.max_pairs);
+  return SWIGLU_OK;
+}
+
 size_t lora_workspace(int64_t M, int64_t in, int64_t outs, int64_t hr, int64_t rank) {
   if (api::check_shape(M, in, outs) != SWIGLU_OK || check_rank(rank) != SWIGLU_OK) return 0;
   return workspace_bytes_for(M, hr);
@@ -275,6 +315,16 @@ swiglu_status_t swiglu_forward_lora(const void* A, const void* Wpacked, void* Y,
   if (st != SWIGLU_OK || M == 0) return st;
   if (adapters == 0) return swiglu_forward(A, Wpacked, Y, M, K, N, stream);
   return run_call(c, reinterpret_cast<cudaStream_t>(stream));
+}
+
+swiglu_status_t swiglu_lora_plan_string(int64_t M, int64_t K, int64_t N, int64_t rank, char* buf,
+                                        size_t buflen) {
+  return lora_plan(M, K, N, rank, false, buf, buflen);
+}
+
+swiglu_status_t swiglu_down_lora_plan_string(int64_t M, int64_t N, int64_t H, int64_t rank, char* buf,
+                                             size_t buflen) {
+  return lora_plan(M, N, H, rank, true, buf, buflen);
 }
 
 size_t swiglu_down_lora_workspace_bytes(int64_t M, int64_t N, int64_t H, int64_t rank) {

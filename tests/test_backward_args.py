@@ -69,3 +69,19 @@ def test_binding_checks(native_lib):
         native_lib.swiglu_backward(a, a, a)
     with pytest.raises(ValueError):
         native_lib.swiglu_down_backward(a, a, a)
+
+
+def test_plan_strings_check_their_arguments(native_lib):
+    import ctypes
+    lib, buf = native_lib.lib, ctypes.create_string_buffer(64)
+    for f in (lib.swiglu_backward_plan_string, lib.swiglu_down_backward_plan_string):
+        assert f(16, 64, 64, None, 0) == native_lib.SWIGLU_ERR_INVALID_ARG
+        assert f(16, 60, 64, buf, 64) == native_lib.SWIGLU_ERR_UNSUPPORTED
+        if not torch.cuda.is_available():
+            assert f(16, 64, 64, buf, 64) == native_lib.SWIGLU_ERR_NO_DEVICE
+    for f in (lib.swiglu_lora_plan_string, lib.swiglu_down_lora_plan_string):
+        assert f(16, 64, 64, 8, None, 0) == native_lib.SWIGLU_ERR_INVALID_ARG
+        assert f(16, 60, 64, 8, buf, 64) == native_lib.SWIGLU_ERR_UNSUPPORTED
+        assert f(16, 64, 64, 12, buf, 64) == native_lib.SWIGLU_ERR_UNSUPPORTED
+        if not torch.cuda.is_available():
+            assert f(16, 64, 64, 8, buf, 64) == native_lib.SWIGLU_ERR_NO_DEVICE

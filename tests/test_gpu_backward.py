@@ -265,3 +265,46 @@ def test_backward_workspace_too_small_is_rejected(native):
     with pytest.raises(native.SwigluError) as err:
         native.swiglu_backward(a, wp, dy, workspace=torch.empty(n - 16, dtype=torch.uint8, device="cuda"))
     assert err.value.code == native.SWIGLU_ERR_INVALID_ARG
+
+
+def test_binding_refuses_what_does_not_fit(native):
+    a, w1, w2, dy = (t.cuda() for t in inputs(20, 64, 128, seed=14))
+    wp = native.swiglu_pack_weights(w1, w2)
+    w3p = native.swiglu_pack_down_weights(w2.t().contiguous())
+    bad = [
+        lambda: native.swiglu_backward(a.float(), wp, dy), lambda: native.swiglu_backward(a, wp, dy.cpu()),
+        lambda: native.swiglu_backward(a[:, :32], wp, dy), lambda: native.swiglu_backward(a, wp, dy[:10]),
+        lambda: native.swiglu_backward(a, wp[:100], dy), lambda: native.swiglu_backward(a, wp, dy.t()),
+        lambda: native.swiglu_backward(a, wp, dy, dA=dy), lambda: native.swiglu_backward(a, wp, dy, dW1=w1.t()),
+        lambda: native.swiglu_backward(a, wp, dy, workspace=torch.empty(1 << 22, dtype=torch.uint8)),
+        lambda: native.swiglu_down_backward(a, w3p, dy[:10]), lambda: native.swiglu_down_backward(a, None, dy),
+        lambda: native.swiglu_down_backward(a, w3p, None),
+        lambda: native.swiglu_down_backward(a, w3p, None, need_weight=False),
+        lambda: native.swiglu_down_backward(a, w3p, dy, N=64), lambda: native.swiglu_down_backward(a, w3p[:9], dy),
+        lambda: native.swiglu_down_backward(a, w3p, dy.half()),
+    ]
+    for i, call in enumerate(bad):
+        with pytest.raises(ValueError):
+            call()
+            pytest.fail(f"call {i} was not refused")
+
+
+def _fields(plan):
+    return {k: int(v) for k, _, v in (f.partition("=") for f in plan.split()) if v.isdigit()}
+
+
+def test_plans_reach_every_form(native):
+    # the tested shapes take sums in one part and in several, whole and half tiles of dG and
+    # dU, and pairs that begin with weight tiles
+    plans = [native.swiglu_backward_plan_string(*s) for s in SHAPES]
+    assert all(p.startswith("backward grad whole=") for p in plans)
+    parts = [[int(v) for v in p.replace("=", " ").split() if v.isdigit()] for p in plans]
+    wholes, halves, _, in_parts, _, w_parts, early, _ = zip(*parts)
+    assert max(in_parts) > 1 and min(in_parts) == 1 and max(w_parts) > 1 and min(w_parts) == 1
+    assert max(halves) > 0 and max(early) > 0
+    big = native.swiglu_backward_plan_string(4096, 3584, 18944)
+    f = _fields(big)
+    assert f["whole"] > 0 and f["early"] > 0 and f["pairs"] > 1, big
+    assert max(wholes) > 0 or f["whole"] > 0
+    assert native.swiglu_down_backward_plan_string(128, 4864, 896).startswith("down_backward input tiles=")
+    assert native.swiglu_down_backward_workspace_bytes(4096, 18944, 3584) == 0

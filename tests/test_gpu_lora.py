@@ -296,3 +296,48 @@ def test_large_table_offsets(native):
         assert_within(y[:M], ref)
         if m > M:
             assert torch.equal(y[m - 1], y[(m - 1) % M])
+
+
+def test_binding_refuses_what_does_not_fit(native):
+    M, K, N, L, r = 20, 64, 128, 3, 8
+    a, w1, w2 = (t.cuda() for t in make_inputs(M, K, N, 15))
+    wp, w3p = native.swiglu_pack_weights(w1, w2), native.swiglu_pack_down_weights(w1)
+    la, lb, scale = (t.cuda() for t in table(L, 2, r, K, N, 15))
+    index = indices(M, L, "mixed", 15).cuda()
+    good = dict(A=a, Wpacked=wp, N=N, La=la, Lb=lb, index=index, scale=scale)
+    down = dict(Y=a, W3packed=w3p, H=N, La=la[:, 0].contiguous(), Lb=lb[:, 0].contiguous(), index=index,
+                scale=scale)
+    native.swiglu_forward_lora(**good)
+    native.swiglu_down_forward_lora(**down)
+    bad = [dict(A=a.float()), dict(A=a.cpu()), dict(A=a[:, :32]), dict(Wpacked=wp[:64]), dict(N=136),
+           dict(La=la[:, :1]), dict(La=la[..., :32].contiguous()), dict(La=la[0]), dict(Lb=lb[:2]),
+           dict(Lb=lb.transpose(2, 3)), dict(index=index.long()), dict(index=index[:5]), dict(index=index.cpu()),
+           dict(scale=scale.half()), dict(scale=scale[:2]), dict(scale=scale.cpu()),
+           dict(Y=torch.empty(M, K, dtype=torch.bfloat16, device="cuda")),
+           dict(workspace=torch.empty(1 << 20, dtype=torch.uint8))]
+    for change in bad:
+        with pytest.raises(ValueError):
+            native.swiglu_forward_lora(**{**good, **change})
+            pytest.fail(f"not refused: {list(change)}")
+    for change in (dict(Y=a.half()), dict(W3packed=w3p[:9]), dict(H=256), dict(La=la), dict(R=a),
+                   dict(index=index[::2]), dict(Out=a.float())):
+        with pytest.raises(ValueError):
+            native.swiglu_down_forward_lora(**{**down, **change})
+            pytest.fail(f"not refused: {list(change)}")
+    # a rank that is no multiple of 8 is a matter of the library
+    with pytest.raises(native.SwigluError) as err:
+        native.swiglu_forward_lora(**{**good, "La": la[:, :, :4].contiguous(), "Lb": lb[..., :4].contiguous()})
+    assert err.value.code == native.SWIGLU_ERR_UNSUPPORTED
+
+
+def test_plans_reach_every_form(native):
+    # the tested shapes take both kernels, one and several token groups, K in one and several parts
+    plans = [native.swiglu_lora_plan_string(M, K, N, r) for M, K, N, _, r, _ in SHAPES]
+    assert any("large_m_pair" in p for p in plans) and any("groups=1 " in p for p in plans)
+    assert any("small_m" in p and "groups=3" in p for p in plans)
+    assert any("splits=8" in p for p in plans) and any("splits=1" in p for p in plans)
+    assert any("shrink dots" in p for p in plans) and any("shrink tiles" in p for p in plans)
+    down = [native.swiglu_down_lora_plan_string(M, N, H, r) for M, N, H, _, r, _ in SHAPES]
+    assert all(p.startswith("down lora shrink") for p in down)
+    assert "large_m_pair" in native.swiglu_lora_plan_string(4096, 3584, 18944, 64)
+    assert "small_m mt=16" in native.swiglu_lora_plan_string(16, 3584, 18944, 16)
