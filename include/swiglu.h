@@ -428,10 +428,8 @@ SWIGLU_API swiglu_status_t swiglu_down_backward(const void* dOut, const void* W3
  *
  * Sums are fp32, Gate, Up and their deltas meet in fp32 before SiLU, and each
  * output is rounded once; V is rounded to bf16, an operand of the tensor cores.
- * La and scale of one adapter never reach another's tokens, whatever their
- * values. Lb, like the shared weight, must be finite: an infinity or NaN in it
- * may also reach other tokens of the batch. Adapters that no token names are not
- * read.
+ * La, Lb and scale of one adapter never reach another's tokens, whatever their
+ * values. Adapters that no token names are not read.
  *
  * swiglu_lora_workspace_bytes(M, K, N, rank) and
  * swiglu_down_lora_workspace_bytes(M, N, H, rank): bytes of the workspace

@@ -27,7 +27,7 @@ STAMP = os.path.join(BUILD_DIR, "libswiglu.stamp")
 SOURCES = ["swiglu_api.cu", "pack.cu", "fused_large_m.cu", "fused_large_m_pair.cu", "fused_small_m.cu",
            "fused_sequential.cu", "fused_split_k.cu", "fused_resident_pair.cu", "backward_pair.cu",
            "backward_api.cu", "lora_shrink.cu", "lora_api.cu"]
-HEADERS = ["kernels.h", "ptx.cuh", "api_shared.h"]
+HEADERS = ["kernels.h", "ptx.cuh", "lora_lb.cuh", "api_shared.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-fvisibility=hidden",
                  "-Xptxas", "-v", "-I" + INCLUDE, "-I" + CSRC]

@@ -83,9 +83,13 @@
 // stage's. (Alternating adapter and K slices instead: 660 against 640 us on the
 // 7B shape, 4096 tokens of rank 64.) Measured there: 613 us against 572 without
 // adapters; the adapter slices' MMAs are 2 % of the tensor pipe's work, the waits
-// around them the rest. A zero row times a non-finite Lb value is NaN: adapters' Lb must be
-// finite, as the shared weight must.
+// around them the rest. Non-finite entries of an Lb stay with the tokens of that
+// adapter (lora_lb.cuh); each CTA's warps look through the rows that its own copy
+// brought, so an Lb copy signals its own CTA, and those warps the even one. (They write
+// the V of the next slice first: 631 us with the look as without it; 640 where they
+// looked through each slice before the next V.)
 #include "kernels.h"
+#include "lora_lb.cuh"
 #include "ptx.cuh"
 
 namespace swg {
@@ -107,14 +111,15 @@ struct PairCfg {
   static constexpr int kTmemCols = 2 * kAccCols;         // double buffered (bf16, per-tensor FP8)
   static constexpr int kStgBytes = 32 * 32 * 2;          // 32 rows x 64 B store staging
   static constexpr int kNumStg = 8;                      // 2 per warp, or 1 per warp with 8 warps
-  static constexpr int kBarBytes = 256;
+  static constexpr int kTaints = 16;  // adapters: tile rounds that keep a mark
+  static constexpr int kBarBytes = kLora ? 512 : 256;
   // block-scaled FP8: 1.5 KB of scales per stage (A block, gate and up weight blocks)
   static constexpr size_t kSmem = 1024 + size_t(kStages) * kStageBytes +
                                   size_t(kNumStg) * kStgBytes +
                                   (kMx ? size_t(kStages) * kSfStageBytes : 0) + kBarBytes;
   static_assert(kSmem <= 232448, "shared memory budget");
-  static constexpr int kBars = (kLora ? 4 : 3) * kStages + 6;
-  static_assert(8 * kBars + 8 <= kBarBytes, "barrier slots");
+  static constexpr int kBars = (kLora ? 5 : 3) * kStages + 6;
+  static_assert(8 * kBars + 8 + (kLora ? 4 * kTaints : 0) <= kBarBytes, "barrier slots");
   static constexpr int kSfCol = kAccCols;  // scale slots after the single accumulator
   static_assert(!kMx || kSfCol + kStages * kSfTmemCols <= kTmemCols, "tensor memory budget");
 };
@@ -190,14 +195,19 @@ __global__ void __launch_bounds__(PairCfg<kMx, kLora>::kThreadsT, 1)
                      (kMx ? size_t(C::kStages) * kSfStageBytes : 0);
   const uint32_t bar0 = smem_addr(bar_ptr);
   // barrier slots: full[S] | empty[S] | tmem_full[2] | tmem_empty[2] | drain |
-  // scales_ready[S] (adapters: V rows ready) | scale-copy drain | V slot free[S] (adapters)
+  // scales_ready[S] (adapters: V rows ready) | scale-copy drain | adapters: V slot free[S] |
+  // this CTA's Lb rows landed[S]
   const uint32_t full0 = bar0, empty0 = bar0 + 8u * C::kStages;
   const uint32_t tfull0 = bar0 + 16u * C::kStages, tempty0 = tfull0 + 16u;
   const uint32_t drain_bar = tempty0 + 16u;
   const uint32_t sready0 = drain_bar + 8u, sdrain_bar = sready0 + 8u * C::kStages;
-  const uint32_t vfree0 = sdrain_bar + 8u;
+  const uint32_t vfree0 = sdrain_bar + 8u, lbfull0 = vfree0 + 8u * C::kStages;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_ptr + 8 * C::kBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  // [round % kTaints] = round + 1: some Lb row of that round's tile was not finite.
+  // (The V warps are at most two accumulators and six stages ahead of the epilogue.)
+  volatile int* taint = abort_flag + 1;
+  static_assert(C::kTaints > 2 + C::kStages, "marks outlive the rounds in flight");
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -239,8 +249,13 @@ __global__ void __launch_bounds__(PairCfg<kMx, kLora>::kThreadsT, 1)
     // scale-copy commit, or (adapters) 4 warps x 2 CTAs (used on rank 0)
     for (int s = 0; s < C::kStages; ++s) mbar_init(sready0 + 8u * s, kLora ? 8 : 1);
     mbar_init(sdrain_bar, 1);
-    if constexpr (kLora)
-      for (int s = 0; s < C::kStages; ++s) mbar_init(vfree0 + 8u * s, 1);  // this CTA's producer
+    if constexpr (kLora) {
+      for (int s = 0; s < C::kStages; ++s) {
+        mbar_init(vfree0 + 8u * s, 1);  // this CTA's producer
+        mbar_init(lbfull0 + 8u * s, 1);
+      }
+      for (int i = 0; i < C::kTaints; ++i) taint[i] = 0;
+    }
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -260,6 +275,7 @@ __global__ void __launch_bounds__(PairCfg<kMx, kLora>::kThreadsT, 1)
       int s = 0;
       uint32_t ph = 0;
       uint32_t filled = 0, fill_ph = 0;
+      uint32_t lb_filled = 0, lb_ph = 0;  // adapters: phase of each stage's Lb barrier
       bool skip_once = p.inject_stall != 0;
       bool ok = true;
       // round pacing on the even CTA (the odd one follows through the empty
@@ -337,14 +353,17 @@ __global__ void __launch_bounds__(PairCfg<kMx, kLora>::kThreadsT, 1)
             }
             mbar_arrive(vfree0 + 8u * s);  // the stage's A half is free for V rows
             // this CTA's half of the MMA's N rows: 64 gate (up) columns, or 128 output columns
-            if (leader) mbar_arrive_expect_tx(full0 + 8u * s, 2 * C::kBBytes / kHalves);
+            if (leader) mbar_arrive(full0 + 8u * s);  // nothing to wait for: the V warps do
+            mbar_arrive_expect_tx(lbfull0 + 8u * s, C::kBBytes / kHalves);
             const int a = list[1 + i / kHalves];
             const int n0 = kDown ? nb * 2 * C::kBN + static_cast<int>(rank) * C::kBN
                                  : nb * C::kBN + static_cast<int>(rank) * (C::kBN / 2);
-            tma_load_3d_pair(sB + s * C::kBBytes, &p.tmap_lb, full0_lead + 8u * s, 0, n0,
-                             a * kHalves + i % kHalves);
+            tma_load_3d(sB + s * C::kBBytes, &p.tmap_lb, lbfull0 + 8u * s, 0, n0,
+                        a * kHalves + i % kHalves);
             filled |= 1u << s;
             fill_ph = (fill_ph & ~(1u << s)) | (ph << s);
+            lb_filled |= 1u << s;
+            lb_ph ^= 1u << s;
             if (++s == C::kStages) {
               s = 0;
               ph ^= 1u;
@@ -359,6 +378,8 @@ __global__ void __launch_bounds__(PairCfg<kMx, kLora>::kThreadsT, 1)
       if (leader)
         for (int i = 0; i < C::kStages; ++i)
           if (filled & (1u << i)) mbar_wait_drain(full0 + 8u * i, (fill_ph >> i) & 1u, wc);
+      for (int i = 0; kLora && i < C::kStages; ++i)  // lb_ph has been flipped past the last use
+        if (lb_filled & (1u << i)) mbar_wait_drain(lbfull0 + 8u * i, ((lb_ph >> i) & 1u) ^ 1u, wc);
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -489,10 +510,14 @@ __global__ void __launch_bounds__(PairCfg<kMx, kLora>::kThreadsT, 1)
     const int row = threadIdx.x - (64 + 32 * C::kEpiWarps);
     const uint32_t sready0_lead = mapa_shared(sready0, 0);
     const int chunks = p.lora_rank / 8, padded = (p.lora_rank + 15) / 16 * 2;
+    // this thread's Lb row of a slice: all of one of 128, or half of one of 64
+    const int lb_row = kDown ? row : row & 63, lb_begin = kDown ? 0 : row >> 6 << 2;
+    const int lb_end = kDown ? chunks : min(chunks, lb_begin + 4);
     int s = 0;        // stage, in step with the producer
-    uint32_t ph = 0;  // phase of each stage's V-slot-free barrier
+    uint32_t vph = 0, ph = 0;  // phases of each stage's V-slot-free and Lb barriers
+    int round = 0;
     bool ok = true;
-    for (int t = pair; ok && t < num_tiles; t += pairs) {
+    for (int t = pair; ok && t < num_tiles; t += pairs, ++round) {
       int mb, nb;
       pair_tile_coords(t, p.tiles_m, p.tiles_n, p.group_m, mb, nb);
       const int* list = p.lora_lists + static_cast<size_t>(mb) * kLoraListInts;
@@ -514,26 +539,37 @@ __global__ void __launch_bounds__(PairCfg<kMx, kLora>::kThreadsT, 1)
                                                                  : make_uint4(0u, 0u, 0u, 0u);
       const int ahead = list[1 + min(lane, max(extra / kHalves - 1, 0))];
       s = (s + num_kb) % C::kStages;
-      for (int i = 0; i < extra; ++i) {
-        const int at = i / kHalves;
-        const int a = at < 32 ? __shfl_sync(0xffffffffu, ahead, at) : list[1 + at];
-        int go = 1;
-        if (lane == 0) go = mbar_wait(vfree0 + 8u * s, (ph >> s) & 1u, wc, kSiteLora) ? 1 : 0;
-        go = __shfl_sync(0xffffffffu, go, 0);
-        if (!go) {
-          ok = false;
-          break;
-        }
-        ph ^= 1u << s;
-        const uint32_t dst = sA + s * C::kABytes + row * 128;
+      // V of slice i is written before the Lb rows of slice i - 1 are looked through: the
+      // stage after this one is free by then (more than two stages)
+      for (int i = 0; i <= extra; ++i) {
+        if (i < extra) {
+          const int at = i / kHalves, sv = (s + min(i, 1)) % C::kStages;
+          const int a = at < 32 ? __shfl_sync(0xffffffffu, ahead, at) : list[1 + at];
+          ok = __all_sync(0xffffffffu, mbar_wait(vfree0 + 8u * sv, (vph >> sv) & 1u, wc, kSiteLora));
+          if (!ok) break;
+          vph ^= 1u << sv;
+          const uint32_t dst = sA + sv * C::kABytes + row * 128;
 #pragma unroll
-        for (int c = 0; c < kChunks; ++c)
-          if (c < padded) {
-            uint4 w = make_uint4(0u, 0u, 0u, 0u);
-            if (a == own) w = kHalves == 2 && (i & 1) ? x[kHalves - 1][c] : x[0][c];
-            st_shared_v4(dst + ((c ^ (row & 7)) << 4), w.x, w.y, w.z, w.w);
-          }
-        fence_proxy_async_smem();
+          for (int c = 0; c < kChunks; ++c)
+            if (c < padded) {
+              uint4 w = make_uint4(0u, 0u, 0u, 0u);
+              if (a == own) w = kHalves == 2 && (i & 1) ? x[kHalves - 1][c] : x[0][c];
+              st_shared_v4(dst + ((c ^ (row & 7)) << 4), w.x, w.y, w.z, w.w);
+            }
+          fence_proxy_async_smem();
+        }
+        if (i == 0) continue;
+        ok = __all_sync(0xffffffffu, mbar_wait(lbfull0 + 8u * s, (ph >> s) & 1u, wc, kSiteLora));
+        if (!ok) break;
+        ph ^= 1u << s;
+        if (clean_lb_row<kDown ? kChunks : kChunks / 2>(sB + s * C::kBBytes, lb_row, lb_begin, lb_end)) {
+          // both CTAs' epilogues read columns made from this row
+          const uint32_t mark = smem_addr(const_cast<int*>(taint)) + 4u * (round % C::kTaints);
+          st_shared_cluster(mapa_shared(mark, 0), round + 1);
+          st_shared_cluster(mapa_shared(mark, 1), round + 1);
+          fence_proxy_async_smem();
+          __threadfence();
+        }
         __syncwarp();
         // Every writer has made its rows visible to the tensor core's reads of this
         // CTA's own shared memory; the arrival only lets the even CTA issue the MMA.
@@ -552,7 +588,8 @@ __global__ void __launch_bounds__(PairCfg<kMx, kLora>::kThreadsT, 1)
     int buf = 0;
     uint32_t acc_ph = 0;
     int sbuf = 0;
-    for (int t = pair; t < num_tiles; t += pairs) {
+    int round = 0;
+    for (int t = pair; t < num_tiles; t += pairs, ++round) {
       int mb, nb;
       pair_tile_coords(t, p.tiles_m, p.tiles_n, p.group_m, mb, nb);
       const int row0 = mb * 2 * kTileM + static_cast<int>(rank) * kTileM + q * 32;
@@ -563,6 +600,13 @@ __global__ void __launch_bounds__(PairCfg<kMx, kLora>::kThreadsT, 1)
       if (!ok) break;
       tc_fence_after();
       const uint32_t tacc = tmem_base + lane_off + buf * C::kAccCols;
+      // adapters: what this row's own Lb lost (lora_lb.cuh), in a marked tile
+      int own = -1;
+      if (kLora && taint[round % C::kTaints] == round + 1 && row0 + lane < p.M)
+        own = p.lora_index[row0 + lane];
+      const bool restore = own >= 0 && own < p.lora_count;
+      const size_t own_lb = static_cast<size_t>(own) * kHalves * p.N;
+      const size_t own_v = (static_cast<size_t>(row0) + lane) * kHalves;
       if constexpr (kMx) {
         // this warp's 64 output columns [64 h, 64 h + 64): gate and up, all loaded
         // before the accumulator is released to the next tile's MMAs
@@ -623,6 +667,15 @@ __global__ void __launch_bounds__(PairCfg<kMx, kLora>::kThreadsT, 1)
             if (lane == 0) mbar_arrive_cluster(tempty0_lead + 8u * buf);
           }
           const int ncol = col0 + c * 32;
+          if (kLora && restore) {
+#pragma unroll 1
+            for (int j = 0; j < 32 && ncol + j < p.N; ++j) {
+              const float d = nonfinite_delta(p.lora_lb, own_lb + ncol + j, p.lora_v, own_v, p.lora_rank);
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (e == j) a[e] = __float_as_uint(__uint_as_float(a[e]) + d);
+            }
+          }
           float add[32];
 #pragma unroll
           for (int gq = 0; gq < 4; ++gq) {  // 8 columns (16 bytes) at a time; N % 8 == 0
@@ -674,6 +727,21 @@ __global__ void __launch_bounds__(PairCfg<kMx, kLora>::kThreadsT, 1)
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(tempty0_lead + 8u * buf);
+          }
+          if (kLora && restore) {
+            const int ncol = col0 + c * 32;
+#pragma unroll 1
+            for (int j = 0; j < 32 && ncol + j < p.N; ++j) {
+              const size_t lb_row = own_lb + ncol + j;
+              const float dg = nonfinite_delta(p.lora_lb, lb_row, p.lora_v, own_v, p.lora_rank);
+              const float du = nonfinite_delta(p.lora_lb, lb_row + p.N, p.lora_v, own_v + 1, p.lora_rank);
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (e == j) {
+                  g[e] = __float_as_uint(__uint_as_float(g[e]) + dg);
+                  u[e] = __float_as_uint(__uint_as_float(u[e]) + du);
+                }
+            }
           }
           if (lane == 0) bulk_wait_read<1>();
           __syncwarp();
@@ -727,7 +795,9 @@ cudaLaunchConfig_t pair_config(int grid, cudaStream_t stream, cudaLaunchAttribut
   cfg.blockDim = dim3(mx     ? PairCfg<true>::kThreadsT
                       : lora ? PairCfg<false, true>::kThreadsT
                              : PairCfg<false>::kThreadsT);
-  cfg.dynamicSmemBytes = mx ? PairCfg<true>::kSmem : PairCfg<false>::kSmem;
+  cfg.dynamicSmemBytes = mx     ? PairCfg<true>::kSmem
+                         : lora ? PairCfg<false, true>::kSmem
+                                : PairCfg<false>::kSmem;
   cfg.stream = stream;
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;

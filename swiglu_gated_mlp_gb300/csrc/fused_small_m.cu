@@ -53,13 +53,17 @@
 // dealt to the parts. Deltas as fp32 FMAs, thread = weight column, were built
 // first: as fast at 16 tokens of rank 16, but 300 against 71 us at 128 tokens of
 // rank 64 (7B shape), where each token re-read its adapter's rows. Measured, 7B
-// gate/up, 16 tokens, rank 16, with the shrink: 44.8 us for one adapter, 49.3 for
+// gate/up, 16 tokens, rank 16, with the shrink: 44.8 us for one adapter, 49.5 for
 // 8 (284 MB, 5.8 TB/s = 0.86 of copy), against 41 without adapters: 2 us are the
 // second launch, 3.5 us the shrink, then half a microsecond an adapter (1.2 MB of
 // Lb through ring stages that hold 32 KB of weight otherwise).
-// A zero row times a non-finite Lb value is NaN: Lb must be finite, as the
-// shared weight must.
+// Non-finite entries of an Lb stay with the tokens of that adapter (lora_lb.cuh):
+// the epilogue's warps, idle until the accumulators are complete, look through
+// each slice beside the V warps (0.4 us of the 49.5 with 8 adapters, 0.8 of 31 at
+// 333 tokens of 10 adapters; done by the V warps, between writing V and their
+// arrival, it took 1.4 and 2).
 #include "kernels.h"
+#include "lora_lb.cuh"
 #include "ptx.cuh"
 
 namespace swg {
@@ -228,6 +232,7 @@ __global__ void __launch_bounds__(kLora ? kLoraThreads : kThreads, kLora ? 2 : 1
   const uint32_t list_bar = vready0 + 8u * kMaxStages;
   volatile int* list = reinterpret_cast<volatile int*>(lora_ptr + 8 * (2 * kMaxStages + 2));
   int* ids = reinterpret_cast<int*>(lora_ptr + 1024);
+  volatile int* tainted = ids + 132;  // some Lb row of this CTA's adapters was not finite
 
   // accumulators: gate [0, mt), up [mt, 2 mt); then kSfTmemCols scale columns per stage
   const uint32_t sf_col = 2u * mt;
@@ -281,9 +286,10 @@ __global__ void __launch_bounds__(kLora ? kLoraThreads : kThreads, kLora ? 2 : 1
       prefetch_tmap(&p.tmap_lb);
       for (int s = 0; s < stages; ++s) {
         mbar_init(vfree0 + 8u * s, 1);
-        mbar_init(vready0 + 8u * s, 4);
+        mbar_init(vready0 + 8u * s, 8);  // the V warps, and the ones that look through Lb
       }
       mbar_init(list_bar, 4);
+      *tainted = 0;
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -307,6 +313,11 @@ __global__ void __launch_bounds__(kLora ? kLoraThreads : kThreads, kLora ? 2 : 1
   const int lead = min(stages, kb_end - kb_begin);
   const int per_adapter = kLora ? lora_slices_per_adapter(kDown, p.lora_rank) : 0;
   const auto adapter_slices = [&] { return (max(list[0] - kpart, 0) + kparts - 1) / kparts * per_adapter; };
+  // position of an adapter slice in the pipeline: between `rest` weight slices, then after them
+  const auto adapter_use = [&](int i) {
+    const int rest = kb_end - kb_begin - lead;
+    return i <= rest ? lead + 2 * i : kb_end - kb_begin + i;
+  };
   const auto adapter_at = [&](int i) { return list[1 + kpart + i / per_adapter * kparts]; };
 
   if (warp == 0) {
@@ -535,10 +546,9 @@ __global__ void __launch_bounds__(kLora ? kLoraThreads : kThreads, kLora ? 2 : 1
     named_barrier(1, 128);  // the list is complete
     // V of each adapter slice, in the swizzled rows a TMA load would write
     const int extra = adapter_slices();
-    const int rest = kb_end - kb_begin - lead;  // weight slices the adapter slices alternate with
     uint32_t vph = 0;
     for (int i = 0; i < extra; ++i) {
-      const int s = (i <= rest ? lead + 2 * i : kb_end - kb_begin + i) % stages;
+      const int s = adapter_use(i) % stages;
       int go = 1;
       if (lane == 0) go = mbar_wait(vfree0 + 8u * s, (vph >> s) & 1u, wc, kSiteLora) ? 1 : 0;
       go = __shfl_sync(0xffffffffu, go, 0);
@@ -572,9 +582,71 @@ __global__ void __launch_bounds__(kLora ? kLoraThreads : kThreads, kLora ? 2 : 1
     const uint32_t lane_off = static_cast<uint32_t>(q * 32) << 16;
     const int n = nblk * kPackBlockN + q * 32 + lane;  // this thread's output column
     int ok = 1;
+    if constexpr (kLora) {
+      // until the accumulators are complete: each adapter slice's Lb rows, two a thread or
+      // one. (The wait for the stage's V slot keeps the one for its load in step.)
+      const int row = q * 32 + lane;
+      const int extra = __all_sync(0xffffffffu, mbar_wait(list_bar, 0, wc, kSiteLora)) ? adapter_slices() : 0;
+      uint32_t vph = 0;
+      for (int i = 0; i < extra; ++i) {
+        const int use = adapter_use(i), s = use % stages;
+        if (!__all_sync(0xffffffffu, mbar_wait(vfree0 + 8u * s, (vph >> s) & 1u, wc, kSiteLora) &&
+                                         mbar_wait(full0 + 8u * s, (use / stages) & 1, wc, kSiteLora)))
+          break;
+        vph ^= 1u << s;
+        const uint32_t lb = s0 + s * stage_bytes;
+        bool cleaned = clean_lb_row<kLoraMaxRank / 8>(lb, row, 0, p.lora_rank / 8);
+        if (per_adapter == 1)
+          cleaned |= clean_lb_row<kLoraMaxRank / 8>(lb + kWStageBytes / 2, row, 0, p.lora_rank / 8);
+        if (cleaned) {
+          *tainted = 1;
+          fence_proxy_async_smem();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(vready0 + 8u * s);
+      }
+    }
     if (lane == 0) ok = mbar_wait(tfull_bar, 0, wc, kSiteEpiTmemFull) ? 1 : 0;
     ok = __shfl_sync(0xffffffffu, ok, 0);
-    if (ok && kparts > 1) {
+    if (kLora && ok && *tainted) {
+      // As below, a token at a time, each with what its own adapter's Lb row lost
+      tc_fence_after();
+      __nv_bfloat16* y = reinterpret_cast<__nv_bfloat16*>(p.y);
+      const __nv_bfloat16* res = reinterpret_cast<const __nv_bfloat16*>(p.residual);
+      float* part_buf = reinterpret_cast<float*>(smem);
+      const int r = q * 32 + lane;
+      constexpr int kHalves = kDown ? 1 : 2;
+      const int n_lo = kDown ? nblk * 2 * kPackBlockN + r : n, n_hi = kDown ? n_lo + kPackBlockN : n;
+#pragma unroll 1
+      for (int m = 0; m < mcount; ++m) {
+        const uint32_t gw = tmem_ld_x1(tmem_base + lane_off + m);
+        const uint32_t uw = tmem_ld_x1(tmem_base + lane_off + mt + m);
+        tmem_wait_ld();
+        float g = __uint_as_float(gw), u = __uint_as_float(uw);
+        const int a = ids[m];
+        if (a >= 0) {
+          const size_t lb_row = static_cast<size_t>(a) * kHalves * p.N;
+          const size_t v_row = (static_cast<size_t>(m0) + m) * kHalves;
+          if (n_lo < p.N) g += nonfinite_delta(p.lora_lb, lb_row + n_lo, p.lora_v, v_row, p.lora_rank);
+          if (n_hi < p.N)
+            u += nonfinite_delta(p.lora_lb, lb_row + (kDown ? 0 : p.N) + n_hi, p.lora_v,
+                                 v_row + kHalves - 1, p.lora_rank);
+        }
+        __syncwarp();
+        const size_t row = (static_cast<size_t>(m0) + m) * p.N;
+        if (kparts > 1) {
+          part_buf[m * kPackBlockN + r] = g;
+          part_buf[(mt + m) * kPackBlockN + r] = u;
+        } else if (kDown) {
+          if (n_lo < p.N)
+            y[row + n_lo] = __float2bfloat16_rn(g + (res ? __bfloat162float(res[row + n_lo]) : 0.0f));
+          if (n_hi < p.N)
+            y[row + n_hi] = __float2bfloat16_rn(u + (res ? __bfloat162float(res[row + n_hi]) : 0.0f));
+        } else if (n < p.N) {
+          y[row + n] = __float2bfloat16_rn(silu_mul(g, u));
+        }
+      }
+    } else if (ok && kparts > 1) {
       // K part only: fp32 partials to this CTA's shared memory (the ring is idle
       // now), as P[c][r] for accumulator column c (gate 0..mt-1, up mt..2mt-1)
       // and weight row r of the block.

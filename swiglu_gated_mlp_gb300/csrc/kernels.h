@@ -53,6 +53,7 @@ struct LargeMParams {
   int lora;
   int lora_rank, lora_count;
   const void* lora_v;
+  const void* lora_lb;  // Lb itself (lora_lb.cuh)
   const int* lora_index;
   const int* lora_lists;
 };
@@ -92,6 +93,7 @@ struct SmallMParams {
   int lora;
   int lora_rank, lora_count;
   const void* lora_v;
+  const void* lora_lb;  // Lb itself (lora_lb.cuh)
   const int* lora_index;
 };
 

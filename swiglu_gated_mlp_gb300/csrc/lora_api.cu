@@ -212,6 +212,7 @@ swiglu_status_t run_call(const Call& c, cudaStream_t stream) {
     p.lora_rank = static_cast<int>(c.rank);
     p.lora_count = static_cast<int>(c.count);
     p.lora_v = c.ws;
+    p.lora_lb = c.lb;
     p.lora_index = c.index;
     p.tmap_lb = tmap_lb;
     p.status = d.status;
@@ -244,6 +245,7 @@ swiglu_status_t run_call(const Call& c, cudaStream_t stream) {
     p.lora_rank = static_cast<int>(c.rank);
     p.lora_count = static_cast<int>(c.count);
     p.lora_v = c.ws;
+    p.lora_lb = c.lb;
     p.lora_index = c.index;
     p.lora_lists = lists;
     p.status = d.status;

@@ -341,3 +341,53 @@ def test_plans_reach_every_form(native):
     assert all(p.startswith("down lora shrink") for p in down)
     assert "large_m_pair" in native.swiglu_lora_plan_string(4096, 3584, 18944, 64)
     assert "small_m mt=16" in native.swiglu_lora_plan_string(16, 3584, 18944, 16)
+
+
+@pytest.mark.parametrize("rank", [8, 40])
+@pytest.mark.parametrize("M, K, N", [
+    (24, 200, 264),     # decode kernel, K whole
+    (24, 2048, 520),    # K over a cluster, adapters dealt to its CTAs
+    (200, 712, 392),    # token groups
+    (1200, 200, 1032),  # CTA pairs, ragged last tiles
+])
+def test_non_finite_lb_stays_with_its_tokens(native, M, K, N, rank):
+    # some columns of adapter 1's Lb hold an infinity or NaN: exactly its tokens' outputs
+    # there are not finite, every other output keeps its bits
+    a, w1, w2 = (t.cuda() for t in make_inputs(M, K, N, 2))
+    wp = native.swiglu_pack_weights(w1, w2)
+    la, lb, scale = (t.cuda() for t in table(3, 2, rank, K, N, 2))
+    index = (torch.arange(M, dtype=torch.int32, device="cuda") * 7) % 4 - 1
+    theirs = index == 1
+    want = native.swiglu_forward_lora(a, wp, N, la, lb, index, scale)
+    lb[1, 1, 0, 0] = float("nan")          # up
+    lb[1, 1, 70, rank - 1] = float("inf")
+    lb[1, 1, N - 1, 3] = float("-inf")
+    lb[1, 0, 127, 5] = float("nan")        # gate
+    lb[1, 0, 128, :] = float("nan")
+    cols = torch.zeros(N, dtype=torch.bool, device="cuda")
+    cols[[0, 70, 127, 128, N - 1]] = True
+    got = native.swiglu_forward_lora(a, wp, N, la, lb, index, scale)
+    native.swiglu_check_device_status()
+    hit = theirs[:, None] & cols[None, :]
+    assert torch.equal(got[~hit], want[~hit])
+    assert not got[hit].isfinite().any()
+
+    w3p = native.swiglu_pack_down_weights(w1)
+    res = make_inputs(M, N, 8, 5)[0].cuda()
+    la3, lb3, scale3 = (t.cuda() for t in table(3, 1, rank, K, N, 3))
+    want = native.swiglu_down_forward_lora(a, w3p, N, la3, lb3, index, scale3, R=res)
+    lb3[1, 0, 0] = float("nan")
+    lb3[1, 70, rank - 1] = float("inf")
+    lb3[1, N - 1, 3] = float("-inf")
+    lb3[1, [127, 128], 5] = float("nan")
+    got = res.clone()
+    native.swiglu_down_forward_lora(a, w3p, N, la3, lb3, index, scale3, R=got, Out=got)
+    native.swiglu_check_device_status()
+    assert torch.equal(got[~hit], want[~hit])
+    assert not got[hit].isfinite().any()
+    # one infinity: its sign is that of the token's V, which one more call with a zero
+    # weight and a one in its place shows
+    only = torch.zeros_like(lb3)
+    only[1, 70, rank - 1] = 1.0
+    v = native.swiglu_down_forward_lora(a, torch.zeros_like(w3p), N, la3, only, index, scale3)[theirs, 70]
+    assert torch.equal(got[theirs, 70], (v.float() * float("inf")).to(torch.bfloat16))
