@@ -49,14 +49,18 @@
 // up to 32 share a slice, V1 and V2 side by side; above that they take one
 // each). Four more warps, thread = token, list the adapters and write V; the
 // adapter slices alternate with weight slices once the ring has filled, so that
-// they pass while the weight stream is waited for. With K split, adapters are
-// dealt to the parts. Deltas as fp32 FMAs, thread = weight column, were built
-// first: as fast at 16 tokens of rank 16, but 300 against 71 us at 128 tokens of
-// rank 64 (7B shape), where each token re-read its adapter's rows. Measured, 7B
-// gate/up, 16 tokens, rank 16, with the shrink: 44.8 us for one adapter, 49.5 for
-// 8 (284 MB, 5.8 TB/s = 0.86 of copy), against 41 without adapters: 2 us are the
-// second launch, 3.5 us the shrink, then half a microsecond an adapter (1.2 MB of
-// Lb through ring stages that hold 32 KB of weight otherwise).
+// they pass while the weight stream is waited for. For a token or a few of a small
+// rank every CTA makes V itself with these warps and the epilogue's (own_v() in
+// lora_api.cu), without a kernel before it: 9.3 -> 8.1 us for 1 token of rank 8, K
+// 896, N 4864, and one launch less on the host (17.2 -> 15 us from Python).
+// With K split, adapters are dealt to the parts. Deltas as fp32 FMAs, thread =
+// weight column, were built first: as fast at 16 tokens of rank 16, but 300
+// against 71 us at 128 tokens of rank 64 (7B shape), where each token re-read
+// its adapter's rows. Measured, 7B gate/up, 16 tokens, rank 16, with the
+// shrink: 44.8 us for one adapter, 49.5 for 8 (284 MB, 5.8 TB/s = 0.86 of
+// copy), against 41 without adapters: 2 us are the second launch, 3.5 us the
+// shrink, then half a microsecond an adapter (1.2 MB of Lb through ring stages
+// that hold 32 KB of weight otherwise).
 // Non-finite entries of an Lb stay with the tokens of that adapter (lora_lb.cuh):
 // the epilogue's warps, idle until the accumulators are complete, look through
 // each slice beside the V warps (0.4 us of the 49.5 with 8 adapters, 0.8 of 31 at
@@ -195,6 +199,50 @@ __device__ __noinline__ void cross_cluster_finish(const SmallMParams& p, int uni
 
 constexpr int kLoraThreads = kThreads + 128;  // kLora: four warps write V
 constexpr int kLoraSmem = 2048;               // kLora: more barriers, the tokens' and the listed adapters
+constexpr int kLoraOwnWarps = 8;              // kLora: warps that make V where the CTA does
+
+// V = scale_a * x La[a]^T of a few tokens, in shared memory: warp w of kLoraOwnWarps
+// takes every kLoraOwnWarps-th pair of rows of a token, its lanes K, with the loads
+// of 1024 of K under way together.
+__device__ __noinline__ void make_own_v(const SmallMParams& p, int hr, __nv_bfloat16* v, int w) {
+  constexpr int kBatch = 4;
+  const int lane = threadIdx.x & 31;
+  const int chunks = p.K / 8, pairs = hr / 2;
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+  for (int i = w; i < p.M * pairs; i += kLoraOwnWarps) {
+    const int m = i / pairs, r0 = i % pairs * 2;
+    const int a = __ldg(p.lora_index + m);
+    uint32_t out = 0;
+    if (a >= 0 && a < p.lora_count) {
+      const float s = __ldg(p.lora_scale + a);
+      const uint4* x = static_cast<const uint4*>(p.lora_x) + static_cast<size_t>(m) * chunks;
+      const uint4* la = static_cast<const uint4*>(p.lora_la) + (static_cast<size_t>(a) * hr + r0) * chunks;
+      float acc0 = 0.0f, acc1 = 0.0f;
+      for (int c0 = lane; c0 < chunks; c0 += 32 * kBatch) {
+        uint4 xv[kBatch], l0[kBatch], l1[kBatch];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+          const int c = c0 + 32 * j;
+          xv[j] = c < chunks ? __ldg(x + c) : zero;
+          l0[j] = c < chunks ? __ldg(la + c) : zero;
+          l1[j] = c < chunks ? __ldg(la + chunks + c) : zero;
+        }
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+          acc0 = dot8(xv[j], l0[j], acc0);
+          acc1 = dot8(xv[j], l1[j], acc1);
+        }
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        acc0 += __shfl_xor_sync(0xffffffffu, acc0, o);
+        acc1 += __shfl_xor_sync(0xffffffffu, acc1, o);
+      }
+      out = pack_bf16x2(s * acc0, s * acc1);
+    }
+    if (lane == 0) *reinterpret_cast<uint32_t*>(v + m * hr + r0) = out;
+  }
+}
 
 // Slices of one adapter: gate and up of a rank above 32 do not fit one row of V.
 __device__ __forceinline__ int lora_slices_per_adapter(bool down, int rank) {
@@ -233,6 +281,9 @@ __global__ void __launch_bounds__(kLora ? kLoraThreads : kThreads, kLora ? 2 : 1
   volatile int* list = reinterpret_cast<volatile int*>(lora_ptr + 8 * (2 * kMaxStages + 2));
   int* ids = reinterpret_cast<int*>(lora_ptr + 1024);
   volatile int* tainted = ids + 132;  // some Lb row of this CTA's adapters was not finite
+  // V [mcount, halves * rank] from the first kernel, or made here
+  const bool own_v = kLora && p.lora_own_v != 0;
+  __nv_bfloat16* own = reinterpret_cast<__nv_bfloat16*>(lora_ptr + kLoraSmem);
 
   // accumulators: gate [0, mt), up [mt, 2 mt); then kSfTmemCols scale columns per stage
   const uint32_t sf_col = 2u * mt;
@@ -310,7 +361,8 @@ __global__ void __launch_bounds__(kLora ? kLoraThreads : kThreads, kLora ? 2 : 1
 
   // Adapter slices alternate with weight slices after the first `lead` of those;
   // this K part has every kparts-th adapter of the list.
-  const int lead = min(stages, kb_end - kb_begin);
+  // (All after them where V is made here: the first ones would hold up the weight.)
+  const int lead = own_v ? kb_end - kb_begin : min(stages, kb_end - kb_begin);
   const int per_adapter = kLora ? lora_slices_per_adapter(kDown, p.lora_rank) : 0;
   const auto adapter_slices = [&] { return (max(list[0] - kpart, 0) + kparts - 1) / kparts * per_adapter; };
   // position of an adapter slice in the pipeline: between `rest` weight slices, then after them
@@ -504,21 +556,9 @@ __global__ void __launch_bounds__(kLora ? kLoraThreads : kThreads, kLora ? 2 : 1
   } else if (kLora && warp >= 6) {
     // ------------------------------------------------ adapters: list and V
     const int row = threadIdx.x - kThreads;  // this thread's token of the group
-    const int own = row < mcount ? __ldg(p.lora_index + m0 + row) : -1;
-    const bool has = own >= 0 && own < p.lora_count;
-    ids[row] = has ? own : -1;
-    // the token's V, zero past the rank
-    constexpr int kChunks = kLoraMaxRank / 8;
-    constexpr int kHalves = kDown ? 1 : 2;
-    const int chunks = p.lora_rank / 8, ksteps = (p.lora_rank + 15) / 16;
-    const uint4* v = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.lora_v) +
-                                                    (static_cast<size_t>(m0) + row) * p.lora_rank * kHalves);
-    uint4 x[kHalves][kChunks];
-#pragma unroll
-    for (int h = 0; h < kHalves; ++h)
-#pragma unroll
-      for (int c = 0; c < kChunks; ++c)
-        x[h][c] = has && c < chunks ? __ldg(v + h * chunks + c) : make_uint4(0u, 0u, 0u, 0u);
+    const int mine = row < mcount ? __ldg(p.lora_index + m0 + row) : -1;
+    const bool has = mine >= 0 && mine < p.lora_count;
+    ids[row] = has ? mine : -1;
     named_barrier(1, 128);
     // the adapters present, in the order of their first token
     bool first = has;
@@ -527,7 +567,7 @@ __global__ void __launch_bounds__(kLora ? kLoraThreads : kThreads, kLora ? 2 : 1
       const int y[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        if (t + e < row && y[e] == own) first = false;
+        if (t + e < row && y[e] == mine) first = false;
     }
     const uint32_t votes = __ballot_sync(0xffffffffu, first);
     int* counts = ids + 128;
@@ -539,11 +579,28 @@ __global__ void __launch_bounds__(kLora ? kLoraThreads : kThreads, kLora ? 2 : 1
       if (w < warp - 6) at += counts[w];
       present += counts[w];
     }
-    if (first) list[1 + at] = own;
+    if (first) list[1 + at] = mine;
     if (row == 0) list[0] = present;
     __syncwarp();
     if (lane == 0) mbar_arrive(list_bar);
     named_barrier(1, 128);  // the list is complete
+    // the token's V, zero past the rank
+    constexpr int kChunks = kLoraMaxRank / 8;
+    constexpr int kHalves = kDown ? 1 : 2;
+    const int chunks = p.lora_rank / 8, ksteps = (p.lora_rank + 15) / 16;
+    if (own_v) {
+      make_own_v(p, p.lora_rank * kHalves, own, warp - 2);
+      named_barrier(2, 32 * kLoraOwnWarps);
+    }
+    const uint4* v = reinterpret_cast<const uint4*>(
+        own_v ? own : static_cast<const __nv_bfloat16*>(p.lora_v) + static_cast<size_t>(m0) * p.lora_rank * kHalves) +
+        static_cast<size_t>(row) * chunks * kHalves;
+    uint4 x[kHalves][kChunks];
+#pragma unroll
+    for (int h = 0; h < kHalves; ++h)
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c)
+        x[h][c] = has && c < chunks ? v[h * chunks + c] : make_uint4(0u, 0u, 0u, 0u);
     // V of each adapter slice, in the swizzled rows a TMA load would write
     const int extra = adapter_slices();
     uint32_t vph = 0;
@@ -555,7 +612,7 @@ __global__ void __launch_bounds__(kLora ? kLoraThreads : kThreads, kLora ? 2 : 1
       if (!go) break;
       vph ^= 1u << s;
       if (row < mt) {
-        const bool keep = has && adapter_at(i) == own;
+        const bool keep = has && adapter_at(i) == mine;
         const int h = i % per_adapter;
         const uint32_t dst = s0 + s * stage_bytes + kWStageBytes + row * 128;
 #pragma unroll
@@ -586,6 +643,10 @@ __global__ void __launch_bounds__(kLora ? kLoraThreads : kThreads, kLora ? 2 : 1
       // until the accumulators are complete: each adapter slice's Lb rows, two a thread or
       // one. (The wait for the stage's V slot keeps the one for its load in step.)
       const int row = q * 32 + lane;
+      if (own_v) {
+        make_own_v(p, p.lora_rank * (kDown ? 1 : 2), own, warp - 2);
+        named_barrier(2, 32 * kLoraOwnWarps);
+      }
       const int extra = __all_sync(0xffffffffu, mbar_wait(list_bar, 0, wc, kSiteLora)) ? adapter_slices() : 0;
       uint32_t vph = 0;
       for (int i = 0; i < extra; ++i) {
@@ -626,10 +687,11 @@ __global__ void __launch_bounds__(kLora ? kLoraThreads : kThreads, kLora ? 2 : 1
         const int a = ids[m];
         if (a >= 0) {
           const size_t lb_row = static_cast<size_t>(a) * kHalves * p.N;
-          const size_t v_row = (static_cast<size_t>(m0) + m) * kHalves;
-          if (n_lo < p.N) g += nonfinite_delta(p.lora_lb, lb_row + n_lo, p.lora_v, v_row, p.lora_rank);
+          const void* v = own_v ? own : p.lora_v;
+          const size_t v_row = ((own_v ? 0 : static_cast<size_t>(m0)) + m) * kHalves;
+          if (n_lo < p.N) g += nonfinite_delta(p.lora_lb, lb_row + n_lo, v, v_row, p.lora_rank);
           if (n_hi < p.N)
-            u += nonfinite_delta(p.lora_lb, lb_row + (kDown ? 0 : p.N) + n_hi, p.lora_v,
+            u += nonfinite_delta(p.lora_lb, lb_row + (kDown ? 0 : p.N) + n_hi, v,
                                  v_row + kHalves - 1, p.lora_rank);
         }
         __syncwarp();
@@ -880,7 +942,12 @@ cudaError_t launch_small_m(const SmallMParams& p, cudaStream_t stream) {
     return cudaErrorInvalidValue;
   // adapters: a thread for every token of a group, one cluster per unit
   if (p.lora && (p.fp8 || gsplits > 1 || p.mt > 128 || p.lora_rank < 8 || (p.lora_rank % 8) != 0 ||
-                 p.lora_rank > kLoraMaxRank || !p.lora_v || !p.lora_index))
+                 p.lora_rank > kLoraMaxRank || (!p.lora_v && !p.lora_own_v) || !p.lora_index))
+    return cudaErrorInvalidValue;
+  // V made by every CTA: few tokens, in one group
+  const int own_values = p.M * p.lora_rank * (p.down ? 1 : 2);
+  if (p.lora_own_v && (!p.lora || p.mgroups > 1 || p.M > p.mt || own_values > kLoraOwnValues || !p.lora_x ||
+                       !p.lora_la || !p.lora_scale))
     return cudaErrorInvalidValue;
   const int extra = p.mx ? kSfStageBytes : 0;
   SmallMParams q = p;
@@ -888,7 +955,8 @@ cudaError_t launch_small_m(const SmallMParams& p, cudaStream_t stream) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(p.grid);
   cfg.blockDim = dim3(p.lora ? kLoraThreads : kThreads);
-  cfg.dynamicSmemBytes = small_m_smem_bytes(p.mt, p.stages, extra) + (p.lora ? kLoraSmem : 0);
+  cfg.dynamicSmemBytes = small_m_smem_bytes(p.mt, p.stages, extra) + (p.lora ? kLoraSmem : 0) +
+                         (p.lora_own_v ? size_t(own_values) * 2 : 0);
   if (cfg.dynamicSmemBytes > kSmemLimit) return cudaErrorInvalidValue;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];

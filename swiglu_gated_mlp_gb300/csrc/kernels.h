@@ -26,6 +26,7 @@ constexpr int kSfTmemCols = 16;                   // TMEM columns per stage of s
 // to this; the pair kernel's lists hold a count and up to 256 adapters a tile.
 constexpr int kLoraMaxRank = 64;
 constexpr int kLoraListInts = 260;
+constexpr int kLoraOwnValues = 1024;  // V values that a decode CTA may make itself
 
 struct LargeMParams {
   CUtensorMap tmap_a;  // A  [M, K]       box {64, 128}, 128-B swizzle
@@ -95,6 +96,11 @@ struct SmallMParams {
   const void* lora_v;
   const void* lora_lb;  // Lb itself (lora_lb.cuh)
   const int* lora_index;
+  // lora_own_v: every CTA makes V itself, from x, La and the scales; no lora_v
+  int lora_own_v;
+  const void* lora_x;
+  const void* lora_la;
+  const float* lora_scale;
 };
 
 // V = scale_a * x La[a]^T of each token's adapter a = index[token]

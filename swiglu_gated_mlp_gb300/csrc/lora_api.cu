@@ -71,6 +71,22 @@ int shrink_splits(int64_t tiles, int64_t slices, int sm_count) {
   return 1;
 }
 
+// Whether every decode CTA makes V itself (make_own_v()), in place of a kernel
+// before it. A step there, 2 rows of V for each of 8 warps over 1024 of K, takes
+// 1.5 us, a slice of weight that streams meanwhile 0.7. Measured, made inside
+// against outside: K 896 N 4864, 7 slices a CTA, 1 token of rank 8 / 16 / 32 (1, 2, 4
+// steps) 8.3 / 9.5, 9.0 / 9.6, 12.2 / 9.7 us; K 3584 N 18944, 56 slices, 1 token of
+// rank 8 / 32 / 64 (4, 16, 32 steps) 40.8 / 44.7, 43.2 / 44.7, 54.9 / 45.8; down
+// N 4864 H 896, 10 slices, 1 / 2 tokens of rank 16 (5, 10 steps) 9.9 / 11.5,
+// 13.1 / 11.9; down N 18944 H 3584, 37 slices, rank 16 / 32 (19, 38) 26.8 / 26.8,
+// 34.4 / 27.0.
+bool own_v(bool decode, int64_t M, int64_t hr, int64_t in, int splits) {
+  if (!decode || M > 16 || M * hr > kLoraOwnValues) return false;
+  const int64_t steps = ((M * hr + 15) / 16) * ((in + 1023) / 1024);
+  const int64_t slices = (k_slices(in) + splits - 1) / splits;
+  return steps <= 2 || 9 * steps <= 5 * slices;
+}
+
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -161,7 +177,7 @@ swiglu_status_t run_call(const Call& c, cudaStream_t stream) {
   if (st != SWIGLU_OK) return st;
   int* lists = reinterpret_cast<int*>(static_cast<uint8_t*>(c.ws) + v_bytes(c.M, hr));
 
-  LoraShrinkParams sp{};
+  LoraShrinkParams sp{};  // for V, unless the decode CTAs make it
   sp.x = c.x;
   sp.la = c.la;
   sp.index = c.index;
@@ -218,7 +234,11 @@ swiglu_status_t run_call(const Call& c, cudaStream_t stream) {
     p.status = d.status;
     p.timeout_ns = d.timeout_ns;
     p.inject_stall = d.inject_stall;
-    e = launch_lora_shrink(sp, stream);
+    p.lora_own_v = own_v(decode, c.M, hr, c.in, p.splits);
+    p.lora_x = c.x;
+    p.lora_la = c.la;
+    p.lora_scale = c.scale;
+    e = p.lora_own_v ? cudaSuccess : launch_lora_shrink(sp, stream);
     if (e == cudaSuccess) e = launch_small_m(p, stream);
   } else {
     LargeMParams p{};
@@ -279,7 +299,9 @@ swiglu_status_t lora_plan(int64_t M, int64_t in, int64_t outs, int64_t rank, boo
   if (st != SWIGLU_OK) return st;
   const int64_t tiles = div_up(M, kTileM), hr = down ? rank : 2 * rank;
   char shrink[64];
-  if (M <= kGroupTokens)
+  if (own_v(decode, M, hr, in, p.splits))
+    std::snprintf(shrink, sizeof(shrink), "inside");
+  else if (M <= kGroupTokens)
     std::snprintf(shrink, sizeof(shrink), "dots=%lld", static_cast<long long>(M * div_up(hr, 4)));
   else
     std::snprintf(shrink, sizeof(shrink), "tiles=%lld parts=%d", static_cast<long long>(tiles),

@@ -10,6 +10,9 @@
 // V is rounded to bf16, the operand type of the expanding product: the delta it
 // enters is a fraction of the projection, which is itself rounded to bf16.
 //
+// One or a few tokens of a small rank need no kernel here: the decode kernel's
+// CTAs make V (own_v() in lora_api.cu).
+//
 // Few tokens: lora_shrink_dot_kernel, plain dot products in fp32. One CTA takes
 // a token and 4 rows; its 8 warps (32 for a long K) split K, so that few loads
 // follow one another: 3.6 us for 16 tokens, 32 rows, K 3584; 4.9 us for 16 rows,
@@ -44,16 +47,6 @@ namespace {
 
 constexpr int kDotRows = 4;
 constexpr int kDotThreads = 1024;  // at most
-
-__device__ __forceinline__ float dot8(const uint4& a, const uint4& b, float acc) {
-  const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {  // a bf16 is the high half of its fp32
-    acc = fmaf(__uint_as_float(x[i] << 16), __uint_as_float(y[i] << 16), acc);
-    acc = fmaf(__uint_as_float(x[i] & 0xffff0000u), __uint_as_float(y[i] & 0xffff0000u), acc);
-  }
-  return acc;
-}
 
 __global__ void __launch_bounds__(kDotThreads)
     lora_shrink_dot_kernel(const __grid_constant__ LoraShrinkParams p) {

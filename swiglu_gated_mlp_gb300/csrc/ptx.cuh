@@ -43,6 +43,17 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
   return v;
 }
 
+// Adds the fp32 dot product of 8 bf16 pairs.
+__device__ __forceinline__ float dot8(const uint4& a, const uint4& b, float acc) {
+  const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {  // a bf16 is the high half of its fp32
+    acc = fmaf(__uint_as_float(x[i] << 16), __uint_as_float(y[i] << 16), acc);
+    acc = fmaf(__uint_as_float(x[i] & 0xffff0000u), __uint_as_float(y[i] & 0xffff0000u), acc);
+  }
+  return acc;
+}
+
 // SiLU(g) * u in fp32: g / (1 + e^-g) * u. For g -> -inf, e^-g -> +inf and the
 // fast divide returns 0 (the limit); for g -> +inf, e^-g -> 0. No NaN for finite g.
 __device__ __forceinline__ float silu_mul(float g, float u) {

@@ -101,6 +101,22 @@ def test_down_forward_lora_matches_the_formula(native, M, N, H, L, r, how):
     run_down(native, M, N, H, L, r, how, seed=M + N + H + r, residual=M % 2 == 0)
 
 
+# a few tokens: every decode CTA makes V itself
+@pytest.mark.parametrize("M,K,N,L,r,how", [
+    (1, 64, 8, 2, 8, "mixed"), (1, 896, 4864, 3, 16, "one"), (2, 1016, 264, 2, 8, "one"),
+    (1, 3584, 19000, 2, 32, "one"), (4, 2056, 19464, 3, 8, "mixed"), (3, 1032, 20000, 9, 16, "mixed"),
+    (5, 2504, 19464, 5, 8, "none"), (16, 1000, 19464, 5, 8, "runs"),
+])
+@pytest.mark.parametrize("down", [False, True])
+def test_tokens_whose_v_every_cta_makes(native, M, K, N, L, r, how, down):
+    plan = (native.swiglu_down_lora_plan_string if down else native.swiglu_lora_plan_string)(M, K, N, r)
+    assert "shrink inside" in plan or M == 16 or K == 1032, plan
+    if down:
+        run_down(native, M, K, N, L, r, how, seed=M + K + r, residual=M % 2 == 1)
+    else:
+        run_gate_up(native, M, K, N, L, r, how, seed=M + K + r)
+
+
 def rows_of(M, count, seed):
     rng = np.random.default_rng(seed)
     return np.unique(np.concatenate([[0, M - 1], rng.integers(0, M, count)]))
@@ -337,6 +353,7 @@ def test_plans_reach_every_form(native):
     assert any("small_m" in p and "groups=3" in p for p in plans)
     assert any("splits=8" in p for p in plans) and any("splits=1" in p for p in plans)
     assert any("shrink dots" in p for p in plans) and any("shrink tiles" in p for p in plans)
+    assert any("shrink inside" in p for p in plans)
     down = [native.swiglu_down_lora_plan_string(M, N, H, r) for M, N, H, _, r, _ in SHAPES]
     assert all(p.startswith("down lora shrink") for p in down)
     assert "large_m_pair" in native.swiglu_lora_plan_string(4096, 3584, 18944, 64)
@@ -345,6 +362,7 @@ def test_plans_reach_every_form(native):
 
 @pytest.mark.parametrize("rank", [8, 40])
 @pytest.mark.parametrize("M, K, N", [
+    (3, 712, 20000),    # decode kernel, V made by every CTA (rank 8)
     (24, 200, 264),     # decode kernel, K whole
     (24, 2048, 520),    # K over a cluster, adapters dealt to its CTAs
     (200, 712, 392),    # token groups
