@@ -267,11 +267,15 @@ __global__ void __launch_bounds__(PairCfg<kMx, kLora>::kThreadsT, 1)
   cluster_sync();  // both CTAs' barriers initialised and TMEM allocated
   tc_fence_after();
   const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
-  pdl_wait();
+  // With adapters the kernel before this one makes V and the lists, and lets this grid
+  // start when it has itself waited for all before it: the first K slices (by TMA, from
+  // L2) need no wait, what reads V and lists or writes outputs has its own.
+  if (!kLora || !p.lora_early) pdl_wait();
 
   if (warp == 0) {
     // ------------------------------------------------ TMA producer (both CTAs)
     if (lane == 0) {
+      if (kLora) fence_proxy_async();
       int s = 0;
       uint32_t ph = 0;
       uint32_t filled = 0, fill_ph = 0;
@@ -305,12 +309,12 @@ __global__ void __launch_bounds__(PairCfg<kMx, kLora>::kThreadsT, 1)
         const int m0 = mb * 2 * kTileM + static_cast<int>(rank) * kTileM;
         const int wtile = nb * num_kb;                        // (column block nb, K slice 0)
         const int wrow = static_cast<int>(rank) * kPackBlockN;  // gate rows (0) / up rows (1)
-        // adapters present in this tile, read well before they are needed
+        // adapters present in this tile, read well before they are needed (but in the first)
         const int* list = nullptr;
         int extra = 0;
         if constexpr (kLora) {
           list = p.lora_lists + static_cast<size_t>(mb) * kLoraListInts;
-          extra = list[0] * kHalves;
+          if (round > 0) extra = list[0] * kHalves;
         }
         // paced shapes: odd rounds walk K backwards and start on the A slices
         // the previous round (same row tiles) read last, while L2 holds them
@@ -345,6 +349,10 @@ __global__ void __launch_bounds__(PairCfg<kMx, kLora>::kThreadsT, 1)
           }
         }
         if constexpr (kLora) {
+          if (round == 0) {
+            pdl_wait();
+            extra = list[0] * kHalves;
+          }
           // Lb rows of every adapter present in this tile, to the weight half
           for (int i = 0; ok && i < extra; ++i) {
             if (!mbar_wait(empty0 + 8u * s, ph ^ 1u, wc, kSiteProducerEmpty)) {
@@ -393,12 +401,12 @@ __global__ void __launch_bounds__(PairCfg<kMx, kLora>::kThreadsT, 1)
       int buf = 0;
       uint32_t acc_ph = 0;
       uint32_t vph = 0;  // adapters: phase of each stage's V barrier
-      int next_extra = kLora && pair < num_tiles ? lora_slices(pair) : 0;
+      int next_extra = -1;  // adapter slices of the next tile; the first one's are read late
       bool ok = true;
       for (int t = pair; ok && t < num_tiles; t += pairs) {
         // adapter slices of this tile; the next tile's count is on its way
-        const int extra = kLora ? next_extra : 0;
-        if constexpr (kLora) next_extra = t + pairs < num_tiles ? lora_slices(t + pairs) : 0;
+        int extra = kLora ? next_extra : 0;
+        if (kLora && extra >= 0) next_extra = t + pairs < num_tiles ? lora_slices(t + pairs) : 0;
         if (!mbar_wait(tempty0 + 8u * buf, acc_ph ^ 1u, wc, kSiteMmaTmemEmpty)) break;
         tc_fence_after();
         const uint32_t d = tmem_base + buf * C::kAccCols;
@@ -436,6 +444,11 @@ __global__ void __launch_bounds__(PairCfg<kMx, kLora>::kThreadsT, 1)
           }
         }
         if constexpr (kLora) {
+          if (extra < 0) {
+            pdl_wait();
+            extra = lora_slices(t);
+            next_extra = t + pairs < num_tiles ? lora_slices(t + pairs) : 0;
+          }
           constexpr uint32_t kIdescV = idesc_bf16_f32(2 * kTileM, 2 * C::kBN / kHalves);
           const int ksteps = (p.lora_rank + 15) / 16;
           for (int i = 0; ok && i < extra; ++i) {
@@ -507,6 +520,7 @@ __global__ void __launch_bounds__(PairCfg<kMx, kLora>::kThreadsT, 1)
     // ------------------------------------------------ masked V rows (both CTAs)
     // Thread = row of this CTA's 128; the row's own adapter's slices get its V,
     // every other slice zeros, in the swizzled layout a TMA load would write.
+    pdl_wait();
     const int row = threadIdx.x - (64 + 32 * C::kEpiWarps);
     const uint32_t sready0_lead = mapa_shared(sready0, 0);
     const int chunks = p.lora_rank / 8, padded = (p.lora_rank + 15) / 16 * 2;
@@ -585,6 +599,7 @@ __global__ void __launch_bounds__(PairCfg<kMx, kLora>::kThreadsT, 1)
     const int ew = warp - 2;
     const uint32_t lane_off = static_cast<uint32_t>(q * 32) << 16;
     const float sg = kFp8 ? p.scale_gate : 1.0f, su = kFp8 ? p.scale_up : 1.0f;
+    if (kLora) pdl_wait();
     int buf = 0;
     uint32_t acc_ph = 0;
     int sbuf = 0;

@@ -48,8 +48,8 @@
 // accumulators (rank / 16 of them each for gate and up, so gate and up of a rank
 // up to 32 share a slice, V1 and V2 side by side; above that they take one
 // each). Four more warps, thread = token, list the adapters and write V; the
-// adapter slices alternate with weight slices once the ring has filled, so that
-// they pass while the weight stream is waited for. For a token or a few of a small
+// adapter slices alternate with the last weight slices, so that they pass while the
+// weight stream is waited for and V is made while it runs. For a token or a few of a small
 // rank every CTA makes V itself with these warps and the epilogue's (own_v() in
 // lora_api.cu), without a kernel before it: 9.3 -> 8.1 us for 1 token of rank 8, K
 // 896, N 4864, and one launch less on the host (17.2 -> 15 us from Python).
@@ -357,18 +357,22 @@ __global__ void __launch_bounds__(kLora ? kLoraThreads : kThreads, kLora ? 2 : 1
   // one (which needs little room) may line up from the start: its launch and the
   // one after it then do not add up at the end of this grid.
   if constexpr (kLora) pdl_launch_dependents();
-  pdl_wait();  // the set-up and L2 staging above overlap the previous grid; loads start here
+  // The set-up and L2 staging above overlap the previous grid; loads start here. With
+  // V from the kernel before this one, only the warps that read V or write outputs wait
+  // for that: it lets this grid start when it has itself waited for all before it, so
+  // tokens, indices and adapters are there (read from L2 only: TMA, ld.cg).
+  if (!kLora || own_v) pdl_wait();
 
-  // Adapter slices alternate with weight slices after the first `lead` of those;
-  // this K part has every kparts-th adapter of the list.
-  // (All after them where V is made here: the first ones would hold up the weight.)
-  const int lead = own_v ? kb_end - kb_begin : min(stages, kb_end - kb_begin);
+  // Adapter slices alternate with the last weight slices, as V comes late (after them all
+  // where it is made here), but the list is known after `first` of those; this K part has
+  // every kparts-th adapter of the list.
+  const int num_slices = kb_end - kb_begin, first_slices = own_v ? num_slices : min(stages, num_slices);
   const int per_adapter = kLora ? lora_slices_per_adapter(kDown, p.lora_rank) : 0;
   const auto adapter_slices = [&] { return (max(list[0] - kpart, 0) + kparts - 1) / kparts * per_adapter; };
-  // position of an adapter slice in the pipeline: between `rest` weight slices, then after them
-  const auto adapter_use = [&](int i) {
-    const int rest = kb_end - kb_begin - lead;
-    return i <= rest ? lead + 2 * i : kb_end - kb_begin + i;
+  // weight slices before the first adapter slice, and a slice's place among them all
+  const auto lead_of = [&](int extra) { return max(first_slices, num_slices - extra); };
+  const auto adapter_use = [&](int i, int lead) {
+    return i <= num_slices - lead ? lead + 2 * i : num_slices + i;
   };
   const auto adapter_at = [&](int i) { return list[1 + kpart + i / per_adapter * kparts]; };
 
@@ -377,12 +381,13 @@ __global__ void __launch_bounds__(kLora ? kLoraThreads : kThreads, kLora ? 2 : 1
     if (lane == 0) {
       const uint64_t pol_w = policy_evict_first();  // weights: read once
       const uint64_t pol_x = policy_evict_last();   // activations: re-read by every CTA
+      if (kLora && !own_v) fence_proxy_async();  // the tokens: see the grid-dependency wait above
       const int wtile = nblk * num_kb;  // packed tile index of (this column block, K slice 0)
       int s = 0;
       uint32_t ph = 0;
       uint32_t filled = 0, fill_ph = 0;
       bool skip_once = p.inject_stall != 0, ok = true;
-      int extra = 0, done = 0;  // adapter slices, and how many are loaded
+      int extra = 0, done = 0, lead = num_slices;  // adapter slices, how many are loaded
       // Lb rows of the next adapter slice to the stage's weight half
       const auto load_adapter = [&] {
         if (!mbar_wait(empty0 + 8u * s, ph ^ 1u, wc, kSiteProducerEmpty)) return false;
@@ -409,9 +414,10 @@ __global__ void __launch_bounds__(kLora ? kLoraThreads : kThreads, kLora ? 2 : 1
       };
       for (int kb = kb_begin; kb < kb_end; ++kb) {
         if constexpr (kLora) {
-          if (kb - kb_begin == lead) {
+          if (kb - kb_begin == first_slices) {
             ok = mbar_wait(list_bar, 0, wc, kSiteLora);
             extra = ok ? adapter_slices() : 0;
+            lead = lead_of(extra);
           }
           if (ok && kb - kb_begin >= lead && done < extra) ok = load_adapter();
           if (!ok) break;
@@ -445,7 +451,7 @@ __global__ void __launch_bounds__(kLora ? kLoraThreads : kThreads, kLora ? 2 : 1
         }
       }
       if constexpr (kLora) {
-        if (ok && kb_end - kb_begin == lead) {
+        if (ok && num_slices == first_slices) {
           ok = mbar_wait(list_bar, 0, wc, kSiteLora);
           extra = ok ? adapter_slices() : 0;
         }
@@ -465,7 +471,7 @@ __global__ void __launch_bounds__(kLora ? kLoraThreads : kThreads, kLora ? 2 : 1
       int s = 0;
       uint32_t ph = 0;
       bool ok = true;
-      int extra = 0, done = 0;  // adapter slices, and how many are issued
+      int extra = 0, done = 0, lead = num_slices;  // adapter slices, how many are issued
       uint32_t vph = 0;         // phase of each stage's V barrier
       const auto mma_adapter = [&] {
         if (!mbar_wait(full0 + 8u * s, ph, wc, kSiteMmaFull) ||
@@ -496,9 +502,10 @@ __global__ void __launch_bounds__(kLora ? kLoraThreads : kThreads, kLora ? 2 : 1
       };
       for (int kb = kb_begin; kb < kb_end; ++kb) {
         if constexpr (kLora) {
-          if (kb - kb_begin == lead) {
+          if (kb - kb_begin == first_slices) {
             ok = mbar_wait(list_bar, 0, wc, kSiteLora);
             extra = ok ? adapter_slices() : 0;
+            lead = lead_of(extra);
           }
           if (ok && kb - kb_begin >= lead && done < extra) ok = mma_adapter();
           if (!ok) break;
@@ -542,7 +549,7 @@ __global__ void __launch_bounds__(kLora ? kLoraThreads : kThreads, kLora ? 2 : 1
         }
       }
       if constexpr (kLora) {
-        if (ok && kb_end - kb_begin == lead) {
+        if (ok && num_slices == first_slices) {
           ok = mbar_wait(list_bar, 0, wc, kSiteLora);
           extra = ok ? adapter_slices() : 0;
         }
@@ -556,7 +563,7 @@ __global__ void __launch_bounds__(kLora ? kLoraThreads : kThreads, kLora ? 2 : 1
   } else if (kLora && warp >= 6) {
     // ------------------------------------------------ adapters: list and V
     const int row = threadIdx.x - kThreads;  // this thread's token of the group
-    const int mine = row < mcount ? __ldg(p.lora_index + m0 + row) : -1;
+    const int mine = row < mcount ? __ldcg(p.lora_index + m0 + row) : -1;
     const bool has = mine >= 0 && mine < p.lora_count;
     ids[row] = has ? mine : -1;
     named_barrier(1, 128);
@@ -591,6 +598,8 @@ __global__ void __launch_bounds__(kLora ? kLoraThreads : kThreads, kLora ? 2 : 1
     if (own_v) {
       make_own_v(p, p.lora_rank * kHalves, own, warp - 2);
       named_barrier(2, 32 * kLoraOwnWarps);
+    } else {
+      pdl_wait();
     }
     const uint4* v = reinterpret_cast<const uint4*>(
         own_v ? own : static_cast<const __nv_bfloat16*>(p.lora_v) + static_cast<size_t>(m0) * p.lora_rank * kHalves) +
@@ -602,10 +611,10 @@ __global__ void __launch_bounds__(kLora ? kLoraThreads : kThreads, kLora ? 2 : 1
       for (int c = 0; c < kChunks; ++c)
         x[h][c] = has && c < chunks ? v[h * chunks + c] : make_uint4(0u, 0u, 0u, 0u);
     // V of each adapter slice, in the swizzled rows a TMA load would write
-    const int extra = adapter_slices();
+    const int extra = adapter_slices(), lead = lead_of(extra);
     uint32_t vph = 0;
     for (int i = 0; i < extra; ++i) {
-      const int s = adapter_use(i) % stages;
+      const int s = adapter_use(i, lead) % stages;
       int go = 1;
       if (lane == 0) go = mbar_wait(vfree0 + 8u * s, (vph >> s) & 1u, wc, kSiteLora) ? 1 : 0;
       go = __shfl_sync(0xffffffffu, go, 0);
@@ -648,9 +657,10 @@ __global__ void __launch_bounds__(kLora ? kLoraThreads : kThreads, kLora ? 2 : 1
         named_barrier(2, 32 * kLoraOwnWarps);
       }
       const int extra = __all_sync(0xffffffffu, mbar_wait(list_bar, 0, wc, kSiteLora)) ? adapter_slices() : 0;
+      const int lead = lead_of(extra);
       uint32_t vph = 0;
       for (int i = 0; i < extra; ++i) {
-        const int use = adapter_use(i), s = use % stages;
+        const int use = adapter_use(i, lead), s = use % stages;
         if (!__all_sync(0xffffffffu, mbar_wait(vfree0 + 8u * s, (vph >> s) & 1u, wc, kSiteLora) &&
                                          mbar_wait(full0 + 8u * s, (use / stages) & 1, wc, kSiteLora)))
           break;
@@ -666,6 +676,7 @@ __global__ void __launch_bounds__(kLora ? kLoraThreads : kThreads, kLora ? 2 : 1
         __syncwarp();
         if (lane == 0) mbar_arrive(vready0 + 8u * s);
       }
+      if (!own_v) pdl_wait();
     }
     if (lane == 0) ok = mbar_wait(tfull_bar, 0, wc, kSiteEpiTmemFull) ? 1 : 0;
     ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -951,7 +962,8 @@ cudaError_t launch_small_m(const SmallMParams& p, cudaStream_t stream) {
     return cudaErrorInvalidValue;
   const int extra = p.mx ? kSfStageBytes : 0;
   SmallMParams q = p;
-  q.l2_prefetch = small_m_l2_prefetch(p.grid, p.splits);
+  // with V from a kernel before this one the loads themselves begin as early
+  q.l2_prefetch = p.lora && !p.lora_own_v ? 0 : small_m_l2_prefetch(p.grid, p.splits);
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(p.grid);
   cfg.blockDim = dim3(p.lora ? kLoraThreads : kThreads);

@@ -57,6 +57,7 @@ struct LargeMParams {
   const void* lora_lb;  // Lb itself (lora_lb.cuh)
   const int* lora_index;
   const int* lora_lists;
+  int lora_early;  // the first K slices do not wait for the kernel that makes V
 };
 
 struct SmallMParams {

@@ -23,9 +23,11 @@ constexpr int64_t kGroupTokens = 128;
 // tokens, and more groups where 256-row pair tiles would leave the SMs idle or
 // take a nearly empty round. A pair's slice takes about 0.3 us, a decode CTA's
 // of 128 tokens 0.6 us (each group streams the weight), a K split 3 us. Measured,
-// decode against pairs: 333 tokens K 1416 N 5000 32.7 / 39.5 us; down 333 tokens
-// N 4864 H 896 (K over 8 CTAs) 28.6 / 42.8; 400 tokens K 2048 N 4000 39.6 / 31.8;
-// down 700 tokens N 18944 H 3584 286 / 124.
+// decode against pairs (in each the kernel that makes V is out of the way): 333
+// tokens of 10 adapters, K 1416 N 5000, 33.9 / 47.8 us, K 2048 N 4000 35.3 / 33.3;
+// 500 tokens of 3, K 2048 N 4000, 39.4 / 30.4; down, 200 tokens of 4, N 4864 H 896 (K
+// over 8 CTAs) 23.7 / 32.3; down, 800 tokens of 2, N 18944 H 3584, 272 / 118. The rule
+// is off by up to a fifth where they meet (333 tokens, K 512 N 2000: pairs, 25.4 / 20.7).
 swiglu_status_t plan_decode(int64_t M, int64_t blocks, int64_t slices, const DeviceView& d,
                             SmallMParams* p, bool* decode) {
   const int64_t groups = (M + kGroupTokens - 1) / kGroupTokens;
@@ -268,6 +270,11 @@ swiglu_status_t run_call(const Call& c, cudaStream_t stream) {
     p.lora_lb = c.lb;
     p.lora_index = c.index;
     p.lora_lists = lists;
+    // Where both grids fit on the SMs together V takes no time of its own (down, 333
+    // tokens of 10 adapters, N 18944, H 3584: 174 -> 98 us). Where they do not, some pairs
+    // start before others: 4096 tokens, K 3584 645 -> 630 us, but with long tiles, which
+    // then share less of L2, 350 -> 358 us (down, N 18944).
+    p.lora_early = sp.tiles * sp.splits + p.grid <= d.sm_count || slices < 128;
     p.status = d.status;
     p.timeout_ns = d.timeout_ns;
     p.inject_stall = d.inject_stall;

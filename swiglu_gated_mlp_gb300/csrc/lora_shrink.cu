@@ -18,8 +18,15 @@
 // follow one another: 3.6 us for 16 tokens, 32 rows, K 3584; 4.9 us for 16 rows,
 // K 18944. Each token reads its adapter's rows again from L2, so 128 tokens of 128
 // rows take about 20 us; tensor-core tiles there were slower with more than two
-// adapters (88 against 71 us for the call with 8). The decode kernel does its
-// set-up and stages its first weight tiles in L2 while this one runs.
+// adapters (88 against 71 us for the call with 8).
+//
+// Either kernel lets the projection's start as soon as it has itself waited for the
+// grids before it, so that the weight stream (or the first K slices) runs beside it
+// and V only has to be there for the adapter slices at its end: 333 tokens, K 1416,
+// N 5000 30.5 -> 24.4 us, 200 tokens, down, N 18944 79 -> 45, 128 tokens, down, N 4864
+// 18.0 -> 16.4, 16 tokens, K 3584, N 18944 49.8 -> 48.3. (Before, the projection's
+// kernel started with this one, did its set-up and staged weight tiles in L2, then
+// waited for all of V; for 16 tokens, down, N 18944 that was as fast, 28.9 / 29.2.)
 //
 // Many tokens: lora_shrink_tile_kernel, tcgen05 with 128 tokens as the MMA's
 // M side and the rows of the adapters present in the tile as its N side. The
@@ -51,10 +58,10 @@ constexpr int kDotThreads = 1024;  // at most
 __global__ void __launch_bounds__(kDotThreads)
     lora_shrink_dot_kernel(const __grid_constant__ LoraShrinkParams p) {
   __shared__ float sums[kDotThreads / 32][kDotRows];
-  // The projection's kernel may start at once: it waits for this grid before it
-  // reads anything but weight tiles into L2, and this grid takes little room.
-  pdl_launch_dependents();
+  // The decode kernel starts its weight stream when this grid has seen all before it
+  // complete, and waits for this grid where it reads V; this grid takes little room.
   pdl_wait();
+  pdl_launch_dependents();
   const int threads = blockDim.x;
   const int row_blocks = (p.hr + kDotRows - 1) / kDotRows;
   const int m = blockIdx.x / row_blocks;
@@ -171,6 +178,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     first[0][i] = first[1][i] = kTileThreads;
   }
   pdl_wait();
+  pdl_launch_dependents();  // as above
   // The producer's first token loads do not need the adapters.
   const int early = min(kEarlyLoads, end - begin);
   if (tid == 0 && !p.inject_stall) {
@@ -224,7 +232,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     if (tid == 0) list[0] = n256;
   }
   __syncthreads();
-  pdl_launch_dependents();
 
   const int per_pass = p.per_pass;  // adapters side by side in the accumulator
   const int passes = (n128 + per_pass - 1) / per_pass;

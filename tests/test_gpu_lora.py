@@ -409,3 +409,48 @@ def test_non_finite_lb_stays_with_its_tokens(native, M, K, N, rank):
     only[1, 70, rank - 1] = 1.0
     v = native.swiglu_down_forward_lora(a, torch.zeros_like(w3p), N, la3, only, index, scale3)[theirs, 70]
     assert torch.equal(got[theirs, 70], (v.float() * float("inf")).to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("M, K, N, r, L", [
+    (1, 264, 1000, 8, 2), (16, 264, 1000, 16, 5), (100, 512, 2000, 64, 3), (200, 264, 2000, 24, 9),
+    (600, 512, 1000, 40, 4),
+])
+def test_calls_one_after_another_see_each_others_outputs(native, M, K, N, r, L):
+    # each call's kernels start while those before it run: what a call reads, the last one
+    # wrote; a chain must give the bits that it gives with a synchronisation after each call
+    a, w1, w2 = (t.cuda() for t in make_inputs(M, K, N, 7))
+    w3 = make_inputs(8, N, K, 8)[1].cuda() / 32  # small: the chain must not grow
+    wp, w3p = native.swiglu_pack_weights(w1, w2), native.swiglu_pack_down_weights(w3)
+    la, lb, scale = (t.cuda() for t in table(L, 2, r, K, N, 7))
+    la3, lb3, scale3 = (t.cuda() for t in table(L, 1, r, N, K, 8))
+    lb3 = lb3 / 32
+    other = [make_inputs(M, K, 8, s)[0].cuda() for s in (11, 12, 13)]  # every step's x differs
+    index = indices(M, L, "mixed", 3).cuda()
+    ws = native.swiglu_lora_workspace(M, K, N, r)
+    ws3 = native.swiglu_down_lora_workspace(M, N, K, r)
+
+    def chain(sync, steps=12):
+        x = a.clone()
+        y = torch.full((M, N), float("nan"), dtype=torch.bfloat16, device="cuda")
+        for i in range(steps):
+            native.swiglu_forward_lora(x, wp, N, la, lb, index, scale, Y=y, workspace=ws)
+            if sync:
+                torch.cuda.synchronize()
+            native.swiglu_down_forward_lora(y, w3p, K, la3, lb3, index, scale3, R=other[i % 3], Out=x,
+                                               workspace=ws3)
+            if sync:
+                torch.cuda.synchronize()
+        return x
+
+    want = chain(True)
+    assert want.isfinite().all()
+    for _ in range(5):
+        assert torch.equal(chain(False), want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = chain(False)
+    for _ in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+    native.swiglu_check_device_status()
