@@ -63,6 +63,8 @@
 // the same weights: 172 us for 272 MB read twice and 272 MB written (writes alone
 // run at 4.0 TB/s here). 0.5B block, 128 tokens: 29 us, three launches that each
 // wait for one another (10, 16 and 4 us alone).
+#include <type_traits>
+
 #include "kernels.h"
 #include "ptx.cuh"
 
@@ -216,6 +218,7 @@ __global__ void __launch_bounds__(kBackThreads, 1)
         // reaches rows that are not stored, or is left out of the sum.
         const bool rows_here = weight || r0 < g.rows;
         const bool rows_peer = weight || mb * 2 * kTileM + kTileM < g.rows;  // the odd CTA's
+        const CUtensorMap* map_b = bn == kPackBlockN ? &g.tmap_b0 : &g.tmap_b1;  // kGrad
         const uint32_t bytes = g.a_bytes * (rows_peer ? 2 : 1) + 2 * (weight ? g.a_bytes : bn * kBlockK * 2);
         for (int i = begin; i < end; ++i) {
           if (!mbar_wait(empty0 + 8u * s, ph ^ 1u, wc, kSiteProducerEmpty)) {
@@ -231,7 +234,7 @@ __global__ void __launch_bounds__(kBackThreads, 1)
             if constexpr (kGrad) {
               // A rows [r0, +128); bn gate (rank 0) or up (rank 1) rows of tile (nb, i)
               if (rows_here) tma_load_2d_pair(da, &g.tmap_a0, fb, i * kBlockK, r0);
-              tma_load_3d_pair(db, bn == kPackBlockN ? &g.tmap_b0 : &g.tmap_b1, fb, 0,
+              tma_load_3d_pair(db, map_b, fb, 0,
                                static_cast<int>(rank) * kPackBlockN + off, nb * g.slices + i);
             } else if (!weight) {
               // stages 2 d, 2 d + 1: rows [128 h, +128) of packed tile row j (a gate/up
@@ -287,57 +290,71 @@ __global__ void __launch_bounds__(kBackThreads, 1)
         tc_fence_after();
         const uint32_t d = tmem_base + buf * kAccCols;
         if constexpr (kGrad) {
-          const uint32_t idesc = idesc_bf16_f32(2 * kTileM, u < p.full_units ? 256 : 128);
-          for (int i = begin; i < end; ++i) {
-            if (!mbar_wait(full0 + 8u * s, ph, wc, kSiteMmaFull)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            const uint64_t adesc = smem_desc_sw128(sA + s * kOperandBytes);
-            const uint64_t bdesc = smem_desc_sw128(sB + s * kOperandBytes);
+          // the descriptors as constants: 4 % of this kernel on the 7B shape
+          const auto issue = [&](auto columns) {
+            constexpr uint32_t kIdesc = idesc_bf16_f32(2 * kTileM, decltype(columns)::value);
+            for (int i = begin; i < end; ++i) {
+              if (!mbar_wait(full0 + 8u * s, ph, wc, kSiteMmaFull)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              const uint64_t adesc = smem_desc_sw128(sA + s * kOperandBytes);
+              const uint64_t bdesc = smem_desc_sw128(sB + s * kOperandBytes);
 #pragma unroll
-            for (uint32_t k = 0; k < 4; ++k)
-              mma_bf16_pair(d, adesc + 2u * k, bdesc + 2u * k, idesc, (i != begin || k != 0) ? 1u : 0u);
-            mma_commit_pair_multicast(empty0 + 8u * s, 0x3);  // frees the stage in both CTAs
-            if (++s == kStages) {
-              s = 0;
-              ph ^= 1u;
+              for (uint32_t k = 0; k < 4; ++k)
+                mma_bf16_pair(d, adesc + 2u * k, bdesc + 2u * k, kIdesc, (i != begin || k != 0) ? 1u : 0u);
+              mma_commit_pair_multicast(empty0 + 8u * s, 0x3);  // frees the stage in both CTAs
+              if (++s == kStages) {
+                s = 0;
+                ph ^= 1u;
+              }
             }
-          }
+          };
+          if (u < p.full_units)
+            issue(std::integral_constant<int, 2 * kPackBlockN>{});
+          else
+            issue(std::integral_constant<int, kPackBlockN>{});
         } else {
           // Bits 15 (left) and 16 (right) of the descriptor mark MN-major operands.
           // 16 of the sum are 16 rows of 128 bytes of an MN-major operand, 32 bytes
           // along a K-major row (four in each of the two stages).
-          const uint32_t idesc =
-              idesc_bf16_f32(2 * kTileM, kAccCols) | (weight ? 1u << 15 : 0u) | (1u << 16);
-          for (int i = begin; i < end; i += 2) {  // s is even: every unit has whole pairs of stages
-            if (!mbar_wait(full0 + 8u * s, ph, wc, kSiteMmaFull) ||
-                !mbar_wait(full0 + 8u * (s + 1), ph, wc, kSiteMmaFull)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            const uint32_t pa = sA + s * kOperandBytes;
-            const uint64_t adesc = weight ? smem_desc_sw128_mn(pa, kOperandBytes) : smem_desc_sw128(pa);
-            const uint64_t bdesc = smem_desc_sw128_mn(sB + s * kOperandBytes, kOperandBytes);
-            // weight gradient: no MMA for 16 tokens that do not exist
-            const int ksteps = weight ? min(8, (g.sum - (i >> 1) * 2 * kBlockK + 15) / 16) : 8;
+          const auto issue = [&](auto of_weight) {
+            constexpr bool kWeight = decltype(of_weight)::value;
+            constexpr uint32_t kIdesc =
+                idesc_bf16_f32(2 * kTileM, kAccCols) | (kWeight ? 1u << 15 : 0u) | (1u << 16);
+            for (int i = begin; i < end; i += 2) {  // s is even: every unit has whole pairs of stages
+              if (!mbar_wait(full0 + 8u * s, ph, wc, kSiteMmaFull) ||
+                  !mbar_wait(full0 + 8u * (s + 1), ph, wc, kSiteMmaFull)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              const uint32_t pa = sA + s * kOperandBytes;
+              const uint64_t adesc = kWeight ? smem_desc_sw128_mn(pa, kOperandBytes) : smem_desc_sw128(pa);
+              const uint64_t bdesc = smem_desc_sw128_mn(sB + s * kOperandBytes, kOperandBytes);
+              // weight gradient: no MMA for 16 tokens that do not exist
+              const int ksteps = kWeight ? min(8, (g.sum - (i >> 1) * 2 * kBlockK + 15) / 16) : 8;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const uint64_t da = adesc + (weight ? (2048u >> 4) * k
-                                                  : 2u * (k & 3) + (k >> 2) * (kOperandBytes >> 4));
-              if (k < ksteps)
-                mma_bf16_pair(d, da, bdesc + (2048u >> 4) * k, idesc, (i != begin || k != 0) ? 1u : 0u);
+              for (int k = 0; k < 8; ++k) {
+                const uint64_t da = adesc + (kWeight ? (2048u >> 4) * k
+                                                    : 2u * (k & 3) + (k >> 2) * (kOperandBytes >> 4));
+                if (k < ksteps)
+                  mma_bf16_pair(d, da, bdesc + (2048u >> 4) * k, kIdesc, (i != begin || k != 0) ? 1u : 0u);
+              }
+              mma_commit_pair_multicast(empty0 + 8u * s, 0x3);  // frees the stages in both CTAs
+              mma_commit_pair_multicast(empty0 + 8u * (s + 1), 0x3);
+              s += 2;
+              if (s == kStages) {
+                s = 0;
+                ph ^= 1u;
+              }
             }
-            mma_commit_pair_multicast(empty0 + 8u * s, 0x3);  // frees the stages in both CTAs
-            mma_commit_pair_multicast(empty0 + 8u * (s + 1), 0x3);
-            s += 2;
-            if (s == kStages) {
-              s = 0;
-              ph ^= 1u;
-            }
-          }
+          };
+          if (weight)
+            issue(std::true_type{});
+          else
+            issue(std::false_type{});
         }
         if (!ok) break;
         mma_commit_pair_multicast(tfull0 + 8u * buf, 0x3);  // both halves of the accumulator ready
@@ -365,7 +382,6 @@ __global__ void __launch_bounds__(kBackThreads, 1)
       int mb, nb;
       tile_coords(tile, pr.tiles_m, pr.tiles_n, pr.group_m, mb, nb);
       const int row0 = mb * 2 * kTileM + static_cast<int>(rank) * kTileM + q * 32;
-      const int chunks = bn / 64;  // kGrad: 32-column chunks of this warp
       uint4 dyv[4];
       const __nv_bfloat16* dy_row = nullptr;
       const int col0 = nb * kPackBlockN + off + half * (bn / 2);
@@ -389,56 +405,64 @@ __global__ void __launch_bounds__(kBackThreads, 1)
       tc_fence_after();
       const uint32_t tacc = tmem_base + lane_off + buf * kAccCols;
       if constexpr (kGrad) {
+        // the width as a constant: 3 % of this kernel on the 7B shape
+        const auto chunk_loop = [&](auto width) {
+          constexpr int kBN = decltype(width)::value, kChunks = kBN / 64;  // 32 columns of this warp
 #pragma unroll 1
-        for (int c = 0; c < chunks; ++c) {
-          uint32_t g[32], u[32];
-          tmem_ld_x32(tacc + half * (bn / 2) + c * 32, g);
-          tmem_ld_x32(tacc + bn + half * (bn / 2) + c * 32, u);
-          uint4 dyc[4];
+          for (int c = 0; c < kChunks; ++c) {
+            uint32_t g[32], u[32];
+            tmem_ld_x32(tacc + half * (kBN / 2) + c * 32, g);
+            tmem_ld_x32(tacc + kBN + half * (kBN / 2) + c * 32, u);
+            uint4 dyc[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) dyc[e] = dyv[e];
-          if (c + 1 < chunks) load_dy(c + 1);
-          tmem_wait_ld();
-          reg_fence(g);
-          reg_fence(u);
-          if (c == chunks - 1) {  // this warp's part of the accumulator is read
-            tc_fence_before();
+            for (int e = 0; e < 4; ++e) dyc[e] = dyv[e];
+            if (c + 1 < kChunks) load_dy(c + 1);
+            tmem_wait_ld();
+            reg_fence(g);
+            reg_fence(u);
+            if (c == kChunks - 1) {  // this warp's part of the accumulator is read
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive_cluster(tempty0_lead + 8u * buf);
+            }
+            if (lane == 0) bulk_wait_read<0>();  // the previous store has read the staging
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(tempty0_lead + 8u * buf);
-          }
-          if (lane == 0) bulk_wait_read<0>();  // the previous store has read the staging
-          __syncwarp();
-          const uint32_t row_addr = stg + lane * 64;
+            const uint32_t row_addr = stg + lane * 64;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            uint32_t wg[4], wu[4];
-            const uint32_t dw[4] = {dyc[j].x, dyc[j].y, dyc[j].z, dyc[j].w};
+            for (int j = 0; j < 4; ++j) {
+              uint32_t wg[4], wu[4];
+              const uint32_t dw[4] = {dyc[j].x, dyc[j].y, dyc[j].z, dyc[j].w};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int i0 = 8 * j + 2 * e;
-              const __nv_bfloat162 h = *reinterpret_cast<const __nv_bfloat162*>(&dw[e]);
-              float dg0, du0, dg1, du1;
-              gate_grads(__uint_as_float(g[i0]), __uint_as_float(u[i0]), __low2float(h), dg0, du0);
-              gate_grads(__uint_as_float(g[i0 + 1]), __uint_as_float(u[i0 + 1]), __high2float(h),
-                         dg1, du1);
-              wg[e] = pack_bf16x2(dg0, dg1);
-              wu[e] = pack_bf16x2(du0, du1);
+              for (int e = 0; e < 4; ++e) {
+                const int i0 = 8 * j + 2 * e;
+                const __nv_bfloat162 h = *reinterpret_cast<const __nv_bfloat162*>(&dw[e]);
+                float dg0, du0, dg1, du1;
+                gate_grads(__uint_as_float(g[i0]), __uint_as_float(u[i0]), __low2float(h), dg0, du0);
+                gate_grads(__uint_as_float(g[i0 + 1]), __uint_as_float(u[i0 + 1]), __high2float(h),
+                           dg1, du1);
+                wg[e] = pack_bf16x2(dg0, dg1);
+                wu[e] = pack_bf16x2(du0, du1);
+              }
+              const uint32_t off = (j ^ ((lane >> 1) & 3)) << 4;
+              st_shared_v4(row_addr + off, wg[0], wg[1], wg[2], wg[3]);
+              st_shared_v4(row_addr + 2048 + off, wu[0], wu[1], wu[2], wu[3]);
             }
-            const uint32_t off = (j ^ ((lane >> 1) & 3)) << 4;
-            st_shared_v4(row_addr + off, wg[0], wg[1], wg[2], wg[3]);
-            st_shared_v4(row_addr + 2048 + off, wu[0], wu[1], wu[2], wu[3]);
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            const int ncol = col0 + c * 32;
-            if (ncol < pr.cols && row0 < pr.rows) {
-              tma_store_2d(&pr.tmap_o0, stg, ncol, row0);
-              tma_store_2d(&pr.tmap_o1, stg + 2048, ncol, row0);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              const int ncol = col0 + c * 32;
+              if (ncol < pr.cols && row0 < pr.rows) {
+                tma_store_2d(&pr.tmap_o0, stg, ncol, row0);
+                tma_store_2d(&pr.tmap_o1, stg + 2048, ncol, row0);
+              }
+              bulk_commit();
             }
-            bulk_commit();
           }
-        }
+        };
+        if (bn == kPackBlockN)
+          chunk_loop(std::integral_constant<int, kPackBlockN>{});
+        else
+          chunk_loop(std::integral_constant<int, kPackBlockN / 2>{});
       } else {
         // this warp's 128 columns, 64 at a time: fp32 parts (32 columns, 128-byte
         // rows, a store) to the workspace, or 64 bf16 columns to the output
