@@ -198,7 +198,9 @@ __global__ void __launch_bounds__(kBackThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------ TMA producer (both CTAs)
-    if (lane == 0) {
+    // (the whole warp waits and counts, one lane issues, as below)
+    {
+      const bool one = elect_one();
       int s = 0;
       uint32_t ph = 0;
       uint32_t filled = 0, fill_ph = 0;
@@ -221,62 +223,70 @@ __global__ void __launch_bounds__(kBackThreads, 1)
         const CUtensorMap* map_b = bn == kPackBlockN ? &g.tmap_b0 : &g.tmap_b1;  // kGrad
         const uint32_t bytes = g.a_bytes * (rows_peer ? 2 : 1) + 2 * (weight ? g.a_bytes : bn * kBlockK * 2);
         for (int i = begin; i < end; ++i) {
-          if (!mbar_wait(empty0 + 8u * s, ph ^ 1u, wc, kSiteProducerEmpty)) {
+          if (!mbar_wait_warp(empty0 + 8u * s, ph ^ 1u, wc, kSiteProducerEmpty)) {
             ok = false;
             break;
           }
           if (skip_once) {
             skip_once = false;  // testing hook: both CTAs leave this stage unfilled
           } else {
-            if (leader) mbar_arrive_expect_tx(full0 + 8u * s, bytes);
-            const uint32_t fb = full0_lead + 8u * s;
-            const uint32_t da = sA + s * kOperandBytes, db = sB + s * kOperandBytes;
-            if constexpr (kGrad) {
-              // A rows [r0, +128); bn gate (rank 0) or up (rank 1) rows of tile (nb, i)
-              if (rows_here) tma_load_2d_pair(da, &g.tmap_a0, fb, i * kBlockK, r0);
-              tma_load_3d_pair(db, map_b, fb, 0,
-                               static_cast<int>(rank) * kPackBlockN + off, nb * g.slices + i);
-            } else if (!weight) {
-              // stages 2 d, 2 d + 1: rows [128 h, +128) of packed tile row j (a gate/up
-              // tile holds 128 gate then 128 up columns of the sum, a down tile 256);
-              // left operand: 64 of those columns of the sum a stage; right operand:
-              // all 128, for 64 of this CTA's 128 output columns a stage (a block past
-              // the last one reads another tile or zeros; its columns lie outside the
-              // output and are not stored)
-              const int j = i >> 2, h = (i >> 1) & 1, e = i & 1;
-              const int col = (g.two ? j * kPackBlockN : j * 2 * kPackBlockN + h * kPackBlockN) + e * kBlockK;
-              if (rows_here) tma_load_2d_pair(da, g.two && h ? &g.tmap_a1 : &g.tmap_a0, fb, col, r0);
-              tma_load_3d_pair(db, &g.tmap_b0, fb, 0, h * kPackBlockN,
-                               j * g.col_slices + nb * 4 + static_cast<int>(rank) * 2 + e);
-            } else {
-              // stages 2 d, 2 d + 1: tokens [128 d, +128), 64 of this CTA's 128 output
-              // rows and 64 of its 128 output columns a stage
-              const int m = (i >> 1) * 2 * kBlockK, e = (i & 1) * kBlockK;
-              const int c0 =
-                  g.two ? nb * kTileM : nb * 2 * kTileM + static_cast<int>(rank) * kTileM;
-              tma_load_2d_pair(da, &g.tmap_a0, fb, r0 + e, m);
-              tma_load_2d_pair(db, g.two && rank ? &g.tmap_b1 : &g.tmap_b0, fb, c0 + e, m);
+            if (one) {
+              if (leader) mbar_arrive_expect_tx(full0 + 8u * s, bytes);
+              const uint32_t fb = full0_lead + 8u * s;
+              const uint32_t da = sA + s * kOperandBytes, db = sB + s * kOperandBytes;
+              if constexpr (kGrad) {
+                // A rows [r0, +128); bn gate (rank 0) or up (rank 1) rows of tile (nb, i)
+                if (rows_here) tma_load_2d_pair(da, &g.tmap_a0, fb, i * kBlockK, r0);
+                tma_load_3d_pair(db, map_b, fb, 0,
+                                 static_cast<int>(rank) * kPackBlockN + off, nb * g.slices + i);
+              } else if (!weight) {
+                // stages 2 d, 2 d + 1: rows [128 h, +128) of packed tile row j (a gate/up
+                // tile holds 128 gate then 128 up columns of the sum, a down tile 256);
+                // left operand: 64 of those columns of the sum a stage; right operand:
+                // all 128, for 64 of this CTA's 128 output columns a stage (a block past
+                // the last one reads another tile or zeros; its columns lie outside the
+                // output and are not stored)
+                const int j = i >> 2, h = (i >> 1) & 1, e = i & 1;
+                const int col = (g.two ? j * kPackBlockN : j * 2 * kPackBlockN + h * kPackBlockN) + e * kBlockK;
+                if (rows_here) tma_load_2d_pair(da, g.two && h ? &g.tmap_a1 : &g.tmap_a0, fb, col, r0);
+                tma_load_3d_pair(db, &g.tmap_b0, fb, 0, h * kPackBlockN,
+                                 j * g.col_slices + nb * 4 + static_cast<int>(rank) * 2 + e);
+              } else {
+                // stages 2 d, 2 d + 1: tokens [128 d, +128), 64 of this CTA's 128 output
+                // rows and 64 of its 128 output columns a stage
+                const int m = (i >> 1) * 2 * kBlockK, e = (i & 1) * kBlockK;
+                const int c0 =
+                    g.two ? nb * kTileM : nb * 2 * kTileM + static_cast<int>(rank) * kTileM;
+                tma_load_2d_pair(da, &g.tmap_a0, fb, r0 + e, m);
+                tma_load_2d_pair(db, g.two && rank ? &g.tmap_b1 : &g.tmap_b0, fb, c0 + e, m);
+              }
             }
             filled |= 1u << s;
             fill_ph = (fill_ph & ~(1u << s)) | (ph << s);
           }
+          __syncwarp();
           if (++s == kStages) {
             s = 0;
             ph ^= 1u;
           }
         }
       }
-      pdl_launch_dependents();
+      if (one) pdl_launch_dependents();
       // Rank 0's full barriers count both CTAs' bytes: once they complete, every
       // copy issued by the pair for those stages has landed.
-      if (leader)
+      if (leader && one)
         for (int i = 0; i < kStages; ++i)
           if (filled & (1u << i)) mbar_wait_drain(full0 + 8u * i, (fill_ph >> i) & 1u, wc);
     }
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------ MMA issuer (rank 0)
-    if (leader && lane == 0) {
+    // The whole warp waits and counts, one lane issues: with one lane in the loop from
+    // the start the descriptors are not warp-uniform to the compiler, and the issue
+    // itself held the tensor pipe up. Here and in the producer, 7B block, 4096 tokens:
+    // dG and dU 1.11 -> 0.99 M cycles, both gradients 2.11 -> 1.98.
+    if (leader) {
+      const bool one = elect_one();
       int s = 0;
       uint32_t ph = 0;
       int buf = 0;
@@ -286,25 +296,28 @@ __global__ void __launch_bounds__(kBackThreads, 1)
         const BackwardProduct& g = weight ? p.w : p.in;
         const int part = u % g.splits;
         const int begin = part_begin<kGrad>(g, part), end = part_begin<kGrad>(g, part + 1);
-        if (!mbar_wait(tempty0 + 8u * buf, acc_ph ^ 1u, wc, kSiteMmaTmemEmpty)) break;
+        if (!mbar_wait_warp(tempty0 + 8u * buf, acc_ph ^ 1u, wc, kSiteMmaTmemEmpty)) break;
         tc_fence_after();
         const uint32_t d = tmem_base + buf * kAccCols;
         if constexpr (kGrad) {
-          // the descriptors as constants: 4 % of this kernel on the 7B shape
+          // the instruction descriptors as constants: 3 % of this kernel on the 7B shape
           const auto issue = [&](auto columns) {
             constexpr uint32_t kIdesc = idesc_bf16_f32(2 * kTileM, decltype(columns)::value);
             for (int i = begin; i < end; ++i) {
-              if (!mbar_wait(full0 + 8u * s, ph, wc, kSiteMmaFull)) {
+              if (!mbar_wait_warp(full0 + 8u * s, ph, wc, kSiteMmaFull)) {
                 ok = false;
                 break;
               }
               tc_fence_after();
               const uint64_t adesc = smem_desc_sw128(sA + s * kOperandBytes);
               const uint64_t bdesc = smem_desc_sw128(sB + s * kOperandBytes);
+              if (one) {
 #pragma unroll
-              for (uint32_t k = 0; k < 4; ++k)
-                mma_bf16_pair(d, adesc + 2u * k, bdesc + 2u * k, kIdesc, (i != begin || k != 0) ? 1u : 0u);
-              mma_commit_pair_multicast(empty0 + 8u * s, 0x3);  // frees the stage in both CTAs
+                for (uint32_t k = 0; k < 4; ++k)
+                  mma_bf16_pair(d, adesc + 2u * k, bdesc + 2u * k, kIdesc, (i != begin || k != 0) ? 1u : 0u);
+                mma_commit_pair_multicast(empty0 + 8u * s, 0x3);  // frees the stage in both CTAs
+              }
+              __syncwarp();
               if (++s == kStages) {
                 s = 0;
                 ph ^= 1u;
@@ -324,8 +337,8 @@ __global__ void __launch_bounds__(kBackThreads, 1)
             constexpr uint32_t kIdesc =
                 idesc_bf16_f32(2 * kTileM, kAccCols) | (kWeight ? 1u << 15 : 0u) | (1u << 16);
             for (int i = begin; i < end; i += 2) {  // s is even: every unit has whole pairs of stages
-              if (!mbar_wait(full0 + 8u * s, ph, wc, kSiteMmaFull) ||
-                  !mbar_wait(full0 + 8u * (s + 1), ph, wc, kSiteMmaFull)) {
+              if (!mbar_wait_warp(full0 + 8u * s, ph, wc, kSiteMmaFull) ||
+                  !mbar_wait_warp(full0 + 8u * (s + 1), ph, wc, kSiteMmaFull)) {
                 ok = false;
                 break;
               }
@@ -335,15 +348,18 @@ __global__ void __launch_bounds__(kBackThreads, 1)
               const uint64_t bdesc = smem_desc_sw128_mn(sB + s * kOperandBytes, kOperandBytes);
               // weight gradient: no MMA for 16 tokens that do not exist
               const int ksteps = kWeight ? min(8, (g.sum - (i >> 1) * 2 * kBlockK + 15) / 16) : 8;
+              if (one) {
 #pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                const uint64_t da = adesc + (kWeight ? (2048u >> 4) * k
-                                                    : 2u * (k & 3) + (k >> 2) * (kOperandBytes >> 4));
-                if (k < ksteps)
-                  mma_bf16_pair(d, da, bdesc + (2048u >> 4) * k, kIdesc, (i != begin || k != 0) ? 1u : 0u);
+                for (int k = 0; k < 8; ++k) {
+                  const uint64_t da = adesc + (kWeight ? (2048u >> 4) * k
+                                                      : 2u * (k & 3) + (k >> 2) * (kOperandBytes >> 4));
+                  if (k < ksteps)
+                    mma_bf16_pair(d, da, bdesc + (2048u >> 4) * k, kIdesc, (i != begin || k != 0) ? 1u : 0u);
+                }
+                mma_commit_pair_multicast(empty0 + 8u * s, 0x3);  // frees the stages in both CTAs
+                mma_commit_pair_multicast(empty0 + 8u * (s + 1), 0x3);
               }
-              mma_commit_pair_multicast(empty0 + 8u * s, 0x3);  // frees the stages in both CTAs
-              mma_commit_pair_multicast(empty0 + 8u * (s + 1), 0x3);
+              __syncwarp();
               s += 2;
               if (s == kStages) {
                 s = 0;
@@ -357,12 +373,14 @@ __global__ void __launch_bounds__(kBackThreads, 1)
             issue(std::false_type{});
         }
         if (!ok) break;
-        mma_commit_pair_multicast(tfull0 + 8u * buf, 0x3);  // both halves of the accumulator ready
+        if (one) mma_commit_pair_multicast(tfull0 + 8u * buf, 0x3);  // both halves of the accumulator ready
         buf ^= 1;
         if (buf == 0) acc_ph ^= 1u;
       }
-      mma_commit_pair_multicast(drain_bar, 0x1);
-      mbar_wait_drain(drain_bar, 0, wc);
+      if (one) {
+        mma_commit_pair_multicast(drain_bar, 0x1);
+        mbar_wait_drain(drain_bar, 0, wc);
+      }
     }
     __syncwarp();
   } else {

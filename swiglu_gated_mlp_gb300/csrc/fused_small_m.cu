@@ -378,7 +378,8 @@ __global__ void __launch_bounds__(kLora ? kLoraThreads : kThreads, kLora ? 2 : 1
 
   if (warp == 0) {
     // ------------------------------------------------ TMA producer -----
-    if (lane == 0) {
+    {
+      const bool one = elect_one();  // as the MMA issuer
       const uint64_t pol_w = policy_evict_first();  // weights: read once
       const uint64_t pol_x = policy_evict_last();   // activations: re-read by every CTA
       if (kLora && !own_v) fence_proxy_async();  // the tokens: see the grid-dependency wait above
@@ -390,19 +391,22 @@ __global__ void __launch_bounds__(kLora ? kLoraThreads : kThreads, kLora ? 2 : 1
       int extra = 0, done = 0, lead = num_slices;  // adapter slices, how many are loaded
       // Lb rows of the next adapter slice to the stage's weight half
       const auto load_adapter = [&] {
-        if (!mbar_wait(empty0 + 8u * s, ph ^ 1u, wc, kSiteProducerEmpty)) return false;
-        mbar_arrive(vfree0 + 8u * s);  // the stage's token half is free for V
-        const uint32_t fb = full0 + 8u * s, sw = s0 + s * stage_bytes;
-        const int a = adapter_at(done), h = done % per_adapter;
-        const int n0 = (kDown ? 2 : 1) * nblk * kPackBlockN;
-        mbar_arrive_expect_tx(fb, per_adapter == 1 ? kWStageBytes : kWStageBytes / 2);
-        if (kDown) {  // output columns n0 .. + 127 and n0 + 128 .. + 255
-          tma_load_3d(sw, &p.tmap_lb, fb, 0, n0, a);
-          tma_load_3d(sw + kWStageBytes / 2, &p.tmap_lb, fb, 0, n0 + kPackBlockN, a);
-        } else {      // gate rows, up rows, or both
-          tma_load_3d(sw, &p.tmap_lb, fb, 0, n0, 2 * a + h);
-          if (per_adapter == 1) tma_load_3d(sw + kWStageBytes / 2, &p.tmap_lb, fb, 0, n0, 2 * a + 1);
+        if (!mbar_wait_warp(empty0 + 8u * s, ph ^ 1u, wc, kSiteProducerEmpty)) return false;
+        if (one) {
+          mbar_arrive(vfree0 + 8u * s);  // the stage's token half is free for V
+          const uint32_t fb = full0 + 8u * s, sw = s0 + s * stage_bytes;
+          const int a = adapter_at(done), h = done % per_adapter;
+          const int n0 = (kDown ? 2 : 1) * nblk * kPackBlockN;
+          mbar_arrive_expect_tx(fb, per_adapter == 1 ? kWStageBytes : kWStageBytes / 2);
+          if (kDown) {  // output columns n0 .. + 127 and n0 + 128 .. + 255
+            tma_load_3d(sw, &p.tmap_lb, fb, 0, n0, a);
+            tma_load_3d(sw + kWStageBytes / 2, &p.tmap_lb, fb, 0, n0 + kPackBlockN, a);
+          } else {      // gate rows, up rows, or both
+            tma_load_3d(sw, &p.tmap_lb, fb, 0, n0, 2 * a + h);
+            if (per_adapter == 1) tma_load_3d(sw + kWStageBytes / 2, &p.tmap_lb, fb, 0, n0, 2 * a + 1);
+          }
         }
+        __syncwarp();
         filled |= 1u << s;
         fill_ph = (fill_ph & ~(1u << s)) | (ph << s);
         if (++s == stages) {
@@ -415,36 +419,39 @@ __global__ void __launch_bounds__(kLora ? kLoraThreads : kThreads, kLora ? 2 : 1
       for (int kb = kb_begin; kb < kb_end; ++kb) {
         if constexpr (kLora) {
           if (kb - kb_begin == first_slices) {
-            ok = mbar_wait(list_bar, 0, wc, kSiteLora);
+            ok = mbar_wait_warp(list_bar, 0, wc, kSiteLora);
             extra = ok ? adapter_slices() : 0;
             lead = lead_of(extra);
           }
           if (ok && kb - kb_begin >= lead && done < extra) ok = load_adapter();
           if (!ok) break;
         }
-        if (!mbar_wait(empty0 + 8u * s, ph ^ 1u, wc, kSiteProducerEmpty)) {
+        if (!mbar_wait_warp(empty0 + 8u * s, ph ^ 1u, wc, kSiteProducerEmpty)) {
           ok = false;
           break;
         }
         if (skip_once) {
           skip_once = false;  // testing hook: leave this stage unfilled
         } else {
-          const uint32_t fb = full0 + 8u * s;
-          const uint32_t sw = s0 + s * stage_bytes;
-          const int k0 = kb * kBK;
-          mbar_arrive_expect_tx(fb, stage_bytes + (kMx ? kSfStageBytes : 0));
-          tma_load_3d_hint(sw, &p.tmap_w, fb, 0, 0, wtile + kb, pol_w);  // one contiguous 32 KB tile
-          tma_load_2d_hint(sw + kWStageBytes, &p.tmap_x, fb, k0, m0, pol_x);
-          if constexpr (kMx) {
-            // 4 rows of 256 bytes: the tile's gate and up scale blocks; 2 rows: the
-            // activations' block (128-row chunk m0 / 128, K slice kb)
-            const uint32_t sf = sf0 + s * kSfStageBytes;
-            tma_load_2d(sf, &p.tmap_sw, fb, 0, 4 * (wtile + kb));
-            tma_load_2d(sf + 2 * kSfBlockBytes, &p.tmap_sa, fb, 0, 2 * ((m0 / 128) * num_kb + kb));
+          if (one) {
+            const uint32_t fb = full0 + 8u * s;
+            const uint32_t sw = s0 + s * stage_bytes;
+            const int k0 = kb * kBK;
+            mbar_arrive_expect_tx(fb, stage_bytes + (kMx ? kSfStageBytes : 0));
+            tma_load_3d_hint(sw, &p.tmap_w, fb, 0, 0, wtile + kb, pol_w);  // one contiguous 32 KB tile
+            tma_load_2d_hint(sw + kWStageBytes, &p.tmap_x, fb, k0, m0, pol_x);
+            if constexpr (kMx) {
+              // 4 rows of 256 bytes: the tile's gate and up scale blocks; 2 rows: the
+              // activations' block (128-row chunk m0 / 128, K slice kb)
+              const uint32_t sf = sf0 + s * kSfStageBytes;
+              tma_load_2d(sf, &p.tmap_sw, fb, 0, 4 * (wtile + kb));
+              tma_load_2d(sf + 2 * kSfBlockBytes, &p.tmap_sa, fb, 0, 2 * ((m0 / 128) * num_kb + kb));
+            }
           }
           filled |= 1u << s;
           fill_ph = (fill_ph & ~(1u << s)) | (ph << s);
         }
+        __syncwarp();
         if (++s == stages) {
           s = 0;
           ph ^= 1u;
@@ -452,19 +459,22 @@ __global__ void __launch_bounds__(kLora ? kLoraThreads : kThreads, kLora ? 2 : 1
       }
       if constexpr (kLora) {
         if (ok && num_slices == first_slices) {
-          ok = mbar_wait(list_bar, 0, wc, kSiteLora);
+          ok = mbar_wait_warp(list_bar, 0, wc, kSiteLora);
           extra = ok ? adapter_slices() : 0;
         }
         while (ok && done < extra) ok = load_adapter();
       }
-      pdl_launch_dependents();
-      for (int i = 0; i < stages; ++i)
+      if (one) pdl_launch_dependents();
+      for (int i = 0; one && i < stages; ++i)
         if (filled & (1u << i)) mbar_wait_drain(full0 + 8u * i, (fill_ph >> i) & 1u, wc);
     }
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------ MMA issuer -------
-    if (lane == 0) {
+    {
+      // waits and counts by the whole warp, one lane issues, as in the pair kernel: 7B
+      // decode 42.3 -> 41.2 us, with adapters 48.0 -> 46.4; 1 token, K 896, 8.2 -> 7.0
+      const bool one = elect_one();
       const uint32_t idesc = kFp8 ? idesc_e4m3_f32(128, mt) : idesc_bf16_f32(128, mt);
       const uint32_t d_gate = tmem_base;
       const uint32_t d_up = tmem_base + static_cast<uint32_t>(mt);
@@ -474,8 +484,8 @@ __global__ void __launch_bounds__(kLora ? kLoraThreads : kThreads, kLora ? 2 : 1
       int extra = 0, done = 0, lead = num_slices;  // adapter slices, how many are issued
       uint32_t vph = 0;         // phase of each stage's V barrier
       const auto mma_adapter = [&] {
-        if (!mbar_wait(full0 + 8u * s, ph, wc, kSiteMmaFull) ||
-            !mbar_wait(vready0 + 8u * s, (vph >> s) & 1u, wc, kSiteLora))
+        if (!mbar_wait_warp(full0 + 8u * s, ph, wc, kSiteMmaFull) ||
+            !mbar_wait_warp(vready0 + 8u * s, (vph >> s) & 1u, wc, kSiteLora))
           return false;
         vph ^= 1u << s;
         tc_fence_after();
@@ -483,16 +493,19 @@ __global__ void __launch_bounds__(kLora ? kLoraThreads : kThreads, kLora ? 2 : 1
         const uint64_t lo = smem_desc_sw128(sw), hi = smem_desc_sw128(sw + kWStageBytes / 2);
         const uint64_t v = smem_desc_sw128(sw + kWStageBytes);
         const int ksteps = (p.lora_rank + 15) / 16, h = done % per_adapter;
-        for (int k = 0; k < ksteps; ++k) {
-          // down: both halves from one V; gate/up: V1 and V2 side by side, or one of them
-          if (per_adapter == 1) {
-            mma_bf16(d_gate, lo + 2u * k, v + 2u * k, idesc, 1u);
-            mma_bf16(d_up, hi + 2u * k, v + 2u * (kDown ? k : ksteps + k), idesc, 1u);
-          } else {
-            mma_bf16(h ? d_up : d_gate, lo + 2u * k, v + 2u * k, idesc, 1u);
+        if (one) {
+          for (int k = 0; k < ksteps; ++k) {
+            // down: both halves from one V; gate/up: V1 and V2 side by side, or one of them
+            if (per_adapter == 1) {
+              mma_bf16(d_gate, lo + 2u * k, v + 2u * k, idesc, 1u);
+              mma_bf16(d_up, hi + 2u * k, v + 2u * (kDown ? k : ksteps + k), idesc, 1u);
+            } else {
+              mma_bf16(h ? d_up : d_gate, lo + 2u * k, v + 2u * k, idesc, 1u);
+            }
           }
+          mma_commit(empty0 + 8u * s);
         }
-        mma_commit(empty0 + 8u * s);
+        __syncwarp();
         if (++s == stages) {
           s = 0;
           ph ^= 1u;
@@ -503,14 +516,14 @@ __global__ void __launch_bounds__(kLora ? kLoraThreads : kThreads, kLora ? 2 : 1
       for (int kb = kb_begin; kb < kb_end; ++kb) {
         if constexpr (kLora) {
           if (kb - kb_begin == first_slices) {
-            ok = mbar_wait(list_bar, 0, wc, kSiteLora);
+            ok = mbar_wait_warp(list_bar, 0, wc, kSiteLora);
             extra = ok ? adapter_slices() : 0;
             lead = lead_of(extra);
           }
           if (ok && kb - kb_begin >= lead && done < extra) ok = mma_adapter();
           if (!ok) break;
         }
-        if (!mbar_wait(full0 + 8u * s, ph, wc, kSiteMmaFull)) {
+        if (!mbar_wait_warp(full0 + 8u * s, ph, wc, kSiteMmaFull)) {
           ok = false;
           break;
         }
@@ -521,28 +534,31 @@ __global__ void __launch_bounds__(kLora ? kLoraThreads : kThreads, kLora ? 2 : 1
         const uint64_t xdesc = smem_desc_sw128(sw + kWStageBytes);          // tokens
         // scale slot of this stage: gate [0, 4), up [4, 8), tokens [8, 12)
         const uint32_t tsf = tmem_base + sf_col + uint32_t(s) * kSfTmemCols;
-        if constexpr (kMx) {
-          const uint32_t sf = sf0 + s * kSfStageBytes;
-          tmem_cp_sf(tsf, smem_desc_sf(sf));
-          tmem_cp_sf(tsf + 4, smem_desc_sf(sf + kSfBlockBytes));
-          tmem_cp_sf(tsf + 8, smem_desc_sf(sf + 2 * kSfBlockBytes));
-        }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {  // four 32-byte K steps per 128-byte row
-          const uint32_t acc = (kb != kb_begin || k != 0) ? 1u : 0u;
-          if constexpr (kMx) {  // K step k consumes scale group k of the slice
-            const uint32_t id = idesc_mx_e4m3(128, mt, k);
-            mma_mx(d_gate, gdesc + 2u * k, xdesc + 2u * k, id, tsf, tsf + 8, acc);
-            mma_mx(d_up, udesc + 2u * k, xdesc + 2u * k, id, tsf + 4, tsf + 8, acc);
-          } else if constexpr (kFp8) {
-            mma_e4m3(d_gate, gdesc + 2u * k, xdesc + 2u * k, idesc, acc);
-            mma_e4m3(d_up, udesc + 2u * k, xdesc + 2u * k, idesc, acc);
-          } else {
-            mma_bf16(d_gate, gdesc + 2u * k, xdesc + 2u * k, idesc, acc);
-            mma_bf16(d_up, udesc + 2u * k, xdesc + 2u * k, idesc, acc);
+        if (one) {
+          if constexpr (kMx) {
+            const uint32_t sf = sf0 + s * kSfStageBytes;
+            tmem_cp_sf(tsf, smem_desc_sf(sf));
+            tmem_cp_sf(tsf + 4, smem_desc_sf(sf + kSfBlockBytes));
+            tmem_cp_sf(tsf + 8, smem_desc_sf(sf + 2 * kSfBlockBytes));
           }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {  // four 32-byte K steps per 128-byte row
+            const uint32_t acc = (kb != kb_begin || k != 0) ? 1u : 0u;
+            if constexpr (kMx) {  // K step k consumes scale group k of the slice
+              const uint32_t id = idesc_mx_e4m3(128, mt, k);
+              mma_mx(d_gate, gdesc + 2u * k, xdesc + 2u * k, id, tsf, tsf + 8, acc);
+              mma_mx(d_up, udesc + 2u * k, xdesc + 2u * k, id, tsf + 4, tsf + 8, acc);
+            } else if constexpr (kFp8) {
+              mma_e4m3(d_gate, gdesc + 2u * k, xdesc + 2u * k, idesc, acc);
+              mma_e4m3(d_up, udesc + 2u * k, xdesc + 2u * k, idesc, acc);
+            } else {
+              mma_bf16(d_gate, gdesc + 2u * k, xdesc + 2u * k, idesc, acc);
+              mma_bf16(d_up, udesc + 2u * k, xdesc + 2u * k, idesc, acc);
+            }
+          }
+          mma_commit(empty0 + 8u * s);
         }
-        mma_commit(empty0 + 8u * s);
+        __syncwarp();
         if (++s == stages) {
           s = 0;
           ph ^= 1u;
@@ -550,14 +566,16 @@ __global__ void __launch_bounds__(kLora ? kLoraThreads : kThreads, kLora ? 2 : 1
       }
       if constexpr (kLora) {
         if (ok && num_slices == first_slices) {
-          ok = mbar_wait(list_bar, 0, wc, kSiteLora);
+          ok = mbar_wait_warp(list_bar, 0, wc, kSiteLora);
           extra = ok ? adapter_slices() : 0;
         }
         while (ok && done < extra) ok = mma_adapter();
       }
-      if (ok) mma_commit(tfull_bar);
-      mma_commit(drain_bar);
-      mbar_wait_drain(drain_bar, 0, wc);
+      if (one) {
+        if (ok) mma_commit(tfull_bar);
+        mma_commit(drain_bar);
+        mbar_wait_drain(drain_bar, 0, wc);
+      }
     }
     __syncwarp();
   } else if (kLora && warp >= 6) {

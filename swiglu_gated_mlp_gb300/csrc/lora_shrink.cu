@@ -243,14 +243,15 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   float* part = reinterpret_cast<float*>(passes <= 1 ? smem : smem + ring);
   const uint32_t sla = s0 + stages * kXBytes;
   if (warp == 0) {
-    if (lane == 0) {
+    {
+      const bool one = elect_one();
       int s = 0;
       uint32_t ph = 0, filled = 0, fill_ph = 0;
       bool skip_once = p.inject_stall != 0, ok = true;
       for (int pass = 0; ok && pass < passes; ++pass) {
         const int g0 = pass * per_pass, gn = min(per_pass, n128 - g0);
         for (int i = begin; i < end; ++i) {
-          if (!mbar_wait(empty0 + 8u * s, ph ^ 1u, wc, kSiteProducerEmpty)) {
+          if (!mbar_wait_warp(empty0 + 8u * s, ph ^ 1u, wc, kSiteProducerEmpty)) {
             ok = false;
             break;
           }
@@ -259,63 +260,72 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           } else {
             const uint32_t fb = full0 + 8u * s;
             const bool loaded = pass == 0 && i - begin < early && !p.inject_stall;
-            mbar_arrive_expect_tx(fb, (loaded ? 0 : kXBytes) + gn * la_bytes);
-            if (!loaded) tma_load_2d(s0 + s * kXBytes, &p.tmap_x, fb, i * kBlockK, m0);
-            for (int g = 0; g < gn; ++g)
-              tma_load_2d(sla + s * la_stage + g * la_bytes, &p.tmap_la, fb, i * kBlockK,
-                          mine[g0 + g] * p.hr);
+            if (one) {
+              mbar_arrive_expect_tx(fb, (loaded ? 0 : kXBytes) + gn * la_bytes);
+              if (!loaded) tma_load_2d(s0 + s * kXBytes, &p.tmap_x, fb, i * kBlockK, m0);
+              for (int g = 0; g < gn; ++g)
+                tma_load_2d(sla + s * la_stage + g * la_bytes, &p.tmap_la, fb, i * kBlockK,
+                            mine[g0 + g] * p.hr);
+            }
             filled |= 1u << s;
             fill_ph = (fill_ph & ~(1u << s)) | (ph << s);
           }
+          __syncwarp();
           if (++s == stages) {
             s = 0;
             ph ^= 1u;
           }
         }
       }
-      if (passes == 0 && !p.inject_stall)  // no adapter: let the early loads land
+      if (one && passes == 0 && !p.inject_stall)  // no adapter: let the early loads land
         for (int s2 = 0; s2 < early; ++s2) {
           mbar_arrive(full0 + 8u * s2);
           mbar_wait_drain(full0 + 8u * s2, 0, wc);
         }
-      for (int i = 0; i < stages; ++i)
+      for (int i = 0; one && i < stages; ++i)
         if (filled & (1u << i)) mbar_wait_drain(full0 + 8u * i, (fill_ph >> i) & 1u, wc);
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0) {
+    {
+      const bool one = elect_one();  // waits and counts by the whole warp: see the pair kernel
       const uint32_t idesc = idesc_bf16_f32(kTileM, rb);
       int s = 0;
       uint32_t ph = 0;
       bool ok = true;
       for (int pass = 0; ok && pass < passes; ++pass) {
         const int gn = min(per_pass, n128 - pass * per_pass);
-        if (pass > 0 && !mbar_wait(tempty, (pass - 1) & 1, wc, kSiteMmaTmemEmpty)) break;
+        if (pass > 0 && !mbar_wait_warp(tempty, (pass - 1) & 1, wc, kSiteMmaTmemEmpty)) break;
         tc_fence_after();
         for (int i = begin; i < end; ++i) {
-          if (!mbar_wait(full0 + 8u * s, ph, wc, kSiteMmaFull)) {
+          if (!mbar_wait_warp(full0 + 8u * s, ph, wc, kSiteMmaFull)) {
             ok = false;
             break;
           }
           tc_fence_after();
           const uint64_t xdesc = smem_desc_sw128(s0 + s * kXBytes);
-          for (int g = 0; g < gn; ++g) {
-            const uint64_t ldesc = smem_desc_sw128(sla + s * la_stage + g * la_bytes);
+          if (one) {
+            for (int g = 0; g < gn; ++g) {
+              const uint64_t ldesc = smem_desc_sw128(sla + s * la_stage + g * la_bytes);
 #pragma unroll
-            for (uint32_t k = 0; k < 4; ++k)
-              mma_bf16(tmem_base + g * rb, xdesc + 2u * k, ldesc + 2u * k, idesc,
-                       (i != begin || k != 0) ? 1u : 0u);
+              for (uint32_t k = 0; k < 4; ++k)
+                mma_bf16(tmem_base + g * rb, xdesc + 2u * k, ldesc + 2u * k, idesc,
+                         (i != begin || k != 0) ? 1u : 0u);
+            }
+            mma_commit(empty0 + 8u * s);
           }
-          mma_commit(empty0 + 8u * s);
+          __syncwarp();
           if (++s == stages) {
             s = 0;
             ph ^= 1u;
           }
         }
-        if (ok) mma_commit(tfull);
+        if (ok && one) mma_commit(tfull);
       }
-      mma_commit(drain_bar);
-      mbar_wait_drain(drain_bar, 0, wc);
+      if (one) {
+        mma_commit(drain_bar);
+        mbar_wait_drain(drain_bar, 0, wc);
+      }
     }
     __syncwarp();
   } else if (warp < 6) {
