@@ -58,7 +58,7 @@
 // Measured, 7B block, 4096 tokens, one call at a time: dG and dU 567-573 us (1.95
 // PFLOP/s), both gradients 1114-1125 us (1.98), tensor pipe 92 % busy in each; back
 // to back at the power cap 1974 us in all (1.69 PFLOP/s). 16 tokens on the same
-// weights: 172 us for 272 MB read twice and 272 MB written (writes alone run at 4.0
+// weights: 174 us for 272 MB read twice and 272 MB written (writes alone run at 4.0
 // TB/s here). 0.5B block, 128 tokens: 27.7 us, three launches that each wait for one
 // another (9, 15 and 4 us alone).
 #include <type_traits>

@@ -81,7 +81,7 @@
 // half; four warps write the masked V rows into its A half (thread = row) and
 // signal a barrier of their own, which the MMA issuer waits for beside the
 // stage's. (Alternating adapter and K slices instead: 660 against 640 us on the
-// 7B shape, 4096 tokens of rank 64.) Measured there: 613 us against 572 without
+// 7B shape, 4096 tokens of rank 64.) Measured there: 585 us against 541 without
 // adapters; the adapter slices' MMAs are 2 % of the tensor pipe's work, the waits
 // around them the rest. Non-finite entries of an Lb stay with the tokens of that
 // adapter (lora_lb.cuh); each CTA's warps look through the rows that its own copy

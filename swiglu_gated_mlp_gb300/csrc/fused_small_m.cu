@@ -56,16 +56,15 @@
 // With K split, adapters are dealt to the parts. Deltas as fp32 FMAs, thread =
 // weight column, were built first: as fast at 16 tokens of rank 16, but 300
 // against 71 us at 128 tokens of rank 64 (7B shape), where each token re-read
-// its adapter's rows. Measured, 7B gate/up, 16 tokens, rank 16, with the
-// shrink: 44.8 us for one adapter, 49.5 for 8 (284 MB, 5.8 TB/s = 0.86 of
-// copy), against 41 without adapters: 2 us are the second launch, 3.5 us the
-// shrink, then half a microsecond an adapter (1.2 MB of Lb through ring stages
-// that hold 32 KB of weight otherwise).
+// its adapter's rows. Measured, 7B gate/up, 16 tokens, rank 16: 45.0 us for one
+// adapter, 46.1 for 8 (284 MB, 6.2 TB/s = 0.92 of copy), against 41 without
+// adapters: the second launch, and the first loads that wait for it, are most of
+// the difference.
 // Non-finite entries of an Lb stay with the tokens of that adapter (lora_lb.cuh):
 // the epilogue's warps, idle until the accumulators are complete, look through
-// each slice beside the V warps (0.4 us of the 49.5 with 8 adapters, 0.8 of 31 at
-// 333 tokens of 10 adapters; done by the V warps, between writing V and their
-// arrival, it took 1.4 and 2).
+// each slice beside the V warps (when it was added, 0.4 us more with 8 adapters, 0.8
+// at 333 tokens of 10; done by the V warps, between writing V and their arrival,
+// 1.4 and 2).
 #include "kernels.h"
 #include "lora_lb.cuh"
 #include "ptx.cuh"

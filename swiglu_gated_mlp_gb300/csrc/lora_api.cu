@@ -22,12 +22,14 @@ constexpr int64_t kGroupTokens = 128;
 // Whether the decode kernel runs, with its work split. It takes one group of
 // tokens, and more groups where 256-row pair tiles would leave the SMs idle or
 // take a nearly empty round. A pair's slice takes about 0.3 us, a decode CTA's
-// of 128 tokens 0.6 us (each group streams the weight), a K split 3 us. Measured,
-// decode against pairs (in each the kernel that makes V is out of the way): 333
-// tokens of 10 adapters, K 1416 N 5000, 33.9 / 47.8 us, K 2048 N 4000 35.3 / 33.3;
-// 500 tokens of 3, K 2048 N 4000, 39.4 / 30.4; down, 200 tokens of 4, N 4864 H 896 (K
-// over 8 CTAs) 23.7 / 32.3; down, 800 tokens of 2, N 18944 H 3584, 272 / 118. The rule
-// is off by up to a fifth where they meet (333 tokens, K 512 N 2000: pairs, 25.4 / 20.7).
+// of 128 tokens 0.5 us (each group streams the weight; 0.6 with many groups), a K
+// split 1 us. Measured, decode against pairs (in both the kernel that makes V is out
+// of the way): 333 tokens of 10 adapters, K 1416 N 5000, 30.6 / 43.7 us; 200 tokens of
+// 4, K 2048 N 4000 (K over 2 CTAs) 18.6 / 20.4, 500 of 3 (4 groups, K whole) 36.3 /
+// 28.5; down, N 18944 H 3584, 500 tokens of 3 (K over 2) 78.9 / 92.6, 800 of 2 (7
+// groups, K whole) 252 / 108; down, N 4864 H 896, 800 of 2 (7 groups, K over 4) 25.2 /
+// 31.7. Where the two meet the rule is off by up to a tenth, with 8 slices and many
+// adapters by a fifth (333 tokens of 10, K 512 N 2000: pairs, 24.1 / 19.2).
 swiglu_status_t plan_decode(int64_t M, int64_t blocks, int64_t slices, const DeviceView& d,
                             SmallMParams* p, bool* decode) {
   const int64_t groups = (M + kGroupTokens - 1) / kGroupTokens;
@@ -37,7 +39,7 @@ swiglu_status_t plan_decode(int64_t M, int64_t blocks, int64_t slices, const Dev
   if (st != SWIGLU_OK || *decode || d.max_pairs < 1) return st;
   const int64_t tiles = (M + 2 * kTileM - 1) / (2 * kTileM) * blocks;
   const int64_t rounds = (tiles + d.max_pairs - 1) / d.max_pairs;
-  *decode = 2 * slices / p->splits + (p->splits > 1 ? 10 : 0) <= rounds * slices;
+  *decode = (groups <= 4 ? 17 : 21) * slices / p->splits + (p->splits > 1 ? 40 : 0) <= 10 * rounds * slices;
   return SWIGLU_OK;
 }
 
@@ -75,18 +77,19 @@ int shrink_splits(int64_t tiles, int64_t slices, int sm_count) {
 
 // Whether every decode CTA makes V itself (make_own_v()), in place of a kernel
 // before it. A step there, 2 rows of V for each of 8 warps over 1024 of K, takes
-// 1.5 us, a slice of weight that streams meanwhile 0.7. Measured, made inside
-// against outside: K 896 N 4864, 7 slices a CTA, 1 token of rank 8 / 16 / 32 (1, 2, 4
-// steps) 8.3 / 9.5, 9.0 / 9.6, 12.2 / 9.7 us; K 3584 N 18944, 56 slices, 1 token of
-// rank 8 / 32 / 64 (4, 16, 32 steps) 40.8 / 44.7, 43.2 / 44.7, 54.9 / 45.8; down
-// N 4864 H 896, 10 slices, 1 / 2 tokens of rank 16 (5, 10 steps) 9.9 / 11.5,
-// 13.1 / 11.9; down N 18944 H 3584, 37 slices, rank 16 / 32 (19, 38) 26.8 / 26.8,
-// 34.4 / 27.0.
+// 1.5 us, a slice of weight that streams meanwhile 0.7; with more than 8000
+// multiply-adds for each of those the kernel beside the stream wins. Measured, made
+// inside against outside: K 896 N 4864, 7 slices a CTA, 1 token of rank 8 / 16 / 32
+// (1, 2, 4 steps) 7.3 / 8.8, 8.6 / 9.1, 11.8 / 9.2 us; K 3584 N 18944, 56 slices, 1
+// token of rank 8 / 32, 2 of 32 (4, 16, 32 steps) 41.0 / 43.9, 43.3 / 44.1, 44.8 / 44.7;
+// down N 4864 H 896, 10 slices, 1 / 2 tokens of rank 16 (5, 10 steps) 9.3 / 9.7,
+// 12.5 / 9.9; down N 18944 H 3584, 37 slices, 1 token of rank 8 / 16 (19 steps; 4100
+// and 8200 multiply-adds a slice) 23.8 / 25.0, 25.9 / 24.8.
 bool own_v(bool decode, int64_t M, int64_t hr, int64_t in, int splits) {
   if (!decode || M > 16 || M * hr > kLoraOwnValues) return false;
   const int64_t steps = ((M * hr + 15) / 16) * ((in + 1023) / 1024);
   const int64_t slices = (k_slices(in) + splits - 1) / splits;
-  return steps <= 2 || 9 * steps <= 5 * slices;
+  return steps <= 2 || (9 * steps <= 5 * slices && M * hr * in <= 8000 * slices);
 }
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
