@@ -344,8 +344,9 @@ __global__ void __launch_bounds__(kBackThreads, 1)
               const uint32_t pa = sA + s * kOperandBytes;
               const uint64_t adesc = kWeight ? smem_desc_sw128_mn(pa, kOperandBytes) : smem_desc_sw128(pa);
               const uint64_t bdesc = smem_desc_sw128_mn(sB + s * kOperandBytes, kOperandBytes);
-              // weight gradient: no MMA for 16 tokens that do not exist
-              const int ksteps = kWeight ? min(8, (g.sum - (i >> 1) * 2 * kBlockK + 15) / 16) : 8;
+              // weight gradient: no MMA for 16 tokens that do not exist (capped before it is
+              // rounded up, as up to 2^31 - 1 tokens are left)
+              const int ksteps = kWeight ? (min(g.sum - (i >> 1) * 2 * kBlockK, 2 * kBlockK) + 15) / 16 : 8;
               if (one) {
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {

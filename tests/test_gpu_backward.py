@@ -308,3 +308,52 @@ def test_plans_reach_every_form(native):
     assert max(wholes) > 0 or f["whole"] > 0
     assert native.swiglu_down_backward_plan_string(128, 4864, 896).startswith("down_backward input tiles=")
     assert native.swiglu_down_backward_workspace_bytes(4096, 18944, 3584) == 0
+
+
+def _repeated(block, rows):
+    """`block`'s rows repeated down to `rows` of them, on the GPU."""
+    return block.cuda().repeat(-(-rows // block.shape[0]), 1)[:rows]
+
+
+def _few_rows(block, M):
+    """Tokens at both ends and in the middle of M, and a [M, cols] that is zero but for theirs."""
+    rows = torch.cat([torch.arange(260), torch.tensor([(1 << 30) - 1, 1 << 30]), torch.arange(M - 260, M)])
+    out = torch.zeros(M, block.shape[1], dtype=torch.bfloat16, device="cuda")
+    out[rows.cuda()] = block[rows % block.shape[0]].cuda()
+    return rows, out
+
+
+def test_backward_largest_m(native):
+    # 2^31 - 1 tokens, the largest M the ABI accepts: A repeats a block of rows, dY is zero but
+    # for some tokens, whose sum the weight gradients are (about 172 GB on the device)
+    M, K, N, blk = (1 << 31) - 1, 8, 8, 4096
+    a, w1, w2, dy = inputs(blk, K, N, seed=74)
+    ad = dyd = outs = None
+    try:
+        ad = _repeated(a, M)
+        rows, dyd = _few_rows(dy, M)
+        outs = native.swiglu_backward(ad, native.swiglu_pack_weights(w1.cuda(), w2.cuda()), dyd)
+        native.swiglu_check_device_status()
+        args = (f64(a[rows % blk]), f64(w1), f64(w2), f64(dy[rows % blk]))
+        assert_within([outs[0][rows.cuda()], *outs[1:]], backward_values(*args), backward_bounds(*args))
+    finally:
+        ad = dyd = outs = None
+        torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("M", [(1 << 31) - 1, (1 << 31) - 15])
+def test_down_backward_largest_m(native, M):
+    # dOut is zero but for some tokens, Y repeats a block of rows (about 103 GB on the device)
+    N, H, blk = 8, 8, 4096
+    dout, w3, y = down_inputs(blk, N, H, seed=75)
+    dod = yd = outs = None
+    try:
+        yd = _repeated(y, M)
+        rows, dod = _few_rows(dout, M)
+        outs = native.swiglu_down_backward(dod, native.swiglu_pack_down_weights(w3.cuda()), yd)
+        native.swiglu_check_device_status()
+        args = (f64(dout[rows % blk]), f64(w3), f64(y[rows % blk]))
+        assert_within([outs[0][rows.cuda()], outs[1]], down_backward_values(*args), down_backward_bounds(*args))
+    finally:
+        dod = yd = outs = None
+        torch.cuda.empty_cache()
