@@ -454,3 +454,35 @@ def test_calls_one_after_another_see_each_others_outputs(native, M, K, N, r, L):
         torch.cuda.synchronize()
         assert torch.equal(got, want)
     native.swiglu_check_device_status()
+
+
+@pytest.mark.parametrize("down", [False, True])
+def test_lora_largest_m(native, down):
+    # 2^31 - 1 tokens, the largest M the ABI accepts: x, index and residual repeat a block of
+    # rows, so each sampled row's reference is that of its row in the block (about 155 GB)
+    M, K, N, L, r, blk = (1 << 31) - 1, 8, 8, 5, 8, 4096
+    a, w1, w2 = make_inputs(blk, K, N, seed=76)
+    la, lb, scale = table(L, 1 if down else 2, r, K, N, 76)
+    index = indices(blk, L, "mixed", 76)
+    res = make_inputs(blk, N, 8, 77)[0] if down else None
+    reps = -(-M // blk)
+    ad = idx = rd = y = None
+    try:
+        ad, idx = a.cuda().repeat(reps, 1)[:M], index.cuda().repeat(reps)[:M]
+        if down:
+            rd = res.cuda().repeat(reps, 1)[:M]
+            y = native.swiglu_down_forward_lora(ad, native.swiglu_pack_down_weights(w1.cuda()), N, la.cuda(),
+                                                lb.cuda(), idx, scale.cuda(), R=rd, Out=rd)
+        else:
+            y = native.swiglu_forward_lora(ad, native.swiglu_pack_weights(w1.cuda(), w2.cuda()), N, la.cuda(),
+                                           lb.cuda(), idx, scale.cuda())
+        native.swiglu_check_device_status()
+        rows = np.array([0, 1, blk - 1, blk, (1 << 30) - 1, 1 << 30, M - 257, M - 256, M - 129, M - 2, M - 1])
+        at = rows % blk
+        got = y[torch.from_numpy(rows).cuda()]
+        x, i, s = f64(a)[at], index.numpy()[at], f64(scale)
+        assert_within(got, down_forward_lora(x, f64(w1), f64(res)[at], f64(la), f64(lb), i, s) if down else
+                      forward_lora(x, f64(w1), f64(w2), f64(la), f64(lb), i, s))
+    finally:
+        ad = idx = rd = y = None
+        torch.cuda.empty_cache()
