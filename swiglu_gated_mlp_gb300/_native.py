@@ -160,6 +160,36 @@ class _on_device:
         return False
 
 
+def _new_tensor(shape, dtype, device, stream=None, returned=True) -> torch.Tensor:
+    """An uninitialised tensor for a call that runs on `stream` (None: the current one).
+
+    The allocator hands a freed block out again in the order of one stream. So the
+    memory of a tensor that another stream than the current one will write comes from
+    that stream's blocks: one of the current stream's could still be in use by work
+    queued there. A returned tensor that its owner frees is kept until the current
+    stream is done with it too.
+    """
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    index = device if isinstance(device, int) else device.index
+    handle = int(stream.cuda_stream) if isinstance(stream, torch.cuda.Stream) else int(stream)
+    if (0 if handle == 1 else handle) == _stream_handle(None, torch.device("cuda", index)):
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):  # 0 and 1 both name the default stream
+        stream = (torch.cuda.ExternalStream(handle, device=index) if handle > 1
+                  else torch.cuda.default_stream(index))
+    with _on_device(torch.device("cuda", index)):
+        current = torch.cuda.current_stream(index)
+        torch.cuda.set_stream(stream)
+        try:
+            t = torch.empty(shape, dtype=dtype, device=device)
+        finally:
+            torch.cuda.set_stream(current)
+    if returned:
+        t.record_stream(current)
+    return t
+
+
 def _dev_bf16(t: torch.Tensor, name: str) -> None:
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
@@ -190,8 +220,7 @@ def swiglu_pack_weights(W1: torch.Tensor, W2: torch.Tensor, Wpacked: torch.Tenso
         raise ValueError("W1 and W2 must both be [K, N]")
     K, N = W1.shape
     if Wpacked is None:  # opaque buffer of swiglu_packed_weight_bytes(K, N) bytes
-        Wpacked = torch.empty(swiglu_packed_weight_bytes(K, N) // 2, dtype=torch.bfloat16,
-                              device=W1.device)
+        Wpacked = _new_tensor(swiglu_packed_weight_bytes(K, N) // 2, torch.bfloat16, W1.device, stream)
     _dev_bf16(Wpacked, "Wpacked")
     if Wpacked.numel() * 2 < swiglu_packed_weight_bytes(K, N):
         raise ValueError("Wpacked is too small")
@@ -211,7 +240,7 @@ def swiglu_forward_variant(A: torch.Tensor, Wpacked: torch.Tensor, N: int, varia
     if Wpacked.numel() * 2 < swiglu_packed_weight_bytes(K, N):
         raise ValueError("Wpacked does not hold a packed weight for this K and N")
     if Y is None:
-        Y = torch.empty((M, N), dtype=torch.bfloat16, device=A.device)
+        Y = _new_tensor((M, N), torch.bfloat16, A.device, stream)
     _dev_bf16(Y, "Y")
     if tuple(Y.shape) != (M, N):
         raise ValueError("Y must be [M, N]")
@@ -260,8 +289,7 @@ def swiglu_pack_weights_fp8(W1: torch.Tensor, W2: torch.Tensor, Wpacked: torch.T
         raise ValueError("W1 and W2 must both be [K, N]")
     K, N = W1.shape
     if Wpacked is None:
-        Wpacked = torch.empty(swiglu_packed_weight_bytes_fp8(K, N), dtype=torch.uint8,
-                              device=W1.device)
+        Wpacked = _new_tensor(swiglu_packed_weight_bytes_fp8(K, N), torch.uint8, W1.device, stream)
     if Wpacked.numel() * Wpacked.element_size() < swiglu_packed_weight_bytes_fp8(K, N):
         raise ValueError("Wpacked is too small")
     with _on_device(W1.device):
@@ -282,7 +310,7 @@ def swiglu_forward_fp8(A: torch.Tensor, Wpacked: torch.Tensor, N: int, scale_a: 
     if Wpacked.numel() * Wpacked.element_size() < swiglu_packed_weight_bytes_fp8(K, N):
         raise ValueError("Wpacked does not hold a packed FP8 weight for this K and N")
     if Y is None:
-        Y = torch.empty((M, N), dtype=torch.bfloat16, device=A.device)
+        Y = _new_tensor((M, N), torch.bfloat16, A.device, stream)
     _dev_bf16(Y, "Y")
     if tuple(Y.shape) != (M, N):
         raise ValueError("Y must be [M, N]")
@@ -325,8 +353,7 @@ def swiglu_pack_weights_mxfp8(W1: torch.Tensor, S1: torch.Tensor, W2: torch.Tens
     if tuple(S1.shape) != (K // 32, N) or tuple(S2.shape) != (K // 32, N):
         raise ValueError("S1 and S2 must be [K/32, N]")
     if Wpacked is None:
-        Wpacked = torch.empty(swiglu_packed_weight_bytes_mxfp8(K, N), dtype=torch.uint8,
-                              device=W1.device)
+        Wpacked = _new_tensor(swiglu_packed_weight_bytes_mxfp8(K, N), torch.uint8, W1.device, stream)
     if Wpacked.numel() * Wpacked.element_size() < swiglu_packed_weight_bytes_mxfp8(K, N):
         raise ValueError("Wpacked is too small")
     with _on_device(W1.device):
@@ -345,8 +372,7 @@ def swiglu_pack_act_scales_mxfp8(SA: torch.Tensor, SAtiled: torch.Tensor | None 
         raise ValueError("SA must be [M, K/32]")
     M, K = SA.shape[0], 32 * SA.shape[1]
     if SAtiled is None:
-        SAtiled = torch.empty(max(swiglu_act_scale_bytes_mxfp8(M, K), 16), dtype=torch.uint8,
-                              device=SA.device)
+        SAtiled = _new_tensor(max(swiglu_act_scale_bytes_mxfp8(M, K), 16), torch.uint8, SA.device, stream)
     if SAtiled.numel() * SAtiled.element_size() < swiglu_act_scale_bytes_mxfp8(M, K):
         raise ValueError("SAtiled is too small")
     with _on_device(SA.device):
@@ -368,7 +394,7 @@ def swiglu_forward_mxfp8(A: torch.Tensor, SAtiled: torch.Tensor, Wpacked: torch.
     if SAtiled.numel() * SAtiled.element_size() < swiglu_act_scale_bytes_mxfp8(M, K):
         raise ValueError("SAtiled does not hold A's scales for this M and K")
     if Y is None:
-        Y = torch.empty((M, N), dtype=torch.bfloat16, device=A.device)
+        Y = _new_tensor((M, N), torch.bfloat16, A.device, stream)
     _dev_bf16(Y, "Y")
     if tuple(Y.shape) != (M, N):
         raise ValueError("Y must be [M, N]")
@@ -398,8 +424,7 @@ def swiglu_pack_down_weights(W3: torch.Tensor, W3packed: torch.Tensor | None = N
         raise ValueError("W3 must be [N, H]")
     N, H = W3.shape
     if W3packed is None:
-        W3packed = torch.empty(swiglu_down_packed_bytes(N, H) // 2, dtype=torch.bfloat16,
-                               device=W3.device)
+        W3packed = _new_tensor(swiglu_down_packed_bytes(N, H) // 2, torch.bfloat16, W3.device, stream)
     _dev_bf16(W3packed, "W3packed")
     if W3packed.numel() * 2 < swiglu_down_packed_bytes(N, H):
         raise ValueError("W3packed is too small")
@@ -470,7 +495,7 @@ def swiglu_down_forward(Y: torch.Tensor, W3packed: torch.Tensor, H: int,
         if tuple(R.shape) != (M, H):
             raise ValueError("R must be [M, H]")
     if Out is None:
-        Out = torch.empty((M, H), dtype=torch.bfloat16, device=Y.device)
+        Out = _new_tensor((M, H), torch.bfloat16, Y.device, stream)
     _dev_bf16(Out, "Out")
     if tuple(Out.shape) != (M, H):
         raise ValueError("Out must be [M, H]")
@@ -524,20 +549,10 @@ def _all_bf16(tensors, names: tuple) -> int:
 _cur_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-def _on_stream(t: torch.Tensor, stream) -> torch.Tensor:
-    """`t`, which this binding allocated on the current stream, kept until `stream` is done with it."""
-    if stream is not None:
-        if not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(int(stream), device=t.device)
-        t.record_stream(stream)
-    return t
-
-
 def _output(t, name: str, rows: int, cols: int, dev: int, stream) -> torch.Tensor:
     """A caller's output tensor, checked, or a new one."""
     if t is None:
-        t = torch.empty((rows, cols), dtype=_BF16, device=dev)
-        return t if stream is None else _on_stream(t, stream)
+        return _new_tensor((rows, cols), _BF16, dev, stream)
     if t.dtype is not _BF16 or t.get_device() != dev or not t.is_contiguous():
         _refuse(dev, (t,), (name,))
     if t.shape != (rows, cols):
@@ -548,7 +563,7 @@ def _output(t, name: str, rows: int, cols: int, dev: int, stream) -> torch.Tenso
 def _scratch(ws, dev: int, stream, bytes_fn, *shape) -> torch.Tensor:
     """A caller's workspace, checked, or a new one of bytes_fn(*shape)."""
     if ws is None:
-        return _on_stream(torch.empty(bytes_fn(*shape), dtype=torch.uint8, device=dev), stream)
+        return _new_tensor(bytes_fn(*shape), torch.uint8, dev, stream, returned=False)
     if ws.get_device() != dev or not ws.is_contiguous():
         raise ValueError(f"workspace must be a contiguous CUDA tensor on cuda:{dev}")
     return ws
