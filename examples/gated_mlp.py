@@ -32,10 +32,11 @@ class GatedMLP(torch.autograd.Function):
     def backward(ctx, d_out):
         x, y, wp, w3p = ctx.saved_tensors
         d_out = d_out.contiguous()
-        need_x, need_w = ctx.needs_input_grad[0], ctx.needs_input_grad[1]
-        d_y, d_w3 = sg.swiglu_down_backward(d_out, w3p, y, need_weight=ctx.needs_input_grad[3])
-        d_x, d_w1, d_w2 = sg.swiglu_backward(x, wp, d_y, need_input=need_x, need_weight=need_w)
-        return d_x + d_out if need_x else None, d_w1, d_w2, d_w3
+        need_x, need_w1, need_w2, need_w3 = ctx.needs_input_grad
+        d_y, d_w3 = sg.swiglu_down_backward(d_out, w3p, y, need_weight=need_w3)
+        # one product makes both of the gate's and the up weight's gradients
+        d_x, d_w1, d_w2 = sg.swiglu_backward(x, wp, d_y, need_input=need_x, need_weight=need_w1 or need_w2)
+        return d_x + d_out if need_x else None, d_w1 if need_w1 else None, d_w2 if need_w2 else None, d_w3
 
 
 def train(hidden, intermediate, tokens, steps, lr=2e-2):

@@ -50,3 +50,18 @@ def test_frozen_weights_need_no_weight_gradients(example):
     x = torch.randn(5, 64, generator=g, device="cuda").bfloat16().requires_grad_()
     example.GatedMLP.apply(x, *w).float().sum().backward()
     assert x.grad is not None and x.grad.isfinite().all()
+
+
+@pytest.mark.parametrize("frozen", [1, 2])
+def test_one_of_the_two_first_weights_frozen(example, frozen):
+    # the other one's gradient is the one that it gets when both are trained
+    g = torch.Generator(device="cuda").manual_seed(4)
+    shapes = ((40, 64), (64, 136), (64, 136), (136, 64))
+    values = [(torch.randn(*s, generator=g, device="cuda") / 8).bfloat16() for s in shapes]
+    d_out = torch.randn(40, 64, generator=g, device="cuda").bfloat16()
+    both = [v.clone().requires_grad_() for v in values]
+    one = [v.clone().requires_grad_(i != frozen) for i, v in enumerate(values)]
+    for args in (both, one):
+        example.GatedMLP.apply(*args).backward(d_out)
+    for i in range(4):
+        assert one[i].grad is None if i == frozen else torch.equal(one[i].grad, both[i].grad)
