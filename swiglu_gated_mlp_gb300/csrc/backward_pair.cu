@@ -407,7 +407,7 @@ __global__ void __launch_bounds__(kBackThreads, 1)
         for (int e = 0; e < 4; ++e) {
           const int col = col0 + 32 * c + 8 * e;
           dyv[e] = row0 + lane < pr.rows && col < pr.cols
-                       ? __ldg(reinterpret_cast<const uint4*>(dy_row + col))
+                       ? *reinterpret_cast<const uint4*>(dy_row + col)
                        : make_uint4(0u, 0u, 0u, 0u);
         }
       };

@@ -580,7 +580,7 @@ __global__ void __launch_bounds__(PairCfg<kMx, kLora>::kThreadsT, 1)
       for (int h = 0; h < kHalves; ++h)
 #pragma unroll
         for (int c = 0; c < kChunks; ++c)
-          x[h][c] = own >= 0 && own < p.lora_count && c < chunks ? __ldg(v + h * chunks + c)
+          x[h][c] = own >= 0 && own < p.lora_count && c < chunks ? v[h * chunks + c]
                                                                  : make_uint4(0u, 0u, 0u, 0u);
       const int ahead = list[1 + min(lane, max(extra / kHalves - 1, 0))];
       s = (s + num_kb) % C::kStages;

@@ -210,10 +210,10 @@ __device__ __noinline__ void make_own_v(const SmallMParams& p, int hr, __nv_bflo
   const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
   for (int i = w; i < p.M * pairs; i += kLoraOwnWarps) {
     const int m = i / pairs, r0 = i % pairs * 2;
-    const int a = __ldg(p.lora_index + m);
+    const int a = p.lora_index[m];
     uint32_t out = 0;
     if (a >= 0 && a < p.lora_count) {
-      const float s = __ldg(p.lora_scale + a);
+      const float s = p.lora_scale[a];
       const uint4* x = static_cast<const uint4*>(p.lora_x) + static_cast<size_t>(m) * chunks;
       const uint4* la = static_cast<const uint4*>(p.lora_la) + (static_cast<size_t>(a) * hr + r0) * chunks;
       float acc0 = 0.0f, acc1 = 0.0f;
@@ -222,9 +222,9 @@ __device__ __noinline__ void make_own_v(const SmallMParams& p, int hr, __nv_bflo
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) {
           const int c = c0 + 32 * j;
-          xv[j] = c < chunks ? __ldg(x + c) : zero;
-          l0[j] = c < chunks ? __ldg(la + c) : zero;
-          l1[j] = c < chunks ? __ldg(la + chunks + c) : zero;
+          xv[j] = c < chunks ? ld_global_v4(x + c) : zero;
+          l0[j] = c < chunks ? ld_global_v4(la + c) : zero;
+          l1[j] = c < chunks ? ld_global_v4(la + chunks + c) : zero;
         }
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) {

@@ -76,10 +76,10 @@ __global__ void __launch_bounds__(kDotThreads)
   float acc[kDotRows] = {};
 #pragma unroll 4
   for (int i = threadIdx.x; i < chunks; i += threads) {
-    const uint4 xv = __ldg(x + i);
+    const uint4 xv = x[i];
 #pragma unroll
     for (int r = 0; r < kDotRows; ++r)  // hr is a multiple of 8: every row exists
-      acc[r] = dot8(xv, __ldg(la + static_cast<size_t>(r) * chunks + i), acc[r]);
+      acc[r] = dot8(xv, la[static_cast<size_t>(r) * chunks + i], acc[r]);
   }
 #pragma unroll
   for (int r = 0; r < kDotRows; ++r)
