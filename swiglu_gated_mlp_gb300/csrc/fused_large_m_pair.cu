@@ -285,9 +285,11 @@ __global__ void __launch_bounds__(PairCfg<kMx, kLora>::kThreadsT, 1)
       bool skip_once = p.inject_stall != 0;
       bool ok = true;
       // round pacing on the even CTA (the odd one follows through the empty
-      // barriers); the launch number is drawn after the grid-dependency wait,
-      // when the previous launch in the stream has finished. The launch's
-      // draws add up to kPaceBlock, so the next launch starts a fresh block.
+      // barriers); the launch number is drawn when the previous launch of this
+      // kernel in the stream has finished: after the grid-dependency wait, or (adapters
+      // with lora_early) because the kernel that makes V had its wait behind it when it
+      // let this one start. The launch's draws add up to kPaceBlock, so the next
+      // launch starts a fresh block.
       const bool can_pace = pairs <= static_cast<int>(kPaceBlock);
       unsigned long long epoch = 0;  // of the issuing lane
       if (leader && can_pace && one) {

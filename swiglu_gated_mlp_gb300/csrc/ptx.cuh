@@ -297,12 +297,22 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
 
 // ------------------------------------------- programmatic dependent launch ---
 // With the launch attribute set, a grid may start while the previous grid in
-// the stream finishes. Nothing in global memory is touched before pdl_wait(),
-// which returns once the previous grid has completed and its writes are
-// visible (immediately when launched without the attribute).
+// the stream finishes. pdl_wait() returns once the previous grid has completed
+// and its writes are visible (immediately when launched without the attribute).
+// Every grid launched with it waits in each CTA before that CTA ends, so when a
+// grid has completed all before it have.
+// What a grid may do before its own wait depends on the one before it:
+//   - in general nothing in global memory is touched (L2 may be asked to fetch);
+//   - the projections with adapters load tokens, weights, the index and the table
+//     before it. Only the kernel that makes V is launched before them, and every
+//     thread of that one waits before it lets its dependents start: all grids
+//     before it have completed by then. V, the lists and the residual are read,
+//     and outputs written, after the projection's own wait.
+// So a kernel whose dependent reads before waiting waits before it triggers.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
-// Lets the next grid in the stream begin its launch (it still waits in pdl_wait()).
+// Lets the next grid in the stream begin its launch (see above for what that one
+// may do before its pdl_wait()).
 __device__ __forceinline__ void pdl_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
@@ -529,11 +539,12 @@ __device__ __forceinline__ void cluster_sync() {
                    "memory");
 }
 
-// 16-byte load from the shared memory of any CTA of the cluster.
+// 4-byte store to the shared memory of any CTA of the cluster.
 __device__ __forceinline__ void st_shared_cluster(uint32_t cluster_addr, int v) {
   asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
 }
 
+// 16-byte load from the shared memory of any CTA of the cluster.
 __device__ __forceinline__ float4 ld_shared_cluster_v4(uint32_t cluster_addr) {
   float4 v;
   asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
