@@ -124,3 +124,19 @@ def test_down_forward_lora_error_norms(native, M, H, N, L, r):
     native.swiglu_check_device_status()
     ref, variance = adapted(y.double(), w3.double(), la.double(), lb.double(), index, scale.double())
     check(out, ref + res.double(), variance)
+
+
+@pytest.mark.parametrize("M,K,N,L,r,kernel", [
+    (4096, 8192, 8192, 6, 64, "large_m_pair"),  # 14 rounds of tiles
+    (1300, 8192, 520, 3, 16, "large_m_pair"),   # one, beside the kernel that makes V
+    (300, 8192, 1032, 3, 16, "small_m"),
+])
+def test_adapters_of_a_long_hidden_size(native, M, K, N, L, r, kernel):
+    # K >= 8192: the CTA pairs keep their rounds of tiles together and walk every second one backwards
+    assert kernel in native.swiglu_lora_plan_string(M, K, N, r)
+    for _ in range(2):  # the launch numbers of a second call
+        test_forward_lora_error_norms(native, M, K, N, L, r)
+
+
+def test_backward_of_a_long_hidden_size(native):
+    test_backward_error_norms(native, 1024, 8192, 4096)
