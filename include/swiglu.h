@@ -412,6 +412,63 @@ SWIGLU_API swiglu_status_t swiglu_down_backward(const void* dOut, const void* W3
                                                 size_t workspace_bytes, swiglu_stream_t stream);
 
 /*
+ * 8-bit integers: the format of quantised tokens and of kept activations. No
+ * passage of the pages gives one (section "Problem Statement" names
+ * quantisation only as the reason the SwiGLU steps weigh more). A group of
+ * values x is held as int8 codes q and one fp32 scale s, x ~ q s:
+ *   m = max(max |x|, 2^-100),   s = m / 127,   q = 127 x / m to the nearest
+ * (halves to even). A group that holds an infinity or a NaN has the scale NaN,
+ * and its codes mean nothing.
+ *
+ * swiglu_quantize_int8: X [M, K] bf16 -> Q [M, K] int8 and scale [M] fp32, a
+ *   group per token. All device, row-major, 16-byte aligned, none overlapping.
+ *   K a multiple of 8. M = 0 is a no-op. Errors as swiglu_forward.
+ */
+SWIGLU_API swiglu_status_t swiglu_quantize_int8(const void* X, void* Q, float* scale, int64_t M, int64_t K,
+                                                swiglu_stream_t stream);
+
+/*
+ * Training with Gate and Up kept in 8 bits: the forward stores them (2 bytes a
+ * column of the intermediate size and token, what Y alone takes in bf16), and
+ * the backward pass neither recomputes them nor needs Y.
+ *
+ * The checkpoint: `gate` and `up`, int8 codes [M, N] row-major, and `scale`
+ * fp32 [2, ceil(N / 128), M], one group per token and 128 columns:
+ *   G[m][n] ~ gate[m][n] * scale[0][n / 128][m]
+ *   U[m][n] ~ up[m][n]   * scale[1][n / 128][m]
+ * in the format above (the codes from the fp32 accumulators: one within their
+ * error of a half may go either way).
+ *
+ * swiglu_forward_checkpoint: Y as swiglu_forward (from the fp32 accumulators,
+ *   not from the codes), and the checkpoint. All outputs are written in full,
+ *   16-byte aligned, overlapping nothing.
+ * swiglu_checkpoint_output: Y [M, N] bf16 = SiLU(G) (.) U of the checkpoint's
+ *   values, for the down-projection's weight gradient, so that Y need not be
+ *   kept. M = 0 is a no-op.
+ * swiglu_backward_checkpoint: dA, dW1, dW2 as swiglu_backward, with the
+ *   checkpoint's G and U. scale_a NULL: A is bf16 [M, K]. Otherwise A is kept
+ *   too: int8 codes [M, K] with one scale per token, scale_a [M] (as from
+ *   swiglu_quantize_int8); its values are rounded to bf16 as tensor-core
+ *   operands. A and scale_a are not read when dW1 is NULL, Wpacked not when dA
+ *   is (each may then be NULL). Outputs, NULLs, workspace and M = 0 as for
+ *   swiglu_backward; swiglu_backward_checkpoint_workspace_bytes(M, K, N) bytes.
+ *   Any scales are taken as they are (finite or not).
+ * Errors as swiglu_forward.
+ */
+SWIGLU_API swiglu_status_t swiglu_forward_checkpoint(const void* A, const void* Wpacked, void* Y, void* gate,
+                                                     void* up, float* scale, int64_t M, int64_t K, int64_t N,
+                                                     swiglu_stream_t stream);
+SWIGLU_API swiglu_status_t swiglu_checkpoint_output(const void* gate, const void* up, const float* scale,
+                                                    void* Y, int64_t M, int64_t N, swiglu_stream_t stream);
+SWIGLU_API size_t swiglu_backward_checkpoint_workspace_bytes(int64_t M, int64_t K, int64_t N);
+SWIGLU_API swiglu_status_t swiglu_backward_checkpoint(const void* A, const float* scale_a,
+                                                      const void* Wpacked, const void* dY, const void* gate,
+                                                      const void* up, const float* scale, void* dA, void* dW1,
+                                                      void* dW2, int64_t M, int64_t K, int64_t N,
+                                                      void* workspace, size_t workspace_bytes,
+                                                      swiglu_stream_t stream);
+
+/*
  * The two projections with low-rank adapters of many requests: one shared
  * packed weight, and per token m one adapter a = index[m] of a table (a value
  * outside [0, adapters) means none). No passage of the pages covers adapters;

@@ -109,6 +109,16 @@ lib.swiglu_down_lora_workspace_bytes.restype = _sz
 lib.swiglu_down_forward_lora.argtypes = [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _i64,
                                          _i64, _vp, _sz, _vp]
 lib.swiglu_down_forward_lora.restype = _int
+lib.swiglu_quantize_int8.argtypes = [_vp, _vp, _vp, _i64, _i64, _vp]
+lib.swiglu_quantize_int8.restype = _int
+lib.swiglu_forward_checkpoint.argtypes = [_vp] * 6 + [_i64, _i64, _i64, _vp]
+lib.swiglu_forward_checkpoint.restype = _int
+lib.swiglu_checkpoint_output.argtypes = [_vp] * 4 + [_i64, _i64, _vp]
+lib.swiglu_checkpoint_output.restype = _int
+lib.swiglu_backward_checkpoint_workspace_bytes.argtypes = [_i64, _i64, _i64]
+lib.swiglu_backward_checkpoint_workspace_bytes.restype = _sz
+lib.swiglu_backward_checkpoint.argtypes = [_vp] * 10 + [_i64, _i64, _i64, _vp, _sz, _vp]
+lib.swiglu_backward_checkpoint.restype = _int
 for _f in (lib.swiglu_backward_plan_string, lib.swiglu_down_backward_plan_string):
     _f.argtypes, _f.restype = [_i64, _i64, _i64, ctypes.c_char_p, _sz], _int
 for _f in (lib.swiglu_lora_plan_string, lib.swiglu_down_lora_plan_string):
@@ -649,6 +659,148 @@ def swiglu_backward(A: torch.Tensor, Wpacked: torch.Tensor, dY: torch.Tensor,
                              _ptr(dW2), M, K, N, ws.data_ptr(), ws.nbytes, _handle(stream, dev))
     if rc:
         _check(rc, "swiglu_backward")
+    return dA, dW1, dW2
+
+
+def _typed(t, name: str, dtype, shape: tuple, dev: int) -> torch.Tensor:
+    """`t`, checked: a contiguous `dtype` tensor of this shape on this device."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor on cuda:{dev}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    return t
+
+
+def _typed_output(t, name: str, dtype, shape: tuple, dev: int, stream) -> torch.Tensor:
+    return _new_tensor(shape, dtype, dev, stream) if t is None else _typed(t, name, dtype, shape, dev)
+
+
+def swiglu_quantize_int8(X: torch.Tensor, Q: torch.Tensor | None = None,
+                         scale: torch.Tensor | None = None, stream=None):
+    """(Q [M, K] int8, scale [M] float32) of X [M, K] bf16: X ~ Q * scale, one scale per token.
+
+    With m = max(max |x|, 2^-100) over a token's row, scale = m / 127 and Q = 127 x / m, rounded.
+    """
+    dev = _all_bf16((X,), ("X",))
+    if X.dim() != 2:
+        raise ValueError("X must be [M, K]")
+    M, K = X.shape
+    if _cur_device() != dev:
+        with torch.cuda.device(dev):
+            return swiglu_quantize_int8(X, Q, scale, stream)
+    Q = _typed_output(Q, "Q", torch.int8, (M, K), dev, stream)
+    scale = _typed_output(scale, "scale", torch.float32, (M,), dev, stream)
+    rc = lib.swiglu_quantize_int8(X.data_ptr(), Q.data_ptr(), scale.data_ptr(), M, K, _handle(stream, dev))
+    if rc:
+        _check(rc, "swiglu_quantize_int8")
+    return Q, scale
+
+
+def _scale_shape(M: int, N: int) -> tuple:
+    return (2, -(-N // 128), M)
+
+
+def swiglu_forward_checkpoint(A: torch.Tensor, Wpacked: torch.Tensor, N: int,
+                              Y: torch.Tensor | None = None, gate: torch.Tensor | None = None,
+                              up: torch.Tensor | None = None, scale: torch.Tensor | None = None,
+                              stream=None):
+    """(Y, gate, up, scale): swiglu_forward's Y, and Gate and Up kept in 8 bits for the backward pass.
+
+    gate, up [M, N] int8; scale [2, ceil(N / 128), M] float32, of Gate and of Up, one per token and
+    128 columns: Gate[m, n] ~ gate[m, n] * scale[0, n // 128, m].
+    """
+    dev = _all_bf16((A, Wpacked), ("A", "Wpacked"))
+    if A.dim() != 2:
+        raise ValueError("A must be [M, K]")
+    M, K = A.shape
+    _holds(Wpacked, -(-N // 128), K, "Wpacked")
+    if _cur_device() != dev:
+        with torch.cuda.device(dev):
+            return swiglu_forward_checkpoint(A, Wpacked, N, Y, gate, up, scale, stream)
+    Y = _output(Y, "Y", M, N, dev, stream)
+    gate = _typed_output(gate, "gate", torch.int8, (M, N), dev, stream)
+    up = _typed_output(up, "up", torch.int8, (M, N), dev, stream)
+    scale = _typed_output(scale, "scale", torch.float32, _scale_shape(M, N), dev, stream)
+    rc = lib.swiglu_forward_checkpoint(A.data_ptr(), Wpacked.data_ptr(), Y.data_ptr(), gate.data_ptr(),
+                                       up.data_ptr(), scale.data_ptr(), M, K, N, _handle(stream, dev))
+    if rc:
+        _check(rc, "swiglu_forward_checkpoint")
+    return Y, gate, up, scale
+
+
+def _checkpoint(gate, up, scale) -> tuple:
+    """(M, N, device) of a checkpoint's tensors, checked."""
+    if not isinstance(gate, torch.Tensor) or not gate.is_cuda or gate.dim() != 2:
+        raise ValueError("gate must be a CUDA tensor [M, N]")
+    M, N = gate.shape
+    dev = gate.get_device()
+    _typed(gate, "gate", torch.int8, (M, N), dev)
+    _typed(up, "up", torch.int8, (M, N), dev)
+    _typed(scale, "scale", torch.float32, _scale_shape(M, N), dev)
+    return M, N, dev
+
+
+def swiglu_checkpoint_output(gate: torch.Tensor, up: torch.Tensor, scale: torch.Tensor,
+                             Y: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Y [M, N] bf16 = SiLU(Gate) * Up of the values that a checkpoint stands for."""
+    M, N, dev = _checkpoint(gate, up, scale)
+    if _cur_device() != dev:
+        with torch.cuda.device(dev):
+            return swiglu_checkpoint_output(gate, up, scale, Y, stream)
+    Y = _output(Y, "Y", M, N, dev, stream)
+    rc = lib.swiglu_checkpoint_output(gate.data_ptr(), up.data_ptr(), scale.data_ptr(), Y.data_ptr(), M, N,
+                                      _handle(stream, dev))
+    if rc:
+        _check(rc, "swiglu_checkpoint_output")
+    return Y
+
+
+def swiglu_backward_checkpoint_workspace_bytes(M: int, K: int, N: int) -> int:
+    return int(lib.swiglu_backward_checkpoint_workspace_bytes(int(M), int(K), int(N)))
+
+
+def swiglu_backward_checkpoint_workspace(M: int, K: int, N: int, device=None) -> torch.Tensor:
+    """A workspace for swiglu_backward_checkpoint; one serves any number of calls in stream order."""
+    return _new_workspace(swiglu_backward_checkpoint_workspace_bytes, device, M, K, N)
+
+
+def swiglu_backward_checkpoint(A: torch.Tensor, Wpacked: torch.Tensor, dY: torch.Tensor,
+                               gate: torch.Tensor, up: torch.Tensor, scale: torch.Tensor,
+                               scale_a: torch.Tensor | None = None, dA: torch.Tensor | None = None,
+                               dW1: torch.Tensor | None = None, dW2: torch.Tensor | None = None,
+                               need_input: bool = True, need_weight: bool = True,
+                               workspace: torch.Tensor | None = None, stream=None):
+    """(dA, dW1, dW2) as swiglu_backward, with Gate and Up from a checkpoint of swiglu_forward_checkpoint.
+
+    A [M, K] is bf16, or int8 codes with one scale per token in scale_a [M] (swiglu_quantize_int8).
+    """
+    dev = _all_bf16((Wpacked, dY), ("Wpacked", "dY"))
+    M, N, at = _checkpoint(gate, up, scale)
+    if at != dev:
+        raise ValueError(f"gate must be on cuda:{dev}")
+    if dY.shape != (M, N) or not isinstance(A, torch.Tensor) or A.dim() != 2 or A.shape[0] != M:
+        raise ValueError("A must be [M, K] and dY [M, N]")
+    K = A.shape[1]
+    if scale_a is None:
+        _all_bf16((A, dY), ("A", "dY"))
+    else:
+        _typed(A, "A", torch.int8, (M, K), dev)
+        _typed(scale_a, "scale_a", torch.float32, (M,), dev)
+    _holds(Wpacked, -(-N // 128), K, "Wpacked")
+    if _cur_device() != dev:
+        with torch.cuda.device(dev):
+            return swiglu_backward_checkpoint(A, Wpacked, dY, gate, up, scale, scale_a, dA, dW1, dW2,
+                                              need_input, need_weight, workspace, stream)
+    dA = _output(dA, "dA", M, K, dev, stream) if need_input else None
+    dW1 = _output(dW1, "dW1", K, N, dev, stream) if need_weight else None
+    dW2 = _output(dW2, "dW2", K, N, dev, stream) if need_weight else None
+    ws = _scratch(workspace, dev, stream, swiglu_backward_checkpoint_workspace_bytes, M, K, N)
+    rc = lib.swiglu_backward_checkpoint(A.data_ptr(), _ptr(scale_a), Wpacked.data_ptr(), dY.data_ptr(),
+                                        gate.data_ptr(), up.data_ptr(), scale.data_ptr(), _ptr(dA),
+                                        _ptr(dW1), _ptr(dW2), M, K, N, ws.data_ptr(), ws.nbytes,
+                                        _handle(stream, dev))
+    if rc:
+        _check(rc, "swiglu_backward_checkpoint")
     return dA, dW1, dW2
 
 

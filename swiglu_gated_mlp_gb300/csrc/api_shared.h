@@ -51,5 +51,31 @@ bool encode_3d(CUtensorMap* map, const void* base, const uint64_t dims[3],
 bool encode_packed_w(CUtensorMap* map, const void* base, int64_t K, int64_t N, uint32_t rows);
 bool encode_packed_down(CUtensorMap* map, const void* base, int64_t N, int64_t H, uint32_t rows);
 
+inline swiglu_status_t launched(cudaError_t e) {
+  if (e == cudaSuccess) return SWIGLU_OK;
+  cudaGetLastError();
+  return SWIGLU_ERR_CUDA;
+}
+
+struct Span {
+  const void* p;
+  size_t bytes;
+};
+
+// Whether a written span overlaps any other written or read span (null: absent).
+inline bool any_overlap(const Span* out, int outs, const Span* in, int ins) {
+  for (int i = 0; i < outs; ++i) {
+    if (!out[i].p) continue;
+    for (int j = 0; j < ins; ++j)
+      if (in[j].p && overlaps(out[i].p, out[i].bytes, in[j].p, in[j].bytes)) return true;
+    for (int j = 0; j < i; ++j)
+      if (out[j].p && overlaps(out[i].p, out[i].bytes, out[j].p, out[j].bytes)) return true;
+  }
+  return false;
+}
+
+// Scales of Gate and Up kept in 8 bits: one of each per token and 128 columns.
+inline size_t checkpoint_scales(int64_t M, int64_t N) { return 2 * size_t(M) * size_t((N + 127) / 128); }
+
 }  // namespace api
 }  // namespace swg

@@ -159,12 +159,6 @@ bool encode_operand(CUtensorMap* map, const void* base, int64_t rows, int64_t co
   return encode_2d(map, base, cols, rows, cols * 2, kBlockK, token_rows(rows), CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-swiglu_status_t launched(cudaError_t e) {
-  if (e == cudaSuccess) return SWIGLU_OK;
-  cudaGetLastError();
-  return SWIGLU_ERR_CUDA;
-}
-
 // Launches the input and weight gradients and adds what is in parts.
 swiglu_status_t run_gradients(const BackwardParams& p, const GradientPlan& pl, const ReduceParams& sums,
                               cudaStream_t stream) {
@@ -175,23 +169,6 @@ swiglu_status_t run_gradients(const BackwardParams& p, const GradientPlan& pl, c
 
 swiglu_status_t zero(void* p, size_t bytes, cudaStream_t stream) {
   return launched(cudaMemsetAsync(p, 0, bytes, stream));
-}
-
-struct Span {
-  const void* p;
-  size_t bytes;
-};
-
-// Whether a written span overlaps any other written or read span (null: absent).
-bool any_overlap(const Span* out, int outs, const Span* in, int ins) {
-  for (int i = 0; i < outs; ++i) {
-    if (!out[i].p) continue;
-    for (int j = 0; j < ins; ++j)
-      if (in[j].p && overlaps(out[i].p, out[i].bytes, in[j].p, in[j].bytes)) return true;
-    for (int j = 0; j < i; ++j)
-      if (out[j].p && overlaps(out[i].p, out[i].bytes, out[j].p, out[j].bytes)) return true;
-  }
-  return false;
 }
 
 struct BackwardPlan {
@@ -228,8 +205,67 @@ int format_gradients(GradientPlan g, int max_pairs, char* buf, size_t buflen) {
                        p.early_rounds, g.pairs);
 }
 
+// dW1 and dW2 of no tokens.
+swiglu_status_t no_tokens(void* dW1, void* dW2, size_t w_bytes, cudaStream_t cs) {
+  if (!dW1) return SWIGLU_OK;
+  if (overlaps(dW1, w_bytes, dW2, w_bytes)) return SWIGLU_ERR_INVALID_ARG;
+  DeviceView d;
+  swiglu_status_t st = device_view(&d);
+  if (st == SWIGLU_OK) st = zero(dW1, w_bytes, cs);
+  return st == SWIGLU_OK ? zero(dW2, w_bytes, cs) : st;
+}
+
+// dA, dW1 and dW2 (null: not asked for) from dG and dU.
+swiglu_status_t gate_up_gradients(const void* A, const void* Wpacked, const void* dG, const void* dU, void* dA,
+                                  void* dW1, void* dW2, int64_t M, int64_t K, int64_t N, GradientPlan g,
+                                  uint8_t* parts, const DeviceView& d, int pairs, cudaStream_t cs) {
+  BackwardParams p{};
+  ReduceParams sums{};
+  deal_units(&g, dA != nullptr, dW1 != nullptr, pairs, &p);
+  fill_status(&p, d);
+  if (dA) {
+    fill(&p.in, g.in, M, K, M);
+    p.in.two = 1;
+    p.in.col_slices = static_cast<int>(k_slices(K));
+    if (!encode_operand(&p.in.tmap_a0, dG, M, N) ||
+        !encode_operand(&p.in.tmap_a1, dU, M, N) ||
+        !encode_packed_w(&p.in.tmap_b0, Wpacked, K, N, kPackBlockN) ||
+        !encode_output(&p.in.tmap_o0, dA, parts, g.in, M, K, &sums))
+      return SWIGLU_ERR_CUDA;
+  }
+  if (dW1) {
+    uint8_t* w_parts = parts + g.in.part_bytes;
+    fill(&p.w, g.w, K, N, M);
+    p.w.sum = static_cast<int>(M);
+    p.w.two = 1;
+    if (!encode_operand(&p.w.tmap_a0, A, M, K) ||
+        !encode_operand(&p.w.tmap_b0, dG, M, N) ||
+        !encode_operand(&p.w.tmap_b1, dU, M, N) ||
+        !encode_output(&p.w.tmap_o0, dW1, w_parts, g.w, K, N, &sums) ||
+        !encode_output(&p.w.tmap_o1, dW2, w_parts + g.w.part_bytes, g.w, K, N, &sums))
+      return SWIGLU_ERR_CUDA;
+  }
+  return run_gradients(p, g, sums, cs);
+}
+
 GradientPlan plan_down_backward(int64_t M, int64_t N, int64_t H, int pairs) {
   return plan_gradients(M, N, 4 * div_up(H, kTile), N, H, 1, pairs);
+}
+
+// Workspace of the backward pass from a checkpoint: dG, dU, the input's values
+// (where it was kept as codes), then the parts.
+struct CheckpointPlan {
+  GradientPlan gradients;
+  size_t grad_bytes = 0, input_bytes = 0;
+  size_t bytes() const { return 2 * grad_bytes + input_bytes + gradients.parts_bytes(); }
+};
+
+CheckpointPlan plan_checkpoint(int64_t M, int64_t K, int64_t N, int pairs) {
+  CheckpointPlan pl;
+  pl.gradients = plan_gradients(M, K, 4 * div_up(N, kTileM), K, N, 2, pairs);
+  pl.grad_bytes = align256(size_t(M) * size_t(N) * 2);
+  pl.input_bytes = align256(size_t(M) * size_t(K) * 2);
+  return pl;
 }
 
 }  // namespace
@@ -256,14 +292,7 @@ swiglu_status_t swiglu_backward(const void* A, const void* Wpacked, const void* 
   const size_t w_bytes = size_t(K) * size_t(N) * 2;
   const size_t a_bytes = size_t(M) * size_t(K) * 2, y_bytes = size_t(M) * size_t(N) * 2;
   const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-  if (M == 0) {  // a sum over no tokens
-    if (!dW1) return SWIGLU_OK;
-    if (overlaps(dW1, w_bytes, dW2, w_bytes)) return SWIGLU_ERR_INVALID_ARG;
-    DeviceView d;
-    st = device_view(&d);
-    if (st == SWIGLU_OK) st = zero(dW1, w_bytes, cs);
-    return st == SWIGLU_OK ? zero(dW2, w_bytes, cs) : st;
-  }
+  if (M == 0) return no_tokens(dW1, dW2, w_bytes, cs);
   if (!A || !Wpacked || !dY || !workspace) return SWIGLU_ERR_INVALID_ARG;
   if (!aligned16(A) || !aligned16(Wpacked) || !aligned16(dY) || !aligned16(workspace))
     return SWIGLU_ERR_INVALID_ARG;
@@ -297,34 +326,75 @@ swiglu_status_t swiglu_backward(const void* A, const void* Wpacked, const void* 
     st = launched(launch_backward_pair(p, true, std::min(p.in_units, pairs), cs));
     if (st != SWIGLU_OK) return st;
   }
-  GradientPlan g = pl.gradients;
-  BackwardParams p{};
-  ReduceParams sums{};
-  deal_units(&g, dA != nullptr, dW1 != nullptr, pairs, &p);
-  fill_status(&p, d);
-  if (dA) {
-    fill(&p.in, g.in, M, K, M);
-    p.in.two = 1;
-    p.in.col_slices = static_cast<int>(k_slices(K));
-    if (!encode_operand(&p.in.tmap_a0, dG, M, N) ||
-        !encode_operand(&p.in.tmap_a1, dU, M, N) ||
-        !encode_packed_w(&p.in.tmap_b0, Wpacked, K, N, kPackBlockN) ||
-        !encode_output(&p.in.tmap_o0, dA, parts, g.in, M, K, &sums))
-      return SWIGLU_ERR_CUDA;
+  return gate_up_gradients(A, Wpacked, dG, dU, dA, dW1, dW2, M, K, N, pl.gradients, parts, d, pairs, cs);
+}
+
+size_t swiglu_backward_checkpoint_workspace_bytes(int64_t M, int64_t K, int64_t N) {
+  if (swg::api::check_shape(M, K, N) != SWIGLU_OK || M == 0) return 0;
+  DeviceView d;
+  int pairs = 0;
+  if (backward_device(&d, &pairs) != SWIGLU_OK) return 0;
+  return plan_checkpoint(M, K, N, pairs).bytes();
+}
+
+swiglu_status_t swiglu_backward_checkpoint(const void* A, const float* scale_a, const void* Wpacked,
+                                           const void* dY, const void* gate, const void* up,
+                                           const float* scale, void* dA, void* dW1, void* dW2, int64_t M,
+                                           int64_t K, int64_t N, void* workspace, size_t workspace_bytes,
+                                           swiglu_stream_t stream) {
+  swiglu_status_t st = swg::api::check_shape(M, K, N);
+  if (st != SWIGLU_OK) return st;
+  if ((dW1 == nullptr) != (dW2 == nullptr)) return SWIGLU_ERR_INVALID_ARG;
+  if (!dA && !dW1) return SWIGLU_OK;
+  if ((dA && !aligned16(dA)) || (dW1 && (!aligned16(dW1) || !aligned16(dW2))))
+    return SWIGLU_ERR_INVALID_ARG;
+  const size_t w_bytes = size_t(K) * size_t(N) * 2, codes = size_t(M) * size_t(N);
+  const size_t a_bytes = size_t(M) * size_t(K) * (scale_a ? 1 : 2);
+  const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  if (M == 0) return no_tokens(dW1, dW2, w_bytes, cs);
+  // the packed weight for dA, the input for dW1 and dW2
+  if (!dY || !gate || !up || !scale || !workspace || (dA && !Wpacked) || (dW1 && !A))
+    return SWIGLU_ERR_INVALID_ARG;
+  if ((dW1 && (!aligned16(A) || (scale_a && !aligned16(scale_a)))) || (dA && !aligned16(Wpacked)) ||
+      !aligned16(dY) || !aligned16(gate) || !aligned16(up) || !aligned16(scale) || !aligned16(workspace))
+    return SWIGLU_ERR_INVALID_ARG;
+  const Span in[7] = {{dW1 ? A : nullptr, a_bytes},
+                      {dW1 ? scale_a : nullptr, size_t(M) * 4},
+                      {dA ? Wpacked : nullptr, swiglu_packed_weight_bytes(K, N)},
+                      {dY, codes * 2},
+                      {gate, codes},
+                      {up, codes},
+                      {scale, checkpoint_scales(M, N) * 4}};
+  const Span out[4] = {{dA, size_t(M) * size_t(K) * 2}, {dW1, w_bytes}, {dW2, w_bytes}, {workspace, workspace_bytes}};
+  if (any_overlap(out, 4, in, 7)) return SWIGLU_ERR_INVALID_ARG;
+  DeviceView d;
+  int pairs = 0;
+  st = backward_device(&d, &pairs);
+  if (st != SWIGLU_OK) return st;
+  const CheckpointPlan pl = plan_checkpoint(M, K, N, pairs);
+  if (workspace_bytes < pl.bytes()) return SWIGLU_ERR_INVALID_ARG;
+  if (pl.gradients.too_many()) return SWIGLU_ERR_UNSUPPORTED;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  CheckpointParams c{};
+  c.gate = gate;
+  c.up = up;
+  c.scale = scale;
+  c.dy = dY;
+  c.out0 = ws;
+  c.out1 = ws + pl.grad_bytes;
+  c.M = static_cast<int>(M);
+  c.N = static_cast<int>(N);
+  c.K = static_cast<int>(K);
+  if (scale_a && dW1) {
+    c.a_codes = A;
+    c.a_scale = scale_a;
+    c.a_out = ws + 2 * pl.grad_bytes;
+    A = c.a_out;
   }
-  if (dW1) {
-    uint8_t* w_parts = parts + g.in.part_bytes;
-    fill(&p.w, g.w, K, N, M);
-    p.w.sum = static_cast<int>(M);
-    p.w.two = 1;
-    if (!encode_operand(&p.w.tmap_a0, A, M, K) ||
-        !encode_operand(&p.w.tmap_b0, dG, M, N) ||
-        !encode_operand(&p.w.tmap_b1, dU, M, N) ||
-        !encode_output(&p.w.tmap_o0, dW1, w_parts, g.w, K, N, &sums) ||
-        !encode_output(&p.w.tmap_o1, dW2, w_parts + g.w.part_bytes, g.w, K, N, &sums))
-      return SWIGLU_ERR_CUDA;
-  }
-  return run_gradients(p, g, sums, cs);
+  st = launched(launch_checkpoint(c, true, cs));
+  if (st != SWIGLU_OK) return st;
+  return gate_up_gradients(A, Wpacked, c.out0, c.out1, dA, dW1, dW2, M, K, N, pl.gradients,
+                           ws + 2 * pl.grad_bytes + pl.input_bytes, d, pairs, cs);
 }
 
 swiglu_status_t swiglu_backward_plan_string(int64_t M, int64_t K, int64_t N, char* buf, size_t buflen) {

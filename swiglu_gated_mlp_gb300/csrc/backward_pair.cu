@@ -123,15 +123,6 @@ __device__ __forceinline__ int part_begin(const BackwardProduct& g, int part) {
   return static_cast<int>(int64_t(part) * (g.slices / kUnit) / g.splits) * kUnit;
 }
 
-// dG and dU of one element. For |g| large s (1 - s) g -> 0 and no term
-// overflows: e^-g = +inf gives s = 0 and g * 0 = -0 for finite g.
-__device__ __forceinline__ void gate_grads(float g, float u, float dy, float& dg, float& du) {
-  const float s = __fdividef(1.0f, 1.0f + __expf(-g));
-  const float gs = g * s;
-  du = dy * gs;
-  dg = dy * u * (s + gs * (1.0f - s));
-}
-
 // A kGrad unit: a whole tile, or from unit full_units on a half of one.
 __device__ __forceinline__ void grad_unit(const BackwardParams& p, int u, int& tile, int& bn, int& off) {
   const int h = u - p.full_units;

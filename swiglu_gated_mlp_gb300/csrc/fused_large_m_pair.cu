@@ -88,6 +88,7 @@
 // brought, so an Lb copy signals its own CTA, and those warps the even one. (They write
 // the V of the next slice first: 631 us with the look as without it; 640 where they
 // looked through each slice before the next V.)
+#include "int8.cuh"
 #include "kernels.h"
 #include "lora_lb.cuh"
 #include "ptx.cuh"
@@ -95,7 +96,7 @@
 namespace swg {
 namespace {
 
-template <bool kMx, bool kLora = false>
+template <bool kMx, bool kLora = false, bool kKeep = false>
 struct PairCfg {
   static constexpr int kBN = 128;                        // output columns per tile
   static constexpr int kABytes = 128 * kBlockK * 2;      // 16 KB: this CTA's 128 A rows
@@ -111,12 +112,14 @@ struct PairCfg {
   static constexpr int kTmemCols = 2 * kAccCols;         // double buffered (bf16, per-tensor FP8)
   static constexpr int kStgBytes = 32 * 32 * 2;          // 32 rows x 64 B store staging
   static constexpr int kNumStg = 8;                      // 2 per warp, or 1 per warp with 8 warps
+  static constexpr int kKeepStg = kKeep ? 32 * 64 : 0;   // per epilogue warp: 32 rows x (32 + 32) codes
   static constexpr int kTaints = 16;  // adapters: tile rounds that keep a mark
   static constexpr int kBarBytes = kLora ? 512 : 256;
   // block-scaled FP8: 1.5 KB of scales per stage (A block, gate and up weight blocks)
   static constexpr size_t kSmem = 1024 + size_t(kStages) * kStageBytes +
                                   size_t(kNumStg) * kStgBytes +
-                                  (kMx ? size_t(kStages) * kSfStageBytes : 0) + kBarBytes;
+                                  (kMx ? size_t(kStages) * kSfStageBytes : 0) + kBarBytes +
+                                  size_t(kEpiWarps) * kKeepStg;
   static_assert(kSmem <= 232448, "shared memory budget");
   static constexpr int kBars = (kLora ? 5 : 3) * kStages + 6;
   static_assert(8 * kBars + 8 + (kLora ? 4 * kTaints : 0) <= kBarBytes, "barrier slots");
@@ -175,10 +178,11 @@ __device__ __forceinline__ void pace_count(int r, unsigned long long epoch) {
   } while (old != assumed);
 }
 
-template <bool kFp8, bool kDown, bool kMx, bool kLora>
-__global__ void __launch_bounds__(PairCfg<kMx, kLora>::kThreadsT, 1)
+template <bool kFp8, bool kDown, bool kMx, bool kLora, bool kKeep = false>
+__global__ void __launch_bounds__(PairCfg<kMx, kLora, kKeep>::kThreadsT, 1)
     fused_large_m_pair_kernel(const __grid_constant__ LargeMParams p) {
-  using C = PairCfg<kMx, kLora>;
+  using C = PairCfg<kMx, kLora, kKeep>;
+  static_assert(!kKeep || (!kFp8 && !kDown && !kLora), "Gate and Up are kept by the bf16 forward");
   static_assert(!kLora || !kFp8, "adapters go with bf16");
   static_assert(!kMx || (kFp8 && !kDown), "block scales go with E4M3 gate/up inputs");
   constexpr int kAccBufs = kMx ? 1 : 2;  // accumulator buffers in tensor memory
@@ -763,6 +767,33 @@ __global__ void __launch_bounds__(PairCfg<kMx, kLora>::kThreadsT, 1)
           sbuf ^= 1;
         }
       } else {
+        QuantScale qg, qu;
+        if constexpr (kKeep) {
+          // this token's largest gate and up of the block's 128 columns (zero past N), read
+          // from tensor memory once more
+          float mg = 0.0f, mu = 0.0f;
+#pragma unroll 1
+          for (int c = 0; c < C::kBN / 32; ++c) {
+            uint32_t g[32], u[32];
+            tmem_ld_x32(tacc + c * 32, g);
+            tmem_ld_x32(tacc + C::kBN + c * 32, u);
+            tmem_wait_ld();
+            reg_fence(g);
+            reg_fence(u);
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              mg = max_abs3(mg, __uint_as_float(g[i]), __uint_as_float(g[i + 1]));
+              mu = max_abs3(mu, __uint_as_float(u[i]), __uint_as_float(u[i + 1]));
+            }
+          }
+          qg = quant_scale(mg);
+          qu = quant_scale(mu);
+          if (row0 + lane < p.M) {
+            float* s = p.keep_scale + static_cast<size_t>(nb) * p.M + row0 + lane;
+            s[0] = qg.scale;
+            s[static_cast<size_t>(p.tiles_n) * p.M] = qu.scale;
+          }
+        }
 #pragma unroll 1
         for (int c = 0; c < C::kBN / 32; ++c) {
           uint32_t g[32], u[32];
@@ -815,6 +846,34 @@ __global__ void __launch_bounds__(PairCfg<kMx, kLora>::kThreadsT, 1)
             bulk_commit();
           }
           sbuf ^= 1;
+          if constexpr (kKeep) {
+            // codes of this thread's row: 32 gate, then 32 up, 64 bytes of staging, from where
+            // four lanes write each row's 32 (N is a multiple of 8, so are the row starts)
+            const uint32_t keep = bar0 + C::kBarBytes + ew * C::kKeepStg;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              uint32_t w[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const uint32_t* v = (j < 2 ? g : u) + 16 * (j & 1) + 4 * e;
+                const float r = j < 2 ? qg.inverse : qu.inverse;
+                w[e] = pack_low_bytes(quant_code(__uint_as_float(v[0]), r), quant_code(__uint_as_float(v[1]), r),
+                                      quant_code(__uint_as_float(v[2]), r), quant_code(__uint_as_float(v[3]), r));
+              }
+              st_shared_v4(keep + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4), w[0], w[1], w[2], w[3]);
+            }
+            __syncwarp();
+            const int piece = lane & 3, ncol = col0 + c * 32 + piece * 8;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int r = (i & 3) * 8 + (lane >> 2), j = (i >> 2) * 2 + (piece >> 1);
+              const uint2 v = ld_shared_v2(keep + r * 64 + ((j ^ ((r >> 1) & 3)) << 4) + (piece & 1) * 8);
+              if (row0 + r < p.M && ncol < p.N)
+                *reinterpret_cast<uint2*>(static_cast<uint8_t*>(i < 4 ? p.keep_gate : p.keep_up) +
+                                          static_cast<size_t>(row0 + r) * p.N + ncol) = v;
+            }
+            __syncwarp();
+          }
         }
       }
       if (++buf == kAccBufs) {
@@ -837,7 +896,7 @@ __global__ void __launch_bounds__(PairCfg<kMx, kLora>::kThreadsT, 1)
 }
 
 cudaLaunchConfig_t pair_config(int grid, cudaStream_t stream, cudaLaunchAttribute* attr,
-                               bool with_pdl, bool mx = false, bool lora = false) {
+                               bool with_pdl, bool mx = false, bool lora = false, bool keep = false) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(mx     ? PairCfg<true>::kThreadsT
@@ -845,6 +904,7 @@ cudaLaunchConfig_t pair_config(int grid, cudaStream_t stream, cudaLaunchAttribut
                              : PairCfg<false>::kThreadsT);
   cfg.dynamicSmemBytes = mx     ? PairCfg<true>::kSmem
                          : lora ? PairCfg<false, true>::kSmem
+                         : keep ? PairCfg<false, false, true>::kSmem
                                 : PairCfg<false>::kSmem;
   cfg.stream = stream;
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -896,6 +956,12 @@ cudaError_t configure_large_m_pair_lora() {
                               static_cast<int>(PairCfg<false, true>::kSmem));
 }
 
+cudaError_t configure_large_m_pair_keep() {
+  return cudaFuncSetAttribute(fused_large_m_pair_kernel<false, false, false, false, true>,
+                              cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              static_cast<int>(PairCfg<false, false, true>::kSmem));
+}
+
 size_t large_m_pair_smem_bytes() { return PairCfg<false>::kSmem; }
 int large_m_pair_stages(bool mx) { return mx ? PairCfg<true>::kStages : PairCfg<false>::kStages; }
 
@@ -906,14 +972,17 @@ cudaError_t large_m_pair_pace_run_out(unsigned long long* count) {
 cudaError_t launch_large_m_pair(const LargeMParams& p, cudaStream_t stream) {
   if (p.grid < 2 || (p.grid % 2) != 0 || p.bn != PairCfg<false>::kBN) return cudaErrorInvalidValue;
   cudaLaunchAttribute attr[2];
-  cudaLaunchConfig_t cfg = pair_config(p.grid, stream, attr, pdl_enabled(), p.mx != 0, p.lora != 0);
+  cudaLaunchConfig_t cfg = pair_config(p.grid, stream, attr, pdl_enabled(), p.mx != 0, p.lora != 0, p.keep != 0);
+  if (p.keep && (p.fp8 || p.down || p.lora || !p.keep_gate || !p.keep_up || !p.keep_scale))
+    return cudaErrorInvalidValue;
   if (p.fp8 && p.down) return cudaErrorInvalidValue;  // no FP8 down-projection
   if (p.mx && !p.fp8) return cudaErrorInvalidValue;   // block scales go with E4M3 values
   if (p.lora && (p.fp8 || p.lora_rank < 8 || p.lora_rank > kLoraMaxRank || (p.lora_rank % 8) != 0 ||
                  !p.lora_v || !p.lora_index || !p.lora_lists))
     return cudaErrorInvalidValue;
   const cudaError_t e =
-      p.lora && p.down ? cudaLaunchKernelEx(&cfg, fused_large_m_pair_kernel<false, true, false, true>, p)
+      p.keep ? cudaLaunchKernelEx(&cfg, fused_large_m_pair_kernel<false, false, false, false, true>, p)
+      : p.lora && p.down ? cudaLaunchKernelEx(&cfg, fused_large_m_pair_kernel<false, true, false, true>, p)
       : p.lora ? cudaLaunchKernelEx(&cfg, fused_large_m_pair_kernel<false, false, false, true>, p)
       : p.down  ? cudaLaunchKernelEx(&cfg, fused_large_m_pair_kernel<false, true, false, false>, p)
       : p.mx  ? cudaLaunchKernelEx(&cfg, fused_large_m_pair_kernel<true, false, true, false>, p)

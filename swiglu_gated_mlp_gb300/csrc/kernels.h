@@ -58,6 +58,11 @@ struct LargeMParams {
   const int* lora_index;
   const int* lora_lists;
   int lora_early;  // the first K slices do not wait for the kernel that makes V
+  // Gate and Up kept in 8 bits (pair kernel, bf16): codes [M, N] and scales [2, tiles_n, M]
+  int keep;
+  void* keep_gate;
+  void* keep_up;
+  float* keep_scale;
 };
 
 struct SmallMParams {
@@ -145,6 +150,7 @@ cudaError_t launch_large_m(const LargeMParams& p, cudaStream_t stream);
 // also reports how many pairs can be resident at once.
 cudaError_t configure_large_m_pair(int* max_pairs);
 cudaError_t configure_large_m_pair_lora();
+cudaError_t configure_large_m_pair_keep();
 size_t large_m_pair_smem_bytes();
 int large_m_pair_stages(bool mx = false);
 // Number of the pair kernel's tile-round pacing waits that ran out on the
@@ -218,6 +224,27 @@ cudaError_t configure_backward_pair(int* max_pairs);
 cudaError_t launch_backward_pair(const BackwardParams& p, bool grad, int pairs, cudaStream_t stream);
 // Adds the fp32 parts of each output in order and rounds once.
 cudaError_t launch_reduce_parts(const ReduceParams& p, cudaStream_t stream);
+
+// Tokens in 8-bit integers with a scale each (quantize.cu); K a multiple of 8.
+cudaError_t launch_quantize_rows(const void* x, void* codes, float* scale, int M, int K, cudaStream_t stream);
+
+// Gate and Up kept in 8 bits (checkpoint.cu).
+struct CheckpointParams {
+  const void* gate;    // codes [M, N]
+  const void* up;
+  const float* scale;  // [2, ceil(N / 128), M]
+  const void* dy;      // gradients: dY [M, N] bf16
+  void* out0;          // Y, or dG [M, N] bf16
+  void* out1;          // dU
+  int M, N;
+  // gradients: the input's codes [M, K] and scales [M] (null: not kept so), its values in bf16
+  const void* a_codes;
+  const float* a_scale;
+  void* a_out;
+  int K;
+  int col_blocks;      // set by the launch
+};
+cudaError_t launch_checkpoint(const CheckpointParams& p, bool grads, cudaStream_t stream);
 
 // Words of the static scratch array behind swiglu_forward_noalloc (256 bytes);
 // a call uses the first kStatusWords of them for its status record.

@@ -43,6 +43,12 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
   return v;
 }
 
+__device__ __forceinline__ uint2 ld_shared_v2(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+
 // 16 bytes of global memory that the grid before this one may have written. Ordered
 // behind the grid-dependency wait, as a read-only load would not be; as an ordinary C++
 // load the compiler spread a batch of them over branches (1 token, down, N 18944, with
@@ -70,6 +76,15 @@ __device__ __forceinline__ float dot8(const uint4& a, const uint4& b, float acc)
 // fast divide returns 0 (the limit); for g -> +inf, e^-g -> 0. No NaN for finite g.
 __device__ __forceinline__ float silu_mul(float g, float u) {
   return __fdividef(g, 1.0f + __expf(-g)) * u;
+}
+
+// dG and dU of one element. For |g| large s (1 - s) g -> 0 and no term
+// overflows: e^-g = +inf gives s = 0 and g * 0 = -0 for finite g.
+__device__ __forceinline__ void gate_grads(float g, float u, float dy, float& dg, float& du) {
+  const float s = __fdividef(1.0f, 1.0f + __expf(-g));
+  const float gs = g * s;
+  du = dy * gs;
+  dg = dy * u * (s + gs * (1.0f - s));
 }
 
 // -------------------------------------------------------------- mbarrier ---
