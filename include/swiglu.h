@@ -428,6 +428,57 @@ SWIGLU_API swiglu_status_t swiglu_quantize_int8(const void* X, void* Q, float* s
                                                 swiglu_stream_t stream);
 
 /*
+ * The projections in 8-bit integers: codes of the tokens with a scale per token
+ * (swiglu_quantize_int8), codes of the weights with a scale per output column
+ * (channel), both symmetric:
+ *   G[m][n] = (sum_k A8[m][k] W1_8[k][n]) * scale_a[m] * scale_w1[n]   (U likewise)
+ *   Y = SiLU(G) (.) U
+ *   Out[m][h] = (sum_n Y8[m][n] W3_8[n][h]) * scale_y[m] * scale_w3[h] + R[m][h]
+ * All codes from -128 to 127 may occur. The sums are fp32 over exact products
+ * (exact while below 2^24); Y and Out are rounded once to bf16. Scales are
+ * fp32 and taken as they are (one that is not finite reaches its token or its
+ * column only). A, Y (as the down-projection's input): int8 row-major; weights
+ * int8 [K, N] and [N, H] row-major, packed once per weight set.
+ *
+ * swiglu_packed_weight_bytes_int8, swiglu_down_packed_bytes_int8: one byte per
+ *   value, N rounded up to 128 (H to 256), K (N) to 128; 0 on a bad shape.
+ * swiglu_pack_weights_int8, swiglu_pack_down_weights_int8: the packed layout is
+ *   that of the FP8 weights (the down-projection's: 256 columns of W3 a tile)
+ *   with every code's sign bit flipped.
+ * swiglu_int8_workspace_bytes, swiglu_down_int8_workspace_bytes: what a call
+ *   needs on the current device (0 for up to 64 tokens; 2 bytes per token code
+ *   beyond). The workspace's contents need no set-up and mean nothing after
+ *   the call; calls that may run at the same time need separate ones. NULL
+ *   where 0 bytes are needed.
+ * swiglu_forward_int8, swiglu_down_forward_int8: device pointers, 16-byte
+ *   aligned, outputs and workspace overlapping nothing else but Out R (in
+ *   place). R may be NULL. M = 0 is a no-op. K (N for the down-projection) a
+ *   multiple of 16, other sizes of 8 (else UNSUPPORTED). Errors as
+ *   swiglu_forward.
+ * swiglu_plan_string_int8, swiglu_down_plan_string_int8: the launch shape for a
+ *   shape on the current device, as text; buf NULL or buflen 0: INVALID_ARG.
+ */
+SWIGLU_API size_t swiglu_packed_weight_bytes_int8(int64_t K, int64_t N);
+SWIGLU_API swiglu_status_t swiglu_pack_weights_int8(const void* W1, const void* W2, void* Wpacked, int64_t K,
+                                                    int64_t N, swiglu_stream_t stream);
+SWIGLU_API size_t swiglu_int8_workspace_bytes(int64_t M, int64_t K, int64_t N);
+SWIGLU_API swiglu_status_t swiglu_forward_int8(const void* A, const float* scale_a, const void* Wpacked,
+                                               const float* scale_w1, const float* scale_w2, void* Y, int64_t M,
+                                               int64_t K, int64_t N, void* workspace, size_t workspace_bytes,
+                                               swiglu_stream_t stream);
+SWIGLU_API swiglu_status_t swiglu_plan_string_int8(int64_t M, int64_t K, int64_t N, char* buf, size_t buflen);
+SWIGLU_API size_t swiglu_down_packed_bytes_int8(int64_t N, int64_t H);
+SWIGLU_API swiglu_status_t swiglu_pack_down_weights_int8(const void* W3, void* W3packed, int64_t N, int64_t H,
+                                                         swiglu_stream_t stream);
+SWIGLU_API size_t swiglu_down_int8_workspace_bytes(int64_t M, int64_t N, int64_t H);
+SWIGLU_API swiglu_status_t swiglu_down_forward_int8(const void* Y, const float* scale_y, const void* W3packed,
+                                                    const float* scale_w3, const void* R, void* Out, int64_t M,
+                                                    int64_t N, int64_t H, void* workspace,
+                                                    size_t workspace_bytes, swiglu_stream_t stream);
+SWIGLU_API swiglu_status_t swiglu_down_plan_string_int8(int64_t M, int64_t N, int64_t H, char* buf,
+                                                        size_t buflen);
+
+/*
  * Training with Gate and Up kept in 8 bits: the forward stores them (2 bytes a
  * column of the intermediate size and token, what Y alone takes in bf16), and
  * the backward pass neither recomputes them nor needs Y.

@@ -26,6 +26,10 @@ _EXPORTS = {
     "swiglu_down_forward_lora", "swiglu_down_lora_workspace", "swiglu_down_lora_workspace_bytes",
     "swiglu_backward_plan_string", "swiglu_down_backward_plan_string", "swiglu_lora_plan_string",
     "swiglu_down_lora_plan_string",
+    "swiglu_packed_weight_bytes_int8", "swiglu_pack_weights_int8", "swiglu_forward_int8",
+    "swiglu_int8_workspace", "swiglu_int8_workspace_bytes", "swiglu_plan_string_int8",
+    "swiglu_down_packed_bytes_int8", "swiglu_pack_down_weights_int8", "swiglu_down_forward_int8",
+    "swiglu_down_int8_workspace", "swiglu_down_int8_workspace_bytes", "swiglu_down_plan_string_int8",
     "swiglu_quantize_int8", "swiglu_forward_checkpoint", "swiglu_checkpoint_output",
     "swiglu_backward_checkpoint", "swiglu_backward_checkpoint_workspace",
     "swiglu_backward_checkpoint_workspace_bytes",

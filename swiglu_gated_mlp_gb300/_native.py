@@ -111,6 +111,18 @@ lib.swiglu_down_forward_lora.argtypes = [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _
 lib.swiglu_down_forward_lora.restype = _int
 lib.swiglu_quantize_int8.argtypes = [_vp, _vp, _vp, _i64, _i64, _vp]
 lib.swiglu_quantize_int8.restype = _int
+for _f in (lib.swiglu_packed_weight_bytes_int8, lib.swiglu_down_packed_bytes_int8):
+    _f.argtypes, _f.restype = [_i64, _i64], _sz
+for _f in (lib.swiglu_int8_workspace_bytes, lib.swiglu_down_int8_workspace_bytes):
+    _f.argtypes, _f.restype = [_i64, _i64, _i64], _sz
+lib.swiglu_pack_weights_int8.argtypes = [_vp, _vp, _vp, _i64, _i64, _vp]
+lib.swiglu_pack_weights_int8.restype = _int
+lib.swiglu_pack_down_weights_int8.argtypes = [_vp, _vp, _i64, _i64, _vp]
+lib.swiglu_pack_down_weights_int8.restype = _int
+for _f in (lib.swiglu_forward_int8, lib.swiglu_down_forward_int8):
+    _f.argtypes, _f.restype = [_vp] * 6 + [_i64, _i64, _i64, _vp, _sz, _vp], _int
+for _f in (lib.swiglu_plan_string_int8, lib.swiglu_down_plan_string_int8):
+    _f.argtypes, _f.restype = [_i64, _i64, _i64, ctypes.c_char_p, _sz], _int
 lib.swiglu_forward_checkpoint.argtypes = [_vp] * 6 + [_i64, _i64, _i64, _vp]
 lib.swiglu_forward_checkpoint.restype = _int
 lib.swiglu_checkpoint_output.argtypes = [_vp] * 4 + [_i64, _i64, _vp]
@@ -694,6 +706,134 @@ def swiglu_quantize_int8(X: torch.Tensor, Q: torch.Tensor | None = None,
     if rc:
         _check(rc, "swiglu_quantize_int8")
     return Q, scale
+
+
+def swiglu_packed_weight_bytes_int8(K: int, N: int) -> int:
+    return int(lib.swiglu_packed_weight_bytes_int8(int(K), int(N)))
+
+
+def swiglu_down_packed_bytes_int8(N: int, H: int) -> int:
+    return int(lib.swiglu_down_packed_bytes_int8(int(N), int(H)))
+
+
+def _dev_int8(t, name: str) -> int:
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype is not torch.int8 or t.dim() != 2 or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int8 matrix, got {t.dtype} {list(t.shape)}")
+    return t.get_device()
+
+
+def _pack_int8(weights: tuple, names: tuple, packed, packed_name: str, bytes_fn, call, stream) -> torch.Tensor:
+    dev = _dev_int8(weights[0], names[0])
+    rows, cols = weights[0].shape
+    for t, name in zip(weights[1:], names[1:]):
+        _typed(t, name, torch.int8, (rows, cols), dev)
+    with _on_device(weights[0].device):
+        if packed is None:
+            packed = _new_tensor(bytes_fn(rows, cols), torch.uint8, dev, stream)
+        if packed.get_device() != dev or not packed.is_contiguous() or packed.nbytes < bytes_fn(rows, cols):
+            raise ValueError(f"{packed_name} must be a contiguous tensor of {bytes_fn(rows, cols)} bytes on cuda:{dev}")
+        _check(call(*(t.data_ptr() for t in weights), packed.data_ptr(), rows, cols, _handle(stream, dev)),
+               "swiglu_pack_weights_int8" if len(weights) == 2 else "swiglu_pack_down_weights_int8")
+    return packed
+
+
+def swiglu_pack_weights_int8(W1: torch.Tensor, W2: torch.Tensor, Wpacked: torch.Tensor | None = None,
+                             stream=None) -> torch.Tensor:
+    """Packed 8-bit gate/up weight (flat uint8 buffer) from the int8 codes W1, W2 [K, N] (CUDA)."""
+    return _pack_int8((W1, W2), ("W1", "W2"), Wpacked, "Wpacked", swiglu_packed_weight_bytes_int8,
+                      lib.swiglu_pack_weights_int8, stream)
+
+
+def swiglu_pack_down_weights_int8(W3: torch.Tensor, W3packed: torch.Tensor | None = None,
+                                  stream=None) -> torch.Tensor:
+    """Packed 8-bit down-projection weight (flat uint8 buffer) from the int8 codes W3 [N, H] (CUDA)."""
+    return _pack_int8((W3,), ("W3",), W3packed, "W3packed", swiglu_down_packed_bytes_int8,
+                      lib.swiglu_pack_down_weights_int8, stream)
+
+
+def swiglu_int8_workspace_bytes(M: int, K: int, N: int) -> int:
+    return int(lib.swiglu_int8_workspace_bytes(int(M), int(K), int(N)))
+
+
+def swiglu_int8_workspace(M: int, K: int, N: int, device=None) -> torch.Tensor:
+    """A workspace for swiglu_forward_int8 at (M, K, N), possibly of no bytes."""
+    return _new_workspace(swiglu_int8_workspace_bytes, device, M, K, N)
+
+
+def swiglu_down_int8_workspace_bytes(M: int, N: int, H: int) -> int:
+    return int(lib.swiglu_down_int8_workspace_bytes(int(M), int(N), int(H)))
+
+
+def swiglu_down_int8_workspace(M: int, N: int, H: int, device=None) -> torch.Tensor:
+    """A workspace for swiglu_down_forward_int8 at (M, N, H), possibly of no bytes."""
+    return _new_workspace(swiglu_down_int8_workspace_bytes, device, M, N, H)
+
+
+def swiglu_plan_string_int8(M: int, K: int, N: int) -> str:
+    return _plan("swiglu_plan_string_int8", M, K, N)
+
+
+def swiglu_down_plan_string_int8(M: int, N: int, H: int) -> str:
+    return _plan("swiglu_down_plan_string_int8", M, N, H)
+
+
+def swiglu_forward_int8(A: torch.Tensor, scale_a: torch.Tensor, Wpacked: torch.Tensor, N: int,
+                        scale_w1: torch.Tensor, scale_w2: torch.Tensor, Y: torch.Tensor | None = None,
+                        workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Y [M, N] bf16 = SiLU(G) * U, G = (A W1) * scale_a[m] * scale_w1[n] of int8 codes, U likewise.
+
+    A [M, K] int8 and scale_a [M] float32, as from swiglu_quantize_int8; scale_w1, scale_w2 [N]
+    float32. Without `workspace` (from swiglu_int8_workspace) one is allocated if the call needs it.
+    """
+    dev = _dev_int8(A, "A")
+    M, K = A.shape
+    _typed(scale_a, "scale_a", torch.float32, (M,), dev)
+    _typed(scale_w1, "scale_w1", torch.float32, (N,), dev)
+    _typed(scale_w2, "scale_w2", torch.float32, (N,), dev)
+    if Wpacked.get_device() != dev or not Wpacked.is_contiguous() or Wpacked.nbytes < -(-N // 128) * -(-K // 128) * 32768:
+        raise ValueError("Wpacked does not hold a packed 8-bit weight of this shape")
+    if _cur_device() != dev:
+        with torch.cuda.device(dev):
+            return swiglu_forward_int8(A, scale_a, Wpacked, N, scale_w1, scale_w2, Y, workspace, stream)
+    Y = _output(Y, "Y", M, N, dev, stream)
+    ws = _scratch(workspace, dev, stream, swiglu_int8_workspace_bytes, M, K, N)
+    rc = lib.swiglu_forward_int8(A.data_ptr(), scale_a.data_ptr(), Wpacked.data_ptr(), scale_w1.data_ptr(),
+                                 scale_w2.data_ptr(), Y.data_ptr(), M, K, N, ws.data_ptr(), ws.nbytes,
+                                 _handle(stream, dev))
+    if rc:
+        _check(rc, "swiglu_forward_int8")
+    return Y
+
+
+def swiglu_down_forward_int8(Y: torch.Tensor, scale_y: torch.Tensor, W3packed: torch.Tensor, H: int,
+                             scale_w3: torch.Tensor, R: torch.Tensor | None = None,
+                             Out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                             stream=None) -> torch.Tensor:
+    """Out [M, H] bf16 = (Y W3) * scale_y[m] * scale_w3[h] (+ R) of int8 codes Y [M, N]; Out may be R.
+
+    Without `workspace` (from swiglu_down_int8_workspace) one is allocated if the call needs it.
+    """
+    dev = _dev_int8(Y, "Y")
+    M, N = Y.shape
+    _typed(scale_y, "scale_y", torch.float32, (M,), dev)
+    _typed(scale_w3, "scale_w3", torch.float32, (H,), dev)
+    if R is not None:
+        _typed(R, "R", _BF16, (M, H), dev)
+    if W3packed.get_device() != dev or not W3packed.is_contiguous() or W3packed.nbytes < -(-H // 256) * -(-N // 128) * 32768:
+        raise ValueError("W3packed does not hold a packed 8-bit weight of this shape")
+    if _cur_device() != dev:
+        with torch.cuda.device(dev):
+            return swiglu_down_forward_int8(Y, scale_y, W3packed, H, scale_w3, R, Out, workspace, stream)
+    Out = _output(Out, "Out", M, H, dev, stream)
+    ws = _scratch(workspace, dev, stream, swiglu_down_int8_workspace_bytes, M, N, H)
+    rc = lib.swiglu_down_forward_int8(Y.data_ptr(), scale_y.data_ptr(), W3packed.data_ptr(), scale_w3.data_ptr(),
+                                      _ptr(R), Out.data_ptr(), M, N, H, ws.data_ptr(), ws.nbytes,
+                                      _handle(stream, dev))
+    if rc:
+        _check(rc, "swiglu_down_forward_int8")
+    return Out
 
 
 def _scale_shape(M: int, N: int) -> tuple:

@@ -228,6 +228,40 @@ cudaError_t launch_reduce_parts(const ReduceParams& p, cudaStream_t stream);
 // Tokens in 8-bit integers with a scale each (quantize.cu); K a multiple of 8.
 cudaError_t launch_quantize_rows(const void* x, void* codes, float* scale, int M, int K, cudaStream_t stream);
 
+// Projections in 8-bit integers (int8_gemm.cu).
+struct Int8Params {
+  CUtensorMap tmap_x;   // tokens: codes [M, K] box {128, mt}, or (wide) fp16 [M, K] box {64, mt}; 128-B swizzle
+  CUtensorMap tmap_w;   // packed codes {128, 256, tiles} box {128, 128 * halves, 1}, 128-B swizzle
+  void* y;              // [M, N] bf16
+  const void* residual; // [M, N] bf16 or null (down-projection)
+  const float* scale_x; // [M]
+  const float* scale0;  // [N]: of W1, or W3
+  const float* scale1;  // [N]: of W2
+  int M, K, N;
+  int halves;           // 128-row groups of weight rows a unit has: gate and up, or 1 or 2 of W3's columns
+  int blocks;           // units of columns
+  int mt, mgroups;      // tokens of a group (a multiple of 16, at most 128), groups
+  int group_m;          // token groups that go by before the next columns
+  int wide;             // tokens are fp16
+  int splits;           // K parts, a cluster of CTAs
+  int stages;
+  int slots;            // set by the launch
+  int grid;
+  int l2_prefetch;
+  uint32_t* status;
+  uint64_t timeout_ns;
+  int inject_stall;
+};
+// clusters[s]: clusters of s CTAs that can be resident at once (s = 1 .. 8).
+cudaError_t configure_int8(int (&clusters)[9]);
+int int8_stages(int halves, int mt, bool wide);
+cudaError_t launch_int8_gemm(const Int8Params& p, bool down, cudaStream_t stream);
+// int8 codes as fp16 values; `values` a multiple of 16.
+cudaError_t launch_widen(const void* codes, void* out, size_t values, cudaStream_t stream);
+// Weight codes to packed tiles of 256 x 128 biased codes: gate and up, or W3 (down).
+cudaError_t launch_pack_int8(const void* w1, const void* w2, void* wp, int K, int N, bool down,
+                             cudaStream_t stream);
+
 // Gate and Up kept in 8 bits (checkpoint.cu).
 struct CheckpointParams {
   const void* gate;    // codes [M, N]

@@ -137,6 +137,7 @@ enum WaitSite : uint32_t {
   kSiteDrain = 5,
   kSiteScaleCopy = 6,
   kSiteLora = 7,
+  kSiteConvert = 8,
 };
 
 struct WaitCtx {
