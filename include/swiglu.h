@@ -442,11 +442,11 @@ SWIGLU_API swiglu_status_t swiglu_quantize_int8(const void* X, void* Q, float* s
  *
  * swiglu_packed_weight_bytes_int8, swiglu_down_packed_bytes_int8: one byte per
  *   value, N rounded up to 128 (H to 256), K (N) to 128; 0 on a bad shape.
- * swiglu_pack_weights_int8, swiglu_pack_down_weights_int8: the packed layout is
- *   that of the FP8 weights (the down-projection's: 256 columns of W3 a tile)
- *   with every code's sign bit flipped.
+ * swiglu_pack_weights_int8, swiglu_pack_down_weights_int8: tiles of 256 rows x
+ *   128 of K, every code with its sign bit flipped; a row is a column of W3, or
+ *   16 columns of W1 and the same 16 of W2 in turn. Runs once per weight set.
  * swiglu_int8_workspace_bytes, swiglu_down_int8_workspace_bytes: what a call
- *   needs on the current device (0 for up to 64 tokens; 2 bytes per token code
+ *   needs on the current device (0 for few tokens; 2 bytes per token code
  *   beyond). The workspace's contents need no set-up and mean nothing after
  *   the call; calls that may run at the same time need separate ones. NULL
  *   where 0 bytes are needed.

@@ -6,6 +6,7 @@
 #include <algorithm>
 #include <atomic>
 #include <cstdio>
+#include <cstdlib>
 #include <mutex>
 
 #include "api_shared.h"
@@ -20,56 +21,60 @@ struct Int8State {
   std::atomic<bool> ready{false};
   swiglu_status_t status = SWIGLU_OK;
   int clusters[9] = {};
+  int pairs = 0;
 };
 Int8State g_int8[kMaxDevices];
 std::mutex g_int8_mu;
 
-swiglu_status_t int8_device(DeviceView* d, const int** clusters) {
+swiglu_status_t int8_device(DeviceView* d, const Int8State** out) {
   const swiglu_status_t st = device_view(d);
   if (st != SWIGLU_OK) return st;
   Int8State& s = g_int8[d->index];
   if (!s.ready.load(std::memory_order_acquire)) {
     std::lock_guard<std::mutex> lock(g_int8_mu);
     if (!s.ready.load(std::memory_order_relaxed)) {
-      if (configure_int8(s.clusters) != cudaSuccess) {
+      if (configure_int8(s.clusters, &s.pairs) != cudaSuccess) {
         cudaGetLastError();
         s.status = SWIGLU_ERR_CUDA;
       }
       s.ready.store(true, std::memory_order_release);
     }
   }
-  *clusters = s.clusters;
+  *out = &s;
   return s.status;
 }
 
 int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-constexpr int64_t kFewTokens = 64;   // tokens whose codes the kernel widens itself
 constexpr int64_t kMaxUnits = 1 << 30;
+const int kL2Ahead = std::getenv("SWIGLU_I8_AHEAD") ? std::atoi(std::getenv("SWIGLU_I8_AHEAD")) : 16;
 
 struct Int8Plan {
-  int halves = 2, mt = 16, splits = 1, stages = 0, grid = 0;
+  bool pair = false;  // units on CTA pairs, tokens widened by a kernel before
+  int mt = 16, splits = 1, stages = 0, grid = 0;
   int64_t blocks = 0, mgroups = 1;
-  bool wide = false;
-  size_t workspace(int64_t M, int64_t K) const { return wide ? size_t(M) * size_t(K) * 2 : 0; }
+  size_t workspace(int64_t M, int64_t K) const { return pair ? size_t(M) * size_t(K) * 2 : 0; }
 };
 
 // M tokens, sums over K, N outputs.
-Int8Plan make_plan(int64_t M, int64_t K, int64_t N, bool down, int sms, const int* clusters) {
+Int8Plan make_plan(int64_t M, int64_t K, int64_t N, bool down, int sms, const Int8State& s) {
   Int8Plan pl;
-  pl.wide = M > kFewTokens;
-  // few tokens: 128 columns of the down-projection a unit, for more units
-  pl.halves = down && !pl.wide ? 1 : 2;
-  pl.blocks = down ? div_up(N, 128 * pl.halves) : div_up(N, 128);
-  int64_t most = 128;
-  if (pl.wide && pl.blocks * div_up(M, 128) * 2 <= sms) most = 64;  // fill more SMs
+  const int64_t slices = div_up(K, kBlockK8);
+  const int64_t halves = div_up(N, down ? 128 : 64);  // packed blocks of 128 rows
+  pl.pair = s.pairs > 0 && M > 4 * kInt8Tokens;
+  const int64_t most = pl.pair ? kInt8PairTokens : kInt8Tokens, unit = pl.pair ? 32 : 16;
+  pl.blocks = pl.pair ? div_up(halves, 2) : halves;
   pl.mgroups = div_up(M, most);
-  pl.mt = static_cast<int>(div_up(div_up(M, pl.mgroups), 16) * 16);
-  pl.stages = int8_stages(pl.halves, pl.mt, pl.wide);
-  const int64_t units = pl.blocks * pl.mgroups, slices = div_up(K, kBlockK8);
+  pl.mt = static_cast<int>(div_up(div_up(M, pl.mgroups), unit) * unit);
+  pl.stages = int8_stages(pl.mt, pl.pair);
+  const int64_t units = pl.blocks * pl.mgroups;
+  if (pl.pair) {
+    pl.grid = 2 * static_cast<int>(std::min<int64_t>(units, s.pairs));
+    return pl;
+  }
   // K over clusters, as many CTAs as the SMs hold at once
-  for (int s = 2; s <= 8; ++s)
-    if (units * s <= sms && s <= slices && clusters[s] >= units) pl.splits = s;
+  for (int c = 2; c <= 8; ++c)
+    if (units * c <= sms && c <= slices && s.clusters[c] >= units) pl.splits = c;
   pl.grid = static_cast<int>(pl.splits > 1 ? units * pl.splits : std::min<int64_t>(units, sms));
   return pl;
 }
@@ -104,9 +109,9 @@ swiglu_status_t pack(const void* w1, const void* w2, void* wp, int64_t K, int64_
 size_t workspace_for(int64_t M, int64_t K, int64_t N, bool down) {
   if (check(M, K, N) != SWIGLU_OK || M == 0) return 0;
   DeviceView d;
-  const int* clusters = nullptr;
-  if (int8_device(&d, &clusters) != SWIGLU_OK) return 0;
-  return make_plan(M, K, N, down, d.sm_count, clusters).workspace(M, K);
+  const Int8State* s = nullptr;
+  if (int8_device(&d, &s) != SWIGLU_OK) return 0;
+  return make_plan(M, K, N, down, d.sm_count, *s).workspace(M, K);
 }
 
 // One projection: x [M, K] codes -> y [M, N].
@@ -129,10 +134,10 @@ swiglu_status_t project(const void* x, const float* scale_x, const void* wp, con
   const Span out[2] = {{y, y_bytes}, {workspace, workspace_bytes}};
   if (any_overlap(out, 2, in, 6)) return SWIGLU_ERR_INVALID_ARG;
   DeviceView d;
-  const int* clusters = nullptr;
-  st = int8_device(&d, &clusters);
+  const Int8State* s = nullptr;
+  st = int8_device(&d, &s);
   if (st != SWIGLU_OK) return st;
-  const Int8Plan pl = make_plan(M, K, N, down, d.sm_count, clusters);
+  const Int8Plan pl = make_plan(M, K, N, down, d.sm_count, *s);
   if (pl.blocks * pl.mgroups > kMaxUnits) return SWIGLU_ERR_UNSUPPORTED;
   const size_t need = pl.workspace(M, K);
   if (need > 0 && (!workspace || workspace_bytes < need)) return SWIGLU_ERR_INVALID_ARG;
@@ -140,11 +145,11 @@ swiglu_status_t project(const void* x, const float* scale_x, const void* wp, con
   Int8Params p{};
   const int64_t slices = div_up(K, kBlockK8), tiles = (down ? div_up(N, 256) : div_up(N, 128)) * slices;
   const uint64_t dims[3] = {128, 256, static_cast<uint64_t>(tiles)}, strides[2] = {128, 32768};
-  const uint32_t box[3] = {128, static_cast<uint32_t>(128 * pl.halves), 1};
+  const uint32_t box[3] = {128, 128, 1};
   if (!encode_3d(&p.tmap_w, wp, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_DATA_TYPE_UINT8))
     return SWIGLU_ERR_CUDA;
-  if (pl.wide) {
-    if (!encode_2d(&p.tmap_x, workspace, K, M, K * 2, 64, pl.mt, CU_TENSOR_MAP_SWIZZLE_128B)) return SWIGLU_ERR_CUDA;
+  if (pl.pair) {
+    if (!encode_2d(&p.tmap_x, workspace, K, M, K * 2, 64, pl.mt / 2, CU_TENSOR_MAP_SWIZZLE_128B)) return SWIGLU_ERR_CUDA;
     st = launched(launch_widen(x, workspace, size_t(M) * size_t(K), cs));
     if (st != SWIGLU_OK) return st;
   } else if (!encode_2d(&p.tmap_x, x, K, M, K, 128, pl.mt, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -159,18 +164,15 @@ swiglu_status_t project(const void* x, const float* scale_x, const void* wp, con
   p.M = static_cast<int>(M);
   p.K = static_cast<int>(K);
   p.N = static_cast<int>(N);
-  p.halves = pl.halves;
+  p.pair = pl.pair ? 1 : 0;
   p.blocks = static_cast<int>(pl.blocks);
   p.mt = pl.mt;
   p.mgroups = static_cast<int>(pl.mgroups);
   p.group_m = static_cast<int>(std::min<int64_t>(pl.mgroups, 32));
-  p.wide = pl.wide ? 1 : 0;
   p.splits = pl.splits;
   p.stages = pl.stages;
   p.grid = pl.grid;
-  // about 64 MB of weights on their way to L2 while the kernel before this one ends, as for the
-  // bf16 decode kernel
-  p.l2_prefetch = static_cast<int>(std::clamp<int64_t>((int64_t(64) << 20) / (int64_t(pl.grid) * 16384 * pl.halves), 2, 16));
+  p.l2_prefetch = pl.pair ? 2 : kL2Ahead;
   p.status = d.status;
   p.timeout_ns = d.timeout_ns;
   p.inject_stall = d.inject_stall;
@@ -183,13 +185,13 @@ swiglu_status_t plan_string(const char* what, int64_t M, int64_t K, int64_t N, b
   swiglu_status_t st = check(M, K, N);
   if (st != SWIGLU_OK) return st;
   DeviceView d;
-  const int* clusters = nullptr;
-  st = int8_device(&d, &clusters);
+  const Int8State* s = nullptr;
+  st = int8_device(&d, &s);
   if (st != SWIGLU_OK) return st;
-  const Int8Plan pl = make_plan(std::max<int64_t>(M, 1), K, N, down, d.sm_count, clusters);
-  std::snprintf(buf, buflen, "%s rows=%d mt=%d groups=%lld blocks=%lld splits=%d stages=%d grid=%d tokens=%s", what,
-                128 * pl.halves, pl.mt, static_cast<long long>(pl.mgroups), static_cast<long long>(pl.blocks),
-                pl.splits, pl.stages, pl.grid, pl.wide ? "widened before" : "codes");
+  const Int8Plan pl = make_plan(std::max<int64_t>(M, 1), K, N, down, d.sm_count, *s);
+  std::snprintf(buf, buflen, "%s %s mt=%d groups=%lld blocks=%lld splits=%d stages=%d grid=%d", what,
+                pl.pair ? "pairs" : "ctas", pl.mt, static_cast<long long>(pl.mgroups),
+                static_cast<long long>(pl.blocks), pl.splits, pl.stages, pl.grid);
   return SWIGLU_OK;
 }
 

@@ -229,21 +229,22 @@ cudaError_t launch_reduce_parts(const ReduceParams& p, cudaStream_t stream);
 cudaError_t launch_quantize_rows(const void* x, void* codes, float* scale, int M, int K, cudaStream_t stream);
 
 // Projections in 8-bit integers (int8_gemm.cu).
+constexpr int kInt8Tokens = 64;       // tokens of a unit on one CTA, at most
+constexpr int kInt8PairTokens = 192;  // and on a CTA pair
 struct Int8Params {
-  CUtensorMap tmap_x;   // tokens: codes [M, K] box {128, mt}, or (wide) fp16 [M, K] box {64, mt}; 128-B swizzle
-  CUtensorMap tmap_w;   // packed codes {128, 256, tiles} box {128, 128 * halves, 1}, 128-B swizzle
+  CUtensorMap tmap_x;   // tokens: codes [M, K] box {128, mt}, or (pair) fp16 [M, K] box {64, mt / 2}; 128-B swizzle
+  CUtensorMap tmap_w;   // packed codes {128, 256, tiles} box {128, 128, 1}, 128-B swizzle
   void* y;              // [M, N] bf16
   const void* residual; // [M, N] bf16 or null (down-projection)
   const float* scale_x; // [M]
   const float* scale0;  // [N]: of W1, or W3
   const float* scale1;  // [N]: of W2
   int M, K, N;
-  int halves;           // 128-row groups of weight rows a unit has: gate and up, or 1 or 2 of W3's columns
-  int blocks;           // units of columns
-  int mt, mgroups;      // tokens of a group (a multiple of 16, at most 128), groups
+  int pair;             // units of 256 packed rows on CTA pairs; else of 128 on one CTA
+  int blocks;           // units of packed rows
+  int mt, mgroups;      // tokens of a group (a multiple of 16, in pairs of 32), groups
   int group_m;          // token groups that go by before the next columns
-  int wide;             // tokens are fp16
-  int splits;           // K parts, a cluster of CTAs
+  int splits;           // K parts, a cluster of CTAs (not in pairs)
   int stages;
   int slots;            // set by the launch
   int grid;
@@ -252,9 +253,9 @@ struct Int8Params {
   uint64_t timeout_ns;
   int inject_stall;
 };
-// clusters[s]: clusters of s CTAs that can be resident at once (s = 1 .. 8).
-cudaError_t configure_int8(int (&clusters)[9]);
-int int8_stages(int halves, int mt, bool wide);
+// clusters[s]: clusters of s CTAs that can be resident at once (s = 1 .. 8); pairs: CTA pairs.
+cudaError_t configure_int8(int (&clusters)[9], int* pairs);
+int int8_stages(int mt, bool pair);
 cudaError_t launch_int8_gemm(const Int8Params& p, bool down, cudaStream_t stream);
 // int8 codes as fp16 values; `values` a multiple of 16.
 cudaError_t launch_widen(const void* codes, void* out, size_t values, cudaStream_t stream);

@@ -303,8 +303,8 @@ def test_refusals(native):
                 lambda: native.swiglu_forward_int8(a, sa.cpu(), wp, 136, s, s)):
         with pytest.raises(ValueError):
             bad()
-    big = codes(g, 100, 64).cuda()
-    one = torch.ones(100, device="cuda")
+    big = codes(g, 600, 64).cuda()
+    one = torch.ones(600, device="cuda")
     with pytest.raises(native.SwigluError):  # the tokens need a workspace
         native.swiglu_forward_int8(big, one, wp, 136, s, s, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
     with pytest.raises(native.SwigluError):  # rows of 24 bytes
