@@ -444,7 +444,8 @@ SWIGLU_API swiglu_status_t swiglu_quantize_int8(const void* X, void* Q, float* s
  *   value, N rounded up to 128 (H to 256), K (N) to 128; 0 on a bad shape.
  * swiglu_pack_weights_int8, swiglu_pack_down_weights_int8: tiles of 256 rows x
  *   128 of K, every code with its sign bit flipped; a row is a column of W3, or
- *   16 columns of W1 and the same 16 of W2 in turn. Runs once per weight set.
+ *   16 columns of W1 and the same 16 of W2 in turn; its 16-byte pieces c are
+ *   stored in the order c ^ (row % 8). Runs once per weight set.
  * swiglu_int8_workspace_bytes, swiglu_down_int8_workspace_bytes: what a call
  *   needs on the current device (0 for few tokens; 2 bytes per token code
  *   beyond). The workspace's contents need no set-up and mean nothing after

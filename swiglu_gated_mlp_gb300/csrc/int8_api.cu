@@ -47,6 +47,7 @@ swiglu_status_t int8_device(DeviceView* d, const Int8State** out) {
 int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 constexpr int64_t kMaxUnits = 1 << 30;
+const int kKeepAhead = std::getenv("SWIGLU_I8_KEEP") ? 1 : 0;
 const int kL2Ahead = std::getenv("SWIGLU_I8_AHEAD") ? std::atoi(std::getenv("SWIGLU_I8_AHEAD")) : 16;
 
 struct Int8Plan {
@@ -67,6 +68,7 @@ Int8Plan make_plan(int64_t M, int64_t K, int64_t N, bool down, int sms, const In
   pl.mgroups = div_up(M, most);
   pl.mt = static_cast<int>(div_up(div_up(M, pl.mgroups), unit) * unit);
   pl.stages = int8_stages(pl.mt, pl.pair);
+  if (std::getenv("SWIGLU_I8_STAGES")) pl.stages = std::min(pl.stages, std::atoi(std::getenv("SWIGLU_I8_STAGES")));
   const int64_t units = pl.blocks * pl.mgroups;
   if (pl.pair) {
     pl.grid = 2 * static_cast<int>(std::min<int64_t>(units, s.pairs));
@@ -143,11 +145,7 @@ swiglu_status_t project(const void* x, const float* scale_x, const void* wp, con
   if (need > 0 && (!workspace || workspace_bytes < need)) return SWIGLU_ERR_INVALID_ARG;
   const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   Int8Params p{};
-  const int64_t slices = div_up(K, kBlockK8), tiles = (down ? div_up(N, 256) : div_up(N, 128)) * slices;
-  const uint64_t dims[3] = {128, 256, static_cast<uint64_t>(tiles)}, strides[2] = {128, 32768};
-  const uint32_t box[3] = {128, 128, 1};
-  if (!encode_3d(&p.tmap_w, wp, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_DATA_TYPE_UINT8))
-    return SWIGLU_ERR_CUDA;
+  p.w = wp;
   if (pl.pair) {
     if (!encode_2d(&p.tmap_x, workspace, K, M, K * 2, 64, pl.mt / 2, CU_TENSOR_MAP_SWIZZLE_128B)) return SWIGLU_ERR_CUDA;
     st = launched(launch_widen(x, workspace, size_t(M) * size_t(K), cs));
@@ -173,6 +171,7 @@ swiglu_status_t project(const void* x, const float* scale_x, const void* wp, con
   p.stages = pl.stages;
   p.grid = pl.grid;
   p.l2_prefetch = pl.pair ? 2 : kL2Ahead;
+  p.keep_ahead = kKeepAhead;
   p.status = d.status;
   p.timeout_ns = d.timeout_ns;
   p.inject_stall = d.inject_stall;

@@ -19,9 +19,9 @@
 //   warps 2-9   thread = weight row: 64 codes from shared memory (16-byte pieces of
 //               a 128-byte swizzled row, free of bank conflicts), each byte b = q + 128
 //               set into the fp16 1024 + b and 1152 taken away (2 instructions for 2
-//               codes), then one tcgen05.st of 32 columns. A slot of tensor memory
-//               holds 64 of K; a ring of them runs ahead of the MMAs, and four of the
-//               warps fill every other one.
+//               codes), then one tcgen05.st of 32 columns; four of the warps do the first
+//               64 of K of every stage, four the rest. A slot of tensor memory holds a
+//               stage; a ring of them runs ahead of the MMAs.
 //   warps 10-17 epilogue, under the next unit's MMAs (two accumulators)
 //
 // Few tokens (kPair false): a unit is 128 weight rows and up to 64 tokens on one CTA. The epilogue's
@@ -44,12 +44,11 @@ namespace {
 
 constexpr int kConvWarps = 8, kEpiWarps8 = 8;
 constexpr int kThreads8 = 32 * (2 + kConvWarps + kEpiWarps8);
-constexpr int kMaxStages8 = 8;
-constexpr int kMaxSlots = 16;
+constexpr int kMaxStages8 = 10;
 constexpr int kTmem8 = 512;
-constexpr int kBarBytes8 = 512;
+constexpr int kBarBytes8 = 768;
 constexpr size_t kSmemLimit8 = 232448;
-constexpr int kSubK = 64;    // K values of a slot
+constexpr int kSubK = 64;    // K values of a 128-byte row of fp16
 constexpr int kRows8 = 128;  // packed weight rows of a CTA's unit
 
 // Four codes, biased to bytes 0..255, as two words of fp16 pairs: byte b under 0x64 is 1024 + b.
@@ -100,6 +99,27 @@ __device__ __forceinline__ void mma_f16_ts_pair(uint32_t d_tmem, uint32_t a_tmem
       "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+
+// `bytes` (a multiple of 16) of consecutive global memory to shared memory, or on their way to L2.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+
+__device__ __forceinline__ void bulk_load_hint(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar,
+                                               uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(
+          dst),
+      "l"(src), "r"(bytes), "r"(bar), "l"(policy)
+      : "memory");
+}
+
+__device__ __forceinline__ void bulk_prefetch_l2(const void* src, uint32_t bytes, uint64_t policy) {
+  asm volatile("cp.async.bulk.prefetch.L2.global.L2::cache_hint [%0], %1, %2;" ::"l"(src), "r"(bytes), "l"(policy)
+               : "memory");
 }
 
 struct Unit {
@@ -159,12 +179,14 @@ __global__ void __launch_bounds__(kThreads8, 1) int8_gemm_kernel(const __grid_co
   const uint32_t s0 = smem_addr(smem);
   uint8_t* bar_ptr = smem + size_t(stages) * stage_bytes;
   const uint32_t bar0 = smem_addr(bar_ptr);
-  // barrier slots: full[8] | tokens[8] | empty[8] | slot ready[16] | slot free[16] | sums[2] | sums read[2] | drain.
-  // full: weights (and codes of tokens) landed, this CTA's; tokens: fp16 values there, the even CTA's.
-  const uint32_t full0 = bar0, tok0 = full0 + 8u * kMaxStages8, empty0 = tok0 + 8u * kMaxStages8;
-  const uint32_t ready0 = empty0 + 8u * kMaxStages8, free0 = ready0 + 8u * kMaxSlots;
-  const uint32_t tfull0 = free0 + 8u * kMaxSlots, tempty0 = tfull0 + 16u, drain = tempty0 + 16u;
-  constexpr int kBars = 3 * kMaxStages8 + 2 * kMaxSlots + 5;
+  // barrier slots: full[10] | ready[10] | done[10] | sums[2] | sums read[2] | drain, of a stage:
+  // full: weights (and codes of tokens) landed, in this CTA; ready: both operands are in fp16, in the
+  // CTA that issues; done: its MMAs are, which frees its shared memory and its slot. One commit
+  // and one wait of the issuing warp a stage: with a ready and a free barrier for each 64 of K
+  // beside the tokens' that warp was what the decode kernel waited for.
+  const uint32_t full0 = bar0, ready0 = full0 + 8u * kMaxStages8, done0 = ready0 + 8u * kMaxStages8;
+  const uint32_t tfull0 = done0 + 8u * kMaxStages8, tempty0 = tfull0 + 16u, drain = tempty0 + 16u;
+  constexpr int kBars = 3 * kMaxStages8 + 5;
   static_assert(8 * kBars + 8 <= kBarBytes8, "barrier slots");
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_ptr + 8 * kBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -182,20 +204,21 @@ __global__ void __launch_bounds__(kThreads8, 1) int8_gemm_kernel(const __grid_co
   const WaitCtx wc{abort_flag, p.status, p.timeout_ns};
   // weight block of 128 packed rows: the upper or lower half of a packed tile
   const auto block_of = [&](const Unit& u) { return kPair ? 2 * u.block + static_cast<int>(rank) : u.block; };
+  const auto weights = [&](int ub, int kb) {
+    return static_cast<const uint8_t*>(p.w) + (static_cast<size_t>(ub >> 1) * num_kb + kb) * (2 * kWBytes) +
+           (ub & 1) * kWBytes;
+  };
   // the even CTA's barriers, as seen from either CTA of a pair
-  const uint32_t tok0_lead = kPair ? mapa_shared(tok0, 0) : tok0;
   const uint32_t ready0_lead = kPair ? mapa_shared(ready0, 0) : ready0;
   const uint32_t tempty0_lead = kPair ? mapa_shared(tempty0, 0) : tempty0;
 
   if (threadIdx.x == 0) {
     prefetch_tmap(&p.tmap_x);
-    prefetch_tmap(&p.tmap_w);
     // weights are no product of the kernel before this one: its first tiles on their way to L2
     // meanwhile (L2 is coherent: safe even if they were)
     const uint64_t pol = policy_evict_first();
     for (int i = 0, u = first, kb = kb_begin; i < p.l2_prefetch && u < units; ++i) {
-      const int ub = block_of(unit_of(p, u));
-      tma_prefetch_l2_3d_hint(&p.tmap_w, 0, (ub & 1) * kRows8, (ub >> 1) * num_kb + kb, pol);
+      bulk_prefetch_l2(weights(block_of(unit_of(p, u)), kb), kWBytes, pol);
       if (++kb == kb_end) {
         kb = kb_begin;
         u += step;
@@ -203,12 +226,9 @@ __global__ void __launch_bounds__(kThreads8, 1) int8_gemm_kernel(const __grid_co
     }
     for (int s = 0; s < stages; ++s) {
       mbar_init(full0 + 8u * s, 1);
-      mbar_init(tok0 + 8u * s, kPair ? 1 : kEpiWarps8);
-      mbar_init(empty0 + 8u * s, 1);
-    }
-    for (int t = 0; t < slots; ++t) {
-      mbar_init(ready0 + 8u * t, kPair ? 8 : 4);  // the warps that write a slot
-      mbar_init(free0 + 8u * t, 1);
+      // the converting warps (of both CTAs), and the ones that widen tokens, or the even producer
+      mbar_init(ready0 + 8u * s, kPair ? 2 * kConvWarps + 1 : kConvWarps + kEpiWarps8);
+      mbar_init(done0 + 8u * s, 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(tfull0 + 8u * b, 1);
@@ -235,7 +255,7 @@ __global__ void __launch_bounds__(kThreads8, 1) int8_gemm_kernel(const __grid_co
   tc_fence_after();
   const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
   // the slots, then the accumulators, two of mt columns
-  const uint32_t acc0 = tmem_base + static_cast<uint32_t>(slots * 32);
+  const uint32_t acc0 = tmem_base + static_cast<uint32_t>(slots * 64);
   pdl_wait();
 
   if (warp == 0) {
@@ -247,15 +267,15 @@ __global__ void __launch_bounds__(kThreads8, 1) int8_gemm_kernel(const __grid_co
     bool ok = true, skip_once = p.inject_stall != 0;
     // the slice that goes to L2 with each load, l2_prefetch slices further (one token group: many
     // groups share their weights anyway)
-    const bool ahead = !kPair && p.mgroups == 1;
+    const bool ahead = !kPair && p.mgroups == 1 && p.keep_ahead;
     const int mine_kb = kb_end - kb_begin;
     int au = first + p.l2_prefetch / mine_kb * step, akb = kb_begin + p.l2_prefetch % mine_kb;
     for (int u = first; ok && u < units; u += step) {
       const Unit un = unit_of(p, u);
-      const int ub = block_of(un), tile = (ub >> 1) * num_kb, row = (ub & 1) * kRows8;
+      const int ub = block_of(un);
       const int m0 = un.group * mt + (kPair ? static_cast<int>(rank) * mine : 0);
       for (int kb = kb_begin; kb < kb_end; ++kb) {
-        if (!mbar_wait_warp(empty0 + 8u * s, ph ^ 1u, wc, kSiteProducerEmpty)) {
+        if (!mbar_wait_warp(done0 + 8u * s, ph ^ 1u, wc, kSiteProducerEmpty)) {
           ok = false;
           break;
         }
@@ -266,19 +286,19 @@ __global__ void __launch_bounds__(kThreads8, 1) int8_gemm_kernel(const __grid_co
             const uint32_t fb = full0 + 8u * s, sw = s0 + s * stage_bytes, sx = sw + kWBytes;
             mbar_arrive_expect_tx(fb, kWBytes + raw_bytes);
             if constexpr (kPair) {
-              if (leader) mbar_arrive_expect_tx(tok0 + 8u * s, 2 * x_bytes);
-              tma_load_3d(sw, &p.tmap_w, fb, 0, row, tile + kb);
-              tma_load_2d_pair(sx, &p.tmap_x, tok0_lead + 8u * s, kb * kBlockK8, m0);
-              tma_load_2d_pair(sx + x_bytes / 2, &p.tmap_x, tok0_lead + 8u * s, kb * kBlockK8 + kSubK, m0);
+              if (leader) mbar_arrive_expect_tx(ready0 + 8u * s, 2 * x_bytes);
+              bulk_load(sw, weights(ub, kb), kWBytes, fb);
+              tma_load_2d_pair(sx, &p.tmap_x, ready0_lead + 8u * s, kb * kBlockK8, m0);
+              tma_load_2d_pair(sx + x_bytes / 2, &p.tmap_x, ready0_lead + 8u * s, kb * kBlockK8 + kSubK, m0);
             } else {
               if (p.mgroups > 1)  // other CTAs read the same weights
-                tma_load_3d(sw, &p.tmap_w, fb, 0, row, tile + kb);
+                bulk_load(sw, weights(ub, kb), kWBytes, fb);
               else
-                tma_load_3d_hint(sw, &p.tmap_w, fb, 0, row, tile + kb, pol_w);
+                bulk_load_hint(sw, weights(ub, kb), kWBytes, fb, pol_w);
               tma_load_2d_hint(sx + x_bytes, &p.tmap_x, fb, kb * kBlockK8, m0, pol_x);
             }
             if (ahead && au < units)  // one group: a unit is a block
-              tma_prefetch_l2_3d_hint(&p.tmap_w, 0, (au & 1) * kRows8, (au >> 1) * num_kb + akb, pol_w);
+              bulk_prefetch_l2(weights(au, akb), kWBytes, pol_w);
           }
           if (++akb == kb_end) {
             akb = kb_begin;
@@ -299,7 +319,7 @@ __global__ void __launch_bounds__(kThreads8, 1) int8_gemm_kernel(const __grid_co
     for (int i = 0; one && i < stages; ++i)
       if (filled & (1u << i)) {
         mbar_wait_drain(full0 + 8u * i, (fill_ph >> i) & 1u, wc);
-        if (kPair && leader) mbar_wait_drain(tok0 + 8u * i, (fill_ph >> i) & 1u, wc);
+        if (kPair && leader) mbar_wait_drain(ready0 + 8u * i, (fill_ph >> i) & 1u, wc);
       }
     __syncwarp();
   } else if (warp == 1) {
@@ -308,50 +328,38 @@ __global__ void __launch_bounds__(kThreads8, 1) int8_gemm_kernel(const __grid_co
       const bool one = elect_one();
       const uint32_t idesc = idesc_f16_f32(kPair ? 256 : 128, mt);
       int s = 0, t = 0, buf = 0;
-      uint32_t ph = 0, tph = 0, acc_ph = 0;
+      uint32_t ph = 0, acc_ph = 0;
       bool ok = true;
       for (int u = first; ok && u < units; u += step) {
         if (!mbar_wait_warp(tempty0 + 8u * buf, acc_ph ^ 1u, wc, kSiteMmaTmemEmpty)) break;
         tc_fence_after();
         const uint32_t d = acc0 + static_cast<uint32_t>(buf * mt);
-        for (int kb = kb_begin; ok && kb < kb_end; ++kb) {
-          if (!mbar_wait_warp(tok0 + 8u * s, ph, wc, kSiteMmaFull)) {
+        for (int kb = kb_begin; kb < kb_end; ++kb) {
+          if (!mbar_wait_warp(ready0 + 8u * s, ph, wc, kSiteMmaFull)) {
             ok = false;
             break;
           }
-          const uint32_t sx = s0 + s * stage_bytes + kWBytes;
+          tc_fence_after();
+          const uint64_t xdesc = smem_desc_sw128(s0 + s * stage_bytes + kWBytes);
+          const uint64_t next = x_bytes / 2 >> 4;  // the tokens' second 64 of K
+          const uint32_t a = tmem_base + static_cast<uint32_t>(t) * 64;
+          if (one) {
 #pragma unroll
-          for (int sub = 0; sub < 2; ++sub) {
-            if (!mbar_wait_warp(ready0 + 8u * t, tph, wc, kSiteConvert)) {
-              ok = false;
-              break;
+            for (int k = 0; k < 8; ++k) {  // 16 of K: 8 columns of the slot, 32 bytes of a token's row
+              const uint32_t acc = (kb != kb_begin || k != 0) ? 1u : 0u;
+              const uint64_t x = xdesc + 2u * (k & 3) + (k >> 2) * next;
+              if constexpr (kPair)
+                mma_f16_ts_pair(d, a + 8 * k, x, idesc, acc);
+              else
+                mma_f16_ts(d, a + 8 * k, x, idesc, acc);
             }
-            tc_fence_after();
-            const uint64_t xdesc = smem_desc_sw128(sx + sub * (x_bytes / 2));
-            const uint32_t a = tmem_base + static_cast<uint32_t>(t) * 32;
-            if (one) {
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {  // 16 of K: 8 columns of the slot, 32 bytes of a token's row
-                const uint32_t acc = (kb != kb_begin || sub != 0 || k != 0) ? 1u : 0u;
-                if constexpr (kPair)
-                  mma_f16_ts_pair(d, a + 8 * k, xdesc + 2u * k, idesc, acc);
-                else
-                  mma_f16_ts(d, a + 8 * k, xdesc + 2u * k, idesc, acc);
-              }
-              if constexpr (kPair) {
-                mma_commit_pair_multicast(free0 + 8u * t, 0x3);
-                if (sub == 1) mma_commit_pair_multicast(empty0 + 8u * s, 0x3);
-              } else {
-                mma_commit(free0 + 8u * t);
-                if (sub == 1) mma_commit(empty0 + 8u * s);
-              }
-            }
-            __syncwarp();
-            if (++t == slots) {
-              t = 0;
-              tph ^= 1u;
-            }
+            if constexpr (kPair)
+              mma_commit_pair_multicast(done0 + 8u * s, 0x3);
+            else
+              mma_commit(done0 + 8u * s);
           }
+          __syncwarp();
+          if (++t == slots) t = 0;
           if (++s == stages) {
             s = 0;
             ph ^= 1u;
@@ -381,8 +389,11 @@ __global__ void __launch_bounds__(kThreads8, 1) int8_gemm_kernel(const __grid_co
     const int sub = (warp - 2) >> 2, q = warp & 3;  // this warp's half of a stage, its lanes
     const int row = q * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>(q * 32) << 16;
-    int s = 0, t = sub;
-    uint32_t ph = 0, tph = 0;
+    // The slot of this stage was last that of the stage `slots` before; where the ring of stages is
+    // no longer than that of slots, this stage's copies already waited for that one.
+    const bool behind = slots < stages;
+    int s = 0, t = 0, old = stages - slots;  // old: the ring index of the stage `slots` before
+    uint32_t ph = 0, old_ph = 1;             // a first use waits for nothing
     bool ok = true;
     for (int u = first; ok && u < units; u += step) {
       for (int kb = kb_begin; kb < kb_end; ++kb) {
@@ -394,7 +405,7 @@ __global__ void __launch_bounds__(kThreads8, 1) int8_gemm_kernel(const __grid_co
         uint4 v[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[j] = ld_shared_v4(src + (((sub * 4 + j) ^ (row & 7)) << 4));
-        if (!mbar_wait_warp(free0 + 8u * t, tph ^ 1u, wc, kSiteConvert)) {
+        if (behind && !mbar_wait_warp(done0 + 8u * old, old_ph, wc, kSiteConvert)) {
           ok = false;
           break;
         }
@@ -407,7 +418,7 @@ __global__ void __launch_bounds__(kThreads8, 1) int8_gemm_kernel(const __grid_co
           widen4(v[j].z, r[8 * j + 4], r[8 * j + 5]);
           widen4(v[j].w, r[8 * j + 6], r[8 * j + 7]);
         }
-        tmem_st_x32(tmem_base + static_cast<uint32_t>(t) * 32 + lane_off, r);
+        tmem_st_x32(tmem_base + static_cast<uint32_t>(t) * 64 + sub * 32 + lane_off, r);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
@@ -415,14 +426,14 @@ __global__ void __launch_bounds__(kThreads8, 1) int8_gemm_kernel(const __grid_co
         // so the arrival needs no release at cluster scope, which took 1000 cycles)
         if (lane == 0) {
           if constexpr (kPair)
-            mbar_arrive_remote(ready0_lead + 8u * t);
+            mbar_arrive_remote(ready0_lead + 8u * s);
           else
-            mbar_arrive(ready0 + 8u * t);
+            mbar_arrive(ready0 + 8u * s);
         }
-        t += 2;
-        if (t >= slots) {
-          t -= slots;
-          tph ^= 1u;
+        if (++t == slots) t = 0;
+        if (++old == stages) {
+          old = 0;
+          old_ph ^= 1u;
         }
         if (++s == stages) {
           s = 0;
@@ -463,7 +474,7 @@ __global__ void __launch_bounds__(kThreads8, 1) int8_gemm_kernel(const __grid_co
           }
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(tok0 + 8u * s);
+          if (lane == 0) mbar_arrive(ready0 + 8u * s);
           if (++s == stages) {
             s = 0;
             ph ^= 1u;
@@ -605,7 +616,9 @@ __global__ void __launch_bounds__(256) widen_kernel(const uint4* codes, uint4* o
 }
 
 // Weight codes [rows of the sum, columns] to packed tiles [256][128], biased to q + 128 (128
-// where there is none): 256 columns of one matrix, or 128 of two, 16 of each in turn.
+// where there is none): 256 columns of one matrix, or 128 of two, 16 of each in turn. A unit's
+// 128 rows are one contiguous copy of 16 KB: as a tiled TMA load (128 rows of 128 bytes, about 4
+// cycles a row) it was what the decode kernel waited for.
 __global__ void __launch_bounds__(256)
     pack_int8_kernel(const uint8_t* w1, const uint8_t* w2, uint32_t* wp, int K, int N, int k_slices, int down) {
   __shared__ uint8_t tile[kBlockK8][2 * kRows8 + 4];  // [k][packed row]
@@ -620,9 +633,10 @@ __global__ void __launch_bounds__(256)
     tile[t][row] = 0x80u ^ (k < K && n < N ? src[static_cast<size_t>(k) * N + n] : uint8_t(0));
   }
   __syncthreads();
+  // 16-byte pieces of a row in the order c ^ (row % 8), as the converting warps read them
   uint32_t* out = wp + (static_cast<size_t>(j) * k_slices + b) * (2 * kRows8 * kBlockK8 / 4);
   for (int idx = threadIdx.x; idx < 2 * kRows8 * kBlockK8 / 4; idx += 256) {
-    const int i = idx / (kBlockK8 / 4), t = idx % (kBlockK8 / 4) * 4;
+    const int i = idx / (kBlockK8 / 4), t = (idx % (kBlockK8 / 4) * 4) ^ ((i & 7) << 4);
     out[idx] = tile[t][i] | uint32_t(tile[t + 1][i]) << 8 | uint32_t(tile[t + 2][i]) << 16 | uint32_t(tile[t + 3][i]) << 24;
   }
 }
@@ -680,8 +694,7 @@ cudaError_t launch_int8_gemm(const Int8Params& p, bool down, cudaStream_t stream
       (!pair && p.splits > 1 && (p.grid / per != units || size_t(p.mt) * kRows8 * 4 > p.stages * stage_bytes8(p.mt, pair))))
     return cudaErrorInvalidValue;
   Int8Params q = p;
-  const int slots = (kTmem8 - 2 * p.mt) / 64 * 2;  // an even number: the converting warps take them in turn
-  q.slots = slots > kMaxSlots ? kMaxSlots : slots;
+  q.slots = (kTmem8 - 2 * p.mt) / 64;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(p.grid);
   cfg.blockDim = dim3(kThreads8);

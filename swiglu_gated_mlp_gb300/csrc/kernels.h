@@ -233,7 +233,7 @@ constexpr int kInt8Tokens = 64;       // tokens of a unit on one CTA, at most
 constexpr int kInt8PairTokens = 192;  // and on a CTA pair
 struct Int8Params {
   CUtensorMap tmap_x;   // tokens: codes [M, K] box {128, mt}, or (pair) fp16 [M, K] box {64, mt / 2}; 128-B swizzle
-  CUtensorMap tmap_w;   // packed codes {128, 256, tiles} box {128, 128, 1}, 128-B swizzle
+  const void* w;        // packed codes: tiles of 256 x 128
   void* y;              // [M, N] bf16
   const void* residual; // [M, N] bf16 or null (down-projection)
   const float* scale_x; // [M]
@@ -248,7 +248,8 @@ struct Int8Params {
   int stages;
   int slots;            // set by the launch
   int grid;
-  int l2_prefetch;
+  int l2_prefetch;      // 16 KB copies that a CTA asks L2 for ahead of its loads
+  int keep_ahead;
   uint32_t* status;
   uint64_t timeout_ns;
   int inject_stall;
