@@ -6,7 +6,6 @@
 #include <algorithm>
 #include <atomic>
 #include <cstdio>
-#include <cstdlib>
 #include <mutex>
 
 #include "api_shared.h"
@@ -47,38 +46,68 @@ swiglu_status_t int8_device(DeviceView* d, const Int8State** out) {
 int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 constexpr int64_t kMaxUnits = 1 << 30;
-const int kKeepAhead = std::getenv("SWIGLU_I8_KEEP") ? 1 : 0;
-const int kL2Ahead = std::getenv("SWIGLU_I8_AHEAD") ? std::atoi(std::getenv("SWIGLU_I8_AHEAD")) : 16;
-
 struct Int8Plan {
   bool pair = false;  // units on CTA pairs, tokens widened by a kernel before
   int mt = 16, splits = 1, stages = 0, grid = 0;
-  int64_t blocks = 0, mgroups = 1;
+  int64_t blocks = 0, mgroups = 1, group_m = 1;
   size_t workspace(int64_t M, int64_t K) const { return pair ? size_t(M) * size_t(K) * 2 : 0; }
 };
 
-// M tokens, sums over K, N outputs.
-Int8Plan make_plan(int64_t M, int64_t K, int64_t N, bool down, int sms, const Int8State& s) {
+// What launches take, in units of 2 ns, from measurements at 16 to 4096 tokens: a stage (128 of
+// K) of a unit, and all that comes before and after the stages (on pairs the kernel that widens
+// the tokens too). Stages are bound by the MMAs from about 140 tokens, else by their hand-overs.
+int64_t cta_stage(int64_t mt) { return 160 + mt * 4 / 3; }
+int64_t pair_stage(int64_t mt) { return std::max<int64_t>(172, mt + 32); }
+constexpr int64_t kCtaOnce = 2400, kPairOnce = 3600;
+
+// One CTA a unit: groups of at most 64 tokens, K over clusters, as many CTAs as the SMs hold at once.
+Int8Plan cta_plan(int64_t M, int64_t slices, int64_t halves, int sms, const Int8State& s, int64_t* cost) {
   Int8Plan pl;
-  const int64_t slices = div_up(K, kBlockK8);
-  const int64_t halves = div_up(N, down ? 128 : 64);  // packed blocks of 128 rows
-  pl.pair = s.pairs > 0 && M > 4 * kInt8Tokens;
-  const int64_t most = pl.pair ? kInt8PairTokens : kInt8Tokens, unit = pl.pair ? 32 : 16;
-  pl.blocks = pl.pair ? div_up(halves, 2) : halves;
-  pl.mgroups = div_up(M, most);
-  pl.mt = static_cast<int>(div_up(div_up(M, pl.mgroups), unit) * unit);
-  pl.stages = int8_stages(pl.mt, pl.pair);
-  if (std::getenv("SWIGLU_I8_STAGES")) pl.stages = std::min(pl.stages, std::atoi(std::getenv("SWIGLU_I8_STAGES")));
+  pl.blocks = halves;
+  pl.mgroups = div_up(M, kInt8Tokens);
+  pl.mt = static_cast<int>(div_up(div_up(M, pl.mgroups), 16) * 16);
+  pl.group_m = std::min<int64_t>(pl.mgroups, 32);
+  pl.stages = int8_stages(pl.mt, false);
   const int64_t units = pl.blocks * pl.mgroups;
-  if (pl.pair) {
-    pl.grid = 2 * static_cast<int>(std::min<int64_t>(units, s.pairs));
-    return pl;
-  }
-  // K over clusters, as many CTAs as the SMs hold at once
   for (int c = 2; c <= 8; ++c)
     if (units * c <= sms && c <= slices && s.clusters[c] >= units) pl.splits = c;
   pl.grid = static_cast<int>(pl.splits > 1 ? units * pl.splits : std::min<int64_t>(units, sms));
+  *cost = div_up(units, sms) * div_up(slices, pl.splits) * cta_stage(pl.mt) + kCtaOnce;
   return pl;
+}
+
+// CTA pairs: the tokens of a unit that make the rounds of all units shortest.
+Int8Plan pair_plan(int64_t M, int64_t K, int64_t slices, int64_t halves, const Int8State& s, int64_t* cost) {
+  Int8Plan pl;
+  pl.pair = true;
+  pl.blocks = div_up(halves, 2);
+  *cost = INT64_MAX;
+  for (int64_t mt = 32; mt <= kInt8PairTokens; mt += 16) {
+    const int64_t c = div_up(pl.blocks * div_up(M, mt), s.pairs) * slices * pair_stage(mt) + kPairOnce;
+    if (c > *cost) continue;
+    *cost = c;
+    pl.mgroups = div_up(M, mt);
+  }
+  pl.mt = static_cast<int>(std::max<int64_t>(32, div_up(div_up(M, pl.mgroups), 16) * 16));
+  // token groups whose values stay in L2 (half of it) while the columns go by; at 4096 tokens: K
+  // 18944 all 26 groups at once 335 us, 9 of them 327; K 3584 6 groups 552, 11 540, all 22 532
+  pl.group_m = std::clamp<int64_t>((int64_t(64) << 20) / (pl.mt * K * 2), 1, std::min<int64_t>(pl.mgroups, 32));
+  pl.stages = int8_stages(pl.mt, true);
+  pl.grid = 2 * static_cast<int>(std::min<int64_t>(pl.blocks * pl.mgroups, s.pairs));
+  return pl;
+}
+
+// M tokens, sums over K, N outputs. Measured, CTAs / pairs (us): K 896 N 4864, 128 tokens 7.1 / 8.2,
+// 256 11.9 / 10.3; K 3584 N 18944, 80 tokens 56 / 27; down, N 18944 H 3584, 128 tokens 38 / 53, 256
+// 71 / 56; N 4864 H 896, 512 tokens 13.4 / 20.3, 1000 21.2 / 21.8.
+Int8Plan make_plan(int64_t M, int64_t K, int64_t N, bool down, int sms, const Int8State& s) {
+  const int64_t slices = div_up(K, kBlockK8);
+  const int64_t halves = div_up(N, down ? 128 : 64);  // packed blocks of 128 rows
+  int64_t cta_cost = 0, pair_cost = 0;
+  const Int8Plan on_ctas = cta_plan(M, slices, halves, sms, s, &cta_cost);
+  if (s.pairs < 1) return on_ctas;
+  const Int8Plan on_pairs = pair_plan(M, K, slices, halves, s, &pair_cost);
+  return pair_cost < cta_cost ? on_pairs : on_ctas;
 }
 
 swiglu_status_t check(int64_t M, int64_t K, int64_t N) {
@@ -146,11 +175,12 @@ swiglu_status_t project(const void* x, const float* scale_x, const void* wp, con
   const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   Int8Params p{};
   p.w = wp;
+  const uint32_t box = static_cast<uint32_t>(pl.pair ? pl.mt / 2 : pl.mt);
   if (pl.pair) {
-    if (!encode_2d(&p.tmap_x, workspace, K, M, K * 2, 64, pl.mt / 2, CU_TENSOR_MAP_SWIZZLE_128B)) return SWIGLU_ERR_CUDA;
+    if (!encode_2d(&p.tmap_x, workspace, K, M, K * 2, 64, box, CU_TENSOR_MAP_SWIZZLE_128B)) return SWIGLU_ERR_CUDA;
     st = launched(launch_widen(x, workspace, size_t(M) * size_t(K), cs));
     if (st != SWIGLU_OK) return st;
-  } else if (!encode_2d(&p.tmap_x, x, K, M, K, 128, pl.mt, CU_TENSOR_MAP_SWIZZLE_128B,
+  } else if (!encode_2d(&p.tmap_x, x, K, M, K, 128, box, CU_TENSOR_MAP_SWIZZLE_128B,
                         CU_TENSOR_MAP_DATA_TYPE_UINT8)) {
     return SWIGLU_ERR_CUDA;
   }
@@ -166,12 +196,10 @@ swiglu_status_t project(const void* x, const float* scale_x, const void* wp, con
   p.blocks = static_cast<int>(pl.blocks);
   p.mt = pl.mt;
   p.mgroups = static_cast<int>(pl.mgroups);
-  p.group_m = static_cast<int>(std::min<int64_t>(pl.mgroups, 32));
+  p.group_m = static_cast<int>(pl.group_m);
   p.splits = pl.splits;
   p.stages = pl.stages;
   p.grid = pl.grid;
-  p.l2_prefetch = pl.pair ? 2 : kL2Ahead;
-  p.keep_ahead = kKeepAhead;
   p.status = d.status;
   p.timeout_ns = d.timeout_ns;
   p.inject_stall = d.inject_stall;

@@ -19,9 +19,10 @@
 //   warps 2-9   thread = weight row: 64 codes from shared memory (16-byte pieces of
 //               a 128-byte swizzled row, free of bank conflicts), each byte b = q + 128
 //               set into the fp16 1024 + b and 1152 taken away (2 instructions for 2
-//               codes), then one tcgen05.st of 32 columns; four of the warps do the first
-//               64 of K of every stage, four the rest. A slot of tensor memory holds a
-//               stage; a ring of them runs ahead of the MMAs.
+//               codes), then one tcgen05.st of 32 columns; four warps do the first 64 of K
+//               of a stage, four the rest (16 warps in two sets: slower, the polls of more
+//               waiting warps cost more than the work: 7B, 16 tokens 24.7 -> 27.5 us).
+//               A slot of tensor memory holds a stage; a ring of them runs ahead of the MMAs.
 //   warps 10-17 epilogue, under the next unit's MMAs (two accumulators)
 //
 // Few tokens (kPair false): a unit is 128 weight rows and up to 64 tokens on one CTA. The epilogue's
@@ -32,7 +33,8 @@
 // More tokens (kPair): a unit is 256 weight rows and up to 192 tokens on a CTA pair
 // (cta_group::2: each CTA holds 128 weight rows in its tensor memory and half of the
 // tokens in its shared memory); a kernel before this one turns the tokens' codes into
-// fp16 once for all column blocks.
+// fp16 once for all column blocks, which leaves the epilogue to run under the next unit's
+// MMAs (widened by the epilogue's warps here too: 333 tokens, K 1424, N 5000 19.5 us, so 15.6).
 #include <cuda_fp16.h>
 
 #include "int8.cuh"
@@ -115,11 +117,6 @@ __device__ __forceinline__ void bulk_load_hint(uint32_t dst, const void* src, ui
           dst),
       "l"(src), "r"(bytes), "r"(bar), "l"(policy)
       : "memory");
-}
-
-__device__ __forceinline__ void bulk_prefetch_l2(const void* src, uint32_t bytes, uint64_t policy) {
-  asm volatile("cp.async.bulk.prefetch.L2.global.L2::cache_hint [%0], %1, %2;" ::"l"(src), "r"(bytes), "l"(policy)
-               : "memory");
 }
 
 struct Unit {
@@ -214,16 +211,6 @@ __global__ void __launch_bounds__(kThreads8, 1) int8_gemm_kernel(const __grid_co
 
   if (threadIdx.x == 0) {
     prefetch_tmap(&p.tmap_x);
-    // weights are no product of the kernel before this one: its first tiles on their way to L2
-    // meanwhile (L2 is coherent: safe even if they were)
-    const uint64_t pol = policy_evict_first();
-    for (int i = 0, u = first, kb = kb_begin; i < p.l2_prefetch && u < units; ++i) {
-      bulk_prefetch_l2(weights(block_of(unit_of(p, u)), kb), kWBytes, pol);
-      if (++kb == kb_end) {
-        kb = kb_begin;
-        u += step;
-      }
-    }
     for (int s = 0; s < stages; ++s) {
       mbar_init(full0 + 8u * s, 1);
       // the converting warps (of both CTAs), and the ones that widen tokens, or the even producer
@@ -265,11 +252,6 @@ __global__ void __launch_bounds__(kThreads8, 1) int8_gemm_kernel(const __grid_co
     int s = 0;
     uint32_t ph = 0, filled = 0, fill_ph = 0;
     bool ok = true, skip_once = p.inject_stall != 0;
-    // the slice that goes to L2 with each load, l2_prefetch slices further (one token group: many
-    // groups share their weights anyway)
-    const bool ahead = !kPair && p.mgroups == 1 && p.keep_ahead;
-    const int mine_kb = kb_end - kb_begin;
-    int au = first + p.l2_prefetch / mine_kb * step, akb = kb_begin + p.l2_prefetch % mine_kb;
     for (int u = first; ok && u < units; u += step) {
       const Unit un = unit_of(p, u);
       const int ub = block_of(un);
@@ -285,24 +267,17 @@ __global__ void __launch_bounds__(kThreads8, 1) int8_gemm_kernel(const __grid_co
           if (one) {
             const uint32_t fb = full0 + 8u * s, sw = s0 + s * stage_bytes, sx = sw + kWBytes;
             mbar_arrive_expect_tx(fb, kWBytes + raw_bytes);
+            if (p.mgroups > 1)  // other CTAs read the same weights
+              bulk_load(sw, weights(ub, kb), kWBytes, fb);
+            else
+              bulk_load_hint(sw, weights(ub, kb), kWBytes, fb, pol_w);
             if constexpr (kPair) {
               if (leader) mbar_arrive_expect_tx(ready0 + 8u * s, 2 * x_bytes);
-              bulk_load(sw, weights(ub, kb), kWBytes, fb);
               tma_load_2d_pair(sx, &p.tmap_x, ready0_lead + 8u * s, kb * kBlockK8, m0);
               tma_load_2d_pair(sx + x_bytes / 2, &p.tmap_x, ready0_lead + 8u * s, kb * kBlockK8 + kSubK, m0);
             } else {
-              if (p.mgroups > 1)  // other CTAs read the same weights
-                bulk_load(sw, weights(ub, kb), kWBytes, fb);
-              else
-                bulk_load_hint(sw, weights(ub, kb), kWBytes, fb, pol_w);
               tma_load_2d_hint(sx + x_bytes, &p.tmap_x, fb, kb * kBlockK8, m0, pol_x);
             }
-            if (ahead && au < units)  // one group: a unit is a block
-              bulk_prefetch_l2(weights(au, akb), kWBytes, pol_w);
-          }
-          if (++akb == kb_end) {
-            akb = kb_begin;
-            au += step;
           }
           filled |= 1u << s;
           fill_ph = (fill_ph & ~(1u << s)) | (ph << s);
@@ -393,7 +368,7 @@ __global__ void __launch_bounds__(kThreads8, 1) int8_gemm_kernel(const __grid_co
     // no longer than that of slots, this stage's copies already waited for that one.
     const bool behind = slots < stages;
     int s = 0, t = 0, old = stages - slots;  // old: the ring index of the stage `slots` before
-    uint32_t ph = 0, old_ph = 1;             // a first use waits for nothing
+    uint32_t ph = 0, old_ph = 1;               // a first use waits for nothing
     bool ok = true;
     for (int u = first; ok && u < units; u += step) {
       for (int kb = kb_begin; kb < kb_end; ++kb) {
@@ -530,27 +505,62 @@ __global__ void __launch_bounds__(kThreads8, 1) int8_gemm_kernel(const __grid_co
                 mbar_arrive(tempty0 + 8u * buf);
             }
           }
+          // a token's scale in lane (token % 16); columns n and n + 1 meet in one of two lanes, each
+          // with half of the tokens, and go out together. No branch before the stores, so that the
+          // chunk's loads, exchanges and exponentials overlap (one by one: 3000 cycles a chunk).
+          const float scales = p.scale_x[m0 + min(base + (lane & 15), mcount - 1)];
+          const bool odd = lane & 1;
+          __nv_bfloat16* out = y + static_cast<size_t>(m0 + base) * p.N + (n & ~1);
           if constexpr (kDown) {
+            float o[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              if (base + i < mcount && there) {
-                const size_t at = static_cast<size_t>(m0 + base + i) * p.N + n;
-                float o = __uint_as_float(a[i]) * p.scale_x[m0 + base + i] * t0;
-                if (res) o += __bfloat162float(res[at]);
-                y[at] = __float2bfloat16(o);
-              }
+            for (int i = 0; i < 16; ++i)
+              o[i] = __uint_as_float(a[i]) * __shfl_sync(0xffffffffu, scales, i) * t0;
+            const int at = odd ? 8 : 0;  // even lanes take the first 8 tokens
+            uint32_t r[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              r[i] = res && there && base + at + i < mcount
+                         ? *reinterpret_cast<const uint32_t*>(res + static_cast<size_t>(m0 + base + at + i) * p.N +
+                                                              (n & ~1))
+                         : 0u;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float got = __shfl_xor_sync(0xffffffffu, odd ? o[i] : o[i + 8], 1);
+              const float lo = odd ? got : o[i], hi = odd ? o[i + 8] : got;
+              if (there && base + at + i < mcount)
+                *reinterpret_cast<uint32_t*>(out + static_cast<size_t>(at + i) * p.N) =
+                    pack_bf16x2(lo + __uint_as_float(r[i] << 16), hi + __uint_as_float(r[i] & 0xffff0000u));
             }
           } else {
             // of two tokens the lower lanes finish the first, the upper ones the second
+            const int half = lower ? 0 : 1;
+            uint32_t w[4];  // tokens 4 j + half and 4 j + 2 + half
 #pragma unroll
-            for (int i = 0; i < 16; i += 2) {
-              const uint32_t got = __shfl_xor_sync(0xffffffffu, lower ? a[i + 1] : a[i], 16);
-              const float g = __uint_as_float(lower ? a[i] : got), v = __uint_as_float(lower ? got : a[i + 1]);
-              const int m = base + i + (lower ? 0 : 1);
-              if (m < mcount && there) {
-                const float sa = p.scale_x[m0 + m];
-                y[static_cast<size_t>(m0 + m) * p.N + n] = __float2bfloat16(silu_mul(g * sa * t0, v * sa * t1));
+            for (int j = 0; j < 4; ++j) {
+              float o[2];
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const int i = 4 * j + 2 * e;
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, lower ? a[i + 1] : a[i], 16);
+                const float g = __uint_as_float(lower ? a[i] : got), v = __uint_as_float(lower ? got : a[i + 1]);
+                const float sa = __shfl_sync(0xffffffffu, scales, i + half);
+                o[e] = silu_mul(g * sa * t0, v * sa * t1);
               }
+              w[j] = pack_bf16x2(o[0], o[1]);
+            }
+            const int at = (odd ? 8 : 0) + half;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const uint32_t own = odd ? w[j + 2] : w[j];
+              const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? w[j] : w[j + 2], 1);
+              const uint32_t first_of = odd ? got : own, second_of = odd ? own : got;  // columns n & ~1 and n | 1
+              if (there && base + at + 4 * j < mcount)
+                *reinterpret_cast<uint32_t*>(out + static_cast<size_t>(at + 4 * j) * p.N) =
+                    __byte_perm(first_of, second_of, 0x5410);
+              if (there && base + at + 4 * j + 2 < mcount)
+                *reinterpret_cast<uint32_t*>(out + static_cast<size_t>(at + 4 * j + 2) * p.N) =
+                    __byte_perm(first_of, second_of, 0x7632);
             }
           }
         }
@@ -688,7 +698,7 @@ cudaError_t launch_int8_gemm(const Int8Params& p, bool down, cudaStream_t stream
   const int64_t units = int64_t(p.blocks) * p.mgroups;
   const bool pair = p.pair != 0;
   const int per = pair ? 2 : p.splits;
-  if (p.mt < 16 || p.mt > (pair ? kInt8PairTokens : kInt8Tokens) || (p.mt % (pair ? 32 : 16)) != 0 || p.stages < 2 ||
+  if (p.mt < 16 || p.mt > (pair ? kInt8PairTokens : kInt8Tokens) || (p.mt % 16) != 0 || p.stages < 2 ||
       p.stages > int8_stages(p.mt, pair) || p.group_m < 1 || p.splits < 1 || p.splits > 8 || p.splits > num_kb ||
       p.grid < per || (p.grid % per) != 0 || p.grid / per > units ||
       (!pair && p.splits > 1 && (p.grid / per != units || size_t(p.mt) * kRows8 * 4 > p.stages * stage_bytes8(p.mt, pair))))

@@ -242,14 +242,12 @@ struct Int8Params {
   int M, K, N;
   int pair;             // units of 256 packed rows on CTA pairs; else of 128 on one CTA
   int blocks;           // units of packed rows
-  int mt, mgroups;      // tokens of a group (a multiple of 16, in pairs of 32), groups
+  int mt, mgroups;      // tokens of a group (a multiple of 16), groups
   int group_m;          // token groups that go by before the next columns
   int splits;           // K parts, a cluster of CTAs (not in pairs)
   int stages;
   int slots;            // set by the launch
   int grid;
-  int l2_prefetch;      // 16 KB copies that a CTA asks L2 for ahead of its loads
-  int keep_ahead;
   uint32_t* status;
   uint64_t timeout_ns;
   int inject_stall;

@@ -6,6 +6,8 @@
 // codes (the largest a multiple of 127 of some unit), where x * (127 / m) in fp32
 // would round either way; those near a half are decided by comparing 254 |x| with
 // (2 q + 1) m, both exact in fp32.
+#include <algorithm>
+
 #include "int8.cuh"
 #include "kernels.h"
 #include "ptx.cuh"
@@ -13,7 +15,7 @@
 namespace swg {
 namespace {
 
-constexpr int kHeld = 4;  // 16-byte pieces of a row that a thread keeps
+constexpr int kHeld = 8;  // 16-byte pieces of a row that a thread keeps
 
 __device__ __forceinline__ uint32_t max_bits(uint32_t acc, const uint4& v) {
   acc = __vmaxu2(acc, v.x & 0x7fff7fffu);
@@ -74,7 +76,7 @@ __global__ void __launch_bounds__(1024)
   acc = __reduce_max_sync(0xffffffffu, acc);
   if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = acc;
   __syncthreads();
-  acc = part[threadIdx.x & 31 & ((threads >> 5) - 1)];  // a power of two of warps
+  acc = part[min(threadIdx.x & 31, (threads >> 5) - 1)];
   acc = __reduce_max_sync(0xffffffffu, acc);
   const float largest = __uint_as_float(acc << 16);
   const QuantScale q = quant_scale(largest);
@@ -94,9 +96,10 @@ __global__ void __launch_bounds__(1024)
 
 cudaError_t launch_quantize_rows(const void* x, void* codes, float* scale, int M, int K, cudaStream_t stream) {
   const int chunks = K / 8;
-  // two pieces a thread, so that short rows leave room for several blocks an SM
-  int threads = 32;
-  while (threads < 1024 && threads * 2 < chunks) threads *= 2;
+  // many rows: up to 8 pieces a thread, so that several blocks of an SM load while others reduce;
+  // few rows: one or two, for the time of a row
+  const int pieces = M > 304 ? kHeld : 2;
+  const int threads = std::min(1024, (chunks + 32 * pieces - 1) / (32 * pieces) * 32);
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(M));
   cfg.blockDim = dim3(threads);

@@ -303,10 +303,13 @@ def test_refusals(native):
                 lambda: native.swiglu_forward_int8(a, sa.cpu(), wp, 136, s, s)):
         with pytest.raises(ValueError):
             bad()
-    big = codes(g, 600, 64).cuda()
-    one = torch.ones(600, device="cuda")
-    with pytest.raises(native.SwigluError):  # the tokens need a workspace
-        native.swiglu_forward_int8(big, one, wp, 136, s, s, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
+    # many tokens and columns need a workspace
+    big, one, wide = codes(g, 1000, 64).cuda(), torch.ones(1000, device="cuda"), torch.ones(18944, device="cuda")
+    assert native.swiglu_int8_workspace_bytes(1000, 64, 18944) == 2 * 1000 * 64
+    w = codes(g, 64, 18944).cuda()
+    with pytest.raises(native.SwigluError):
+        native.swiglu_forward_int8(big, one, native.swiglu_pack_weights_int8(w, w), 18944, wide, wide,
+                                   workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
     with pytest.raises(native.SwigluError):  # rows of 24 bytes
         native.swiglu_pack_weights_int8(codes(g, 24, 136).cuda(), codes(g, 24, 136).cuda(),
                                         Wpacked=torch.empty(1 << 20, dtype=torch.uint8, device="cuda"))
