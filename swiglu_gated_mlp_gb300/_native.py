@@ -37,6 +37,8 @@ if not os.path.exists(LIB_PATH):
 
 lib = ctypes.CDLL(LIB_PATH)
 
+from . import _torch_calls as _calls  # noqa: E402  (after the library that it uses)
+
 _i64, _vp, _sz, _int, _u32 = ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int, ctypes.c_uint32
 lib.swiglu_packed_weight_bytes.argtypes = [_i64, _i64]
 lib.swiglu_packed_weight_bytes.restype = _sz
@@ -687,12 +689,17 @@ def _typed_output(t, name: str, dtype, shape: tuple, dev: int, stream) -> torch.
     return _new_tensor(shape, dtype, dev, stream) if t is None else _typed(t, name, dtype, shape, dev)
 
 
+# Each 8-bit call first tries torch_calls.cpp, which answers None to all but the common case.
 def swiglu_quantize_int8(X: torch.Tensor, Q: torch.Tensor | None = None,
                          scale: torch.Tensor | None = None, stream=None):
     """(Q [M, K] int8, scale [M] float32) of X [M, K] bf16: X ~ Q * scale, one scale per token.
 
     With m = max(max |x|, 2^-100) over a token's row, scale = m / 127 and Q = 127 x / m, rounded.
     """
+    if Q is None and scale is None and stream is None:
+        done = _calls.quantize_int8(X)
+        if done is not None:
+            return done
     dev = _all_bf16((X,), ("X",))
     if X.dim() != 2:
         raise ValueError("X must be [M, K]")
@@ -787,6 +794,10 @@ def swiglu_forward_int8(A: torch.Tensor, scale_a: torch.Tensor, Wpacked: torch.T
     A [M, K] int8 and scale_a [M] float32, as from swiglu_quantize_int8; scale_w1, scale_w2 [N]
     float32. Without `workspace` (from swiglu_int8_workspace) one is allocated if the call needs it.
     """
+    if Y is None and stream is None:
+        done = _calls.forward_int8(A, scale_a, Wpacked, N, scale_w1, scale_w2, workspace)
+        if done is not None:
+            return done
     dev = _dev_int8(A, "A")
     M, K = A.shape
     _typed(scale_a, "scale_a", torch.float32, (M,), dev)
@@ -815,6 +826,10 @@ def swiglu_down_forward_int8(Y: torch.Tensor, scale_y: torch.Tensor, W3packed: t
 
     Without `workspace` (from swiglu_down_int8_workspace) one is allocated if the call needs it.
     """
+    if Out is None and stream is None:
+        done = _calls.down_forward_int8(Y, scale_y, W3packed, H, scale_w3, R, workspace)
+        if done is not None:
+            return done
     dev = _dev_int8(Y, "Y")
     M, N = Y.shape
     _typed(scale_y, "scale_y", torch.float32, (M,), dev)
@@ -849,6 +864,10 @@ def swiglu_forward_checkpoint(A: torch.Tensor, Wpacked: torch.Tensor, N: int,
     gate, up [M, N] int8; scale [2, ceil(N / 128), M] float32, of Gate and of Up, one per token and
     128 columns: Gate[m, n] ~ gate[m, n] * scale[0, n // 128, m].
     """
+    if Y is None and gate is None and up is None and scale is None and stream is None:
+        done = _calls.forward_checkpoint(A, Wpacked, N)
+        if done is not None:
+            return done
     dev = _all_bf16((A, Wpacked), ("A", "Wpacked"))
     if A.dim() != 2:
         raise ValueError("A must be [M, K]")
@@ -883,6 +902,10 @@ def _checkpoint(gate, up, scale) -> tuple:
 def swiglu_checkpoint_output(gate: torch.Tensor, up: torch.Tensor, scale: torch.Tensor,
                              Y: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Y [M, N] bf16 = SiLU(Gate) * Up of the values that a checkpoint stands for."""
+    if Y is None and stream is None:
+        done = _calls.checkpoint_output(gate, up, scale)
+        if done is not None:
+            return done
     M, N, dev = _checkpoint(gate, up, scale)
     if _cur_device() != dev:
         with torch.cuda.device(dev):
@@ -914,6 +937,10 @@ def swiglu_backward_checkpoint(A: torch.Tensor, Wpacked: torch.Tensor, dY: torch
 
     A [M, K] is bf16, or int8 codes with one scale per token in scale_a [M] (swiglu_quantize_int8).
     """
+    if dA is None and dW1 is None and dW2 is None and need_input and need_weight and stream is None:
+        done = _calls.backward_checkpoint(A, Wpacked, dY, gate, up, scale, scale_a, workspace)
+        if done is not None:
+            return done
     dev = _all_bf16((Wpacked, dY), ("Wpacked", "dY"))
     M, N, at = _checkpoint(gate, up, scale)
     if at != dev:

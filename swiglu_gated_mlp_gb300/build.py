@@ -3,7 +3,9 @@
 Each CUDA translation unit is compiled in parallel into ``_build/`` beside this
 file, then linked into ``libswiglu.so`` in this package directory with the
 CUDA runtime linked statically and only the ``swiglu_*`` symbols exported. A
-stamp of the sources and flags skips the work when nothing changed.
+stamp of the sources and flags skips the work when nothing changed. Beside it
+``torch_calls.cpp`` (Python calls for the installed PyTorch) becomes
+``_torch_calls.so``, which uses libswiglu.so from the same directory.
 
     python -m swiglu_gated_mlp_gb300.build        # build (or check) the library
 """
@@ -14,6 +16,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
@@ -22,12 +25,14 @@ CSRC = os.path.join(PKG_DIR, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG_DIR, "_build")
 LIB_PATH = os.path.join(PKG_DIR, "libswiglu.so")
+CALLS_PATH = os.path.join(PKG_DIR, "_torch_calls.so")
 STAMP = os.path.join(BUILD_DIR, "libswiglu.stamp")
 
 SOURCES = ["swiglu_api.cu", "pack.cu", "fused_large_m.cu", "fused_large_m_pair.cu", "fused_small_m.cu",
            "fused_sequential.cu", "fused_split_k.cu", "fused_resident_pair.cu", "backward_pair.cu",
            "backward_api.cu", "lora_shrink.cu", "lora_api.cu", "quantize.cu", "checkpoint.cu",
            "checkpoint_api.cu", "int8_gemm.cu", "int8_api.cu"]
+CALLS_SOURCE = "torch_calls.cpp"
 HEADERS = ["kernels.h", "ptx.cuh", "lora_lb.cuh", "int8.cuh", "api_shared.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-fvisibility=hidden",
@@ -42,9 +47,24 @@ def _nvcc() -> str:
     raise RuntimeError("nvcc not found: the CUDA toolkit is required to build libswiglu")
 
 
+def _calls_flags() -> tuple:
+    """Compiler and linker flags of _torch_calls.so."""
+    import torch
+    base = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    include = [os.path.join(base, "include"), os.path.join(base, "include/torch/csrc/api/include"),
+               os.path.join(cuda, "include"), sysconfig.get_paths()["include"], INCLUDE]
+    return (["-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"] + ["-I" + i for i in include],
+            ["-L" + os.path.join(base, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+             "-Wl,-rpath," + os.path.join(base, "lib"), "-L" + PKG_DIR, "-l:libswiglu.so", "-Wl,-rpath,$ORIGIN"],
+            torch.__version__ + " " + sysconfig.get_config_var("SOABI"))
+
+
 def _stamp(nvcc: str) -> str:
     h = hashlib.sha256()
-    for name in SOURCES + HEADERS:
+    h.update(repr(_calls_flags()).encode())
+    for name in SOURCES + HEADERS + [CALLS_SOURCE]:
         with open(os.path.join(CSRC, name), "rb") as f:
             h.update(name.encode() + b"\0" + f.read())
     with open(os.path.join(INCLUDE, "swiglu.h"), "rb") as f:
@@ -59,7 +79,7 @@ def build_library(force: bool = False, verbose: bool = False) -> str:
     """Compile and link libswiglu.so if it is missing or stale; return its path."""
     nvcc = _nvcc()
     stamp = _stamp(nvcc)
-    if not force and os.path.exists(LIB_PATH) and os.path.exists(STAMP):
+    if not force and all(os.path.exists(f) for f in (LIB_PATH, CALLS_PATH, STAMP)):
         with open(STAMP) as f:
             if f.read().strip() == stamp:
                 return LIB_PATH
@@ -71,8 +91,19 @@ def build_library(force: bool = False, verbose: bool = False) -> str:
         r = subprocess.run(cmd, capture_output=True, text=True)
         return name, obj, r
 
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    cflags, ldflags, _ = _calls_flags()
+    calls_obj = os.path.join(BUILD_DIR, CALLS_SOURCE.replace(".cpp", ".o"))
+
+    def compile_calls():
+        cmd = ["g++", "-c", os.path.join(CSRC, CALLS_SOURCE), "-o", calls_obj] + cflags
+        return subprocess.run(cmd, capture_output=True, text=True)
+
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        calls = ex.submit(compile_calls)
         results = list(ex.map(compile_one, SOURCES))
+        calls = calls.result()
+    if calls.returncode != 0:
+        raise RuntimeError(f"g++ failed on {CALLS_SOURCE}:\n{calls.stderr}")
     log = []
     for name, _, r in results:
         log.append(f"==== {name}\n{r.stdout}{r.stderr}")
@@ -91,6 +122,11 @@ def build_library(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}{r.stderr}")
     os.replace(tmp, LIB_PATH)
+    tmp = CALLS_PATH + ".tmp"
+    r = subprocess.run(["g++", "-shared", "-o", tmp, calls_obj] + ldflags, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stdout}{r.stderr}")
+    os.replace(tmp, CALLS_PATH)
     with open(STAMP, "w") as f:
         f.write(stamp + "\n")
     if verbose:
