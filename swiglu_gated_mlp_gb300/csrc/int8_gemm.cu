@@ -47,6 +47,7 @@ namespace {
 constexpr int kConvWarps = 8, kEpiWarps8 = 8;
 constexpr int kThreads8 = 32 * (2 + kConvWarps + kEpiWarps8);
 constexpr int kMaxStages8 = 10;
+constexpr int kMaxSplits8 = 8;
 constexpr int kTmem8 = 512;
 constexpr int kBarBytes8 = 768;
 constexpr size_t kSmemLimit8 = 232448;
@@ -582,12 +583,18 @@ __global__ void __launch_bounds__(kThreads8, 1) int8_gemm_kernel(const __grid_co
     for (int i = part * kThreads8 + threadIdx.x; i < mcount * kItems; i += splits * kThreads8) {
       const int m = i / kItems;
       finish4<kDown>(p, m0 + m, un.block, i % kItems, p.scale_x[m0 + m], [&](int r) {
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int k = 0; k < splits; ++k) {
-          const float4 a = ld_shared_cluster_v4(mapa_shared(local, static_cast<uint32_t>(k)) +
-                                                4u * static_cast<uint32_t>(m * kRows8 + r));
-          v.x += a.x; v.y += a.y; v.z += a.z; v.w += a.w;
-        }
+        // all parts' loads before their sum, in rank order
+        float4 a[kMaxSplits8];
+#pragma unroll
+        for (int k = 0; k < kMaxSplits8; ++k)
+          a[k] = ld_shared_cluster_v4(mapa_shared(local, static_cast<uint32_t>(min(k, splits - 1))) +
+                                      4u * static_cast<uint32_t>(m * kRows8 + r));
+        float4 v = a[0];
+#pragma unroll
+        for (int k = 1; k < kMaxSplits8; ++k)
+          if (k < splits) {
+            v.x += a[k].x; v.y += a[k].y; v.z += a[k].z; v.w += a[k].w;
+          }
         return v;
       });
     }
@@ -659,7 +666,7 @@ template <bool kDown, bool kPair>
 cudaError_t configure_t(int* clusters) {
   cudaError_t e = cudaFuncSetAttribute(int8_gemm_kernel<kDown, kPair>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(kSmemLimit8));
-  for (int s = kPair ? 2 : 1; e == cudaSuccess && s <= (kPair ? 2 : 8); ++s) {
+  for (int s = kPair ? 2 : 1; e == cudaSuccess && s <= (kPair ? 2 : kMaxSplits8); ++s) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(s);
     cfg.blockDim = dim3(kThreads8);
@@ -699,7 +706,7 @@ cudaError_t launch_int8_gemm(const Int8Params& p, bool down, cudaStream_t stream
   const bool pair = p.pair != 0;
   const int per = pair ? 2 : p.splits;
   if (p.mt < 16 || p.mt > (pair ? kInt8PairTokens : kInt8Tokens) || (p.mt % 16) != 0 || p.stages < 2 ||
-      p.stages > int8_stages(p.mt, pair) || p.group_m < 1 || p.splits < 1 || p.splits > 8 || p.splits > num_kb ||
+      p.stages > int8_stages(p.mt, pair) || p.group_m < 1 || p.splits < 1 || p.splits > kMaxSplits8 || p.splits > num_kb ||
       p.grid < per || (p.grid % per) != 0 || p.grid / per > units ||
       (!pair && p.splits > 1 && (p.grid / per != units || size_t(p.mt) * kRows8 * 4 > p.stages * stage_bytes8(p.mt, pair))))
     return cudaErrorInvalidValue;

@@ -157,12 +157,14 @@ __device__ __forceinline__ void record_timeout(const WaitCtx& w, uint32_t site) 
 
 static __device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, WaitCtx w,
                                             uint32_t site, bool honour_abort) {
-  const uint64_t t0 = globaltimer_ns();
+  uint64_t t0 = 0;  // read after the first polls: most waits are over by then
   for (uint32_t i = 1;; ++i) {
     if (mbar_try_wait(bar, parity)) return true;
     if ((i & 31u) == 0u) {
       if (honour_abort && *w.abort) return false;
-      if (globaltimer_ns() - t0 > w.timeout_ns) {
+      const uint64_t now = globaltimer_ns();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > w.timeout_ns) {
         record_timeout(w, site);
         return false;
       }
