@@ -82,7 +82,9 @@ swiglu_status_t swiglu_forward_checkpoint(const void* A, const void* Wpacked, vo
   const int64_t tiles_m = (M + 2 * kTileM - 1) / (2 * kTileM), tiles_n = padded_n(N) / kPackBlockN;
   if (tiles_m * tiles_n > 2147483647) return SWIGLU_ERR_UNSUPPORTED;
   LargeMParams p{};
-  if (!encode_2d(&p.tmap_a, A, K, M, K * 2, kBlockK, kTileM, CU_TENSOR_MAP_SWIZZLE_128B) ||
+  const uint32_t box_rows = static_cast<uint32_t>(std::min<int64_t>(kTileM, (M + 15) / 16 * 16));
+  p.keep_a_bytes = static_cast<int>(box_rows) * kBlockK * 2;
+  if (!encode_2d(&p.tmap_a, A, K, M, K * 2, kBlockK, box_rows, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !encode_packed_w(&p.tmap_w, Wpacked, K, N, kPackBlockN) ||
       !encode_2d(&p.tmap_y, Y, N, M, N * 2, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
     return SWIGLU_ERR_CUDA;

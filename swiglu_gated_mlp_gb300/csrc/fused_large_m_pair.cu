@@ -339,10 +339,19 @@ __global__ void __launch_bounds__(PairCfg<kMx, kLora, kKeep>::kThreadsT, 1)
             skip_once = false;  // testing hook: both CTAs leave this stage unfilled
           } else {
             if (one) {
-              if (leader)
-                mbar_arrive_expect_tx(full0 + 8u * s, 2 * (C::kStageBytes + (kMx ? kSfStageBytes : 0)));
               const uint32_t fb = full0_lead + 8u * s;
-              tma_load_2d_pair(sA + s * C::kABytes, &p.tmap_a, fb, kb * kBK, m0);
+              if constexpr (kKeep) {
+                // few tokens: boxes end with the last 16 of them, and a CTA whose rows all lie past
+                // the last token loads none (what the MMA reads there reaches only rows that are not
+                // stored; 1 token, K 3584, N 18944: 63 us with whole boxes, so 45)
+                if (leader)
+                  mbar_arrive_expect_tx(full0 + 8u * s, 2 * C::kBBytes + p.keep_a_bytes * (mb * 2 * kTileM + kTileM < p.M ? 2 : 1));
+                if (m0 < p.M) tma_load_2d_pair(sA + s * C::kABytes, &p.tmap_a, fb, kb * kBK, m0);
+              } else {
+                if (leader)
+                  mbar_arrive_expect_tx(full0 + 8u * s, 2 * (C::kStageBytes + (kMx ? kSfStageBytes : 0)));
+                tma_load_2d_pair(sA + s * C::kABytes, &p.tmap_a, fb, kb * kBK, m0);
+              }
               tma_load_3d_pair(sB + s * C::kBBytes, &p.tmap_w, fb, 0, wrow, wtile + kb);
               if constexpr (kMx) {
                 // this CTA's A rows: block (m0 / 128, kb), 2 rows of 256 bytes; both
@@ -973,7 +982,7 @@ cudaError_t launch_large_m_pair(const LargeMParams& p, cudaStream_t stream) {
   if (p.grid < 2 || (p.grid % 2) != 0 || p.bn != PairCfg<false>::kBN) return cudaErrorInvalidValue;
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg = pair_config(p.grid, stream, attr, pdl_enabled(), p.mx != 0, p.lora != 0, p.keep != 0);
-  if (p.keep && (p.fp8 || p.down || p.lora || !p.keep_gate || !p.keep_up || !p.keep_scale))
+  if (p.keep && (p.keep_a_bytes < 16 * 128 || p.keep_a_bytes > PairCfg<false>::kABytes || p.fp8 || p.down || p.lora || !p.keep_gate || !p.keep_up || !p.keep_scale))
     return cudaErrorInvalidValue;
   if (p.fp8 && p.down) return cudaErrorInvalidValue;  // no FP8 down-projection
   if (p.mx && !p.fp8) return cudaErrorInvalidValue;   // block scales go with E4M3 values

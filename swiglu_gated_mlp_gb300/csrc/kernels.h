@@ -63,6 +63,7 @@ struct LargeMParams {
   void* keep_gate;
   void* keep_up;
   float* keep_scale;
+  int keep_a_bytes;  // of a box of A: 128 rows, or M rounded up to 16 of fewer
 };
 
 struct SmallMParams {
