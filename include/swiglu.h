@@ -421,7 +421,8 @@ SWIGLU_API swiglu_status_t swiglu_down_backward(const void* dOut, const void* W3
  * and its codes mean nothing.
  *
  * swiglu_quantize_int8: X [M, K] bf16 -> Q [M, K] int8 and scale [M] fp32, a
- *   group per token. All device, row-major, 16-byte aligned, none overlapping.
+ *   group per token. All device, row-major, none overlapping; X and Q 16-byte
+ *   aligned, scale 4-byte.
  *   K a multiple of 8. M = 0 is a no-op. Errors as swiglu_forward.
  */
 SWIGLU_API swiglu_status_t swiglu_quantize_int8(const void* X, void* Q, float* scale, int64_t M, int64_t K,
@@ -447,15 +448,14 @@ SWIGLU_API swiglu_status_t swiglu_quantize_int8(const void* X, void* Q, float* s
  *   16 columns of W1 and the same 16 of W2 in turn; its 16-byte pieces c are
  *   stored in the order c ^ (row % 8). Runs once per weight set.
  * swiglu_int8_workspace_bytes, swiglu_down_int8_workspace_bytes: what a call
- *   needs on the current device (0 for few tokens; 2 bytes per token code
- *   beyond). The workspace's contents need no set-up and mean nothing after
- *   the call; calls that may run at the same time need separate ones. NULL
- *   where 0 bytes are needed.
- * swiglu_forward_int8, swiglu_down_forward_int8: device pointers, 16-byte
- *   aligned, outputs and workspace overlapping nothing else but Out R (in
- *   place). R may be NULL. M = 0 is a no-op. K (N for the down-projection) a
- *   multiple of 16, other sizes of 8 (else UNSUPPORTED). Errors as
- *   swiglu_forward.
+ *   needs on the current device: 2 bytes per token code, or 0 for few tokens
+ *   where K (N) is a multiple of 16. The workspace's contents need no set-up
+ *   and mean nothing after the call; calls that may run at the same time need
+ *   separate ones. NULL where 0 bytes are needed.
+ * swiglu_forward_int8, swiglu_down_forward_int8: device pointers, scale_a and
+ *   scale_y 4-byte aligned, the others 16-byte; outputs and workspace overlap
+ *   nothing else but Out R (in place). R may be NULL. M = 0 is a no-op.
+ *   Errors as swiglu_forward.
  * swiglu_plan_string_int8, swiglu_down_plan_string_int8: the launch shape for a
  *   shape on the current device, as text; buf NULL or buflen 0: INVALID_ARG.
  */
@@ -492,8 +492,8 @@ SWIGLU_API swiglu_status_t swiglu_down_plan_string_int8(int64_t M, int64_t N, in
  * error of a half may go either way).
  *
  * swiglu_forward_checkpoint: Y as swiglu_forward (from the fp32 accumulators,
- *   not from the codes), and the checkpoint. All outputs are written in full,
- *   16-byte aligned, overlapping nothing.
+ *   not from the codes), and the checkpoint. All outputs are written in full
+ *   and overlap nothing; scale is 4-byte aligned, the others 16-byte.
  * swiglu_checkpoint_output: Y [M, N] bf16 = SiLU(G) (.) U of the checkpoint's
  *   values, for the down-projection's weight gradient, so that Y need not be
  *   kept. M = 0 is a no-op.

@@ -731,6 +731,13 @@ def _dev_int8(t, name: str) -> int:
     return t.get_device()
 
 
+def _holds_int8(packed, name: str, blocks: int, K: int, dev: int) -> None:
+    """Whether a packed 8-bit weight has room for `blocks` tiles of 32 KB for every 128 of K."""
+    if (not isinstance(packed, torch.Tensor) or packed.get_device() != dev or not packed.is_contiguous()
+            or packed.nbytes < blocks * -(-K // 128) * 32768):
+        raise ValueError(f"{name} does not hold a packed 8-bit weight of this shape on cuda:{dev}")
+
+
 def _pack_int8(weights: tuple, names: tuple, packed, packed_name: str, bytes_fn, call, stream) -> torch.Tensor:
     dev = _dev_int8(weights[0], names[0])
     rows, cols = weights[0].shape
@@ -803,8 +810,7 @@ def swiglu_forward_int8(A: torch.Tensor, scale_a: torch.Tensor, Wpacked: torch.T
     _typed(scale_a, "scale_a", torch.float32, (M,), dev)
     _typed(scale_w1, "scale_w1", torch.float32, (N,), dev)
     _typed(scale_w2, "scale_w2", torch.float32, (N,), dev)
-    if Wpacked.get_device() != dev or not Wpacked.is_contiguous() or Wpacked.nbytes < -(-N // 128) * -(-K // 128) * 32768:
-        raise ValueError("Wpacked does not hold a packed 8-bit weight of this shape")
+    _holds_int8(Wpacked, "Wpacked", -(-N // 128), K, dev)
     if _cur_device() != dev:
         with torch.cuda.device(dev):
             return swiglu_forward_int8(A, scale_a, Wpacked, N, scale_w1, scale_w2, Y, workspace, stream)
@@ -836,8 +842,7 @@ def swiglu_down_forward_int8(Y: torch.Tensor, scale_y: torch.Tensor, W3packed: t
     _typed(scale_w3, "scale_w3", torch.float32, (H,), dev)
     if R is not None:
         _typed(R, "R", _BF16, (M, H), dev)
-    if W3packed.get_device() != dev or not W3packed.is_contiguous() or W3packed.nbytes < -(-H // 256) * -(-N // 128) * 32768:
-        raise ValueError("W3packed does not hold a packed 8-bit weight of this shape")
+    _holds_int8(W3packed, "W3packed", -(-H // 256), N, dev)
     if _cur_device() != dev:
         with torch.cuda.device(dev):
             return swiglu_down_forward_int8(Y, scale_y, W3packed, H, scale_w3, R, Out, workspace, stream)

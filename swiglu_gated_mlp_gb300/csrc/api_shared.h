@@ -75,6 +75,9 @@ inline bool any_overlap(const Span* out, int outs, const Span* in, int ins) {
   return false;
 }
 
+// A vector of floats that is read and written one by one.
+inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
 // Scales of Gate and Up kept in 8 bits: one of each per token and 128 columns.
 inline size_t checkpoint_scales(int64_t M, int64_t N) { return 2 * size_t(M) * size_t((N + 127) / 128); }
 

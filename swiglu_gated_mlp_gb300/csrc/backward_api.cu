@@ -355,8 +355,8 @@ swiglu_status_t swiglu_backward_checkpoint(const void* A, const float* scale_a, 
   // the packed weight for dA, the input for dW1 and dW2
   if (!dY || !gate || !up || !scale || !workspace || (dA && !Wpacked) || (dW1 && !A))
     return SWIGLU_ERR_INVALID_ARG;
-  if ((dW1 && (!aligned16(A) || (scale_a && !aligned16(scale_a)))) || (dA && !aligned16(Wpacked)) ||
-      !aligned16(dY) || !aligned16(gate) || !aligned16(up) || !aligned16(scale) || !aligned16(workspace))
+  if ((dW1 && (!aligned16(A) || (scale_a && !aligned4(scale_a)))) || (dA && !aligned16(Wpacked)) ||
+      !aligned16(dY) || !aligned16(gate) || !aligned16(up) || !aligned4(scale) || !aligned16(workspace))
     return SWIGLU_ERR_INVALID_ARG;
   const Span in[7] = {{dW1 ? A : nullptr, a_bytes},
                       {dW1 ? scale_a : nullptr, size_t(M) * 4},

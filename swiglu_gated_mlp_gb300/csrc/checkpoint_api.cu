@@ -51,7 +51,7 @@ swiglu_status_t swiglu_quantize_int8(const void* X, void* Q, float* scale, int64
   swiglu_status_t st = swg::api::check_shape(M, K, 8);
   if (st != SWIGLU_OK || M == 0) return st;
   if (!X || !Q || !scale) return SWIGLU_ERR_INVALID_ARG;
-  if (!aligned16(X) || !aligned16(Q) || !aligned16(scale)) return SWIGLU_ERR_INVALID_ARG;
+  if (!aligned16(X) || !aligned16(Q) || !aligned4(scale)) return SWIGLU_ERR_INVALID_ARG;
   const Span in[1] = {{X, size_t(M) * size_t(K) * 2}};
   const Span out[2] = {{Q, size_t(M) * size_t(K)}, {scale, size_t(M) * 4}};
   if (any_overlap(out, 2, in, 1)) return SWIGLU_ERR_INVALID_ARG;
@@ -69,7 +69,7 @@ swiglu_status_t swiglu_forward_checkpoint(const void* A, const void* Wpacked, vo
   if (st != SWIGLU_OK || M == 0) return st;
   if (!A || !Wpacked || !Y || !gate || !up || !scale) return SWIGLU_ERR_INVALID_ARG;
   if (!aligned16(A) || !aligned16(Wpacked) || !aligned16(Y) || !aligned16(gate) || !aligned16(up) ||
-      !aligned16(scale))
+      !aligned4(scale))
     return SWIGLU_ERR_INVALID_ARG;
   const size_t codes = size_t(M) * size_t(N);
   const Span in[2] = {{A, size_t(M) * size_t(K) * 2}, {Wpacked, swiglu_packed_weight_bytes(K, N)}};
@@ -112,7 +112,7 @@ swiglu_status_t swiglu_checkpoint_output(const void* gate, const void* up, const
   swiglu_status_t st = swg::api::check_shape(M, 8, N);
   if (st != SWIGLU_OK || M == 0) return st;
   if (!gate || !up || !scale || !Y) return SWIGLU_ERR_INVALID_ARG;
-  if (!aligned16(gate) || !aligned16(up) || !aligned16(scale) || !aligned16(Y)) return SWIGLU_ERR_INVALID_ARG;
+  if (!aligned16(gate) || !aligned16(up) || !aligned4(scale) || !aligned16(Y)) return SWIGLU_ERR_INVALID_ARG;
   const size_t codes = size_t(M) * size_t(N);
   const Span in[3] = {{gate, codes}, {up, codes}, {scale, checkpoint_scales(M, N) * 4}};
   const Span out[1] = {{Y, codes * 2}};

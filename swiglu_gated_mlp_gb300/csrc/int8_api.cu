@@ -106,14 +106,10 @@ Int8Plan make_plan(int64_t M, int64_t K, int64_t N, bool down, int sms, const In
   int64_t cta_cost = 0, pair_cost = 0;
   const Int8Plan on_ctas = cta_plan(M, slices, halves, sms, s, &cta_cost);
   if (s.pairs < 1) return on_ctas;
+  // rows of codes that do not start on 16 bytes cannot be loaded as such: widened first, they do
+  const bool by_rows = K % 16 == 0;
   const Int8Plan on_pairs = pair_plan(M, K, slices, halves, s, &pair_cost);
-  return pair_cost < cta_cost ? on_pairs : on_ctas;
-}
-
-swiglu_status_t check(int64_t M, int64_t K, int64_t N) {
-  const swiglu_status_t st = swg::api::check_shape(M, K, N);
-  if (st != SWIGLU_OK) return st;
-  return K % 16 == 0 ? SWIGLU_OK : SWIGLU_ERR_UNSUPPORTED;  // 16-byte rows of codes
+  return !by_rows || pair_cost < cta_cost ? on_pairs : on_ctas;
 }
 
 size_t packed_bytes(int64_t K, int64_t N, bool down) {
@@ -123,7 +119,7 @@ size_t packed_bytes(int64_t K, int64_t N, bool down) {
 
 swiglu_status_t pack(const void* w1, const void* w2, void* wp, int64_t K, int64_t N, bool down,
                      swiglu_stream_t stream) {
-  swiglu_status_t st = check(0, K, N);
+  swiglu_status_t st = swg::api::check_shape(0, K, N);
   if (st != SWIGLU_OK) return st;
   if (!w1 || !w2 || !wp) return SWIGLU_ERR_INVALID_ARG;
   if (!aligned16(w1) || !aligned16(w2) || !aligned16(wp)) return SWIGLU_ERR_INVALID_ARG;
@@ -138,7 +134,7 @@ swiglu_status_t pack(const void* w1, const void* w2, void* wp, int64_t K, int64_
 }
 
 size_t workspace_for(int64_t M, int64_t K, int64_t N, bool down) {
-  if (check(M, K, N) != SWIGLU_OK || M == 0) return 0;
+  if (swg::api::check_shape(M, K, N) != SWIGLU_OK || M == 0) return 0;
   DeviceView d;
   const Int8State* s = nullptr;
   if (int8_device(&d, &s) != SWIGLU_OK) return 0;
@@ -149,10 +145,10 @@ size_t workspace_for(int64_t M, int64_t K, int64_t N, bool down) {
 swiglu_status_t project(const void* x, const float* scale_x, const void* wp, const float* scale0,
                         const float* scale1, const void* residual, void* y, int64_t M, int64_t K, int64_t N,
                         bool down, void* workspace, size_t workspace_bytes, swiglu_stream_t stream) {
-  swiglu_status_t st = check(M, K, N);
+  swiglu_status_t st = swg::api::check_shape(M, K, N);
   if (st != SWIGLU_OK || M == 0) return st;
   if (!x || !scale_x || !wp || !scale0 || !scale1 || !y) return SWIGLU_ERR_INVALID_ARG;
-  if (!aligned16(x) || !aligned16(scale_x) || !aligned16(wp) || !aligned16(scale0) || !aligned16(scale1) ||
+  if (!aligned16(x) || !aligned4(scale_x) || !aligned16(wp) || !aligned16(scale0) || !aligned16(scale1) ||
       !aligned16(y) || (residual && !aligned16(residual)) || (workspace && !aligned16(workspace)))
     return SWIGLU_ERR_INVALID_ARG;
   const size_t y_bytes = size_t(M) * size_t(N) * 2;
@@ -169,7 +165,7 @@ swiglu_status_t project(const void* x, const float* scale_x, const void* wp, con
   st = int8_device(&d, &s);
   if (st != SWIGLU_OK) return st;
   const Int8Plan pl = make_plan(M, K, N, down, d.sm_count, *s);
-  if (pl.blocks * pl.mgroups > kMaxUnits) return SWIGLU_ERR_UNSUPPORTED;
+  if (pl.blocks * pl.mgroups > kMaxUnits || (!pl.pair && K % 16 != 0)) return SWIGLU_ERR_UNSUPPORTED;
   const size_t need = pl.workspace(M, K);
   if (need > 0 && (!workspace || workspace_bytes < need)) return SWIGLU_ERR_INVALID_ARG;
   const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
@@ -209,7 +205,7 @@ swiglu_status_t project(const void* x, const float* scale_x, const void* wp, con
 swiglu_status_t plan_string(const char* what, int64_t M, int64_t K, int64_t N, bool down, char* buf, size_t buflen) {
   if (!buf || buflen == 0) return SWIGLU_ERR_INVALID_ARG;
   buf[0] = '\0';
-  swiglu_status_t st = check(M, K, N);
+  swiglu_status_t st = swg::api::check_shape(M, K, N);
   if (st != SWIGLU_OK) return st;
   DeviceView d;
   const Int8State* s = nullptr;
@@ -227,7 +223,7 @@ swiglu_status_t plan_string(const char* what, int64_t M, int64_t K, int64_t N, b
 extern "C" {
 
 size_t swiglu_packed_weight_bytes_int8(int64_t K, int64_t N) {
-  return check(0, K, N) == SWIGLU_OK ? packed_bytes(K, N, false) : 0;
+  return swg::api::check_shape(0, K, N) == SWIGLU_OK ? packed_bytes(K, N, false) : 0;
 }
 
 swiglu_status_t swiglu_pack_weights_int8(const void* W1, const void* W2, void* Wpacked, int64_t K, int64_t N,
@@ -249,7 +245,7 @@ swiglu_status_t swiglu_plan_string_int8(int64_t M, int64_t K, int64_t N, char* b
 }
 
 size_t swiglu_down_packed_bytes_int8(int64_t N, int64_t H) {
-  return check(0, N, H) == SWIGLU_OK ? packed_bytes(N, H, true) : 0;
+  return swg::api::check_shape(0, N, H) == SWIGLU_OK ? packed_bytes(N, H, true) : 0;
 }
 
 swiglu_status_t swiglu_pack_down_weights_int8(const void* W3, void* W3packed, int64_t N, int64_t H,

@@ -617,9 +617,16 @@ __global__ void __launch_bounds__(kThreads8, 1) int8_gemm_kernel(const __grid_co
 }
 
 // Codes as fp16 values, 16 a thread and step.
-__global__ void __launch_bounds__(256) widen_kernel(const uint4* codes, uint4* out, size_t items) {
+__global__ void __launch_bounds__(256) widen_kernel(const uint4* codes, uint4* out, size_t items, int tail) {
   pdl_launch_dependents();
   pdl_wait();
+  if (tail && blockIdx.x == 0 && threadIdx.x == 0) {  // the last 8
+    const uint2 v = *reinterpret_cast<const uint2*>(codes + items);
+    uint32_t w[4];
+    widen4(v.x ^ 0x80808080u, w[0], w[1]);
+    widen4(v.y ^ 0x80808080u, w[2], w[3]);
+    out[2 * items] = make_uint4(w[0], w[1], w[2], w[3]);
+  }
   for (size_t i = blockIdx.x * size_t(256) + threadIdx.x; i < items; i += size_t(gridDim.x) * 256) {
     const uint4 v = ld_global_v4(codes + i);
     uint32_t w[8];
@@ -734,7 +741,7 @@ cudaError_t launch_int8_gemm(const Int8Params& p, bool down, cudaStream_t stream
 }
 
 cudaError_t launch_widen(const void* codes, void* out, size_t values, cudaStream_t stream) {
-  const size_t items = values / 16, blocks = (items + 255) / 256;
+  const size_t items = values / 16, blocks = items > 0 ? (items + 255) / 256 : 1;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(blocks < 152 * 8 ? blocks : 152 * 8));
   cfg.blockDim = dim3(256);
@@ -745,7 +752,7 @@ cudaError_t launch_widen(const void* codes, void* out, size_t values, cudaStream
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, widen_kernel, static_cast<const uint4*>(codes),
-                                           static_cast<uint4*>(out), items);
+                                           static_cast<uint4*>(out), items, static_cast<int>(values % 16 / 8));
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 

@@ -257,7 +257,7 @@ struct Int8Params {
 cudaError_t configure_int8(int (&clusters)[9], int* pairs);
 int int8_stages(int mt, bool pair);
 cudaError_t launch_int8_gemm(const Int8Params& p, bool down, cudaStream_t stream);
-// int8 codes as fp16 values; `values` a multiple of 16.
+// int8 codes as fp16 values; `values` a multiple of 8.
 cudaError_t launch_widen(const void* codes, void* out, size_t values, cudaStream_t stream);
 // Weight codes to packed tiles of 256 x 128 biased codes: gate and up, or W3 (down).
 cudaError_t launch_pack_int8(const void* w1, const void* w2, void* wp, int K, int N, bool down,

@@ -41,7 +41,7 @@ def test_bad_shapes(native_lib, M, K, N, want):
 
 @pytest.mark.parametrize("call,change", [
     (quantise, {"X": None}), (quantise, {"Q": None}), (quantise, {"scale": None}), (quantise, {"X": at(0) + 2}),
-    (quantise, {"Q": at(1) + 8}), (quantise, {"scale": at(2) + 4}), (quantise, {"Q": at(0) + 64}),
+    (quantise, {"Q": at(1) + 8}), (quantise, {"scale": at(2) + 2}), (quantise, {"Q": at(0) + 64}),
     (quantise, {"scale": at(1)}),
     (forward, {"A": None}), (forward, {"Wp": None}), (forward, {"Y": None}), (forward, {"gate": None}),
     (forward, {"up": None}), (forward, {"scale": None}), (forward, {"gate": at(3) + 8}), (forward, {"up": at(3)}),
@@ -50,7 +50,7 @@ def test_bad_shapes(native_lib, M, K, N, want):
     (output, {"Y": at(3) + 2}), (output, {"up": at(1) + 8}),
     (backward, {"A": None}), (backward, {"Wp": None}), (backward, {"dY": None}), (backward, {"gate": None}),
     (backward, {"up": None}), (backward, {"scale": None}), (backward, {"ws": None}), (backward, {"dW1": None}),
-    (backward, {"dW2": None}), (backward, {"sa": at(10) + 4}), (backward, {"A": at(0) + 8}),
+    (backward, {"dW2": None}), (backward, {"sa": at(10) + 2}), (backward, {"A": at(0) + 8}),
     (backward, {"dA": at(0)}), (backward, {"dA": at(3)}), (backward, {"dW1": at(10)}), (backward, {"ws": at(5)}),
     (backward, {"dW2": at(7) + 16}), (backward, {"ws": at(9) + 8}),
 ])

@@ -377,6 +377,53 @@ def test_refusals(native):
                                           workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
     with pytest.raises(native.SwigluError):  # an output that is an input
         native.swiglu_backward_checkpoint(a, wp, dy, gate, up, scale, dA=a)
-    with pytest.raises(native.SwigluError):
+    with pytest.raises(native.SwigluError):  # rows that start at 8 bytes
         native.swiglu_checkpoint_output(gate, up, scale, Y=torch.empty(4, 136 + 8, dtype=torch.bfloat16,
                                                                       device="cuda").view(-1)[4:4 + 4 * 136].view(4, 136))
+
+
+@pytest.mark.parametrize("M", [16, 300])
+def test_a_stalled_pipeline_is_reported(native, M):
+    K, N = 512, 264
+    a, w1, w2, dy, ck = gradient_inputs(M, K, N, 2)
+    a, dy, ck = a.cuda(), dy.cuda(), [t.cuda() for t in ck]
+    wp = native.swiglu_pack_weights(w1.cuda(), w2.cuda())
+    want = native.swiglu_forward_checkpoint(a, wp, N), native.swiglu_backward_checkpoint(a, wp, dy, *ck)
+    native.swiglu_check_device_status()
+    for call in (lambda: native.swiglu_forward_checkpoint(a, wp, N),
+                 lambda: native.swiglu_backward_checkpoint(a, wp, dy, *ck)):
+        native.swiglu_testing_inject_stall(True, 20)
+        try:
+            call()
+            with pytest.raises(native.SwigluError) as e:
+                native.swiglu_check_device_status()
+            assert e.value.code == native.SWIGLU_ERR_TIMEOUT
+        finally:
+            native.swiglu_testing_inject_stall(False, 1000)
+        native.swiglu_check_device_status()
+    got = native.swiglu_forward_checkpoint(a, wp, N), native.swiglu_backward_checkpoint(a, wp, dy, *ck)
+    for x, y in zip(want, got):
+        assert all(torch.equal(p, q) for p, q in zip(x, y))
+
+
+def test_many_tiles_of_many_slices(native):
+    # several rounds of tiles for each pair of CTAs, each a long sum: the checkpoint of a workload's
+    # shape on sampled rows and columns, and calls in a row with nothing between them
+    M, K, N = 1024, 3584, 18944
+    a, w1, w2 = make_inputs(M, K, N, 3)
+    wp = native.swiglu_pack_weights(w1.cuda(), w2.cuda())
+    first = native.swiglu_forward_checkpoint(a.cuda(), wp, N)
+    ad = a.cuda()
+    for _ in range(20):
+        last = native.swiglu_forward_checkpoint(ad, wp, N)
+        restored = native.swiglu_checkpoint_output(*last[1:])
+    native.swiglu_check_device_status()
+    assert all(torch.equal(x, y) for x, y in zip(first, last))
+    rows = np.unique(np.random.default_rng(0).integers(0, M, 12))
+    at = torch.from_numpy(rows).cuda()
+    for w, codes, s in ((w1, last[1], last[3][0]), (w2, last[2], last[3][1])):
+        x, step = f64(a[rows]) @ f64(w), ref.wide(f64(s[:, at]), N)
+        err = K * FP32 * (abs(f64(a[rows])) @ abs(f64(w)))
+        assert (abs(f64(codes[at]) * step - x) <= (0.5 + 127 * 2 * FP32) * step + err).all()
+    g, u = (f64(c[at]) * ref.wide(f64(s[:, at]), N) for c, s in ((last[1], last[3][0]), (last[2], last[3][1])))
+    assert_within(restored[at], *ref.gated(g, FP32 * abs(g), u, FP32 * abs(u)))

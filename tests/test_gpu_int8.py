@@ -42,7 +42,7 @@ def scales(g, n, size):
 # groups that fill no tile; K below and past a slice, N below and past a block, K split over clusters
 SHAPES = [(1, 16, 8), (1, 896, 4864), (2, 144, 24), (16, 3584, 264), (17, 48, 136), (33, 1424, 1000), (64, 128, 128),
           (65, 128, 264), (100, 272, 520), (128, 896, 1000), (129, 144, 392), (333, 1424, 5000), (513, 2048, 264),
-          (1025, 16, 136), (3, 18944, 40), (200, 18944, 136)]
+          (1025, 16, 136), (3, 18944, 40), (200, 18944, 136), (1, 8, 8), (5, 72, 136), (33, 520, 264), (301, 1416, 5000)]
 
 
 @pytest.mark.parametrize("M,K,N", SHAPES)
@@ -310,6 +310,62 @@ def test_refusals(native):
     with pytest.raises(native.SwigluError):
         native.swiglu_forward_int8(big, one, native.swiglu_pack_weights_int8(w, w), 18944, wide, wide,
                                    workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
-    with pytest.raises(native.SwigluError):  # rows of 24 bytes
-        native.swiglu_pack_weights_int8(codes(g, 24, 136).cuda(), codes(g, 24, 136).cuda(),
-                                        Wpacked=torch.empty(1 << 20, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("M", [7, 300])
+def test_part_of_a_batch(native, M):
+    # tokens from the third on, as views: codes start on a row, scales on any float
+    K, N = 144, 264
+    g = torch.Generator().manual_seed(3)
+    a, w, r = codes(g, M, K).cuda(), codes(g, K, N).cuda(), make_inputs(M, N, 8, 3)[0].cuda()
+    sa, s = scales(g, M, 0.02).cuda(), scales(g, N, 0.01).cuda()
+    wp, w3p = native.swiglu_pack_weights_int8(w, w), native.swiglu_pack_down_weights_int8(w)
+    assert torch.equal(native.swiglu_forward_int8(a[3:], sa[3:], wp, N, s, s),
+                       native.swiglu_forward_int8(a, sa, wp, N, s, s)[3:])
+    assert torch.equal(native.swiglu_down_forward_int8(a[3:], sa[3:], w3p, N, s, R=r[3:].clone()),
+                       native.swiglu_down_forward_int8(a, sa, w3p, N, s, R=r)[3:])
+
+
+def test_the_common_case_and_the_others_agree(native):
+    # outputs given, a stream given, a subclass of Tensor: checked and called in Python
+    class Mine(torch.Tensor):
+        pass
+
+    M, K, N = 40, 272, 264
+    g = torch.Generator().manual_seed(4)
+    x = make_inputs(M, K, 8, 5)[0].cuda()
+    w, s = codes(g, K, N).cuda(), scales(g, N, 0.01).cuda()
+    wp = native.swiglu_pack_weights_int8(w, w)
+    q, sa = native.swiglu_quantize_int8(x)
+    y = native.swiglu_forward_int8(q, sa, wp, N, s, s)
+    for q2, sa2 in (native.swiglu_quantize_int8(x, Q=torch.empty_like(q)),
+                    native.swiglu_quantize_int8(x, stream=torch.cuda.current_stream()),
+                    native.swiglu_quantize_int8(x.as_subclass(Mine))):
+        assert torch.equal(q, q2) and torch.equal(sa, sa2)
+    for y2 in (native.swiglu_forward_int8(q, sa, wp, N, s, s, Y=torch.empty_like(y)),
+               native.swiglu_forward_int8(q, sa, wp, N, s, s, stream=torch.cuda.current_stream()),
+               native.swiglu_forward_int8(q, sa, wp, np.int64(N), s, s)):
+        assert torch.equal(y, y2)
+    with pytest.raises(TypeError):
+        native.swiglu_quantize_int8()
+    with pytest.raises(ValueError):
+        native.swiglu_quantize_int8(3)
+
+
+def test_one_workspace_in_stream_order(native):
+    # calls of several shapes take turns on one workspace
+    K, N, H = 272, 4096, 264
+    g = torch.Generator().manual_seed(6)
+    w, w3 = codes(g, K, N).cuda(), codes(g, N, H).cuda()
+    s, s3 = scales(g, N, 0.01).cuda(), scales(g, H, 0.01).cuda()
+    wp, w3p = native.swiglu_pack_weights_int8(w, w), native.swiglu_pack_down_weights_int8(w3)
+    runs = []
+    for M in (2000, 1100, 3):
+        a, y, sa = codes(g, M, K).cuda(), codes(g, M, N).cuda(), scales(g, M, 0.02).cuda()
+        runs.append((lambda ws, a=a, sa=sa: native.swiglu_forward_int8(a, sa, wp, N, s, s, workspace=ws)))
+        runs.append((lambda ws, y=y, sa=sa: native.swiglu_down_forward_int8(y, sa, w3p, H, s3, workspace=ws)))
+    need = max(native.swiglu_int8_workspace_bytes(2000, K, N), native.swiglu_down_int8_workspace_bytes(2000, N, H))
+    shared = torch.empty(max(need, 16), dtype=torch.uint8, device="cuda")
+    want = [f(None) for f in runs]
+    got = [f(shared) for _ in range(3) for f in runs]
+    assert all(torch.equal(a, b) for a, b in zip(got, want * 3))
