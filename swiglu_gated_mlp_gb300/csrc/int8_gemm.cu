@@ -206,6 +206,8 @@ __global__ void __launch_bounds__(kThreads8, 1) int8_gemm_kernel(const __grid_co
     return static_cast<const uint8_t*>(p.w) + (static_cast<size_t>(ub >> 1) * num_kb + kb) * (2 * kWBytes) +
            (ub & 1) * kWBytes;
   };
+  // warps that widen tokens: 16 codes a lane and stage
+  const int tok_warps = min(kEpiWarps8, mt / 4);
   // the even CTA's barriers, as seen from either CTA of a pair
   const uint32_t ready0_lead = kPair ? mapa_shared(ready0, 0) : ready0;
   const uint32_t tempty0_lead = kPair ? mapa_shared(tempty0, 0) : tempty0;
@@ -215,7 +217,7 @@ __global__ void __launch_bounds__(kThreads8, 1) int8_gemm_kernel(const __grid_co
     for (int s = 0; s < stages; ++s) {
       mbar_init(full0 + 8u * s, 1);
       // the converting warps (of both CTAs), and the ones that widen tokens, or the even producer
-      mbar_init(ready0 + 8u * s, kPair ? 2 * kConvWarps + 1 : kConvWarps + kEpiWarps8);
+      mbar_init(ready0 + 8u * s, kPair ? 2 * kConvWarps + 1 : kConvWarps + tok_warps);
       mbar_init(done0 + 8u * s, 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -429,13 +431,13 @@ __global__ void __launch_bounds__(kThreads8, 1) int8_gemm_kernel(const __grid_co
     for (int u = first; ok && u < units; u += step) {
       const Unit un = unit_of(p, u);
       if constexpr (!kPair) {
-        for (int kb = kb_begin; kb < kb_end; ++kb) {
+        for (int kb = kb_begin; ew < tok_warps && kb < kb_end; ++kb) {
           if (!mbar_wait_warp(full0 + 8u * s, ph, wc, kSiteConvert)) {
             ok = false;
             break;
           }
           const uint32_t sx = s0 + s * stage_bytes + kWBytes, raw = sx + x_bytes;
-          for (int i = tid; i < mt * 8; i += 32 * kEpiWarps8) {
+          for (int i = tid; i < mt * 8; i += 32 * tok_warps) {
             const int r = i >> 3, c = i & 7;  // 16 codes of token r
             const uint4 v = ld_shared_v4(raw + r * 128 + ((c ^ (r & 7)) << 4));
             uint32_t w[8];
