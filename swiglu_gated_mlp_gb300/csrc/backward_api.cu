@@ -215,10 +215,12 @@ swiglu_status_t no_tokens(void* dW1, void* dW2, size_t w_bytes, cudaStream_t cs)
   return st == SWIGLU_OK ? zero(dW2, w_bytes, cs) : st;
 }
 
-// dA, dW1 and dW2 (null: not asked for) from dG and dU.
-swiglu_status_t gate_up_gradients(const void* A, const void* Wpacked, const void* dG, const void* dU, void* dA,
-                                  void* dW1, void* dW2, int64_t M, int64_t K, int64_t N, GradientPlan g,
-                                  uint8_t* parts, const DeviceView& d, int pairs, cudaStream_t cs) {
+// dA, dW1 and dW2 (null: not asked for) from dG and dU, whose rows hold the factors of
+// `row_scale` (null: none), which dA's lose again.
+swiglu_status_t gate_up_gradients(const void* A, const void* Wpacked, const void* dG, const void* dU,
+                                  const float* row_scale, void* dA, void* dW1, void* dW2, int64_t M, int64_t K,
+                                  int64_t N, GradientPlan g, uint8_t* parts, const DeviceView& d, int pairs,
+                                  cudaStream_t cs) {
   BackwardParams p{};
   ReduceParams sums{};
   deal_units(&g, dA != nullptr, dW1 != nullptr, pairs, &p);
@@ -226,6 +228,7 @@ swiglu_status_t gate_up_gradients(const void* A, const void* Wpacked, const void
   if (dA) {
     fill(&p.in, g.in, M, K, M);
     p.in.two = 1;
+    p.in.row_scale = row_scale;
     p.in.col_slices = static_cast<int>(k_slices(K));
     if (!encode_operand(&p.in.tmap_a0, dG, M, N) ||
         !encode_operand(&p.in.tmap_a1, dU, M, N) ||
@@ -326,7 +329,7 @@ swiglu_status_t swiglu_backward(const void* A, const void* Wpacked, const void* 
     st = launched(launch_backward_pair(p, true, std::min(p.in_units, pairs), cs));
     if (st != SWIGLU_OK) return st;
   }
-  return gate_up_gradients(A, Wpacked, dG, dU, dA, dW1, dW2, M, K, N, pl.gradients, parts, d, pairs, cs);
+  return gate_up_gradients(A, Wpacked, dG, dU, nullptr, dA, dW1, dW2, M, K, N, pl.gradients, parts, d, pairs, cs);
 }
 
 size_t swiglu_backward_checkpoint_workspace_bytes(int64_t M, int64_t K, int64_t N) {
@@ -355,11 +358,11 @@ swiglu_status_t swiglu_backward_checkpoint(const void* A, const float* scale_a, 
   // the packed weight for dA, the input for dW1 and dW2
   if (!dY || !gate || !up || !scale || !workspace || (dA && !Wpacked) || (dW1 && !A))
     return SWIGLU_ERR_INVALID_ARG;
-  if ((dW1 && (!aligned16(A) || (scale_a && !aligned4(scale_a)))) || (dA && !aligned16(Wpacked)) ||
+  if ((dW1 && !aligned16(A)) || (scale_a && !aligned4(scale_a)) || (dA && !aligned16(Wpacked)) ||
       !aligned16(dY) || !aligned16(gate) || !aligned16(up) || !aligned4(scale) || !aligned16(workspace))
     return SWIGLU_ERR_INVALID_ARG;
   const Span in[7] = {{dW1 ? A : nullptr, a_bytes},
-                      {dW1 ? scale_a : nullptr, size_t(M) * 4},
+                      {scale_a, size_t(M) * 4},
                       {dA ? Wpacked : nullptr, swiglu_packed_weight_bytes(K, N)},
                       {dY, codes * 2},
                       {gate, codes},
@@ -385,15 +388,15 @@ swiglu_status_t swiglu_backward_checkpoint(const void* A, const float* scale_a, 
   c.M = static_cast<int>(M);
   c.N = static_cast<int>(N);
   c.K = static_cast<int>(K);
+  c.a_scale = scale_a;
   if (scale_a && dW1) {
     c.a_codes = A;
-    c.a_scale = scale_a;
     c.a_out = ws + 2 * pl.grad_bytes;
     A = c.a_out;
   }
   st = launched(launch_checkpoint(c, true, cs));
   if (st != SWIGLU_OK) return st;
-  return gate_up_gradients(A, Wpacked, c.out0, c.out1, dA, dW1, dW2, M, K, N, pl.gradients,
+  return gate_up_gradients(A, Wpacked, c.out0, c.out1, c.a_scale, dA, dW1, dW2, M, K, N, pl.gradients,
                            ws + 2 * pl.grad_bytes + pl.input_bytes, d, pairs, cs);
 }
 

@@ -63,6 +63,7 @@
 // another (9, 15 and 4 us alone).
 #include <type_traits>
 
+#include "int8.cuh"
 #include "kernels.h"
 #include "ptx.cuh"
 
@@ -131,7 +132,7 @@ __device__ __forceinline__ void grad_unit(const BackwardParams& p, int u, int& t
   off = h < 0 ? 0 : (h & 1) * (kPackBlockN / 2);
 }
 
-template <bool kGrad>
+template <bool kGrad, bool kScaled>
 __global__ void __launch_bounds__(kBackThreads, 1)
     backward_pair_kernel(const __grid_constant__ BackwardParams p) {
   extern __shared__ uint8_t smem_raw[];
@@ -475,6 +476,10 @@ __global__ void __launch_bounds__(kBackThreads, 1)
         // this warp's 128 columns, 64 at a time: fp32 parts (32 columns, 128-byte
         // rows, a store) to the workspace, or 64 bf16 columns to the output
         const bool parts = pr.splits > 1;
+        // kScaled: the rows of dG and dU came with a factor of their token's (checkpoint.cu)
+        float by = 1.0f;
+        if (kScaled && !weight && row0 + lane < pr.rows)
+          by = 1.0f / split_scale(pr.row_scale[row0 + lane]).factor;
 #pragma unroll 1
         for (int c = 0; c < 2; ++c) {
           uint32_t x[32], y[32];
@@ -483,6 +488,13 @@ __global__ void __launch_bounds__(kBackThreads, 1)
           tmem_wait_ld();
           reg_fence(x);
           reg_fence(y);
+          if constexpr (kScaled) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              x[i] = __float_as_uint(__uint_as_float(x[i]) * by);
+              y[i] = __float_as_uint(__uint_as_float(y[i]) * by);
+            }
+          }
           if (c == 1) {
             tc_fence_before();
             __syncwarp();
@@ -613,21 +625,22 @@ bool valid_grad(const BackwardParams& p) {
          valid(p.in, p.full_units + halves / 2);
 }
 
-template <bool kGrad>
+template <bool kGrad, bool kScaled>
 cudaError_t set_smem() {
-  return cudaFuncSetAttribute(backward_pair_kernel<kGrad>,
+  return cudaFuncSetAttribute(backward_pair_kernel<kGrad, kScaled>,
                               cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem));
 }
 
 }  // namespace
 
 cudaError_t configure_backward_pair(int* max_pairs) {
-  cudaError_t e = set_smem<true>();
-  if (e == cudaSuccess) e = set_smem<false>();
+  cudaError_t e = set_smem<true, false>();
+  if (e == cudaSuccess) e = set_smem<false, false>();
+  if (e == cudaSuccess) e = set_smem<false, true>();
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg = backward_config(2, nullptr, attr, false);
-  return cudaOccupancyMaxActiveClusters(max_pairs, backward_pair_kernel<true>, &cfg);
+  return cudaOccupancyMaxActiveClusters(max_pairs, backward_pair_kernel<true, false>, &cfg);
 }
 
 cudaError_t launch_backward_pair(const BackwardParams& p, bool grad, int pairs, cudaStream_t stream) {
@@ -638,8 +651,9 @@ cudaError_t launch_backward_pair(const BackwardParams& p, bool grad, int pairs, 
     return cudaErrorInvalidValue;
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg = backward_config(2 * pairs, stream, attr, pdl_enabled());
-  const cudaError_t e = grad ? cudaLaunchKernelEx(&cfg, backward_pair_kernel<true>, p)
-                             : cudaLaunchKernelEx(&cfg, backward_pair_kernel<false>, p);
+  const cudaError_t e = grad             ? cudaLaunchKernelEx(&cfg, backward_pair_kernel<true, false>, p)
+                        : p.in.row_scale ? cudaLaunchKernelEx(&cfg, backward_pair_kernel<false, true>, p)
+                                         : cudaLaunchKernelEx(&cfg, backward_pair_kernel<false, false>, p);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 

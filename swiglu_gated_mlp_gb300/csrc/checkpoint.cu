@@ -3,8 +3,12 @@
 // a warp of the forward's epilogue, thread = token, writes 32 of them in one line).
 //   checkpoint_output  Y = SiLU(g) u, for the down-projection's weight gradient
 //   checkpoint_grads   dG and dU from dY, in bf16 for the tensor-core products that
-//                      follow (backward_pair.cu says why), and the input's values
-//                      in bf16 where it was kept as codes and scales too
+//                      follow (backward_pair.cu says why). Where the input was kept
+//                      as codes q and a scale s per token too, its values q s would be
+//                      rounded to bf16 as an operand of the weight gradients; with
+//                      s = p f (split_scale()) q p is exact, so that is the operand, and
+//                      the other one is f dG (f dU), rounded once as dG itself would be.
+//                      The input gradient divides its rows by f again, in fp32.
 // Both stream: a thread takes 8 columns of every gridDim.y-th row, and holds the
 // loads of two rows at a time.
 #include "int8.cuh"
@@ -59,7 +63,7 @@ __global__ void __launch_bounds__(kThreadsC)
     for (int64_t m = blockIdx.y; m < p.M; m += rows_step) {
       const size_t at = static_cast<size_t>(m) * p.K + col;
       float v[8];
-      values_of(ld_codes(p.a_codes, at), ld_scale(p.a_scale + m), v);
+      values_of(ld_codes(p.a_codes, at), split_scale(ld_scale(p.a_scale + m)).power, v);
       *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.a_out) + at) = pack8(v);
     }
     return;
@@ -72,7 +76,7 @@ __global__ void __launch_bounds__(kThreadsC)
   for (int64_t m0 = blockIdx.y; m0 < p.M; m0 += int64_t(kRows) * rows_step) {
     uint2 gc[kRows], uc[kRows];
     uint4 dy[kRows];
-    float gs[kRows], us[kRows];
+    float gs[kRows], us[kRows], as[kRows];
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
       const int64_t m = min(m0 + int64_t(r) * rows_step, int64_t(p.M) - 1);
@@ -83,6 +87,7 @@ __global__ void __launch_bounds__(kThreadsC)
         dy[r] = ld_global_v4(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.dy) + at));
       gs[r] = ld_scale(gate_scale + m);
       us[r] = ld_scale(up_scale + m);
+      as[r] = kGrads && p.a_scale ? ld_scale(p.a_scale + m) : 1.0f;
     }
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
@@ -94,11 +99,12 @@ __global__ void __launch_bounds__(kThreadsC)
       values_of(uc[r], us[r], u);
       if constexpr (kGrads) {
         const uint32_t w[4] = {dy[r].x, dy[r].y, dy[r].z, dy[r].w};
+        const float f = split_scale(as[r]).factor;  // dG and dU are linear in dY
         float dg[8], du[8];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          gate_grads(g[2 * i], u[2 * i], __uint_as_float(w[i] << 16), dg[2 * i], du[2 * i]);
-          gate_grads(g[2 * i + 1], u[2 * i + 1], __uint_as_float(w[i] & 0xffff0000u), dg[2 * i + 1],
+          gate_grads(g[2 * i], u[2 * i], f * __uint_as_float(w[i] << 16), dg[2 * i], du[2 * i]);
+          gate_grads(g[2 * i + 1], u[2 * i + 1], f * __uint_as_float(w[i] & 0xffff0000u), dg[2 * i + 1],
                      du[2 * i + 1]);
         }
         *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out0) + at) = pack8(dg);

@@ -42,6 +42,19 @@ __device__ __forceinline__ uint32_t quant_code(float x, float inverse) {
   return __float_as_uint(fmaf(x, inverse, kRoundMagic));
 }
 
+// A scale as a power of two and a factor in [1, 2), s = power * factor: codes times the power are
+// bf16 values exactly, and the factor goes elsewhere in the product. Zero, subnormal, infinite and
+// NaN scales stay whole (factor 1).
+struct ScaleParts {
+  float power, factor;
+};
+
+__device__ __forceinline__ ScaleParts split_scale(float s) {
+  const uint32_t bits = __float_as_uint(s), e = bits >> 23 & 0xffu;
+  if (e == 0u || e == 0xffu) return ScaleParts{s, 1.0f};
+  return ScaleParts{__uint_as_float(bits & 0xff800000u), __uint_as_float((bits & 0x007fffffu) | 0x3f800000u)};
+}
+
 // The low bytes of four words.
 __device__ __forceinline__ uint32_t pack_low_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);

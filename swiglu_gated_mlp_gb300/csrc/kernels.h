@@ -194,6 +194,8 @@ struct BackwardProduct {
   int two;         // input gradient: dG and dU in the sum; weight gradient: dW1 and dW2
   int splits;      // parts of the sum (1: none); > 1: outputs are fp32 parts of
   int part_rows;   // this many rows each (a multiple of 32)
+  const float* row_scale;  // input gradient: rows are divided by the factors of these scales
+                           // (split_scale() in int8.cuh; null: as they are)
 };
 
 struct BackwardParams {
@@ -272,7 +274,8 @@ struct CheckpointParams {
   void* out0;          // Y, or dG [M, N] bf16
   void* out1;          // dU
   int M, N;
-  // gradients: the input's codes [M, K] and scales [M] (null: not kept so), its values in bf16
+  // gradients: the input's scales [M] (null: not kept so), its codes [M, K] (null: no weight
+  // gradients) and codes times the scales' powers of two in bf16
   const void* a_codes;
   const float* a_scale;
   void* a_out;

@@ -155,7 +155,7 @@ def check_gradients(native, M, K, N, seed, eight_bits):
     if eight_bits:
         a, sa = (t.cpu() for t in native.swiglu_quantize_int8(a.cuda()))
         av = f64(a) * f64(sa)[:, None]
-        a_err = (2 * FP32 + ref.BF16) * abs(av)
+        a_err = 2 * FP32 * abs(av)
         sa = sa.cuda()
     outs = native.swiglu_backward_checkpoint(a.cuda(), native.swiglu_pack_weights(w1.cuda(), w2.cuda()), dy.cuda(),
                                              *(t.cuda() for t in ck), scale_a=sa)
@@ -427,3 +427,39 @@ def test_many_tiles_of_many_slices(native):
         assert (abs(f64(codes[at]) * step - x) <= (0.5 + 127 * 2 * FP32) * step + err).all()
     g, u = (f64(c[at]) * ref.wide(f64(s[:, at]), N) for c, s in ((last[1], last[3][0]), (last[2], last[3][1])))
     assert_within(restored[at], *ref.gated(g, FP32 * abs(g), u, FP32 * abs(u)))
+
+
+def test_scales_of_any_size(native):
+    # the input's scales from 2^-110 to 2^100, zero, negative and subnormal: dA does not depend on
+    # them, and the weight gradients are those of the values (rows of large values would drown the
+    # others, so each goes alone)
+    M, K, N = 16, 72, 136
+    a, w1, w2, dy, ck = gradient_inputs(M, K, N, 6)
+    q, _ = (t.cpu() for t in native.swiglu_quantize_int8(a.cuda()))
+    wp = native.swiglu_pack_weights(w1.cuda(), w2.cuda())
+    g, u = values(*ck)
+    for i, s in enumerate((2.0 ** -110, 3e-20, -0.75, 1.0, 1.9999999, 2.0 ** 100, 0.0, 1e-40)):
+        sa = torch.zeros(M)
+        sa[i] = s
+        outs = native.swiglu_backward_checkpoint(q.cuda(), wp, dy.cuda(), *(t.cuda() for t in ck), scale_a=sa.cuda())
+        av = f64(q) * f64(sa)[:, None]
+        args = (av, f64(w1), f64(w2), g, u, f64(dy))
+        # a subnormal scale keeps its codes times itself in bf16, 2^-133 apart
+        bounds = ref.backward_bounds(*args, 2 * FP32 * abs(av) + (2.0 ** -134 if s == 1e-40 else 0.0))
+        for out, want, bound in zip(outs, ref.backward_values(*args), bounds):
+            assert_within(out, want, bound)
+    native.swiglu_check_device_status()
+
+
+def test_an_input_scale_that_is_not_finite(native):
+    # the weight gradients sum over all tokens and are lost; dA of every token is not
+    M, K, N = 40, 72, 136
+    a, w1, w2, dy, ck = gradient_inputs(M, K, N, 7)
+    q, sa = native.swiglu_quantize_int8(a.cuda())
+    wp, dy, ck = native.swiglu_pack_weights(w1.cuda(), w2.cuda()), dy.cuda(), [t.cuda() for t in ck]
+    want = native.swiglu_backward_checkpoint(q, wp, dy, *ck, scale_a=sa)[0]
+    sa[3] = float("nan")
+    da, dw1, dw2 = native.swiglu_backward_checkpoint(q, wp, dy, *ck, scale_a=sa)
+    keep = torch.arange(M) != 3
+    assert torch.equal(da[keep], want[keep]) and torch.isfinite(da).all()
+    assert torch.isnan(dw1).any() and torch.isnan(dw2).any()
