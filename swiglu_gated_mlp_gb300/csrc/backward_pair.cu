@@ -176,15 +176,15 @@ __global__ void __launch_bounds__(kBackThreads, 1)
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 1) {
-    tmem_alloc_pair(smem_addr(tmem_slot), 2 * kAccCols);
-    tmem_relinquish_pair();
-  }
-  tc_fence_before();
-  cluster_sync();  // both CTAs' barriers initialised and TMEM allocated
-  tc_fence_after();
-  const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
+  cluster_sync();  // both CTAs run, their barriers initialised
   pdl_wait();
+  if (warp == 1) tmem_alloc_pair(smem_addr(tmem_slot), 2 * kAccCols);
+  tc_fence_before();
+  cluster_arrive();  // tensor memory allocated; the producer need not wait for that
+  if (warp != 0) cluster_wait();
+  tc_fence_after();
+  if (warp == 1) tmem_relinquish_pair();
+  const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
 
   if (warp == 0) {
     // ------------------------------------------------ TMA producer (both CTAs)
@@ -555,12 +555,14 @@ __global__ void __launch_bounds__(kBackThreads, 1)
 
   // Neither CTA leaves while the pair's MMAs may still read its shared memory
   // or the peer may still arrive on its barriers.
+  if (warp == 0) cluster_wait();
   tc_fence_before();
   cluster_sync();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_pair(tmem_base, 2 * kAccCols);
   }
+  cluster_sync();  // nor while the peer gives its tensor memory back
 }
 
 // out[r][c] = bf16(sum over parts, in order, of parts[part][r][c]) for each

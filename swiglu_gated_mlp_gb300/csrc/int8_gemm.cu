@@ -228,25 +228,28 @@ __global__ void __launch_bounds__(kThreads8, 1) int8_gemm_kernel(const __grid_co
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 1) {
-    if constexpr (kPair) {
-      tmem_alloc_pair(smem_addr(tmem_slot), kTmem8);
-      tmem_relinquish_pair();
-    } else {
+  if constexpr (kPair) {
+    cluster_sync();  // both CTAs run, their barriers initialised
+    pdl_wait();
+    if (warp == 1) tmem_alloc_pair(smem_addr(tmem_slot), kTmem8);
+    tc_fence_before();
+    cluster_arrive();  // tensor memory allocated; the producer need not wait for that
+    if (warp != 0) cluster_wait();
+    tc_fence_after();
+    if (warp == 1) tmem_relinquish_pair();
+  } else {
+    if (warp == 1) {
       tmem_alloc(smem_addr(tmem_slot), kTmem8);
       tmem_relinquish();
     }
-  }
-  tc_fence_before();
-  if constexpr (kPair)
-    cluster_sync();
-  else
+    tc_fence_before();
     __syncthreads();
-  tc_fence_after();
+    tc_fence_after();
+  }
   const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
   // the slots, then the accumulators, two of mt columns
   const uint32_t acc0 = tmem_base + static_cast<uint32_t>(slots * 64);
-  pdl_wait();
+  if (!kPair) pdl_wait();
 
   if (warp == 0) {
     // ------------------------------------------------ TMA producer
@@ -604,6 +607,7 @@ __global__ void __launch_bounds__(kThreads8, 1) int8_gemm_kernel(const __grid_co
   }
   // Neither CTA of a pair leaves while the pair's MMAs may still read its memory or the peer
   // may still arrive on its barriers.
+  if (kPair && warp == 0) cluster_wait();
   tc_fence_before();
   if constexpr (kPair)
     cluster_sync();
@@ -616,6 +620,7 @@ __global__ void __launch_bounds__(kThreads8, 1) int8_gemm_kernel(const __grid_co
     else
       tmem_dealloc(tmem_base, kTmem8);
   }
+  if constexpr (kPair) cluster_sync();  // nor while the peer gives its tensor memory back
 }
 
 // Codes as fp16 values, 16 a thread and step.

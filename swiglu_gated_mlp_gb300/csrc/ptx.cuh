@@ -551,6 +551,15 @@ __device__ __forceinline__ uint32_t mapa_shared(uint32_t addr, uint32_t rank) {
   return r;
 }
 
+// The two halves of cluster_sync(): each warp waits once for each of its arrivals.
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 // All threads of both CTAs: release this CTA's prior writes, acquire the peer's.
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" :::
@@ -605,7 +614,15 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap
       : "memory");
 }
 
-// Executed by one warp in each CTA of the pair; both get the same columns.
+// Executed by one warp in each CTA of the pair; both get the same columns. The two CTAs do this
+// together, so each kernel sees to it that
+//   - both run (a cluster barrier before), and the grids before this one have completed (pdl_wait()
+//     before): their blocks no longer hold one CTA's SM and keep it back behind the other;
+//   - the right to allocate is given up after both have allocated (a cluster barrier between);
+//   - neither CTA ends before both have given the columns back (a cluster barrier behind).
+// With the allocation ahead of pdl_wait(), the right given up at once and no barrier behind, one CTA
+// of a pair could stand in its allocation for ever: once in some thousand launches where a kernel of
+// many small blocks (checkpoint.cu) had let this one start.
 __device__ __forceinline__ void tmem_alloc_pair(uint32_t dst_smem, uint32_t ncols) {
   asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem),
                "r"(ncols)

@@ -463,3 +463,25 @@ def test_an_input_scale_that_is_not_finite(native):
     keep = torch.arange(M) != 3
     assert torch.equal(da[keep], want[keep]) and torch.isfinite(da).all()
     assert torch.isnan(dw1).any() and torch.isnan(dw2).any()
+
+
+def test_pair_kernels_behind_a_kernel_of_many_blocks(native):
+    # CTAs of a pair kernel that start while another kernel's blocks still fill their SMs, each at its
+    # own time: thousands of calls in a row, forward and backward (an allocation of tensor memory that
+    # one CTA of a pair came late to once stood still there)
+    M, K, N = 4096, 64, 18944
+    a, w1, w2 = (t.cuda() for t in make_inputs(M, K, N, 5))
+    wp = native.swiglu_pack_weights(w1, w2)
+    first = native.swiglu_forward_checkpoint(a, wp, N)
+    ws = native.swiglu_backward_checkpoint_workspace(M, K, N)
+    for _ in range(40):
+        for _ in range(100):
+            last = native.swiglu_forward_checkpoint(a, wp, N)
+            y = native.swiglu_checkpoint_output(*last[1:])
+        for _ in range(5):
+            grads = native.swiglu_backward_checkpoint(a, wp, y, *last[1:], workspace=ws)
+        torch.cuda.synchronize()
+    native.swiglu_check_device_status()
+    assert all(torch.equal(x, z) for x, z in zip(first, last))
+    want = native.swiglu_backward_checkpoint(a, wp, y, *first[1:])
+    assert all(torch.equal(x, z) for x, z in zip(grads, want))
