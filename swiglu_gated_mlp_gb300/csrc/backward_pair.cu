@@ -55,6 +55,11 @@
 // reduce_parts_kernel adds the parts in order (results do not depend on
 // timing) and rounds once.
 //
+// With Gate and Up kept by the forward (checkpoint.cu makes dG and dU) only the second
+// launch runs. kScaled: dG and dU hold a factor for each token that is not dA's, so the
+// epilogue divides dA's rows by it (a template argument: as a branch at run time it cost the
+// other launches of this kernel 4 % at the 0.5B shape).
+//
 // Measured, 7B block, 4096 tokens, one call at a time: dG and dU 567-573 us (1.95
 // PFLOP/s), both gradients 1114-1125 us (1.98), tensor pipe 92 % busy in each; back
 // to back at the power cap 1974 us in all (1.69 PFLOP/s). 16 tokens on the same
@@ -176,7 +181,8 @@ __global__ void __launch_bounds__(kBackThreads, 1)
     *abort_flag = 0;
     fence_mbar_init();
   }
-  cluster_sync();  // both CTAs run, their barriers initialised
+  cluster_arrive();  // both CTAs run, their barriers initialised
+  cluster_wait();
   pdl_wait();
   if (warp == 1) tmem_alloc_pair(smem_addr(tmem_slot), 2 * kAccCols);
   tc_fence_before();
@@ -549,6 +555,8 @@ __global__ void __launch_bounds__(kBackThreads, 1)
       buf ^= 1;
       if (buf == 0) acc_ph ^= 1u;
     }
+    tc_fence_before();
+    cluster_arrive();  // the accumulators have been read; the last stores go on
     if (lane == 0) bulk_wait<0>();
     __syncwarp();
   }
@@ -556,13 +564,17 @@ __global__ void __launch_bounds__(kBackThreads, 1)
   // Neither CTA leaves while the pair's MMAs may still read its shared memory
   // or the peer may still arrive on its barriers.
   if (warp == 0) cluster_wait();
-  tc_fence_before();
-  cluster_sync();
+  if (warp < 2) {
+    tc_fence_before();
+    cluster_arrive();
+  }
+  cluster_wait();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_pair(tmem_base, 2 * kAccCols);
   }
-  cluster_sync();  // nor while the peer gives its tensor memory back
+  cluster_arrive();  // nor while the peer gives its tensor memory back
+  cluster_wait();
 }
 
 // out[r][c] = bf16(sum over parts, in order, of parts[part][r][c]) for each

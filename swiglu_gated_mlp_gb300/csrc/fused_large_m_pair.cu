@@ -88,6 +88,15 @@
 // brought, so an Lb copy signals its own CTA, and those warps the even one. (They write
 // the V of the next slice first: 631 us with the look as without it; 640 where they
 // looked through each slice before the next V.)
+//
+// With kKeep (bf16) Gate and Up are kept too, as 8-bit codes with a scale per token and
+// tile, i.e. 128 columns (int8.cuh). A scale needs its row's largest magnitude before the
+// first code, so the epilogue goes over the accumulators twice, from tensor memory (a
+// row's 256 values would not fit its thread's registers); codes leave through a staging
+// buffer of their own. Token boxes end with the tokens. Measured: K 3584, N 18944, 4096
+// tokens 569 us against 555 without, 1000 tokens 150 against 146, tensor pipe 93 % busy;
+// K 896, N 4864, 128 tokens 11.0 against 9.2, bound by its one round of tiles. Eight epilogue warps, as
+// with block scales, gained nothing: two share a row and have to exchange its maximum.
 #include "int8.cuh"
 #include "kernels.h"
 #include "lora_lb.cuh"
@@ -263,7 +272,8 @@ __global__ void __launch_bounds__(PairCfg<kMx, kLora, kKeep>::kThreadsT, 1)
     *abort_flag = 0;
     fence_mbar_init();
   }
-  cluster_sync();  // both CTAs run, their barriers initialised
+  cluster_arrive();  // both CTAs run, their barriers initialised
+  cluster_wait();
   // With adapters the kernel before this one makes V and the lists, and lets this grid
   // start when it has itself waited for all before it: the first K slices (by TMA, from
   // L2) need no wait, what reads V and lists or writes outputs has its own.
@@ -890,6 +900,8 @@ __global__ void __launch_bounds__(PairCfg<kMx, kLora, kKeep>::kThreadsT, 1)
         acc_ph ^= 1u;
       }
     }
+    tc_fence_before();
+    cluster_arrive();  // the accumulators have been read; the last stores go on
     if (lane == 0) bulk_wait<0>();
     __syncwarp();
   }
@@ -897,13 +909,17 @@ __global__ void __launch_bounds__(PairCfg<kMx, kLora, kKeep>::kThreadsT, 1)
   // Neither CTA leaves while the pair's MMAs may still read its shared memory
   // or the peer may still arrive on its barriers.
   if (warp == 0) cluster_wait();
-  tc_fence_before();
-  cluster_sync();
+  if (warp < 2 || warp >= 2 + C::kEpiWarps) {
+    tc_fence_before();
+    cluster_arrive();
+  }
+  cluster_wait();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_pair(tmem_base, C::kTmemCols);
   }
-  cluster_sync();  // nor while the peer gives its tensor memory back
+  cluster_arrive();  // nor while the peer gives its tensor memory back
+  cluster_wait();
 }
 
 cudaLaunchConfig_t pair_config(int grid, cudaStream_t stream, cudaLaunchAttribute* attr,

@@ -82,7 +82,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     *abort_flag = 0;
     fence_mbar_init();
   }
-  cluster_sync();  // both CTAs run, their barriers initialised
+  cluster_arrive();  // both CTAs run, their barriers initialised
+  cluster_wait();
   pdl_wait();
   if (warp == 1) tmem_alloc_pair(smem_addr(tmem_slot), kTmemCols);
   tc_fence_before();
@@ -160,6 +161,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_wait_ld();
       reg_fence(g);
       reg_fence(u);
+      tc_fence_before();
+      cluster_arrive();  // the accumulator has been read; what follows stores
       // staging: slice 0's A region (its MMAs have completed), 2 KB per warp
       const uint32_t stg = s0 + q * (32 * 64);
       const uint32_t row_addr = stg + lane * 64;
@@ -185,19 +188,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         bulk_wait<0>();
       }
       __syncwarp();
+    } else {
+      tc_fence_before();
+      cluster_arrive();
     }
   }
 
   // Neither CTA leaves while the pair's MMAs may still read its shared memory
   // or the peer may still arrive on its barriers.
   if (warp == 0) cluster_wait();
-  tc_fence_before();
-  cluster_sync();
+  if (warp < 2) {
+    tc_fence_before();
+    cluster_arrive();
+  }
+  cluster_wait();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_pair(tmem_base, kTmemCols);
   }
-  cluster_sync();  // nor while the peer gives its tensor memory back
+  cluster_arrive();  // nor while the peer gives its tensor memory back
+  cluster_wait();
 }
 
 }  // namespace

@@ -229,7 +229,8 @@ __global__ void __launch_bounds__(kThreads8, 1) int8_gemm_kernel(const __grid_co
     fence_mbar_init();
   }
   if constexpr (kPair) {
-    cluster_sync();  // both CTAs run, their barriers initialised
+    cluster_arrive();  // both CTAs run, their barriers initialised
+    cluster_wait();
     pdl_wait();
     if (warp == 1) tmem_alloc_pair(smem_addr(tmem_slot), kTmem8);
     tc_fence_before();
@@ -609,10 +610,12 @@ __global__ void __launch_bounds__(kThreads8, 1) int8_gemm_kernel(const __grid_co
   // may still arrive on its barriers.
   if (kPair && warp == 0) cluster_wait();
   tc_fence_before();
-  if constexpr (kPair)
-    cluster_sync();
-  else
+  if constexpr (kPair) {
+    cluster_arrive();
+    cluster_wait();
+  } else {
     __syncthreads();
+  }
   if (warp == 1) {
     tc_fence_after();
     if constexpr (kPair)
@@ -620,7 +623,10 @@ __global__ void __launch_bounds__(kThreads8, 1) int8_gemm_kernel(const __grid_co
     else
       tmem_dealloc(tmem_base, kTmem8);
   }
-  if constexpr (kPair) cluster_sync();  // nor while the peer gives its tensor memory back
+  if constexpr (kPair) {  // nor while the peer gives its tensor memory back
+    cluster_arrive();
+    cluster_wait();
+  }
 }
 
 // Codes as fp16 values, 16 a thread and step.

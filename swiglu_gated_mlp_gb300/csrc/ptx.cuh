@@ -551,9 +551,12 @@ __device__ __forceinline__ uint32_t mapa_shared(uint32_t addr, uint32_t rank) {
   return r;
 }
 
-// The two halves of cluster_sync(): each warp waits once for each of its arrivals.
+// A cluster barrier in two halves (each warp waits once for each of its arrivals) for where CTAs
+// only keep in step: it orders a thread's writes for its own CTA, and those of fence_mbar_init().
+// A release for the cluster would first wait for all of the thread's stores.
 __device__ __forceinline__ void cluster_arrive() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  __threadfence_block();
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
 }
 
 __device__ __forceinline__ void cluster_wait() {
