@@ -6,7 +6,8 @@ The public functions mirror the C ABI in include/swiglu.h (same names):
 ``swiglu_pack_weights``, ``swiglu_forward``, ``swiglu_forward_variant``,
 ``swiglu_forward_from_host``, ``swiglu_packed_weight_bytes``,
 ``swiglu_check_device_status``, ``swiglu_status_string``, ``swiglu_plan_string``
-and the FP8, down-projection and allocation-free forms; ``pack(W1, W2)`` and
+and the FP8, 8-bit integer, down-projection, gradient (recomputing, or from an 8-bit
+checkpoint), adapter and allocation-free forms; ``pack(W1, W2)`` and
 ``forward(A, Wp, N)`` are short names of the first two.
 They load the compiled library on first use and raise if it is missing; there
 is no CPU or PyTorch fallback.

@@ -10,7 +10,9 @@
 //                      the other one is f dG (f dU), rounded once as dG itself would be.
 //                      The input gradient divides its rows by f again, in fp32.
 // Both stream: a thread takes 8 columns of every gridDim.y-th row, and holds the
-// loads of two rows at a time.
+// loads of two rows at a time. Measured, N 18944: Y of 4096 tokens 52-65 us (310 MB, 4.8-6.0
+// TB/s; the larger with cold caches); dG and dU of 2048 tokens 51 us cold, 287 MB, DRAM 71 % and 2.65
+// instructions a cycle: the arithmetic is the next bound. Most of dG and dU stays in L2 for the products.
 #include "int8.cuh"
 #include "kernels.h"
 #include "ptx.cuh"
