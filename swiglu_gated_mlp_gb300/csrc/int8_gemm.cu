@@ -604,7 +604,8 @@ __global__ void __launch_bounds__(kThreads8, 1) int8_gemm_kernel(const __grid_co
         return v;
       });
     }
-    cluster_sync();  // no CTA leaves while a peer may still read its sums
+    cluster_arrive();  // no CTA leaves while a peer may still read its sums (which it has, once it stored them)
+    cluster_wait();
   }
   // Neither CTA of a pair leaves while the pair's MMAs may still read its memory or the peer
   // may still arrive on its barriers.

@@ -555,6 +555,7 @@ __device__ __forceinline__ uint32_t mapa_shared(uint32_t addr, uint32_t rank) {
 // only keep in step: it orders a thread's writes for its own CTA, and those of fence_mbar_init().
 // A release for the cluster would first wait for all of the thread's stores.
 __device__ __forceinline__ void cluster_arrive() {
+  __syncwarp();  // whole warps arrive
   __threadfence_block();
   asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
 }
