@@ -556,7 +556,7 @@ __global__ void __launch_bounds__(kBackThreads, 1)
       if (buf == 0) acc_ph ^= 1u;
     }
     tc_fence_before();
-    cluster_arrive();  // the accumulators have been read; the last stores go on
+    cluster_arrive_release();  // the accumulators have been read; the last stores go on
     if (lane == 0) bulk_wait<0>();
     __syncwarp();
   }
@@ -566,7 +566,7 @@ __global__ void __launch_bounds__(kBackThreads, 1)
   if (warp == 0) cluster_wait();
   if (warp < 2) {
     tc_fence_before();
-    cluster_arrive();
+    cluster_arrive_release();
   }
   cluster_wait();
   if (warp == 1) {

@@ -901,7 +901,7 @@ __global__ void __launch_bounds__(PairCfg<kMx, kLora, kKeep>::kThreadsT, 1)
       }
     }
     tc_fence_before();
-    cluster_arrive();  // the accumulators have been read; the last stores go on
+    cluster_arrive_release();  // the accumulators have been read; the last stores go on
     if (lane == 0) bulk_wait<0>();
     __syncwarp();
   }
@@ -911,7 +911,7 @@ __global__ void __launch_bounds__(PairCfg<kMx, kLora, kKeep>::kThreadsT, 1)
   if (warp == 0) cluster_wait();
   if (warp < 2 || warp >= 2 + C::kEpiWarps) {
     tc_fence_before();
-    cluster_arrive();
+    cluster_arrive_release();
   }
   cluster_wait();
   if (warp == 1) {

@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       reg_fence(g);
       reg_fence(u);
       tc_fence_before();
-      cluster_arrive();  // the accumulator has been read; what follows stores
+      cluster_arrive_release();  // the accumulator has been read; what follows stores
       // staging: slice 0's A region (its MMAs have completed), 2 KB per warp
       const uint32_t stg = s0 + q * (32 * 64);
       const uint32_t row_addr = stg + lane * 64;
@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     } else {
       tc_fence_before();
-      cluster_arrive();
+      cluster_arrive_release();
     }
   }
 
@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) cluster_wait();
   if (warp < 2) {
     tc_fence_before();
-    cluster_arrive();
+    cluster_arrive_release();
   }
   cluster_wait();
   if (warp == 1) {

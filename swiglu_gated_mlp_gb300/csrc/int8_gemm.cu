@@ -612,7 +612,7 @@ __global__ void __launch_bounds__(kThreads8, 1) int8_gemm_kernel(const __grid_co
   if (kPair && warp == 0) cluster_wait();
   tc_fence_before();
   if constexpr (kPair) {
-    cluster_arrive();
+    cluster_arrive_release();
     cluster_wait();
   } else {
     __syncthreads();
