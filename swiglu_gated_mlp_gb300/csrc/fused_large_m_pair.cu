@@ -95,7 +95,7 @@
 // row's 256 values would not fit its thread's registers); codes leave through a staging
 // buffer of their own. Token boxes end with the tokens. Measured: K 3584, N 18944, 4096
 // tokens 569 us against 555 without, 1000 tokens 150 against 146, tensor pipe 93 % busy;
-// K 896, N 4864, 128 tokens 11.0 against 9.2, bound by its one round of tiles. Eight epilogue warps, as
+// K 896, N 4864, 128 tokens 11.2 against 9.4, bound by its one round of tiles. Eight epilogue warps, as
 // with block scales, gained nothing: two share a row and have to exchange its maximum.
 #include "int8.cuh"
 #include "kernels.h"
