@@ -276,8 +276,10 @@ __global__ void __launch_bounds__(PairCfg<kMx, kLora, kKeep>::kThreadsT, 1)
   cluster_wait();
   // With adapters the kernel before this one makes V and the lists, and lets this grid
   // start when it has itself waited for all before it: the first K slices (by TMA, from
-  // L2) need no wait, what reads V and lists or writes outputs has its own.
-  if (!kLora || !p.lora_early) pdl_wait();
+  // L2) need no wait, what reads V and lists or writes outputs has its own. The warp that
+  // allocates tensor memory waits all the same (tmem_alloc_pair() says why), so the first
+  // MMA is issued when V is there.
+  if (!kLora || !p.lora_early || warp == 1) pdl_wait();
   if (warp == 1) tmem_alloc_pair(smem_addr(tmem_slot), C::kTmemCols);
   tc_fence_before();
   cluster_arrive();  // tensor memory allocated; the producer need not wait for that
@@ -490,7 +492,6 @@ __global__ void __launch_bounds__(PairCfg<kMx, kLora, kKeep>::kThreadsT, 1)
         }
         if constexpr (kLora) {
           if (extra < 0) {
-            pdl_wait();
             extra = lora_slices(t);
             next_extra = t + pairs < num_tiles ? lora_slices(t + pairs) : 0;
           }

@@ -26,10 +26,10 @@ constexpr int64_t kGroupTokens = 128;
 // split 1 us. Measured, decode against pairs (in both the kernel that makes V is out
 // of the way): 333 tokens of 10 adapters, K 1416 N 5000, 30.6 / 43.7 us; 200 tokens of
 // 4, K 2048 N 4000 (K over 2 CTAs) 18.6 / 20.4, 500 of 3 (4 groups, K whole) 36.3 /
-// 28.5; down, N 18944 H 3584, 500 tokens of 3 (K over 2) 78.9 / 92.6, 800 of 2 (7
+// 30.5; down, N 18944 H 3584, 500 tokens of 3 (K over 2) 78.9 / 92.6, 800 of 2 (7
 // groups, K whole) 252 / 108; down, N 4864 H 896, 800 of 2 (7 groups, K over 4) 25.2 /
 // 31.7. Where the two meet the rule is off by up to a tenth, with 8 slices and many
-// adapters by a fifth (333 tokens of 10, K 512 N 2000: pairs, 24.1 / 19.2).
+// adapters by a fifth (333 tokens of 10, K 512 N 2000: pairs, 24-26 / 19.2).
 swiglu_status_t plan_decode(int64_t M, int64_t blocks, int64_t slices, const DeviceView& d,
                             SmallMParams* p, bool* decode) {
   const int64_t groups = (M + kGroupTokens - 1) / kGroupTokens;
@@ -273,10 +273,11 @@ swiglu_status_t run_call(const Call& c, cudaStream_t stream) {
     p.lora_lb = c.lb;
     p.lora_index = c.index;
     p.lora_lists = lists;
-    // Where both grids fit on the SMs together V takes no time of its own (down, 333
-    // tokens of 10 adapters, N 18944, H 3584: 174 -> 98 us). Where they do not, some pairs
-    // start before others: 4096 tokens, K 3584 645 -> 630 us, but with long tiles, which
-    // then share less of L2, 350 -> 358 us (down, N 18944).
+    // The first K slices' loads then run beside the kernel that makes V; the MMAs follow it, as
+    // tensor memory is allocated behind it. With and without: 333 tokens of 10 adapters, K 512,
+    // N 2000 24.0-26.4 / 27.6-28.3 us, 500 of 3, K 2048, N 4000 30.5 / 31.8, 700 of 3, K 1416, N
+    // 5000 40.0 / 41.6, 4096, K 3584, N 18944 the same; where the grids do not fit together some pairs
+    // start before others, which long tiles (down, N 18944) do not gain from: they share less of L2.
     p.lora_early = sp.tiles * sp.splits + p.grid <= d.sm_count || slices < 128;
     p.status = d.status;
     p.timeout_ns = d.timeout_ns;

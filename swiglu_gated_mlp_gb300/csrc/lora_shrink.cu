@@ -21,8 +21,9 @@
 // adapters (88 against 71 us for the call with 8).
 //
 // Either kernel lets the projection's start as soon as it has itself waited for the
-// grids before it, so that the weight stream (or the first K slices) runs beside it
-// and V only has to be there for the adapter slices at its end: 333 tokens, K 1416,
+// grids before it. The decode kernel's weight stream runs beside it, and V only has to be
+// there for the adapter slices at its end; CTA pairs load their first K slices beside it and
+// allocate tensor memory when it has ended (lora_api.cu). 333 tokens, K 1416,
 // N 5000 30.5 -> 24.4 us, 200 tokens, down, N 18944 79 -> 45, 128 tokens, down, N 4864
 // 18.0 -> 16.4, 16 tokens, K 3584, N 18944 49.8 -> 48.3. (Before, the projection's
 // kernel started with this one, did its set-up and staged weight tiles in L2, then

@@ -627,7 +627,8 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap
 // Executed by one warp in each CTA of the pair; both get the same columns. The two CTAs do this
 // together, so each kernel sees to it that
 //   - both run (a cluster barrier before), and the grids before this one have completed (pdl_wait()
-//     before): their blocks no longer hold one CTA's SM and keep it back behind the other;
+//     before, of the warp that allocates at the least): their blocks no longer hold one CTA's SM and
+//     keep it back behind the other;
 //   - the right to allocate is given up after both have allocated (a cluster barrier between);
 //   - neither CTA ends before both have given the columns back (a cluster barrier behind).
 // With the allocation ahead of pdl_wait(), the right given up at once and no barrier behind, one CTA

@@ -486,3 +486,32 @@ def test_lora_largest_m(native, down):
     finally:
         ad = idx = rd = y = None
         torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("down", [False, True])
+@pytest.mark.parametrize("M, K, N", [(4096, 64, 2000), (700, 1416, 5000)])
+def test_pairs_behind_a_kernel_of_many_blocks(native, M, K, N, down):
+    # the projection's CTA pairs start while the kernel that makes V, and whatever ran before it,
+    # still fill SMs: many calls in a row behind a kernel of thousands of small blocks
+    L, r = 3, 16
+    plan = (native.swiglu_down_lora_plan_string if down else native.swiglu_lora_plan_string)(M, K, N, r)
+    assert "large_m_pair" in plan
+    a, w1, w2 = (t.cuda() for t in make_inputs(M, K, N, 5))
+    la, lb, scale = (t.cuda() for t in table(L, 1 if down else 2, r, K, N, 5))
+    index = indices(M, L, "mixed", 5).cuda()
+    if down:
+        wp, ws = native.swiglu_pack_down_weights(w1), native.swiglu_down_lora_workspace(M, K, N, r)
+    else:
+        wp, ws = native.swiglu_pack_weights(w1, w2), native.swiglu_lora_workspace(M, K, N, r)
+    call = native.swiglu_down_forward_lora if down else native.swiglu_forward_lora
+    b, v1, v2 = (t.cuda() for t in make_inputs(2048, 64, 18944, 7))
+    kept = native.swiglu_forward_checkpoint(b, native.swiglu_pack_weights(v1, v2), 18944)[1:]
+    first = call(a, wp, N, la, lb, index, scale, workspace=ws)
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for _ in range(50):
+            native.swiglu_checkpoint_output(*kept)
+            last = call(a, wp, N, la, lb, index, scale, workspace=ws)
+        torch.cuda.synchronize()
+    native.swiglu_check_device_status()
+    assert torch.equal(first, last)

@@ -28,3 +28,26 @@ def test_no_read_only_loads_where_grids_overlap(name):
     text = code(os.path.join(CSRC, name))
     for word in ("__ldg", "ld.global.nc", "__restrict__"):
         assert word not in text, word
+
+
+PAIRED = sorted(os.path.basename(p) for p in glob.glob(os.path.join(CSRC, "*.cu")) if "tmem_alloc_pair(" in code(p))
+
+
+def test_the_pair_kernels_are_covered():
+    assert PAIRED == ["backward_pair.cu", "fused_large_m_pair.cu", "fused_resident_pair.cu", "int8_gemm.cu"]
+
+
+@pytest.mark.parametrize("name", PAIRED)
+def test_pairs_allocate_tensor_memory_in_step(name):
+    # Nothing bounds the wait of a CTA pair's allocation, so both CTAs run by then, all grids before
+    # have completed, the right to allocate goes behind a barrier, and neither CTA leaves before both
+    # have given the memory back.
+    text = re.sub(r"\s+", " ", code(os.path.join(CSRC, name)))
+    assert text.count("tmem_alloc_pair(") == 1
+    before, rest = text.split("if (warp == 1) tmem_alloc_pair(")
+    assert re.search(r"cluster_arrive\(\); cluster_wait\(\); [^;]*pdl_wait\(\); $", before), before[-120:]
+    wait = before.rsplit(";", 2)[1]  # what is waited on: always, or with any condition by the warp that allocates
+    assert wait.strip() == "pdl_wait()" or re.search(r"\|\| warp == 1\) pdl_wait\(\)$", wait), wait
+    assert re.search(r"^[^;]*; tc_fence_before\(\); cluster_arrive\(\); if \(warp != 0\) cluster_wait\(\); "
+                     r"tc_fence_after\(\); if \(warp == 1\) tmem_relinquish_pair\(\);", rest), rest[:200]
+    assert "cluster_arrive(); cluster_wait();" in rest.split("tmem_dealloc_pair(")[1]
