@@ -593,8 +593,9 @@ __global__ void __launch_bounds__(kThreads8, 1) int8_gemm_kernel(const __grid_co
         float4 a[kMaxSplits8];
 #pragma unroll
         for (int k = 0; k < kMaxSplits8; ++k)
-          a[k] = ld_shared_cluster_v4(mapa_shared(local, static_cast<uint32_t>(min(k, splits - 1))) +
-                                      4u * static_cast<uint32_t>(m * kRows8 + r));
+          if (k < splits)
+            a[k] = ld_shared_cluster_v4(mapa_shared(local, static_cast<uint32_t>(k)) +
+                                        4u * static_cast<uint32_t>(m * kRows8 + r));
         float4 v = a[0];
 #pragma unroll
         for (int k = 1; k < kMaxSplits8; ++k)
@@ -604,7 +605,10 @@ __global__ void __launch_bounds__(kThreads8, 1) int8_gemm_kernel(const __grid_co
         return v;
       });
     }
-    cluster_arrive();  // no CTA leaves while a peer may still read its sums (which it has, once it stored them)
+    // No CTA leaves while a peer may still read its sums. Every value that a thread read there has gone
+    // into a store of its own by now, so its reads are over when it arrives (a release, ahead of the
+    // stores, would say so to the memory model too: 0.5B down, 128 tokens 9.1 -> 9.7 us, 1 token 6.7 -> 6.9).
+    cluster_arrive();
     cluster_wait();
   }
   // Neither CTA of a pair leaves while the pair's MMAs may still read its memory or the peer

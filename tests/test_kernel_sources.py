@@ -30,6 +30,22 @@ def test_no_read_only_loads_where_grids_overlap(name):
         assert word not in text, word
 
 
+REMOTE = sorted(os.path.basename(p) for p in glob.glob(os.path.join(CSRC, "*.cu")) if "ld_shared_cluster_v4(" in code(p))
+
+
+@pytest.mark.parametrize("name", REMOTE)
+def test_reads_of_a_peers_memory_come_before_its_end(name):
+    # The barrier that holds a CTA until its peers have read its shared memory releases, or (relaxed,
+    # which orders no reads) comes behind stores of all that was read: no part that is left out of
+    # the sums is loaded.
+    text = code(os.path.join(CSRC, name))
+    after = text[text.rindex("ld_shared_cluster_v4("):]
+    first = re.search(r"cluster_(sync|arrive_release|arrive)\(", after).group(1)
+    if first == "arrive":
+        assert re.search(r"if \(k < splits\)\s+a\[k\] = ld_shared_cluster_v4\(mapa_shared\(local, static_cast<uint32_t>\(k\)\)", text)
+        assert text.count("ld_shared_cluster_v4(") == 1
+
+
 PAIRED = sorted(os.path.basename(p) for p in glob.glob(os.path.join(CSRC, "*.cu")) if "tmem_alloc_pair(" in code(p))
 
 
