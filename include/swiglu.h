@@ -447,8 +447,9 @@ SWIGLU_API swiglu_status_t swiglu_quantize_int8(const void* X, void* Q, float* s
  *   128 of K, every code with its sign bit flipped; a row is a column of W3, or
  *   16 columns of W1 and the same 16 of W2 in turn; its 16-byte pieces c are
  *   stored in the order c ^ (row % 8). Runs once per weight set.
- * swiglu_int8_workspace_bytes, swiglu_down_int8_workspace_bytes: what a call
- *   needs on the current device: 2 bytes per token code, or 0 for few tokens
+ * swiglu_int8_workspace_bytes, swiglu_down_int8_workspace_bytes: what calls of
+ *   up to M tokens need on the current device (so one workspace of the largest
+ *   batch serves the smaller ones): 2 bytes per token code, or 0 for few tokens
  *   where K (N) is a multiple of 16. The workspace's contents need no set-up
  *   and mean nothing after the call; calls that may run at the same time need
  *   separate ones. NULL where 0 bytes are needed.

@@ -772,7 +772,7 @@ def swiglu_int8_workspace_bytes(M: int, K: int, N: int) -> int:
 
 
 def swiglu_int8_workspace(M: int, K: int, N: int, device=None) -> torch.Tensor:
-    """A workspace for swiglu_forward_int8 at (M, K, N), possibly of no bytes."""
+    """A workspace for swiglu_forward_int8 at (M, K, N) and any smaller M, possibly of no bytes."""
     return _new_workspace(swiglu_int8_workspace_bytes, device, M, K, N)
 
 
@@ -781,7 +781,7 @@ def swiglu_down_int8_workspace_bytes(M: int, N: int, H: int) -> int:
 
 
 def swiglu_down_int8_workspace(M: int, N: int, H: int, device=None) -> torch.Tensor:
-    """A workspace for swiglu_down_forward_int8 at (M, N, H), possibly of no bytes."""
+    """A workspace for swiglu_down_forward_int8 at (M, N, H) and any smaller M, possibly of no bytes."""
     return _new_workspace(swiglu_down_int8_workspace_bytes, device, M, N, H)
 
 

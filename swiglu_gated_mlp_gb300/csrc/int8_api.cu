@@ -133,12 +133,29 @@ swiglu_status_t pack(const void* w1, const void* w2, void* wp, int64_t K, int64_
                                    reinterpret_cast<cudaStream_t>(stream)));
 }
 
+// Whether calls of M tokens or fewer take pairs. Their rounds, and the tokens of a CTA's unit, are
+// whole numbers, so a batch may go back to single CTAs where a smaller one took pairs (down, K 464, N
+// 9808: pairs at 97 tokens, CTAs at some more). What CTAs take is constant up to the next change of a unit's
+// tokens, what pairs take never falls with M: the first M of each such range decides it. More than
+// kManyTokens count as pairs without a look.
+constexpr int64_t kManyTokens = 4096;
+bool pairs_up_to(int64_t M, int64_t K, int64_t N, bool down, int sms, const Int8State& s) {
+  if (M > kManyTokens) return s.pairs >= 1;
+  for (int64_t m = 1; m <= M;) {
+    const Int8Plan pl = make_plan(m, K, N, down, sms, s);
+    if (pl.pair) return true;
+    m = std::min(kInt8Tokens * pl.mgroups, pl.mt * pl.mgroups) + 1;
+  }
+  return false;
+}
+
+// What calls of up to M tokens need, so that one workspace serves every smaller batch.
 size_t workspace_for(int64_t M, int64_t K, int64_t N, bool down) {
   if (swg::api::check_shape(M, K, N) != SWIGLU_OK || M == 0) return 0;
   DeviceView d;
   const Int8State* s = nullptr;
   if (int8_device(&d, &s) != SWIGLU_OK) return 0;
-  return make_plan(M, K, N, down, d.sm_count, *s).workspace(M, K);
+  return pairs_up_to(M, K, N, down, d.sm_count, *s) ? size_t(M) * size_t(K) * 2 : 0;
 }
 
 // One projection: x [M, K] codes -> y [M, N].

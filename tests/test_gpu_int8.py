@@ -369,3 +369,26 @@ def test_one_workspace_in_stream_order(native):
     want = [f(None) for f in runs]
     got = [f(shared) for _ in range(3) for f in runs]
     assert all(torch.equal(a, b) for a, b in zip(got, want * 3))
+
+
+@pytest.mark.parametrize("K,N,down,Ms", [(2816, 2640, True, (129, 128)), (2096, 5864, True, (134, 127)),
+                                         (464, 9808, True, (200, 150)), (896, 4864, False, (300, 129, 1)),
+                                         (520, 264, False, (70, 69, 1))])
+def test_a_workspace_for_a_batch_serves_smaller_ones(native, K, N, down, Ms):
+    # a larger batch may run on single CTAs, which need none, where a smaller one takes pairs
+    need = native.swiglu_down_int8_workspace_bytes if down else native.swiglu_int8_workspace_bytes
+    plan = native.swiglu_down_plan_string_int8 if down else native.swiglu_plan_string_int8
+    sizes = [need(M, K, N) for M in range(1, 700)]
+    assert sizes == sorted(sizes)
+    assert all(size == 2 * M * K for M, size in enumerate(sizes, 1) if "pairs" in plan(M, K, N))
+    assert need(4097, K, N) >= sizes[-1] and need(1 << 20, K, N) == 2 * K << 20
+    g = torch.Generator().manual_seed(K)
+    w, s = codes(g, K, N).cuda(), scales(g, N, 0.01).cuda()
+    wp = native.swiglu_pack_down_weights_int8(w) if down else native.swiglu_pack_weights_int8(w, w)
+    ws = torch.empty(need(Ms[0], K, N), dtype=torch.uint8, device="cuda")
+    for M in Ms:
+        a, sa = codes(g, M, K).cuda(), scales(g, M, 0.02).cuda()
+        call = (lambda ws: native.swiglu_down_forward_int8(a, sa, wp, N, s, workspace=ws)) if down else \
+            (lambda ws: native.swiglu_forward_int8(a, sa, wp, N, s, s, workspace=ws))
+        assert torch.equal(call(ws), call(None))
+    native.swiglu_check_device_status()
