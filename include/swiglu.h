@@ -371,6 +371,9 @@ SWIGLU_API swiglu_status_t swiglu_down_plan_string_ws(int64_t M, int64_t N, int6
  * swiglu_backward_workspace_bytes(M, K, N): bytes of the workspace the call
  *   needs on the current device (dG and dU, and fp32 partial sums where a
  *   product has few output tiles); 0 on M = 0, a bad shape or no usable device.
+ *   The size is that of this M: fewer tokens may need more (K 896, N 4864: 257
+ *   tokens 11.2 MB, 256 tokens 13.2 MB, as their sums are cut into more parts), so
+ *   a workspace for several M has the largest of their sizes.
  * swiglu_backward: A [M, K], dY [M, N] bf16; Wpacked from swiglu_pack_weights
  *   with the same K and N; dA, dW1, dW2 are written in full, each [.] bf16
  *   row-major as its forward counterpart. dA NULL: not computed (the block's
@@ -504,7 +507,8 @@ SWIGLU_API swiglu_status_t swiglu_down_plan_string_int8(int64_t M, int64_t N, in
  *   swiglu_quantize_int8); its values are not rounded again (the codes are the
  *   tensor-core operand, most of the scale goes with dG and dU). A is not read when dW1 is NULL, Wpacked not when dA is (each may
  *   then be NULL). Outputs, NULLs, workspace and M = 0 as for
- *   swiglu_backward; swiglu_backward_checkpoint_workspace_bytes(M, K, N) bytes.
+ *   swiglu_backward; swiglu_backward_checkpoint_workspace_bytes(M, K, N) bytes
+ *   (of this M, as there).
  *   Any scales are taken as they are (finite or not).
  * Errors as swiglu_forward.
  */

@@ -620,7 +620,10 @@ def swiglu_backward_workspace_bytes(M: int, K: int, N: int) -> int:
 
 
 def swiglu_backward_workspace(M: int, K: int, N: int, device=None) -> torch.Tensor:
-    """A workspace for swiglu_backward at (M, K, N); one serves any number of calls in stream order."""
+    """A workspace for swiglu_backward at (M, K, N); one serves any number of calls in stream order.
+
+    Fewer tokens may need more: a workspace for several M has the largest of their sizes.
+    """
     return _new_workspace(swiglu_backward_workspace_bytes, device, M, K, N)
 
 
@@ -928,7 +931,10 @@ def swiglu_backward_checkpoint_workspace_bytes(M: int, K: int, N: int) -> int:
 
 
 def swiglu_backward_checkpoint_workspace(M: int, K: int, N: int, device=None) -> torch.Tensor:
-    """A workspace for swiglu_backward_checkpoint; one serves any number of calls in stream order."""
+    """A workspace for swiglu_backward_checkpoint at (M, K, N); one serves any number of calls in stream order.
+
+    Fewer tokens may need more: a workspace for several M has the largest of their sizes.
+    """
     return _new_workspace(swiglu_backward_checkpoint_workspace_bytes, device, M, K, N)
 
 
