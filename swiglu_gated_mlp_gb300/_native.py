@@ -2,16 +2,19 @@
 
 Argument marshalling only: every step of the computation runs in the library's
 CUDA kernels. PyTorch supplies device memory and the current stream. There is
-no fallback: if the library is not built, importing this module raises.
+no fallback: if the library is not built, importing this module raises. (Only
+the marshalling of the 8-bit calls has two forms: torch_calls.cpp, and the Python
+below where that module is missing or was built for another PyTorch.)
 """
 from __future__ import annotations
 
 import ctypes
 import os
+import warnings
 
 import torch
 
-from .build import LIB_PATH
+from .build import LIB_PATH, calls_built_for
 
 SWIGLU_OK = 0
 SWIGLU_ERR_INVALID_ARG = 1
@@ -37,7 +40,29 @@ if not os.path.exists(LIB_PATH):
 
 lib = ctypes.CDLL(LIB_PATH)
 
-from . import _torch_calls as _calls  # noqa: E402  (after the library that it uses)
+
+class _NoCalls:
+    """In place of _torch_calls: every call is left to the Python below."""
+
+    def __getattr__(self, name):
+        return lambda *args: None
+
+
+def _load_calls():
+    """The calls of torch_calls.cpp, if they were built for this PyTorch and Python."""
+    try:
+        from . import _torch_calls  # after the library that it uses
+        if _torch_calls.built_for == calls_built_for(torch):
+            return _torch_calls
+        why = f"it was built for {_torch_calls.built_for}"
+    except (ImportError, AttributeError) as e:
+        why = str(e)
+    warnings.warn("the 8-bit calls are made from Python, at some 17 us more of the host's time for each, as _torch_calls.so "
+                  f"cannot be used ({why}); run `python -m swiglu_gated_mlp_gb300.build`", RuntimeWarning, stacklevel=2)
+    return _NoCalls()
+
+
+_calls = _load_calls()
 
 _i64, _vp, _sz, _int, _u32 = ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int, ctypes.c_uint32
 lib.swiglu_packed_weight_bytes.argtypes = [_i64, _i64]

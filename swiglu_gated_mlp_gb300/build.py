@@ -5,7 +5,8 @@ file, then linked into ``libswiglu.so`` in this package directory with the
 CUDA runtime linked statically and only the ``swiglu_*`` symbols exported. A
 stamp of the sources and flags skips the work when nothing changed. Beside it
 ``torch_calls.cpp`` (Python calls for the installed PyTorch) becomes
-``_torch_calls.so``, which uses libswiglu.so from the same directory.
+``_torch_calls.so``, which uses libswiglu.so from the same directory. The C
+library does not need it: without PyTorch, g++ or Python's headers it is left out.
 
     python -m swiglu_gated_mlp_gb300.build        # build (or check) the library
 """
@@ -17,6 +18,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
@@ -47,18 +49,28 @@ def _nvcc() -> str:
     raise RuntimeError("nvcc not found: the CUDA toolkit is required to build libswiglu")
 
 
-def _calls_flags() -> tuple:
-    """Compiler and linker flags of _torch_calls.so."""
-    import torch
+def calls_built_for(torch) -> str:
+    """What _torch_calls.so is built for: it uses the binary interfaces of PyTorch and of Python."""
+    return f"PyTorch {torch.__version__}, Python {sysconfig.get_config_var('SOABI')}"
+
+
+def _calls_flags() -> tuple | None:
+    """Compiler and linker flags of _torch_calls.so, or None where it cannot be built."""
+    try:
+        import torch
+    except ImportError:
+        return None
+    if not shutil.which("g++") or not os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        return None
     base = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
     include = [os.path.join(base, "include"), os.path.join(base, "include/torch/csrc/api/include"),
                os.path.join(cuda, "include"), sysconfig.get_paths()["include"], INCLUDE]
     return (["-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+             f'-DSWIGLU_BUILT_FOR="{calls_built_for(torch)}"',
              f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"] + ["-I" + i for i in include],
             ["-L" + os.path.join(base, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
-             "-Wl,-rpath," + os.path.join(base, "lib"), "-L" + PKG_DIR, "-l:libswiglu.so", "-Wl,-rpath,$ORIGIN"],
-            torch.__version__ + " " + sysconfig.get_config_var("SOABI"))
+             "-Wl,-rpath," + os.path.join(base, "lib"), "-L" + BUILD_DIR, "-l:libswiglu.so", "-Wl,-rpath,$ORIGIN"])
 
 
 def _stamp(nvcc: str) -> str:
@@ -79,10 +91,12 @@ def build_library(force: bool = False, verbose: bool = False) -> str:
     """Compile and link libswiglu.so if it is missing or stale; return its path."""
     nvcc = _nvcc()
     stamp = _stamp(nvcc)
-    if not force and all(os.path.exists(f) for f in (LIB_PATH, CALLS_PATH, STAMP)):
+    if not force and os.path.exists(LIB_PATH) and os.path.exists(STAMP):
         with open(STAMP) as f:
-            if f.read().strip() == stamp:
-                return LIB_PATH
+            was = f.read().split()
+        # (a second word: _torch_calls.so was left out)
+        if was and was[0] == stamp and (len(was) > 1 or os.path.exists(CALLS_PATH)):
+            return LIB_PATH
     os.makedirs(BUILD_DIR, exist_ok=True)
 
     def compile_one(name: str):
@@ -91,19 +105,17 @@ def build_library(force: bool = False, verbose: bool = False) -> str:
         r = subprocess.run(cmd, capture_output=True, text=True)
         return name, obj, r
 
-    cflags, ldflags, _ = _calls_flags()
+    calls_flags = _calls_flags()
     calls_obj = os.path.join(BUILD_DIR, CALLS_SOURCE.replace(".cpp", ".o"))
 
     def compile_calls():
-        cmd = ["g++", "-c", os.path.join(CSRC, CALLS_SOURCE), "-o", calls_obj] + cflags
+        cmd = ["g++", "-c", os.path.join(CSRC, CALLS_SOURCE), "-o", calls_obj] + calls_flags[0]
         return subprocess.run(cmd, capture_output=True, text=True)
 
     with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        calls = ex.submit(compile_calls)
+        calls = ex.submit(compile_calls) if calls_flags else None
         results = list(ex.map(compile_one, SOURCES))
-        calls = calls.result()
-    if calls.returncode != 0:
-        raise RuntimeError(f"g++ failed on {CALLS_SOURCE}:\n{calls.stderr}")
+        calls = calls.result() if calls else None
     log = []
     for name, _, r in results:
         log.append(f"==== {name}\n{r.stdout}{r.stderr}")
@@ -114,21 +126,29 @@ def build_library(force: bool = False, verbose: bool = False) -> str:
     vs = os.path.join(BUILD_DIR, "exports.map")
     with open(vs, "w") as f:
         f.write(VERSION_SCRIPT)
-    tmp = LIB_PATH + ".tmp"
-    cmd = [nvcc, "-shared", "-o", tmp] + [o for _, o, _ in results] + ARCH + [
+    new_lib = os.path.join(BUILD_DIR, os.path.basename(LIB_PATH))
+    cmd = [nvcc, "-shared", "-o", new_lib] + [o for _, o, _ in results] + ARCH + [
         "--cudart", "static", "-Xlinker", "--version-script=" + vs, "-Xlinker", "-z,defs",
         "-lpthread", "-ldl", "-lrt"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}{r.stderr}")
-    os.replace(tmp, LIB_PATH)
-    tmp = CALLS_PATH + ".tmp"
-    r = subprocess.run(["g++", "-shared", "-o", tmp, calls_obj] + ldflags, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}{r.stderr}")
-    os.replace(tmp, CALLS_PATH)
+    new_calls = os.path.join(BUILD_DIR, os.path.basename(CALLS_PATH))
+    if calls and calls.returncode == 0:
+        calls = subprocess.run(["g++", "-shared", "-o", new_calls, calls_obj] + calls_flags[1], capture_output=True,
+                               text=True)
+    left_out = not calls or calls.returncode != 0
+    if left_out:
+        warnings.warn("_torch_calls.so is left out, so the 8-bit calls are made from Python: "
+                      + (calls.stderr if calls else "it needs PyTorch, g++ and Python's headers"), RuntimeWarning)
+    # in place together, after both links
+    os.replace(new_lib, LIB_PATH)
+    if not left_out:
+        os.replace(new_calls, CALLS_PATH)
+    elif os.path.exists(CALLS_PATH):
+        os.remove(CALLS_PATH)
     with open(STAMP, "w") as f:
-        f.write(stamp + "\n")
+        f.write(stamp + (" without-calls" if left_out else "") + "\n")
     if verbose:
         print("\n".join(log))
     return LIB_PATH

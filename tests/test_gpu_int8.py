@@ -392,3 +392,26 @@ def test_a_workspace_for_a_batch_serves_smaller_ones(native, K, N, down, Ms):
             (lambda ws: native.swiglu_forward_int8(a, sa, wp, N, s, s, workspace=ws))
         assert torch.equal(call(ws), call(None))
     native.swiglu_check_device_status()
+
+
+def test_calls_made_from_python_agree(native, monkeypatch):
+    # every 8-bit call without _torch_calls.so
+    M, K, N = 70, 272, 264
+    g = torch.Generator().manual_seed(4)
+    x, b1, b2 = (t.cuda() for t in make_inputs(M, K, N, 5))
+    w, s = codes(g, K, N).cuda(), scales(g, N, 0.01).cuda()
+    wp, w3p, bp = native.swiglu_pack_weights_int8(w, w), native.swiglu_pack_down_weights_int8(w), native.swiglu_pack_weights(b1, b2)
+
+    def calls():
+        q, sa = native.swiglu_quantize_int8(x)
+        y = native.swiglu_forward_int8(q, sa, wp, N, s, s)
+        kept = native.swiglu_forward_checkpoint(x, bp, N)
+        return (q, sa, y, native.swiglu_down_forward_int8(q, sa, w3p, N, s, R=y), *kept, native.swiglu_checkpoint_output(*kept[1:]),
+                *native.swiglu_backward_checkpoint(x, bp, y, *kept[1:]),
+                *native.swiglu_backward_checkpoint(q, bp, y, *kept[1:], scale_a=sa))
+
+    want = calls()
+    monkeypatch.setattr(native, "_calls", native._NoCalls())
+    got = calls()
+    native.swiglu_check_device_status()
+    assert len(want) == len(got) == 15 and all(torch.equal(a, b) for a, b in zip(want, got))
