@@ -485,3 +485,24 @@ def test_pair_kernels_behind_a_kernel_of_many_blocks(native):
     assert all(torch.equal(x, z) for x, z in zip(first, last))
     want = native.swiglu_backward_checkpoint(a, wp, y, *first[1:])
     assert all(torch.equal(x, z) for x, z in zip(grads, want))
+
+
+@pytest.mark.parametrize("M,K,N", [(868, 8192, 10000), (100, 8264, 20000)])
+def test_long_sums_in_several_rounds(native, M, K, N):
+    # from 128 slices of K on rounds of tiles are paced and odd ones walk K backwards: with the
+    # checkpoint's token boxes too (868 tokens: the last tiles' second CTA has none; 100: no second CTA has)
+    assert -(-M // 256) * -(-N // 128) > 2 * 76
+    a, w1, w2 = (t.cuda() for t in make_inputs(M, K, N, 9))
+    wp = native.swiglu_pack_weights(w1, w2)
+    y, gate, up, scale = native.swiglu_forward_checkpoint(a, wp, N)
+    for _ in range(3):
+        again = native.swiglu_forward_checkpoint(a, wp, N)
+    native.swiglu_check_device_status()
+    assert torch.equal(y, native.swiglu_forward_variant(a, wp, N, native.SWIGLU_VARIANT_LARGE_M_PAIR))
+    assert all(torch.equal(p, q) for p, q in zip(again, (y, gate, up, scale)))
+    rows = torch.tensor([0, 1, M // 2, M - 1])
+    at = rows.cuda()
+    for w, c, s in ((w1, gate, scale[0]), (w2, up, scale[1])):
+        x, step = f64(a[at]) @ f64(w), ref.wide(f64(s[:, at]), N)
+        err = K * FP32 * (abs(f64(a[at])) @ abs(f64(w)))
+        assert (abs(f64(c[at]) * step - x) <= (0.5 + 127 * 2 * FP32) * step + err).all()
