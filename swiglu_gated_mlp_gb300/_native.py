@@ -600,6 +600,8 @@ _cur_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 def _output(t, name: str, rows: int, cols: int, dev: int, stream) -> torch.Tensor:
     """A caller's output tensor, checked, or a new one."""
+    if cols < 0:
+        raise ValueError(f"{name} cannot have {cols} columns")
     if t is None:
         return _new_tensor((rows, cols), _BF16, dev, stream)
     if t.dtype is not _BF16 or t.get_device() != dev or not t.is_contiguous():

@@ -62,9 +62,9 @@ struct Args {
     if (ok && a[i] == Py_None) return none;
     return tensor(i);
   }
-  int64_t size(int i) {
+  int64_t size(int i) {  // at most 31 bits, so that the sizes made from it do not overflow
     const int64_t v = ok && PyLong_CheckExact(a[i]) ? PyLong_AsLongLong(a[i]) : -1;
-    if (v < 0) {
+    if (v < 0 || v > 0x7fffffff) {
       PyErr_Clear();
       ok = false;
     }

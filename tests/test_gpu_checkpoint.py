@@ -506,3 +506,13 @@ def test_long_sums_in_several_rounds(native, M, K, N):
         x, step = f64(a[at]) @ f64(w), ref.wide(f64(s[:, at]), N)
         err = K * FP32 * (abs(f64(a[at])) @ abs(f64(w)))
         assert (abs(f64(c[at]) * step - x) <= (0.5 + 127 * 2 * FP32) * step + err).all()
+
+
+@pytest.mark.parametrize("N", [0, -8, 1 << 31, 1 << 55, 1 << 62, 1 << 70, True])
+def test_sizes_that_no_tensor_has(native, N):
+    a, w1, w2 = (t.cuda() for t in make_inputs(4, 64, 136, 1))
+    wp = native.swiglu_pack_weights(w1, w2)
+    for call in (lambda: native.swiglu_forward_checkpoint(a, wp, N),
+                 lambda: native.swiglu_forward_checkpoint(a[:0], wp, N)):
+        with pytest.raises((ValueError, native.SwigluError)):
+            call()
