@@ -220,3 +220,33 @@ def test_the_largest_blocks(native, M, K, N, op):
     gate = ref.product(f64(a), f64(sa), f64(w1[:, at]), f64(s1[cols]))
     up = ref.product(f64(a), f64(sa), f64(w2[:, at]), f64(s2[cols]))
     assert_within(y[:, at], *(ref.gated(*gate, *up) if op == "int8" else ref.added(*gate, 0.0)))
+
+
+def test_two_threads_at_once(native):
+    # the calls let go of the interpreter: two threads, each on its own stream, on shared weights
+    import threading
+
+    K, N = 264, 648
+    (w1, s1), (w2, s2), (w3, s3) = block_weights(native, K, N)
+    wp, w3p = native.swiglu_pack_weights_int8(w1, w2), native.swiglu_pack_down_weights_int8(w3)
+    xs = [make_inputs(M, K, 8, 20 + M)[0].cuda() for M in (3, 200)]
+    alone = [block(native, x, wp, w3p, s1, s2, s3, N, K) for x in xs]
+    streams = [torch.cuda.Stream() for _ in xs]
+    torch.cuda.synchronize()
+    got, ready = [None, None], threading.Barrier(2)
+
+    def work(i):
+        with torch.cuda.stream(streams[i]):
+            ready.wait(30)
+            for _ in range(200):
+                out = block(native, xs[i], wp, w3p, s1, s2, s3, N, K)
+            streams[i].synchronize()
+            got[i] = out
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(60)
+    native.swiglu_check_device_status()
+    assert all(torch.equal(a, b) for a, b in zip(alone, got))
