@@ -501,12 +501,14 @@ SWIGLU_API swiglu_status_t swiglu_down_plan_string_int8(int64_t M, int64_t N, in
  * swiglu_checkpoint_output: Y [M, N] bf16 = SiLU(G) (.) U of the checkpoint's
  *   values, for the down-projection's weight gradient, so that Y need not be
  *   kept. M = 0 is a no-op.
- * swiglu_backward_checkpoint: dA, dW1, dW2 as swiglu_backward, with the
- *   checkpoint's G and U. scale_a NULL: A is bf16 [M, K]. Otherwise A is kept
- *   too: int8 codes [M, K] with one scale per token, scale_a [M] (as from
- *   swiglu_quantize_int8); its values are not rounded again (the codes are the
- *   tensor-core operand, most of the scale goes with dG and dU). A is not read when dW1 is NULL, Wpacked not when dA is (each may
- *   then be NULL). Outputs, NULLs, workspace and M = 0 as for
+ * swiglu_backward_checkpoint: dA, dW1, dW2 as swiglu_backward (dG and dU rounded
+ *   once to bf16 as there), with the checkpoint's G and U. scale_a NULL: A is
+ *   bf16 [M, K]. Otherwise A is kept too: int8 codes [M, K] with one scale per
+ *   token, scale_a [M] (as from swiglu_quantize_int8); its values are not rounded
+ *   again (the codes times the scale's power of two are the tensor-core operand,
+ *   the rest of the scale goes with dG and dU before they are rounded), but where
+ *   the scale is subnormal. A is not read when dW1 is NULL, Wpacked not when dA
+ *   is (each may then be NULL). Outputs, NULLs, workspace and M = 0 as for
  *   swiglu_backward; swiglu_backward_checkpoint_workspace_bytes(M, K, N) bytes
  *   (of this M, as there).
  *   Any scales are taken as they are (finite or not).

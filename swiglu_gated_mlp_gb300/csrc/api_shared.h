@@ -46,8 +46,7 @@ bool encode_2d(CUtensorMap* map, const void* base, uint64_t inner, uint64_t oute
                CUtensorMapSwizzle swizzle,
                CUtensorMapDataType dtype = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16);
 bool encode_3d(CUtensorMap* map, const void* base, const uint64_t dims[3],
-               const uint64_t strides[2], const uint32_t box[3], CUtensorMapSwizzle swizzle,
-               CUtensorMapDataType dtype = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16);
+               const uint64_t strides[2], const uint32_t box[3], CUtensorMapSwizzle swizzle);
 // The packed gate/up weight or down-projection weight in boxes of {64, rows, 1}.
 bool encode_packed_w(CUtensorMap* map, const void* base, int64_t K, int64_t N, uint32_t rows);
 bool encode_packed_down(CUtensorMap* map, const void* base, int64_t N, int64_t H, uint32_t rows);

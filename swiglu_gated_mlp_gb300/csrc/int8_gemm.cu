@@ -104,7 +104,7 @@ __device__ __forceinline__ void mma_f16_ts_pair(uint32_t d_tmem, uint32_t a_tmem
       : "memory");
 }
 
-// `bytes` (a multiple of 16) of consecutive global memory to shared memory, or on their way to L2.
+// `bytes` (a multiple of 16) of consecutive global memory to shared memory.
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
                "l"(src), "r"(bytes), "r"(bar)

@@ -804,11 +804,10 @@ bool encode_2d(CUtensorMap* map, const void* base, uint64_t inner, uint64_t oute
 }
 
 bool encode_3d(CUtensorMap* map, const void* base, const uint64_t dims[3],
-               const uint64_t strides[2], const uint32_t box[3], CUtensorMapSwizzle swizzle,
-               CUtensorMapDataType dtype) {
+               const uint64_t strides[2], const uint32_t box[3], CUtensorMapSwizzle swizzle) {
   const cuuint64_t d[3] = {dims[0], dims[1], dims[2]}, s[2] = {strides[0], strides[1]};
   const cuuint32_t b[3] = {box[0], box[1], box[2]};
-  return encode_cached(map, base, 3, d, s, b, swizzle, dtype);
+  return encode_cached(map, base, 3, d, s, b, swizzle);
 }
 
 bool encode_packed_w(CUtensorMap* map, const void* base, int64_t K, int64_t N, uint32_t rows) {
